@@ -497,6 +497,114 @@ int bf16_linear_mxfp8_with_plan(const void *xq, const void *xs, const void *wq, 
                                 void *out, int M, int N, int K, const bf16l_plan *plan, bf16l_stream_t stream);
 int bf16_linear_mxfp8_split(int M, int N, int K, int threads, int num_sms);
 
+/*
+ * ---- Around the linear: norm, routing, and the 4-bit microscaled form ----
+ *
+ * These follow the conventions at the top of this file (asynchronous, no
+ * allocation, no synchronisation, capturable, errors by return value; flags as
+ * for bf16_linear_ex).  Element-wise arithmetic is fp32 with one rounding where
+ * a narrower type is stored.
+ */
+
+/* Output formats of bf16_rmsnorm beside bf16. */
+typedef enum {
+    BF16L_QUANT_NONE = 0,
+    BF16L_QUANT_FP8 = 1,   /* e4m3 codes with a given per-tensor scale, as bf16_quant_fp8 */
+    BF16L_QUANT_MXFP8 = 2, /* e4m3 codes, one E8M0 scale per 32 elements, as bf16_quant_mxfp8 */
+    BF16L_QUANT_MXFP4 = 3  /* e2m1 codes, one E8M0 scale per 32 elements, as bf16_quant_mxfp4 */
+} bf16l_quant;
+
+/*
+ * bf16_rmsnorm — root-mean-square norm of `rows` rows of H elements:
+ *     h = x                       (residual NULL)
+ *     h = RNE_bf16(x + residual)  (stored in residual_out)
+ *     y = h / sqrt(mean(h^2) + eps) * weight        in fp32
+ *     out = RNE_bf16(y), and / or codes (and scales) of y in the format `quant`
+ * x[rows][ldx] bf16, ldx >= H elements between rows (a column range of a wider
+ * matrix); residual, residual_out, out [rows][H] bf16 dense; weight[H] bf16.
+ * The codes come from the fp32 y, so they round once: codes[rows][H] bytes
+ * (FP8, MXFP8) or [rows][H / 2] (MXFP4), scales[rows][H / 32] (MXFP8, MXFP4);
+ * `scale` is the per-tensor scale of FP8 (device, fp32).  out may be NULL when
+ * quant is not NONE.  residual_out may be residual itself (in place), and
+ * nothing else may overlap an output.  A NaN or an infinity in a row makes that
+ * row's y NaN (as the formula does) and touches no other row.
+ * Any H >= 1; H % 32 == 0 for the MX formats (else BF16L_EUNSUPPORTED).
+ * x needs 2-byte, scale 4-byte, scales 1-byte alignment, the rest 16-byte.
+ */
+int bf16_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
+                 void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,
+                 uint32_t flags, bf16l_stream_t stream);
+
+/* Scores of bf16_route. */
+typedef enum { BF16L_SCORE_SOFTMAX = 0, BF16L_SCORE_SIGMOID = 1 } bf16l_score;
+
+/*
+ * bf16_route — the k experts of each token and their weights, from the router's
+ * logits[tokens][ld] (fp32, or bf16 when logits_bf16 is nonzero; ld >= experts):
+ *   score = softmax over the row's experts, or sigmoid of each logit;
+ *   key   = score + bias (bias[experts] fp32, may be NULL); without bias and
+ *           with group_best == 1 a softmax is ranked by its logits, whose order
+ *           the scores share;
+ *   groups > 1: the experts form `groups` equal runs; a group's key is the sum
+ *           of its group_best (1 or 2) largest keys, and only the experts of
+ *           the top_groups best groups stay;
+ *   ids[tokens][k]: the k largest keys, largest first, equal keys (and groups)
+ *           by lowest index;
+ *   weights[tokens][k]: their scores (never the bias), divided by their sum
+ *           when renormalize is nonzero, times `scale`.
+ * A logit of -inf takes its expert out: score 0, and chosen only when too few
+ * others are left (lowest index first).  A row of -inf alone has weights 0.  A
+ * NaN logit ranks with -inf; it makes every weight of a softmax row NaN.  The
+ * ids are always k different experts.
+ * 1 <= k <= 32, experts <= 1024, groups <= 32 dividing experts, k <= top_groups *
+ * experts / groups, group_best <= experts / groups (else BF16L_EINVAL or, above
+ * the limits, BF16L_EUNSUPPORTED).  Element alignment for every pointer.
+ */
+int bf16_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
+               int experts, int k, int scoring, int groups, int top_groups, int group_best, int renormalize,
+               float scale, int logits_bf16, uint32_t flags, bf16l_stream_t stream);
+
+/*
+ * MXFP4: the OCP microscaling 4-bit format.  Each run of 32 consecutive
+ * elements along K shares one E8M0 scale byte e (value 2^(e - 127)); the
+ * elements are e2m1 codes (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6), two to a byte, the even element in the low half.  Codes are
+ * row-major [rows][K / 2] bytes, scales row-major [rows][K / 32] bytes (no
+ * swizzle).  K % 32 == 0 everywhere (else BF16L_EUNSUPPORTED).
+ *
+ * bf16_quant_mxfp4 — x[rows][K] (bf16) into codes and scales: per block
+ *   s = floor(log2(max |v|)) - 2 clamped below at -127 (an all-zero block gets
+ *   -127), xs = s + 127, codes = e2m1 of v * 2^-s rounded to nearest even,
+ *   saturating at +-6.  A block that holds a NaN gets the scale byte 255 (NaN)
+ *   and codes 0; one that holds an infinity counts its magnitude as 2^128, so
+ *   it keeps the infinity and loses its finite values.
+ * bf16_dequant_mxfp4 — out[rows][K] = RNE_bf16 of the values that codes and
+ *   scales stand for (byte 255: NaN).
+ * Both: x, codes and out 16-byte aligned, no two buffers may overlap.
+ *
+ * bf16_linear_mxfp4 — out[M][N] (bf16) = RNE_bf16( sum over blocks b of
+ *   2^(xs[m][b]-127) * 2^(ws[n][b]-127) * sum_{k in b} e2m1(xq[m][k])
+ *   e2m1(wq[n][k]) (+ bias[n]) ), fp32 accumulation, bias before the one
+ *   rounding.  xq, wq, out and bias 16-byte aligned, xs and ws bytes; out must
+ *   not overlap the inputs.  Any M, any N.  Launches one kernel.
+ *
+ * bf16_linear_mxfp4_dynamic — the same product with x[M][K] in bf16, quantised
+ *   by the call: equal, bit for bit, to bf16_quant_mxfp4 followed by
+ *   bf16_linear_mxfp4.  `workspace` (256-byte aligned, needs no initialisation)
+ *   holds the codes and scales on the way:
+ *   bf16_linear_mxfp4_dynamic_workspace(M, N, K) bytes, 0 where the product
+ *   kernel quantises x itself (then it may be NULL).  A workspace that is too
+ *   small is BF16L_EINVAL.
+ */
+int bf16_quant_mxfp4(const void *x, int64_t rows, int K, void *xq, void *xs, uint32_t flags, bf16l_stream_t stream);
+int bf16_dequant_mxfp4(const void *xq, const void *xs, int64_t rows, int K, void *out, uint32_t flags,
+                       bf16l_stream_t stream);
+int bf16_linear_mxfp4(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                      int M, int N, int K, uint32_t flags, bf16l_stream_t stream);
+int bf16_linear_mxfp4_dynamic(const void *x, const void *wq, const void *ws, const void *bias, void *out, int M, int N,
+                              int K, void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream);
+size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *bf16_linear_strerror(int status);
 

@@ -13,7 +13,8 @@ from ._binding import (BF16LinearError, Call, Device, KERNEL_DOTPROD, KERNEL_NAM
                        KERNEL_WARPMMA, KERNEL_DOTMMA, KERNEL_DOTMMA_WS, KERNEL_TILE_T, new_workspace, plan_ws, run, workspace_size,
                        KERNEL_TILE, LIB_PATH, FLAG_PDL, FLAG_SERIAL, Plan, bf16_linear, bf16_linear_ex, bf16_linear_f32out,
                        bf16_linear_noalloc, bf16_linear_fp8, quant_fp8, fp8_split, quant_mxfp8, bf16_linear_mxfp8,
-                       mxfp8_split, bf16_linear_host,
+                       mxfp8_split, Norm, rmsnorm, route, quant_mxfp4, dequant_mxfp4, bf16_linear_mxfp4,
+                       bf16_linear_mxfp4_dynamic, mxfp4_dynamic_workspace, bf16_linear_host,
                        host_staging_bytes, new_host_staging,
                        bf16_linear_with_plan, device_status,
                        load, make_plan, plan, plan_check, probe_read, selftest_wait, strerror, version)

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libbf16_linear.so")
@@ -69,6 +70,8 @@ _lock = threading.Lock()
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -123,6 +126,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.bf16_linear_mxfp8_with_plan.restype = i32
         lib.bf16_linear_mxfp8_split.argtypes = [i32, i32, i32, i32, i32]
         lib.bf16_linear_mxfp8_split.restype = i32
+        i64, u32, f32 = ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
+        lib.bf16_rmsnorm.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i32, f32, i32, u32, vp]
+        lib.bf16_rmsnorm.restype = i32
+        lib.bf16_route.argtypes = [vp, i64, vp, vp, vp, i64, i32, i32, i32, i32, i32, i32, i32, f32, i32, u32, vp]
+        lib.bf16_route.restype = i32
+        lib.bf16_quant_mxfp4.argtypes = [vp, i64, i32, vp, vp, u32, vp]
+        lib.bf16_quant_mxfp4.restype = i32
+        lib.bf16_dequant_mxfp4.argtypes = [vp, vp, i64, i32, vp, u32, vp]
+        lib.bf16_dequant_mxfp4.restype = i32
+        lib.bf16_linear_mxfp4.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, u32, vp]
+        lib.bf16_linear_mxfp4.restype = i32
+        lib.bf16_linear_mxfp4_dynamic.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, ctypes.c_size_t, u32, vp]
+        lib.bf16_linear_mxfp4_dynamic.restype = i32
+        lib.bf16_linear_mxfp4_dynamic_workspace.argtypes = [i32, i32, i32]
+        lib.bf16_linear_mxfp4_dynamic_workspace.restype = ctypes.c_size_t
         lib.bf16_linear_probe_read.argtypes = [vp, ctypes.c_size_t, i32, i32, vp, ctypes.c_uint32, vp]
         lib.bf16_linear_probe_read.restype = i32
         lib.bf16_linear_noalloc_scratch_bytes.argtypes = []
@@ -494,6 +512,228 @@ def mxfp8_split(M: int, N: int, K: int, threads: int = 128, num_sms: int = 152) 
 def fp8_split(M: int, N: int, K: int, num_sms: int = 152) -> int:
     """The K split bf16_linear_fp8 uses for a shape (host logic, no GPU)."""
     return int(load().bf16_linear_fp8_split(M, N, K, num_sms))
+
+
+def _call(fn, device, stream, *args) -> int:
+    """fn(*args, stream) with `device` current (entering a device context costs more than the call)."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor that work on `stream` (None: the current one) may write at once: it comes from that stream's own memory,
+    so nothing that the current stream still has to read or write can share it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(t, name, dtype, shape, device=None):
+    """t is a contiguous CUDA tensor of this dtype and shape (on `device`, where given)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the input on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, name):
+    """(rows, columns, elements between rows) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name}'s rows must be contiguous and apart, got strides {t.stride()}")
+    return rows, cols, max(ld, cols)
+
+
+QUANT_FORMATS = {None: 0, "fp8": 1, "mxfp8": 2, "mxfp4": 3}
+
+
+class Norm(NamedTuple):
+    """What rmsnorm gives: the norm in bf16, x + residual, and the codes and scales of the asked format (or None)."""
+    out: object
+    residual: object
+    codes: object
+    scales: object
+
+
+def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, quant: str | None = None, scale=None, bf16_out: bool = True,
+            out=None, residual_out=None, codes=None, scales=None, flags: int = 0, stream=None) -> Norm:
+    """Root-mean-square norm of the rows of x[rows, H] (bf16_rmsnorm): h = x, or the bf16 sum x + residual[rows, H];
+    y = h / sqrt(mean(h^2) + eps) * weight[H] in fp32.  Gives y in bf16 (left out with bf16_out=False), h where there is a
+    residual, and y's codes in `quant`: "fp8" (e4m3 with the one-element fp32 CUDA tensor `scale`), "mxfp8" or "mxfp4"
+    (uint8 codes [rows, H] or [rows, H / 2], uint8 E8M0 scales [rows, H / 32]).  All bf16; x may be a column range of a
+    wider matrix.  residual_out may be residual itself (in place)."""
+    import torch
+    bf16 = torch.bfloat16
+    if x.dtype != bf16:
+        raise TypeError(f"x must be torch.bfloat16 (got {x.dtype})")
+    if quant not in QUANT_FORMATS:
+        raise ValueError(f"quant must be one of {list(QUANT_FORMATS)}, got {quant!r}")
+    rows, H, ld = _rows(x, "x")
+    dev, shape = x.device, x.shape
+    w = _need(weight, "weight", bf16, (H,), dev)
+    r = ro = o = c = sc = s1 = None
+    if residual is not None:
+        r = _need(residual, "residual", bf16, shape, dev)
+        if residual_out is None:
+            residual_out = _empty(shape, bf16, dev, stream)
+        ro = _need(residual_out, "residual_out", bf16, shape, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if bf16_out:
+        if out is None:
+            out = _empty(shape, bf16, dev, stream)
+        o = _need(out, "out", bf16, shape, dev)
+    elif out is not None or quant is None:
+        raise ValueError("bf16_out=False needs a quant format and no out")
+    if quant is None:
+        if codes is not None or scales is not None or scale is not None:
+            raise ValueError("codes, scales and scale need a quant format")
+    else:
+        packed = (rows, H // 2 if quant == "mxfp4" else H)
+        if codes is None:
+            codes = _empty(packed, torch.uint8, dev, stream)
+        c = _need(codes, "codes", torch.uint8, packed, dev)
+        if quant == "fp8":
+            if scale is None or scales is not None:
+                raise ValueError("quant='fp8' takes the one-element `scale` and no `scales`")
+            s1 = _need(scale.reshape(-1), "scale", torch.float32, (1,), dev)
+        else:
+            if scale is not None:
+                raise ValueError("scale is for quant='fp8'")
+            if scales is None:
+                scales = _empty((rows, H // 32), torch.uint8, dev, stream)
+            sc = _need(scales, "scales", torch.uint8, (rows, H // 32), dev)
+    st = _call(load().bf16_rmsnorm, dev, stream, x.data_ptr(), ld, r, w, o, ro, c, sc, s1, rows, H, eps,
+               QUANT_FORMATS[quant], flags)
+    if st != OK:
+        _raise(st, f"bf16_rmsnorm(rows={rows}, H={H}, quant={quant})")
+    return Norm(out, residual_out, codes, scales)
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def route(logits, k: int, *, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_best: int = 1, renormalize: bool = True, scale: float = 1.0, weights=None, ids=None, flags: int = 0,
+          stream=None):
+    """The k experts of each token from the router's logits[tokens, experts], fp32 or bf16 (bf16_route): (weights fp32
+    [tokens, k], ids int32 [tokens, k]), the best first.  scoring "softmax" or "sigmoid"; bias[experts] (fp32) is added to
+    the scores for the choice alone; with groups > 1 only the experts of the top_groups best of `groups` equal runs of
+    experts stay, a group ranked by the sum of its group_best largest.  renormalize divides the weights by their sum; scale
+    multiplies them.  Experts with a logit of -inf are out."""
+    import torch
+    if logits.dtype != torch.float32 and logits.dtype != torch.bfloat16:
+        raise TypeError(f"logits must be float32 or bfloat16 (got {logits.dtype})")
+    if scoring not in SCORES:
+        raise ValueError(f"scoring must be one of {list(SCORES)}, got {scoring!r}")
+    T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    b = None if bias is None else _need(bias, "bias", torch.float32, (E,), dev)
+    if weights is None:
+        weights = _empty((T, max(k, 0)), torch.float32, dev, stream)
+    if ids is None:
+        ids = _empty((T, max(k, 0)), torch.int32, dev, stream)
+    st = _call(load().bf16_route, dev, stream, logits.data_ptr(), ld, b, _need(weights, "weights", torch.float32, (T, k), dev),
+               _need(ids, "ids", torch.int32, (T, k), dev), T, E, k, SCORES[scoring], groups, top_groups, group_best,
+               renormalize, scale, logits.dtype == torch.bfloat16, flags)
+    if st != OK:
+        _raise(st, f"bf16_route(tokens={T}, experts={E}, k={k}, groups={groups}, top_groups={top_groups})")
+    return weights, ids
+
+
+def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
+    """MXFP4 quantisation (bf16_quant_mxfp4) of a contiguous bf16 CUDA tensor x[rows, K], K % 32 == 0: returns (codes uint8
+    [rows, K / 2], two to a byte, scales uint8 [rows, K / 32])."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    rows, K = x.shape
+    dev, u8 = x.device, torch.uint8
+    p = _need(x, "x", torch.bfloat16, x.shape)
+    if out is None:
+        out = _empty((rows, K // 2), u8, dev, stream)
+    if scales is None:
+        scales = _empty((rows, K // 32), u8, dev, stream)
+    st = _call(load().bf16_quant_mxfp4, dev, stream, p, rows, K, _need(out, "out", u8, (rows, K // 2), dev),
+               _need(scales, "scales", u8, (rows, K // 32), dev), flags)
+    if st != OK:
+        _raise(st, f"bf16_quant_mxfp4(rows={rows}, K={K})")
+    return out, scales
+
+
+def dequant_mxfp4(codes, scales, out=None, flags: int = 0, stream=None):
+    """The bf16 values [rows, K] that MXFP4 codes [rows, K / 2] and scales [rows, K / 32] stand for (bf16_dequant_mxfp4)."""
+    import torch
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be 2-D, got {tuple(codes.shape)}")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    dev, u8 = codes.device, torch.uint8
+    q = _need(codes, "codes", u8, codes.shape)
+    s = _need(scales, "scales", u8, (rows, K // 32), dev)
+    if out is None:
+        out = _empty((rows, K), torch.bfloat16, dev, stream)
+    st = _call(load().bf16_dequant_mxfp4, dev, stream, q, s, rows, K, _need(out, "out", torch.bfloat16, (rows, K), dev), flags)
+    if st != OK:
+        _raise(st, f"bf16_dequant_mxfp4(rows={rows}, K={K})")
+    return out
+
+
+def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, stream=None):
+    """MXFP4 linear (bf16_linear_mxfp4): packed e2m1 codes xq[M, K / 2], wq[N, K / 2] with E8M0 block scales xs[M, K / 32],
+    ws[N, K / 32] (all uint8), optional bf16 bias[N]; bf16 out[M, N]."""
+    import torch
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError(f"need xq[M, K / 2] and wq[N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
+    (M, h), N, dev, u8 = xq.shape, wq.shape[0], xq.device, torch.uint8
+    args = (_need(xq, "xq", u8, (M, h)), _need(xs, "xs", u8, (M, h // 16), dev), _need(wq, "wq", u8, (N, h), dev),
+            _need(ws, "ws", u8, (N, h // 16), dev), None if bias is None else _need(bias, "bias", torch.bfloat16, (N,), dev))
+    if out is None:
+        out = _empty((M, N), torch.bfloat16, dev, stream)
+    st = _call(load().bf16_linear_mxfp4, dev, stream, *args, _need(out, "out", torch.bfloat16, (M, N), dev), M, N, 2 * h, flags)
+    if st != OK:
+        _raise(st, f"bf16_linear_mxfp4(M={M}, N={N}, K={2 * h})")
+    return out
+
+
+def mxfp4_dynamic_workspace(M: int, N: int, K: int) -> int:
+    """Workspace bytes of bf16_linear_mxfp4_dynamic (0 where the product quantises x itself)."""
+    return int(load().bf16_linear_mxfp4_dynamic_workspace(M, N, K))
+
+
+def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, flags: int = 0, stream=None):
+    """MXFP4 linear with x[M, K] in bf16, quantised by the call (bf16_linear_mxfp4_dynamic): bit for bit quant_mxfp4 and
+    then bf16_linear_mxfp4.  `workspace`: a contiguous CUDA tensor of at least mxfp4_dynamic_workspace(M, N, K) bytes to
+    reuse from call to call on one stream; allocated for the call when None."""
+    import torch
+    if x.dim() != 2 or wq.dim() != 2:
+        raise ValueError(f"need x[M, K] and wq[N, K / 2], got {tuple(x.shape)} and {tuple(wq.shape)}")
+    (M, K), N, dev, u8, bf16 = x.shape, wq.shape[0], x.device, torch.uint8, torch.bfloat16
+    args = (_need(x, "x", bf16, (M, K)), _need(wq, "wq", u8, (N, K // 2), dev), _need(ws, "ws", u8, (N, K // 32), dev),
+            None if bias is None else _need(bias, "bias", bf16, (N,), dev))
+    if out is None:
+        out = _empty((M, N), bf16, dev, stream)
+    lib = load()
+    if workspace is None:
+        need = lib.bf16_linear_mxfp4_dynamic_workspace(M, N, K)
+        if need:
+            workspace = _empty(need, u8, dev, stream)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on x's device")
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = _call(lib.bf16_linear_mxfp4_dynamic, dev, stream, *args, _need(out, "out", bf16, (M, N), dev), M, N, K, wp, wn, flags)
+    if st != OK:
+        _raise(st, f"bf16_linear_mxfp4_dynamic(M={M}, N={N}, K={K})")
+    return out
 
 
 def probe_read(src, grid: int, threads: int, sink, nbytes: int | None = None, stream=None, flags: int = 0):

@@ -65,6 +65,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_warpmma_ks();
         if (!e) e = init_dotmma();
         if (!e) e = init_mxfp8();
+        if (!e) e = init_mxfp4();
     }
     s.err = e;
 }
@@ -192,10 +193,11 @@ __global__ void selftest_wait_kernel(int32_t *status, uint64_t limit_ns) {
 
 }  // namespace
 
-int current_device_checked(bf16l_device *dev) {
+int current_device_checked(bf16l_device *dev, int32_t **status) {
     DeviceState *ds = nullptr;
     const int st = current_device(&ds);
     if (st == BF16L_OK && dev) *dev = ds->dev;
+    if (st == BF16L_OK && status) *status = ds->status;
     return st;
 }
 

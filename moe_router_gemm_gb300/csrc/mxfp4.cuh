@@ -1,0 +1,71 @@
+// mxfp4.cuh — device helpers of the 4-bit microscaled format: 32 elements along
+// K share one E8M0 scale byte e (2^(e - 127), 255 = NaN), the elements are e2m1
+// codes (sign, 2 exponent bits of bias 1, 1 mantissa bit), two to a byte.
+#pragma once
+
+#include "common.cuh"
+
+namespace bf16l {
+
+// 2^(e - 127) as fp32: normal for e in 1..254, the subnormal 2^-127 for 0, NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t e) {
+    return __uint_as_float(e == 0 ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23);
+}
+
+// Eight fp32 values -> eight e2m1 codes in one word, v[0] in the low four bits:
+// round to nearest even, saturating at +-6.
+__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// The block's scale exponent s = max(floor(log2 amax) - top, -127) from amax's
+// bits (fp32, finite or infinite, sign clear): the exponent field is floor(log2)
+// + 127, and 0 (zero and subnormals) lies below the clamp.  top: the exponent of
+// the element format's largest binade (2 for e2m1, 8 for e4m3).
+__device__ __forceinline__ int mx_scale_exp(uint32_t amax_bits, int top) {
+    const int s = (int)(amax_bits >> 23) - 127 - top;
+    return s < -127 ? -127 : s;
+}
+
+// 2^-s for s in [-127, 126]: always a normal fp32 number.
+__device__ __forceinline__ float exp2_neg(int s) { return __uint_as_float((uint32_t)(127 - s) << 23); }
+
+// Quantise 8 consecutive bf16 values (one 16-byte vector) of a block that four
+// neighbouring lanes (a quad) hold: the codes of this lane's 8 values, and the
+// scale byte.  All four lanes of the quad must call it together.  Magnitudes
+// compare as integers, so a NaN is the largest and shows in the maximum.
+__device__ __forceinline__ uint32_t mxfp4_quant_vec(const uint4 &w, unsigned quad, uint32_t &scale_byte) {
+    uint32_t m2 = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                           __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    m2 = __vmaxu2(m2, __shfl_xor_sync(quad, m2, 1));
+    m2 = __vmaxu2(m2, __shfl_xor_sync(quad, m2, 2));
+    const uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
+    const bool nan = amax > 0x7F80u;
+    const int s = mx_scale_exp(amax << 16, 2);
+    const float inv = exp2_neg(nan ? 0 : s);
+    const float f[8] = {bf16_lo(w.x) * inv, bf16_hi(w.x) * inv, bf16_lo(w.y) * inv, bf16_hi(w.y) * inv,
+                        bf16_lo(w.z) * inv, bf16_hi(w.z) * inv, bf16_lo(w.w) * inv, bf16_hi(w.w) * inv};
+    scale_byte = nan ? 255u : (uint32_t)(s + 127);
+    return nan ? 0u : e2m1x8(f);
+}
+
+// Eight e2m1 codes (one word) as e4m3 codes, the even elements in `even` and the
+// odd ones in `odd` (byte i: element 2i or 2i + 1).  The e2m1 fields land in the
+// low exponent and high mantissa bits of e4m3 (bias 7 instead of 1), so each
+// e4m3 value is the e2m1 value times 2^-6, exactly, e2m1's subnormal included.
+__device__ __forceinline__ void e2m1_to_e4m3(uint32_t w, uint32_t &even, uint32_t &odd) {
+    const uint32_t u = w << 4;
+    even = (u & 0x80808080u) | ((u >> 2) & 0x1C1C1C1Cu);
+    odd = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
+}
+
+}  // namespace bf16l

@@ -1,0 +1,208 @@
+"""MXFP4 on the GPU: quantisation and its values bit for bit, the linear within a derived bound (moe_ref.linear_bound)."""
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _u8(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def _spread(rows, K, seed):
+    """bf16 values whose blocks lie 80 binades apart."""
+    g = torch.Generator().manual_seed(seed)
+    mag = torch.exp2(torch.randint(-40, 40, (rows, K // 32), generator=g).double()).repeat_interleave(32, dim=1)
+    return (torch.randn(rows, K, generator=g, dtype=torch.float64) * mag).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (7, 2880), (16, 7168), (129, 160), (1, 64)])
+def test_quant_and_values(lib, rows, K):
+    x = _spread(rows, K, rows + K)
+    q, s = lib.quant_mxfp4(x.to(DEV))
+    wq, ws = ref.quant_mxfp4(ref.f64(x))
+    assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
+    v = lib.dequant_mxfp4(q, s)
+    assert np.array_equal(ref.f64(v), ref.values_mxfp4(wq, ws))
+
+
+def test_quant_edge_blocks(lib):
+    ties = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.5, 6.0, 7.0]
+    blocks = [[0.0] * 32, [-0.0] * 32,
+              (ties + [-t for t in ties] + [0.5] * 32)[:32],             # every tie, the last ones past the largest code
+              [2.0 ** -133, -(2.0 ** -130)] + [0.0] * 30,                # bf16 subnormals: the exponent clamps at -127
+              [2.0 ** 100, 2.0 ** 97, -(2.0 ** 90)] + [3.0] * 29,
+              [1.0] * 31 + [-(2.0 ** 127) * 1.9921875]]                  # bf16's largest magnitude
+    x = ref.bf16(blocks)
+    q, s = lib.quant_mxfp4(x.to(DEV))
+    wq, ws = ref.quant_mxfp4(ref.f64(x))
+    assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
+
+
+def test_quant_nan_and_infinity(lib):
+    x = _spread(4, 96, 3).to(DEV)
+    clean = lib.quant_mxfp4(x)
+    x[1, 40] = float("nan")
+    x[2, 0] = -float("inf")
+    q, s = lib.quant_mxfp4(x)
+    v = lib.dequant_mxfp4(q, s)
+    assert v[1, 32:64].isnan().all() and int(s[1, 1]) == 255 and (q[1, 16:32] == 0).all()
+    assert v[2, 0] == -float("inf") and (v[2, 1:32] == 0).all()
+    keep = torch.ones(4, 3, dtype=torch.bool, device=DEV)
+    keep[1, 1] = keep[2, 0] = False
+    assert torch.equal(s[keep], clean[1][keep])
+    assert torch.equal(q.view(4, 3, 16)[keep], clean[0].view(4, 3, 16)[keep])
+
+
+def test_values_of_every_code_and_scale(lib):
+    """All 16 codes under all 256 scale bytes."""
+    q = np.tile(np.repeat(np.arange(8, dtype=np.uint8) * 2 + 16 * (np.arange(8, dtype=np.uint8) * 2 + 1), 2), (256, 1))
+    s = np.arange(256, dtype=np.uint8)[:, None]
+    v = ref.f64(lib.dequant_mxfp4(_u8(q), _u8(s)))
+    with np.errstate(over="ignore"):
+        want = ref.f64(torch.from_numpy(ref.values_mxfp4(q, s)).to(torch.bfloat16))
+    assert np.array_equal(v, want, equal_nan=True)
+
+
+def _operands(M, N, K, seed, bias):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g).mul(torch.exp2(3 * torch.randn(M, 1, generator=g))).to(torch.bfloat16)
+    w = (torch.randn(N, K, generator=g) * K ** -0.5).to(torch.bfloat16)
+    b = (torch.rand(N, generator=g) - 0.5).to(torch.bfloat16).to(DEV) if bias else None
+    return x.to(DEV), *lib_quant(w), b
+
+
+def lib_quant(w):
+    q, s = ref.quant_mxfp4(ref.f64(w))
+    return _u8(q), _u8(s)
+
+
+SHAPES = [(1, 1, 32), (1, 256, 7168), (4, 256, 2048), (16, 384, 7168), (9, 128, 2880), (5, 33, 96), (8, 2112, 7168),
+          (13, 77, 160), (17, 300, 1024), (32, 1000, 512), (40, 520, 544), (64, 2112, 2880), (100, 64, 4096),
+          (128, 256, 256), (129, 257, 288), (200, 1536, 1024), (300, 700, 2080), (513, 513, 96), (1000, 2112, 640),
+          (257, 4096, 512), (2048, 130, 256), (1, 14336, 4096), (64, 14336, 256), (700, 3000, 32)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear(lib, shape, bias):
+    M, N, K = shape
+    x, wq, ws, b = _operands(M, N, K, M + N + K, bias)
+    xq, xs = lib.quant_mxfp4(x)
+    got = lib.bf16_linear_mxfp4(xq, xs, wq, ws, b)
+    xv = ref.values_mxfp4(xq.cpu().numpy(), xs.cpu().numpy())
+    wv = ref.values_mxfp4(wq.cpu().numpy(), ws.cpu().numpy())
+    ref.check_linear(got, xv, wv, None if b is None else ref.f64(b), K, str(shape))
+    # quantised by the call: the same bits, with and without a workspace of the caller's
+    assert torch.equal(lib.bf16_linear_mxfp4_dynamic(x, wq, ws, b), got)
+    space = torch.full((max(256, lib.mxfp4_dynamic_workspace(M, N, K)),), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(lib.bf16_linear_mxfp4_dynamic(x, wq, ws, b, workspace=space), got)
+    assert torch.equal(lib.bf16_linear_mxfp4(xq, xs, wq, ws, b), got)
+    assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 640), (13, 72, 640), (70, 130, 1184), (300, 600, 1024), (300, 520, 1120)])
+def test_linear_random_codes_and_scales(lib, M, N, K):
+    """Every block's scale has to reach its own block: random codes, scales over 34 binades."""
+    rng = np.random.default_rng(M + N + K)
+    xq, wq = (rng.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    xs, ws = (rng.integers(110, 145, (r, K // 32)).astype(np.uint8) for r in (M, N))
+    got = lib.bf16_linear_mxfp4(_u8(xq), _u8(xs), _u8(wq), _u8(ws))
+    ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 64, 256), (20, 64, 256), (300, 520, 512)])
+def test_linear_extreme_scales(lib, M, N, K):
+    """Scale bytes at the ends of their range whose product is an ordinary number, and a NaN scale."""
+    rng = np.random.default_rng(M)
+    xq, wq = (rng.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    for ex, ew in ((254, 1), (0, 252), (20, 235)):
+        xs, ws = np.full((M, K // 32), ex, np.uint8), np.full((N, K // 32), ew, np.uint8)
+        got = lib.bf16_linear_mxfp4(_u8(xq), _u8(xs), _u8(wq), _u8(ws))
+        ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K, f"{ex} {ew}")
+    xs, ws = np.full((M, K // 32), 127, np.uint8), np.full((N, K // 32), 120, np.uint8)
+    xs[1, 3], ws[5, 0] = 255, 255
+    got = lib.bf16_linear_mxfp4(_u8(xq), _u8(xs), _u8(wq), _u8(ws))
+    ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K, "NaN scale")
+
+
+def test_linear_views_streams_and_graph(lib):
+    """Byte-aligned scales, a side stream, a captured graph: the same bits."""
+    M, N, K = 24, 300, 2880
+    x, wq, ws, b = _operands(M, N, K, 5, True)
+    xq, xs = lib.quant_mxfp4(x)
+    want = lib.bf16_linear_mxfp4(xq, xs, wq, ws, b)
+    odd = [torch.empty(t.numel() + 1, dtype=torch.uint8, device=DEV)[1:].view(t.shape) for t in (xs, ws)]
+    for o, t in zip(odd, (xs, ws)):
+        o.copy_(t)
+    assert torch.equal(lib.bf16_linear_mxfp4(xq, odd[0], wq, odd[1], b), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = lib.bf16_linear_mxfp4_dynamic(x, wq, ws, b, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(want)
+    space = torch.empty(max(256, lib.mxfp4_dynamic_workspace(M, N, K)), dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.bf16_linear_mxfp4_dynamic(x, wq, ws, b, out=out, workspace=space)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_linear_offsets_past_32_bits(lib, M):
+    """A weight of more than 2^32 elements: its last rows against the same rows alone."""
+    N, K = 524280, 8224
+    assert N * K > 2 ** 32
+    wq = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    ws = torch.randint(118, 122, (N, K // 32), dtype=torch.uint8, device=DEV)
+    xq, xs = lib.quant_mxfp4(torch.randn(M, K, device=DEV).to(torch.bfloat16))
+    got = lib.bf16_linear_mxfp4(xq, xs, wq, ws)[:, -40:]
+    xv, wv = ref.values_mxfp4(xq.cpu().numpy(), xs.cpu().numpy()), ref.values_mxfp4(wq[-40:].cpu().numpy(), ws[-40:].cpu().numpy())
+    ref.check_linear(got, xv, wv, None, K)
+
+
+def test_quant_offsets_past_32_bits(lib):
+    rows, K = 600000, 7200
+    assert rows * K > 2 ** 32
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[-5:] = torch.randn(5, K, device=DEV).to(torch.bfloat16)
+    x[:-5] = 1.0
+    q, s = lib.quant_mxfp4(x)
+    wq, ws = ref.quant_mxfp4(ref.f64(x[-5:]))
+    assert np.array_equal(q[-5:].cpu().numpy(), wq) and np.array_equal(s[-5:].cpu().numpy(), ws)
+    assert torch.equal(lib.dequant_mxfp4(q, s, out=x)[-5:], lib.dequant_mxfp4(q[-5:], s[-5:]))
+    assert (x[0] == 1.0).all()
+
+
+def test_empty_and_refusals(lib):
+    x, wq, ws, b = _operands(4, 64, 96, 1, True)
+    xq, xs = lib.quant_mxfp4(x)
+    assert lib.bf16_linear_mxfp4(xq[:0], xs[:0], wq, ws).shape == (0, 64)
+    assert lib.bf16_linear_mxfp4_dynamic(x[:0], wq, ws).shape == (0, 64)
+    assert lib.quant_mxfp4(x[:0])[0].shape == (0, 48)
+    with pytest.raises(lib.BF16LinearError) as e:
+        lib.quant_mxfp4(torch.zeros(2, 48, dtype=torch.bfloat16, device=DEV))
+    assert e.value.status == -6
+    with pytest.raises(ValueError):
+        lib.bf16_linear_mxfp4(xq, xs[:, :2], wq, ws)
+    with pytest.raises(ValueError):
+        lib.bf16_linear_mxfp4(xq, xs, wq[:, :47].contiguous(), ws)
+    with pytest.raises(ValueError):
+        lib.bf16_linear_mxfp4_dynamic(x.float(), wq, ws)
+    with pytest.raises(ValueError):
+        lib.bf16_linear_mxfp4(xq, xs, wq, ws, bias=b.float())
+    with pytest.raises(ValueError):
+        lib.dequant_mxfp4(xq, xs[:3])
+    need = lib.mxfp4_dynamic_workspace(200, 64, 96)
+    big = torch.zeros(200, 96, dtype=torch.bfloat16, device=DEV)
+    if need:
+        with pytest.raises(lib.BF16LinearError) as e:
+            lib.bf16_linear_mxfp4_dynamic(big, wq, ws, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+        assert e.value.status == -1
