@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "moe.h"
 
 namespace bf16l {
 
@@ -193,12 +194,20 @@ __global__ void selftest_wait_kernel(int32_t *status, uint64_t limit_ns) {
 
 }  // namespace
 
-int current_device_checked(bf16l_device *dev, int32_t **status) {
+int current_device_checked(bf16l_device *dev) {
     DeviceState *ds = nullptr;
     const int st = current_device(&ds);
     if (st == BF16L_OK && dev) *dev = ds->dev;
-    if (st == BF16L_OK && status) *status = ds->status;
     return st;
+}
+
+int current_device_status(bf16l_device *dev, int32_t **status) {
+    DeviceState *ds = nullptr;
+    const int st = current_device(&ds);
+    if (st != BF16L_OK) return st;
+    *dev = ds->dev;
+    *status = ds->status;
+    return BF16L_OK;
 }
 
 int note_cuda_error(int cuda_err) { return note(cuda_err); }

@@ -4,7 +4,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "moe.h"
 
 namespace bf16l {
 
@@ -167,7 +167,7 @@ extern "C" int bf16_linear_mxfp4(const void *xq, const void *xs, const void *wq,
     if (clash(outs, ins)) return BF16L_EINVAL;
     bf16l_device dev;
     int32_t *status = nullptr;
-    st = current_device_checked(&dev, &status);
+    st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
     return result(launch_mxfp4(xq, xs, wq, ws, bias, out, M, N, K, mxfp8_split(M, N, K, 128, dev.num_sms), 128, flags,
                                stream, status));

@@ -125,8 +125,7 @@ constexpr int kGb300Sms = 152;
 // The current device, initialised once (kernel attributes) and checked to be
 // compute capability 10.3: BF16L_OK and *dev filled, else the status to return
 // (a failed CUDA call is recorded for bf16_linear_cuda_error).  Defined in api.cu.
-// *status: the device's kernel status word, where asked.
-int current_device_checked(bf16l_device *dev, int32_t **status = nullptr);
+int current_device_checked(bf16l_device *dev);
 // Record a CUDA error code for bf16_linear_cuda_error (0 is ignored); returns it.
 int note_cuda_error(int cuda_err);
 
@@ -193,23 +192,6 @@ int mxtile_max_stages(int bq);
 int launch_mxfp8_tile(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                       int M, int N, int K, int bq, int stages, int group, int grid, uint32_t flags, void *stream,
                       int32_t *status);
-
-// MXFP4 (mxfp4.cu): quantisation and its inverse (n values, n % 32 == 0), and the block-scaled linear on
-// warp-level e4m3 MMAs (K % 32 == 0; grid.z covers any M in groups of 16 tokens; S: CTAs per cluster along K).
-int init_mxfp4();
-int launch_quant_mxfp4(const void *x, void *q, void *scales, long long n, int num_sms, uint32_t flags, void *stream);
-int launch_dequant_mxfp4(const void *q, const void *scales, void *out, long long n, int num_sms, uint32_t flags,
-                         void *stream);
-int launch_mxfp4(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out, int M,
-                 int N, int K, int S, int threads, uint32_t flags, void *stream, int32_t *status);
-// Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
-int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
-                   void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,
-                   int num_sms, uint32_t flags, void *stream);
-constexpr int kRouteMaxExperts = 1024, kRouteMaxPicks = 32, kRouteMaxGroups = 32;
-int launch_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
-                 int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
-                 int logits_bf16, int num_sms, uint32_t flags, void *stream);
 
 // One-time per-device kernel attribute setup (dynamic shared memory limits,
 // non-portable cluster sizes).  Returns a cudaError_t value.

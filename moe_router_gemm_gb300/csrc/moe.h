@@ -1,0 +1,31 @@
+// moe.h — internal interface between the C ABI of the operators around the
+// linear (api_moe.cu) and their kernels.  Launchers return a cudaError_t value
+// (0 on success); arguments have passed the checks of api_moe.cu.
+#pragma once
+
+#include "kernels.h"
+
+namespace bf16l {
+
+// As current_device_checked, with the device's kernel status word.  Defined in api.cu.
+int current_device_status(bf16l_device *dev, int32_t **status);
+
+// MXFP4 (mxfp4.cu): quantisation and its inverse (n values, n % 32 == 0), and the block-scaled linear on
+// warp-level e4m3 MMAs (K % 32 == 0; grid.z covers any M in groups of 16 tokens; S: CTAs per cluster along K).
+int init_mxfp4();
+int launch_quant_mxfp4(const void *x, void *q, void *scales, long long n, int num_sms, uint32_t flags, void *stream);
+int launch_dequant_mxfp4(const void *q, const void *scales, void *out, long long n, int num_sms, uint32_t flags,
+                         void *stream);
+int launch_mxfp4(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out, int M,
+                 int N, int K, int S, int threads, uint32_t flags, void *stream, int32_t *status);
+
+// Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
+int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
+                   void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,
+                   int num_sms, uint32_t flags, void *stream);
+constexpr int kRouteMaxExperts = 1024, kRouteMaxPicks = 32, kRouteMaxGroups = 32;
+int launch_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
+                 int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
+                 int logits_bf16, int num_sms, uint32_t flags, void *stream);
+
+}  // namespace bf16l

@@ -24,7 +24,7 @@
 //     adds bias, rounds, stores: the order never changes.
 #include <cuda_runtime.h>
 
-#include "kernels.h"
+#include "moe.h"
 #include "mxfp4.cuh"
 
 namespace bf16l {

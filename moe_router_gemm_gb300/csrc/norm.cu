@@ -16,7 +16,7 @@
 //     time from L1 or L2).
 #include <cuda_runtime.h>
 
-#include "kernels.h"
+#include "moe.h"
 #include "mxfp4.cuh"
 
 namespace bf16l {

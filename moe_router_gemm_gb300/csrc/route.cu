@@ -9,7 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "moe.h"
 
 namespace bf16l {
 
