@@ -517,10 +517,12 @@ def fp8_split(M: int, N: int, K: int, num_sms: int = 152) -> int:
 def _call(fn, device, stream, *args) -> int:
     """fn(*args, stream) with `device` current (entering a device context costs more than the call)."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+    i = device.index
+    if torch._C._cuda_getDevice() == i:
+        # the raw handle: building a torch.cuda.Stream for it takes as long as the launch
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
     with torch.cuda.device(device):
-        return fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -533,25 +535,28 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need(t, name, dtype, shape, device=None):
-    """t is a contiguous CUDA tensor of this dtype and shape (on `device`, where given)."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the input on {device}")
-    return t.data_ptr()
+def _need(t, name, dtype, shape, device):
+    """The address of t, a contiguous CUDA tensor of this dtype and shape on `device`."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _rows(t, name):
-    """(rows, columns, elements between rows) of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda:
+def _cuda(t, name):
+    """t's device, a CUDA one."""
+    if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
+    return t.device
+
+
+def _pitch(t, name):
+    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
     rows, cols = t.shape
     ld, step = t.stride()
     if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name}'s rows must be contiguous and apart, got strides {t.stride()}")
-    return rows, cols, max(ld, cols)
+    return ld if ld > cols else cols
 
 
 QUANT_FORMATS = {None: 0, "fp8": 1, "mxfp8": 2, "mxfp4": 3}
@@ -573,36 +578,40 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, quant: str | None = 
     (uint8 codes [rows, H] or [rows, H / 2], uint8 E8M0 scales [rows, H / 32]).  All bf16; x may be a column range of a
     wider matrix.  residual_out may be residual itself (in place)."""
     import torch
-    bf16 = torch.bfloat16
-    if x.dtype != bf16:
+    bf16, u8 = torch.bfloat16, torch.uint8
+    if x.dtype is not bf16:
         raise TypeError(f"x must be torch.bfloat16 (got {x.dtype})")
     if quant not in QUANT_FORMATS:
         raise ValueError(f"quant must be one of {list(QUANT_FORMATS)}, got {quant!r}")
-    rows, H, ld = _rows(x, "x")
-    dev, shape = x.device, x.shape
+    dev, shape, ld = _cuda(x, "x"), x.shape, _pitch(x, "x")
+    rows, H = shape
     w = _need(weight, "weight", bf16, (H,), dev)
     r = ro = o = c = sc = s1 = None
     if residual is not None:
         r = _need(residual, "residual", bf16, shape, dev)
         if residual_out is None:
             residual_out = _empty(shape, bf16, dev, stream)
-        ro = _need(residual_out, "residual_out", bf16, shape, dev)
+            ro = residual_out.data_ptr()
+        else:
+            ro = _need(residual_out, "residual_out", bf16, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    if bf16_out:
-        if out is None:
-            out = _empty(shape, bf16, dev, stream)
+    if not bf16_out:
+        if out is not None or quant is None:
+            raise ValueError("bf16_out=False needs a quant format and no out")
+    elif out is None:
+        out = _empty(shape, bf16, dev, stream)
+        o = out.data_ptr()
+    else:
         o = _need(out, "out", bf16, shape, dev)
-    elif out is not None or quant is None:
-        raise ValueError("bf16_out=False needs a quant format and no out")
     if quant is None:
         if codes is not None or scales is not None or scale is not None:
             raise ValueError("codes, scales and scale need a quant format")
     else:
         packed = (rows, H // 2 if quant == "mxfp4" else H)
         if codes is None:
-            codes = _empty(packed, torch.uint8, dev, stream)
-        c = _need(codes, "codes", torch.uint8, packed, dev)
+            codes = _empty(packed, u8, dev, stream)
+        c = _need(codes, "codes", u8, packed, dev)
         if quant == "fp8":
             if scale is None or scales is not None:
                 raise ValueError("quant='fp8' takes the one-element `scale` and no `scales`")
@@ -611,8 +620,8 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, quant: str | None = 
             if scale is not None:
                 raise ValueError("scale is for quant='fp8'")
             if scales is None:
-                scales = _empty((rows, H // 32), torch.uint8, dev, stream)
-            sc = _need(scales, "scales", torch.uint8, (rows, H // 32), dev)
+                scales = _empty((rows, H // 32), u8, dev, stream)
+            sc = _need(scales, "scales", u8, (rows, H // 32), dev)
     st = _call(load().bf16_rmsnorm, dev, stream, x.data_ptr(), ld, r, w, o, ro, c, sc, s1, rows, H, eps,
                QUANT_FORMATS[quant], flags)
     if st != OK:
@@ -632,20 +641,20 @@ def route(logits, k: int, *, scoring: str = "softmax", bias=None, groups: int = 
     experts stay, a group ranked by the sum of its group_best largest.  renormalize divides the weights by their sum; scale
     multiplies them.  Experts with a logit of -inf are out."""
     import torch
-    if logits.dtype != torch.float32 and logits.dtype != torch.bfloat16:
-        raise TypeError(f"logits must be float32 or bfloat16 (got {logits.dtype})")
+    f32, dt = torch.float32, logits.dtype
+    if dt is not f32 and dt is not torch.bfloat16:
+        raise TypeError(f"logits must be float32 or bfloat16 (got {dt})")
     if scoring not in SCORES:
         raise ValueError(f"scoring must be one of {list(SCORES)}, got {scoring!r}")
-    T, E, ld = _rows(logits, "logits")
-    dev = logits.device
-    b = None if bias is None else _need(bias, "bias", torch.float32, (E,), dev)
+    dev, (T, E), ld = _cuda(logits, "logits"), logits.shape, _pitch(logits, "logits")
+    b = None if bias is None else _need(bias, "bias", f32, (E,), dev)
     if weights is None:
-        weights = _empty((T, max(k, 0)), torch.float32, dev, stream)
+        weights = _empty((T, k if k > 0 else 0), f32, dev, stream)
     if ids is None:
-        ids = _empty((T, max(k, 0)), torch.int32, dev, stream)
-    st = _call(load().bf16_route, dev, stream, logits.data_ptr(), ld, b, _need(weights, "weights", torch.float32, (T, k), dev),
+        ids = _empty((T, k if k > 0 else 0), torch.int32, dev, stream)
+    st = _call(load().bf16_route, dev, stream, logits.data_ptr(), ld, b, _need(weights, "weights", f32, (T, k), dev),
                _need(ids, "ids", torch.int32, (T, k), dev), T, E, k, SCORES[scoring], groups, top_groups, group_best,
-               renormalize, scale, logits.dtype == torch.bfloat16, flags)
+               renormalize, scale, dt is not f32, flags) if k > 0 else EINVAL
     if st != OK:
         _raise(st, f"bf16_route(tokens={T}, experts={E}, k={k}, groups={groups}, top_groups={top_groups})")
     return weights, ids
@@ -655,11 +664,9 @@ def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
     """MXFP4 quantisation (bf16_quant_mxfp4) of a contiguous bf16 CUDA tensor x[rows, K], K % 32 == 0: returns (codes uint8
     [rows, K / 2], two to a byte, scales uint8 [rows, K / 32])."""
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    dev, u8 = _cuda(x, "x"), torch.uint8
     rows, K = x.shape
-    dev, u8 = x.device, torch.uint8
-    p = _need(x, "x", torch.bfloat16, x.shape)
+    p = _need(x, "x", torch.bfloat16, (rows, K), dev)
     if out is None:
         out = _empty((rows, K // 2), u8, dev, stream)
     if scales is None:
@@ -674,17 +681,15 @@ def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
 def dequant_mxfp4(codes, scales, out=None, flags: int = 0, stream=None):
     """The bf16 values [rows, K] that MXFP4 codes [rows, K / 2] and scales [rows, K / 32] stand for (bf16_dequant_mxfp4)."""
     import torch
-    if codes.dim() != 2:
-        raise ValueError(f"codes must be 2-D, got {tuple(codes.shape)}")
-    rows, K = codes.shape[0], 2 * codes.shape[1]
-    dev, u8 = codes.device, torch.uint8
-    q = _need(codes, "codes", u8, codes.shape)
-    s = _need(scales, "scales", u8, (rows, K // 32), dev)
+    dev, u8 = _cuda(codes, "codes"), torch.uint8
+    rows, h = codes.shape
+    q, s = _need(codes, "codes", u8, (rows, h), dev), _need(scales, "scales", u8, (rows, h // 16), dev)
     if out is None:
-        out = _empty((rows, K), torch.bfloat16, dev, stream)
-    st = _call(load().bf16_dequant_mxfp4, dev, stream, q, s, rows, K, _need(out, "out", torch.bfloat16, (rows, K), dev), flags)
+        out = _empty((rows, 2 * h), torch.bfloat16, dev, stream)
+    st = _call(load().bf16_dequant_mxfp4, dev, stream, q, s, rows, 2 * h,
+               _need(out, "out", torch.bfloat16, (rows, 2 * h), dev), flags)
     if st != OK:
-        _raise(st, f"bf16_dequant_mxfp4(rows={rows}, K={K})")
+        _raise(st, f"bf16_dequant_mxfp4(rows={rows}, K={2 * h})")
     return out
 
 
@@ -692,14 +697,14 @@ def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, strea
     """MXFP4 linear (bf16_linear_mxfp4): packed e2m1 codes xq[M, K / 2], wq[N, K / 2] with E8M0 block scales xs[M, K / 32],
     ws[N, K / 32] (all uint8), optional bf16 bias[N]; bf16 out[M, N]."""
     import torch
-    if xq.dim() != 2 or wq.dim() != 2:
-        raise ValueError(f"need xq[M, K / 2] and wq[N, K / 2], got {tuple(xq.shape)} and {tuple(wq.shape)}")
-    (M, h), N, dev, u8 = xq.shape, wq.shape[0], xq.device, torch.uint8
-    args = (_need(xq, "xq", u8, (M, h)), _need(xs, "xs", u8, (M, h // 16), dev), _need(wq, "wq", u8, (N, h), dev),
-            _need(ws, "ws", u8, (N, h // 16), dev), None if bias is None else _need(bias, "bias", torch.bfloat16, (N,), dev))
+    dev, u8, bf16 = _cuda(xq, "xq"), torch.uint8, torch.bfloat16
+    (M, h), N = xq.shape, wq.shape[0]
+    a, b = _need(xq, "xq", u8, (M, h), dev), _need(xs, "xs", u8, (M, h // 16), dev)
+    c, d = _need(wq, "wq", u8, (N, h), dev), _need(ws, "ws", u8, (N, h // 16), dev)
+    e = None if bias is None else _need(bias, "bias", bf16, (N,), dev)
     if out is None:
-        out = _empty((M, N), torch.bfloat16, dev, stream)
-    st = _call(load().bf16_linear_mxfp4, dev, stream, *args, _need(out, "out", torch.bfloat16, (M, N), dev), M, N, 2 * h, flags)
+        out = _empty((M, N), bf16, dev, stream)
+    st = _call(load().bf16_linear_mxfp4, dev, stream, a, b, c, d, e, _need(out, "out", bf16, (M, N), dev), M, N, 2 * h, flags)
     if st != OK:
         _raise(st, f"bf16_linear_mxfp4(M={M}, N={N}, K={2 * h})")
     return out
@@ -715,22 +720,26 @@ def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, fl
     then bf16_linear_mxfp4.  `workspace`: a contiguous CUDA tensor of at least mxfp4_dynamic_workspace(M, N, K) bytes to
     reuse from call to call on one stream; allocated for the call when None."""
     import torch
-    if x.dim() != 2 or wq.dim() != 2:
-        raise ValueError(f"need x[M, K] and wq[N, K / 2], got {tuple(x.shape)} and {tuple(wq.shape)}")
-    (M, K), N, dev, u8, bf16 = x.shape, wq.shape[0], x.device, torch.uint8, torch.bfloat16
-    args = (_need(x, "x", bf16, (M, K)), _need(wq, "wq", u8, (N, K // 2), dev), _need(ws, "ws", u8, (N, K // 32), dev),
-            None if bias is None else _need(bias, "bias", bf16, (N,), dev))
+    dev, u8, bf16 = _cuda(x, "x"), torch.uint8, torch.bfloat16
+    (M, K), N = x.shape, wq.shape[0]
+    a = _need(x, "x", bf16, (M, K), dev)
+    c, d = _need(wq, "wq", u8, (N, K // 2), dev), _need(ws, "ws", u8, (N, K // 32), dev)
+    e = None if bias is None else _need(bias, "bias", bf16, (N,), dev)
     if out is None:
         out = _empty((M, N), bf16, dev, stream)
     lib = load()
+    wp, wn = None, 0
     if workspace is None:
-        need = lib.bf16_linear_mxfp4_dynamic_workspace(M, N, K)
-        if need:
-            workspace = _empty(need, u8, dev, stream)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        wn = lib.bf16_linear_mxfp4_dynamic_workspace(M, N, K)
+        if wn:
+            workspace = _empty((wn,), u8, dev, stream)
+            wp = workspace.data_ptr()
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on x's device")
-    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = _call(lib.bf16_linear_mxfp4_dynamic, dev, stream, *args, _need(out, "out", bf16, (M, N), dev), M, N, K, wp, wn, flags)
+    else:
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _call(lib.bf16_linear_mxfp4_dynamic, dev, stream, a, c, d, e, _need(out, "out", bf16, (M, N), dev), M, N, K, wp, wn,
+               flags)
     if st != OK:
         _raise(st, f"bf16_linear_mxfp4_dynamic(M={M}, N={N}, K={K})")
     return out
