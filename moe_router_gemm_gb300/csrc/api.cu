@@ -67,6 +67,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_dotmma();
         if (!e) e = init_mxfp8();
         if (!e) e = init_mxfp4();
+        if (!e) e = init_mxfp4_tile();
     }
     s.err = e;
 }

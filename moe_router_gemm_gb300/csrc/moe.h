@@ -19,6 +19,12 @@ int launch_dequant_mxfp4(const void *q, const void *scales, void *out, long long
 int launch_mxfp4(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out, int M,
                  int N, int K, int S, int threads, uint32_t flags, void *stream, int32_t *status);
 
+// The MXFP4 tile form (mxfp4_tile.cu; tcgen05 block-scaled MMAs): 128 x rows by bq (128 or 256) W rows per tile.
+constexpr int kMxfp4TileThreads = 320;
+int init_mxfp4_tile();
+int launch_mxfp4_tile(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                      int M, int N, int K, int bq, int num_sms, uint32_t flags, void *stream, int32_t *status);
+
 // Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
 int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
                    void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,

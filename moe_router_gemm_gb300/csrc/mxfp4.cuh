@@ -68,4 +68,26 @@ __device__ __forceinline__ void e2m1_to_e4m3(uint32_t w, uint32_t &even, uint32_
     odd = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
 }
 
+// Instruction descriptor of the block-scaled e2m1 MMA (kind::mxf4): A and B e2m1
+// (format 1 at bits 7-9 and 10-12), K-major, N>>3 at bit 17, scale format E8M0
+// at bit 23, M>>4 at bit 24; the first of the two bytes of each 32-bit scale word
+// to use (0 or 2) at bits 4-5 for B and 29-30 for A.  D is fp32.
+__host__ __device__ constexpr uint32_t idesc_mxf4_f32(int mma_m, int mma_n, int sf_id) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)sf_id << 4) | ((uint32_t)(mma_n >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(mma_m >> 4) << 24) | ((uint32_t)sf_id << 29);
+}
+
+// One block-scaled e2m1 MMA, K = 64 codes (two scale blocks, 32 bytes of a row):
+// D[tmem] (+)= (A * sA) (B * sB)^T.  Scale words in TMEM as for mma_mxf8, at
+// columns that are multiples of 8.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
 }  // namespace bf16l
