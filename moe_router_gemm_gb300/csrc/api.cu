@@ -68,6 +68,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_mxfp8();
         if (!e) e = init_mxfp4();
         if (!e) e = init_mxfp4_tile();
+        if (!e) e = init_mxfp4_pair();
     }
     s.err = e;
 }

@@ -170,9 +170,11 @@ extern "C" int bf16_linear_mxfp4(const void *xq, const void *xs, const void *wq,
     st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
     if (M > 16) {
-        const long long tiles256 = (long long)((M + 127) / 128) * ((N + 255) / 256);
-        return result(launch_mxfp4_tile(xq, xs, wq, ws, bias, out, M, N, K, tiles256 >= dev.num_sms ? 256 : 128,
-                                        dev.num_sms, flags, stream, status));
+        const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
+        if (pairs >= 24)
+            return result(launch_mxfp4_pair(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
+        return result(
+            launch_mxfp4_tile(xq, xs, wq, ws, bias, out, M, N, K, 128, dev.num_sms, flags, stream, status));
     }
     return result(launch_mxfp4(xq, xs, wq, ws, bias, out, M, N, K, mxfp8_split(M, N, K, 128, dev.num_sms), 128, flags,
                                stream, status));

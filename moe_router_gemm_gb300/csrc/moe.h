@@ -25,6 +25,11 @@ int init_mxfp4_tile();
 int launch_mxfp4_tile(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                       int M, int N, int K, int bq, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
+// ... and by CTA pairs on 256 x 256 tiles (mxfp4_pair.cu).
+int init_mxfp4_pair();
+int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                      int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
+
 // Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
 int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
                    void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,

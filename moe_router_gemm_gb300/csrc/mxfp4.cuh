@@ -90,4 +90,39 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
+// The same by a CTA pair (M = 256: each CTA's own 128 A rows and accumulator rows, each holds
+// half of the B rows), issued by one thread of the even CTA.  Each CTA's TMEM holds the scales
+// of its own A rows and of all B rows, at the same columns in both.
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of 32 rows of 16 bytes, one after the other (no swizzle;
+// 128 bytes between 8-row groups): the source of tmem_copy_scales_pair.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// In both CTAs of a pair, copy that CTA's own 32 x 16 bytes of shared memory to four
+// TMEM columns, row i to lane i of every lane quarter.  Issued by one thread of the
+// even CTA; runs in order with the MMAs that the same thread issues.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Arrive on an mbarrier of a CTA of the cluster, ordering this thread's earlier
+// accesses for its own CTA only.  Enough where what the arrival announces is read
+// through the async proxy (a fence.proxy.async came before it) or by tcgen05: a
+// release at cluster scope, and the acquire that goes with it, cost about a
+// microsecond a chunk here.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 }  // namespace bf16l

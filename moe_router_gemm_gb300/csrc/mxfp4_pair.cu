@@ -1,0 +1,483 @@
+// mxfp4_pair.cu — the MXFP4 linear as a dense contraction: CTA pairs
+// (tcgen05.mma.cta_group::2.kind::mxf4.block_scale) on 256 x 256 tiles.
+//
+//   * cluster of 2; a ring stage is one 256-code chunk (128-byte swizzle rows, TMA)
+//     of this CTA's own 128 x rows and 128 W rows, 32 KB, and the chunk's scale
+//     bytes of its 128 x rows and of all 256 W rows, 3 KB; the even CTA (the leader)
+//     issues every MMA: four per stage, two 32-code scale blocks each;
+//   * warp 0: TMA producer; warp 1: MMA issuer (leader), TMEM; warps 2-9: epilogue;
+//     warps 10-13: scales.  A stage is full when both CTAs' 64 KB and their eight
+//     scale warps have arrived on the leader's barrier;
+//   * scales: thread i of the scale warps reads 16 scale bytes (two chunks) of x row
+//     i and of W rows i and i + 128 of the tile, two steps ahead, and spreads each
+//     32-bit word (four blocks of a row) into the stage: word of row r at 16 (r % 32)
+//     + 4 (r / 32) of a 512-byte block, the layout from which tcgen05.cp
+//     (32x128b.warpx4) fills four TMEM columns, lane r % 32 of column r / 32 in every
+//     lane quarter.  The MMA thread issues a chunk's six copies before its MMAs; the
+//     tensor core's pipe keeps their order, so nothing waits for them.  (Writing the
+//     words to TMEM with tcgen05.st from the scale warps instead, with the wait and
+//     the arrival that it needs, held the tensor cores to a third of their rate:
+//     8192 x 7168 x 7168 384 us.)
+//   * TMEM: accumulators at columns 0 and 192, 256 columns each, taken in turn: they
+//     share columns 192-255, which the epilogue empties first, so the next tile's
+//     MMAs start when a quarter of this one is out; two scale slots from 448;
+//   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
+// Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any
+// remote arrival) and one before TMEM is freed and the CTAs exit.  Every wait is bounded.
+#include <cuda_runtime.h>
+
+#include "moe.h"
+#include "mxfp4.cuh"
+
+namespace bf16l {
+
+namespace {
+
+constexpr int kHalf = 128;                  // rows of each operand per CTA and chunk
+constexpr int kTileRows = 256;              // x rows, and W rows, of a pair tile
+constexpr int kChunkBytes = 128;            // code bytes of a row per chunk (256 codes)
+constexpr int kHalfBytes = kHalf * kChunkBytes;
+constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kStages = 6;
+constexpr int kScaleBlock = 512;            // a word of 128 rows
+constexpr int kScaleBytes = 6 * kScaleBlock;  // x rows: words 0, 1; W rows: word 0 of rows 0-127, 128-255, word 1 of these
+constexpr int kAcc1Col = 192;               // the second accumulator's first column
+constexpr int kSfCol = 448, kSlotCols = 32;  // scale slots: x words at 0 and 8, W words at 16 and 24
+constexpr int kEpiWarps = 8, kScaleWarps = 4;
+constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
+static_assert(kAcc1Col + kTileRows <= kSfCol && kSfCol + 2 * kSlotCols <= 512, "TMEM columns");
+
+struct PairShared {
+    uint8_t scales[kStages][kScaleBytes];  // first: 16-byte aligned
+    uint64_t full[kStages];    // leader only: both CTAs' codes and scales of the stage are in shared memory
+    uint64_t empty[kStages];   // both: the MMAs (and copies) reading the stage are done
+    uint64_t acc_full[2];      // both: accumulator holds a finished tile
+    uint64_t acc_shared;       // leader only: both CTAs' epilogues have the shared columns of a tile
+    uint32_t tmem_base;
+    int32_t bad_pair, aborted, issued, consumed;
+};
+
+__device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int group, int &p0, int &q0) {
+    const int per_group = group * p_tiles;
+    const int g = u / per_group, r = u - g * per_group;
+    const int gq = (q_tiles - g * group) < group ? (q_tiles - g * group) : group;
+    const int pi = r / gq, qi = g * group + (r - pi * gq);
+    p0 = pi * kTileRows;
+    q0 = qi * kTileRows;
+}
+
+// Scale bytes 16s .. 16s + 15 of one row (nb bytes at `row`; those past nb read as 1.0), for two chunks.
+// W: bytes that the row's start and length are multiples of (16, 8, 4 or 1); lo, hi: the whole array's bounds.
+template <int W>
+__device__ __forceinline__ uint4 scale_bytes(const uint8_t *row, int s, int nb, bool in, const uint8_t *lo,
+                                             const uint8_t *hi) {
+    uint32_t w[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    const int b = 16 * s;
+    if (in && b < nb) {
+        const uint8_t *p = row + b;
+        if (W == 16) return __ldg(reinterpret_cast<const uint4 *>(p));
+        if (W == 8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (b + 8 * i < nb) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+                    w[2 * i] = v.x;
+                    w[2 * i + 1] = v.y;
+                }
+        } else if (W == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (b + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        } else {
+            // aligned words around the bytes, shifted together; a word that the array does not hold whole is read bytewise
+            const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u);
+            const uint8_t *q = p - sh;
+            const int left = nb - b;  // valid bytes
+            uint32_t a[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const uint8_t *c = q + 4 * i;
+                a[i] = 0;
+                if (4 * i - sh >= left) continue;
+                if (c >= lo && c + 4 <= hi) {
+                    a[i] = __ldg(reinterpret_cast<const uint32_t *>(c));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c + j >= lo && c + j < hi) a[i] |= (uint32_t)__ldg(c + j) << (8 * j);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = __funnelshift_r(a[i], a[i + 1], 8 * sh);
+                const int n = left - 4 * i;  // valid bytes of this word
+                const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                w[i] = (v & keep) | (0x7F7F7F7Fu & ~keep);
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int W>
+__global__ void __launch_bounds__(kThreads, 1)
+    mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const uint8_t *__restrict__ xs, const uint8_t *__restrict__ ws,
+                      const uint16_t *__restrict__ bias, uint16_t *__restrict__ out, int M, int N, int K, int group,
+                      int32_t *status) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    PairShared &sh = *reinterpret_cast<PairShared *>(ring + kStages * kStageBytes);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int p_tiles = (M + kTileRows - 1) / kTileRows, q_tiles = (N + kTileRows - 1) / kTileRows;
+    const int units = p_tiles * q_tiles;
+    const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
+    const int C = (K + 2 * kChunkBytes - 1) / (2 * kChunkBytes);
+    const int nb = K >> 5;
+
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_w);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1 + 2 * kScaleWarps);  // the leader producer's arrive.expect_tx, the scale warps
+            mbar_init(&sh.empty[s], 1);                   // the leader's multicast commit
+        }
+        mbar_init(&sh.acc_full[0], 1);
+        mbar_init(&sh.acc_full[1], 1);
+        mbar_init(&sh.acc_shared, 2 * kEpiWarps);
+        sh.aborted = 0;
+        sh.issued = 0;
+        sh.consumed = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&sh.tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    // Both CTAs' barriers and TMEM exist before any cross-CTA arrival or copy.
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    // The pair MMA writes the same TMEM address in both CTAs: check that the joint
+    // allocation gave both the same columns (each CTA reads the other's).
+    if (tid == 0) {
+        uint32_t other;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(other)
+                     : "r"(mapa_shared(smem_u32(&sh.tmem_base), rank ^ 1u))
+                     : "memory");
+        sh.bad_pair = other != tmem;
+        if (other != tmem) record_timeout(status, kSitePairTmem);
+    }
+    __syncthreads();
+    const bool bad_pair = sh.bad_pair != 0;  // the same verdict in both CTAs
+    pdl_launch_dependents();
+    pdl_wait();  // nothing is read before the previous kernel has finished
+
+    if (bad_pair) {
+        // nothing issued: fall through to the exit barrier
+    } else if (warp == 0) {
+        if (lane == 0) {  // ---- TMA producer (both CTAs) ----
+            const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // leader's full[0]
+            int it = 0;
+            for (int u = cl; u < units; u += ncl) {
+                int p0, q0;
+                pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+                const int ap = p0 + (int)rank * kHalf, bq = q0 + (int)rank * kHalf;
+                for (int c = 0; c < C; ++c, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait(&sh.empty[s], ((it / kStages) - 1) & 1, status, kSiteEmpty)) {
+                        atomicExch(&sh.aborted, 1);
+                        goto producer_done;
+                    }
+                    if (*((volatile int32_t *)&sh.aborted)) goto producer_done;
+                    uint8_t *st = ring + s * kStageBytes;
+                    if (leader) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
+                    const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
+                    tma_load_2d_pair(st, &tm_x, fb, c * kChunkBytes, ap);
+                    tma_load_2d_pair(st + kHalfBytes, &tm_w, fb, c * kChunkBytes, bq);
+                }
+            }
+        producer_done:
+            sh.issued = it;
+            // Every commit that arrives on this CTA's `empty` barriers has landed
+            // before the exit barrier (the last kStages chunks).
+            if (!*((volatile int32_t *)&sh.aborted)) {
+                for (int i = (it > kStages ? it - kStages : 0); i < it; ++i)
+                    if (!mbar_wait(&sh.empty[i % kStages], (i / kStages) & 1, status, kSiteDrain)) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {  // ---- MMA issuer (leader only) ----
+            int it = 0, tile = 0;
+            for (int u = cl; u < units; u += ncl, ++tile) {
+                sh.consumed = it;
+                const uint32_t acc = tmem + (uint32_t)((tile & 1) * kAcc1Col);
+                // Both CTAs' epilogues have the columns that this accumulator shares with the previous tile's out,
+                // and, as they take tiles in order, all of the tile before that.
+                bool ok = tile == 0 || mbar_wait(&sh.acc_shared, (tile - 1) & 1, status, kSiteTmemEmpty);
+                for (int c = 0; ok && c < C; ++c, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait(&sh.full[s], (it / kStages) & 1, status, kSiteFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t *st = ring + s * kStageBytes;
+                    const uint64_t adesc = smem_desc_sw128(smem_u32(st));
+                    const uint64_t bdesc = smem_desc_sw128(smem_u32(st + kHalfBytes));
+                    const uint64_t sdesc = smem_desc_rows16(smem_u32(sh.scales[s]));
+                    const uint32_t sf = tmem + (uint32_t)(kSfCol + kSlotCols * (it & 1));
+                    constexpr uint64_t kStep = kScaleBlock >> 4;
+                    tmem_copy_scales_pair(sf, sdesc);
+                    tmem_copy_scales_pair(sf + 16, sdesc + 2 * kStep);
+                    tmem_copy_scales_pair(sf + 20, sdesc + 3 * kStep);
+                    tmem_copy_scales_pair(sf + 8, sdesc + kStep);
+                    tmem_copy_scales_pair(sf + 24, sdesc + 4 * kStep);
+                    tmem_copy_scales_pair(sf + 28, sdesc + 5 * kStep);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // 64 codes, two scale blocks
+                        mma_mxf4_pair(acc, adesc + 2 * kk, bdesc + 2 * kk,
+                                      idesc_mxf4_f32(kTileRows, kTileRows, 2 * (kk & 1)), sf + 8 * (kk >> 1),
+                                      sf + 16 + 8 * (kk >> 1), (c > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
+                }
+                if (!ok) {  // release both epilogues at once
+                    atomicExch(&sh.aborted, 1);
+                    sh.consumed = it;
+                    mbar_arrive(&sh.acc_full[tile & 1]);
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&sh.acc_full[tile & 1]), 1));
+                    break;
+                }
+                mma_commit_pair(&sh.acc_full[tile & 1], (uint16_t)0x3);
+            }
+            sh.consumed = it;
+        }
+        __syncwarp();
+    } else if (warp < 2 + kEpiWarps) {
+        // ---- epilogue: TMEM lane quarter = warp % 4; four 32-column slices each, the shared columns first ----
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int row = quarter * 32 + lane;
+        const bool vec_ok = (N % 8) == 0;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t acc_shared = mapa_shared(smem_u32(&sh.acc_shared), 0);
+        int tile = 0;
+        for (int u = cl; u < units; u += ncl, ++tile) {
+            int p0, q0;
+            pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+            const int m = p0 + (int)rank * kHalf + row;
+            const int second = tile & 1;
+            // slice i of this warp: the shared one (columns 192-255 of the first accumulator, 0-63 of the second), then
+            // three of the other six
+            auto column = [&](int i) {
+                if (i == 0) return second ? 32 * half : 192 + 32 * half;
+                return (second ? 64 : 0) + 96 * half + 32 * (i - 1);
+            };
+            float lb[4];  // the tile's bias, one value per lane and slice, read while the MMAs run
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lb[i] = bias_lane(bias, q0 + column(i), N);
+            const bool ok = mbar_wait(&sh.acc_full[second], (tile >> 1) & 1, status, kSiteAccum);
+            tc_fence_after();
+            // warp-uniform, so that the bias shuffles below run on all 32 lanes
+            const bool have = __all_sync(0xFFFFFFFFu, ok && !*((volatile int32_t *)&sh.aborted));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = q0 + column(i);
+                float v[32];
+                if (have) {
+                    uint32_t r0[16], r1[16];
+                    const uint32_t at = lanes + (uint32_t)(second * kAcc1Col + column(i));
+                    tmem_ld16(at, r0);
+                    tmem_ld16(at + 16, r1);
+                    tmem_ld_wait16(r0);
+                    tmem_ld_wait16(r1);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = __uint_as_float(r0[j]);
+                        v[16 + j] = __uint_as_float(r1[j]);
+                    }
+                }
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(acc_shared);
+                }
+                if (!have) break;
+                if (bias) bias_add32(v, lb[i]);  // warp-uniform condition
+                if (m < M && n < N) {
+                    uint16_t *o = out + (size_t)m * N + n;
+                    if (vec_ok && n + 32 <= N) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) OutStore<uint16_t>::eight(o + j, v + j);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (n + j < N) OutStore<uint16_t>::one(o + j, v[j]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!have) break;
+        }
+    } else {
+        // ---- scales ----
+        const int st = tid - 32 * (2 + kEpiWarps);
+        const int at = 16 * (st & 31) + 4 * (st >> 5);  // this row's word in a block
+        const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
+        const uint8_t *xlo = xs, *xhi = xs + (size_t)M * nb, *wlo = ws, *whi = ws + (size_t)N * nb;
+        const int D = (C + 1) / 2;  // steps of two chunks
+        int it = 0;
+        bool stop = false;
+        for (int u = cl; u < units && !stop; u += ncl) {
+            int p0, q0;
+            pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+            const int ra = p0 + (int)rank * kHalf + st, rb0 = q0 + st, rb1 = rb0 + kHalf;
+            const bool ia = ra < M, ib0 = rb0 < N, ib1 = rb1 < N;
+            const uint8_t *pa = xs + (size_t)(ia ? ra : 0) * nb, *pb0 = ws + (size_t)(ib0 ? rb0 : 0) * nb,
+                          *pb1 = ws + (size_t)(ib1 ? rb1 : 0) * nb;
+            constexpr int PD = 2;
+            uint4 va[PD], vb0[PD], vb1[PD];
+#pragma unroll
+            for (int d = 0; d < PD; ++d) {
+                va[d] = scale_bytes<W>(pa, d, nb, ia, xlo, xhi);
+                vb0[d] = scale_bytes<W>(pb0, d, nb, ib0, wlo, whi);
+                vb1[d] = scale_bytes<W>(pb1, d, nb, ib1, wlo, whi);
+            }
+            for (int s2 = 0; s2 < D && !stop; ++s2) {
+                const uint4 a = va[0], b0 = vb0[0], b1 = vb1[0];
+#pragma unroll
+                for (int d = 0; d + 1 < PD; ++d) va[d] = va[d + 1], vb0[d] = vb0[d + 1], vb1[d] = vb1[d + 1];
+                va[PD - 1] = scale_bytes<W>(pa, s2 + PD, nb, ia, xlo, xhi);
+                vb0[PD - 1] = scale_bytes<W>(pb0, s2 + PD, nb, ib0, wlo, whi);
+                vb1[PD - 1] = scale_bytes<W>(pb1, s2 + PD, nb, ib1, wlo, whi);
+#pragma unroll
+                for (int h = 0; h < 2; ++h, ++it) {  // the step's two chunks
+                    if (2 * s2 + h >= C) break;
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait(&sh.empty[s], ((it / kStages) - 1) & 1, status, kSiteScale))
+                        stop = true;
+                    if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
+                        atomicExch(&sh.aborted, 1);
+                        stop = true;
+                        break;
+                    }
+                    uint8_t *blk = sh.scales[s] + at;
+                    const uint32_t w[6] = {h ? a.z : a.x,   h ? a.w : a.y,   h ? b0.z : b0.x,
+                                           h ? b1.z : b1.x, h ? b0.w : b0.y, h ? b1.w : b1.y};
+#pragma unroll
+                    for (int k = 0; k < 6; ++k) *reinterpret_cast<uint32_t *>(blk + k * kScaleBlock) = w[k];
+                    fence_proxy_async_smem();  // the copies into TMEM read them through the async proxy
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)(s * sizeof(uint64_t)));
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // Drain TMA copies that were issued but never consumed (only after a timeout).
+    if (tid == 0 && leader) {
+        for (int i = sh.consumed; i < sh.issued; ++i)
+            if (!mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, status, kSiteDrain)) break;
+    }
+    // No remote arrival, copy or MMA operand read is left in flight past here.
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+constexpr int kMaxDevices = 64;
+int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
+
+constexpr int smem_bytes() { return 1024 + kStages * kStageBytes + (int)sizeof(PairShared); }
+static_assert(smem_bytes() <= 232448, "shared memory");
+static_assert(smem_bytes() > 116 * 1024, "one CTA per SM: each allocates all 512 TMEM columns");
+
+using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *, const uint16_t *,
+                        uint16_t *, int, int, int, int, int32_t *);
+
+PairFn pick_pair(uintptr_t align) {
+    return align % 16 == 0  ? mxfp4_pair_kernel<16>
+           : align % 8 == 0 ? mxfp4_pair_kernel<8>
+           : align % 4 == 0 ? mxfp4_pair_kernel<4>
+                            : mxfp4_pair_kernel<1>;
+}
+
+cudaLaunchConfig_t pair_config(int clusters, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem_bytes();
+    cfg.stream = (cudaStream_t)stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+}  // namespace
+
+int init_mxfp4_pair() {
+    for (uintptr_t a : {16, 8, 4, 1}) {
+        const int e =
+            (int)cudaFuncSetAttribute(pick_pair(a), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes());
+        if (e) return e;
+    }
+    int dev = 0;
+    const int e = (int)cudaGetDevice(&dev);
+    if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pair_config(kGb300Sms, 0, nullptr, attr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    // A failed query only loses the clamp (launches then use half the SMs' number).
+    if (cudaOccupancyMaxActiveClusters(&n, pick_pair(16), &cfg) != cudaSuccess) {
+        n = 0;
+        (void)cudaGetLastError();
+    }
+    g_clusters[dev] = n;
+    return 0;
+}
+
+int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                      int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status) {
+    CUtensorMap tx, tw;  // 128-byte rows of 256 codes
+    int r = make_tmap_u8_2d(&tx, xq, (uint64_t)M, (uint64_t)(K / 2), kHalf, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (r) return (int)cudaErrorInvalidValue;
+    r = make_tmap_u8_2d(&tw, wq, (uint64_t)N, (uint64_t)(K / 2), kHalf, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (r) return (int)cudaErrorInvalidValue;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
+    // A cluster that cannot be resident with the others would run its tiles after them.
+    const long long units =
+        (long long)((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
+    long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
+    if (units < clusters) clusters = units;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = pair_config((int)clusters, flags, stream, attr);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
+    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a), tx, tw, static_cast<const uint8_t *>(xs),
+                                   static_cast<const uint8_t *>(ws), static_cast<const uint16_t *>(bias),
+                                   static_cast<uint16_t *>(out), M, N, K, 8, status);
+}
+
+}  // namespace bf16l

@@ -105,7 +105,8 @@ def test_linear(lib, shape, bias):
     assert lib.device_status() == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 640), (13, 72, 640), (70, 130, 1184), (300, 600, 1024), (300, 520, 1120)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 640), (13, 72, 640), (70, 130, 1184), (300, 600, 1024), (300, 520, 1120),
+                                   (1300, 1300, 1024), (1100, 1500, 1120), (1281, 1281, 416), (1500, 1100, 256)])
 def test_linear_random_codes_and_scales(lib, M, N, K):
     """Every block's scale has to reach its own block: random codes, scales over 34 binades."""
     rng = np.random.default_rng(M + N + K)
@@ -115,7 +116,7 @@ def test_linear_random_codes_and_scales(lib, M, N, K):
     ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K)
 
 
-@pytest.mark.parametrize("M,N,K", [(2, 64, 256), (20, 64, 256), (300, 520, 512)])
+@pytest.mark.parametrize("M,N,K", [(2, 64, 256), (20, 64, 256), (300, 520, 512), (1300, 1300, 512)])
 def test_linear_extreme_scales(lib, M, N, K):
     """Scale bytes at the ends of their range whose product is an ordinary number, and a NaN scale."""
     rng = np.random.default_rng(M)
@@ -132,7 +133,11 @@ def test_linear_extreme_scales(lib, M, N, K):
 
 def test_linear_views_streams_and_graph(lib):
     """Byte-aligned scales, a side stream, a captured graph: the same bits."""
-    M, N, K = 24, 300, 2880
+    for M, N, K in ((24, 300, 2880), (1300, 1400, 544), (3, 300, 2880)):
+        _views_streams_and_graph(lib, M, N, K)
+
+
+def _views_streams_and_graph(lib, M, N, K):
     x, wq, ws, b = _operands(M, N, K, 5, True)
     xq, xs = lib.quant_mxfp4(x)
     want = lib.bf16_linear_mxfp4(xq, xs, wq, ws, b)
