@@ -103,19 +103,6 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
-// Shared-memory descriptor of 32 rows of 16 bytes, one after the other (no swizzle;
-// 128 bytes between 8-row groups): the source of tmem_copy_scales_pair.
-__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
-
-// In both CTAs of a pair, copy that CTA's own 32 x 16 bytes of shared memory to four
-// TMEM columns, row i to lane i of every lane quarter.  Issued by one thread of the
-// even CTA; runs in order with the MMAs that the same thread issues.
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
 // Arrive on an mbarrier of a CTA of the cluster, ordering this thread's earlier
 // accesses for its own CTA only.  Enough where what the arrival announces is read
 // through the async proxy (a fence.proxy.async came before it) or by tcgen05: a
@@ -124,5 +111,22 @@ __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t s
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
+
+// Barrier `id` for `threads` threads of the CTA (whole warps).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// TMA store of a tile from shared memory (c0 innermost, c0 and c1 not negative), a
+// bulk group of its own; what lies past the matrix is not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+// This thread's bulk stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace bf16l

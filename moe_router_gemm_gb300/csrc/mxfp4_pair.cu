@@ -2,26 +2,32 @@
 // (tcgen05.mma.cta_group::2.kind::mxf4.block_scale) on 256 x 256 tiles.
 //
 //   * cluster of 2; a ring stage is one 256-code chunk (128-byte swizzle rows, TMA)
-//     of this CTA's own 128 x rows and 128 W rows, 32 KB, and the chunk's scale
-//     bytes of its 128 x rows and of all 256 W rows, 3 KB; the even CTA (the leader)
+//     of this CTA's own 128 x rows and 128 W rows, 32 KB; the even CTA (the leader)
 //     issues every MMA: four per stage, two 32-code scale blocks each;
 //   * warp 0: TMA producer; warp 1: MMA issuer (leader), TMEM; warps 2-9: epilogue;
-//     warps 10-13: scales.  A stage is full when both CTAs' 64 KB and their eight
-//     scale warps have arrived on the leader's barrier;
+//     warps 10-13: scales.  A stage is full when both CTAs' 64 KB have landed and the
+//     eight scale warps have arrived on the leader's barrier;
 //   * scales: thread i of the scale warps reads 16 scale bytes (two chunks) of x row
-//     i and of W rows i and i + 128 of the tile, two steps ahead, and spreads each
-//     32-bit word (four blocks of a row) into the stage: word of row r at 16 (r % 32)
-//     + 4 (r / 32) of a 512-byte block, the layout from which tcgen05.cp
-//     (32x128b.warpx4) fills four TMEM columns, lane r % 32 of column r / 32 in every
-//     lane quarter.  The MMA thread issues a chunk's six copies before its MMAs; the
-//     tensor core's pipe keeps their order, so nothing waits for them.  (Writing the
-//     words to TMEM with tcgen05.st from the scale warps instead, with the wait and
-//     the arrival that it needs, held the tensor cores to a third of their rate:
-//     8192 x 7168 x 7168 384 us.)
-//   * TMEM: accumulators at columns 0 and 192, 256 columns each, taken in turn: they
-//     share columns 192-255, which the epilogue empties first, so the next tile's
-//     MMAs start when a quarter of this one is out; two scale slots from 448;
+//     i and of W rows i and i + 128 of the tile, two steps ahead.  The W bytes go
+//     through shared memory, since every TMEM lane quarter needs all 256 rows'; each
+//     warp writes its quarter of a chunk's slot with tcgen05.st.  Reading each row
+//     once per CTA, 16 bytes at a time, matters: a row's bytes are a cache line of
+//     their own;
+//   * TMEM: accumulators at columns 0 and 128, 256 columns each, taken in turn: they
+//     share columns 128-255, which the epilogue empties first, so the next tile's
+//     MMAs start when half of this one is out; four scale slots of 32 columns (x words
+//     at 0 and 8, W words at 16 and 24: every address a multiple of 8) from 384;
+//   * epilogue: 32 x 32 pieces through shared memory and TMA stores (N % 8 == 0); each
+//     lane storing its own row's 16-byte pieces takes a line per lane and held
+//     8192 x 7168 x 7168 at 174 us;
 //   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
+//
+// Measured and not taken (8192 x 7168 x 7168): arrivals released at cluster scope (they
+// wait for the scale loads in flight) 384 us; scales copied by tcgen05.cp from shared
+// memory, in order before their MMAs 196 us, a chunk ahead or between the MMAs 207 us
+// (the copies hold up the MMAs behind them); two or three scale slots, which leave the
+// accumulators fewer shared columns, 185 and 177 us against 174.
+//
 // Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any
 // remote arrival) and one before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>
@@ -39,16 +45,18 @@ constexpr int kChunkBytes = 128;            // code bytes of a row per chunk (25
 constexpr int kHalfBytes = kHalf * kChunkBytes;
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kStages = 6;
-constexpr int kScaleBlock = 512;            // a word of 128 rows
-constexpr int kScaleBytes = 6 * kScaleBlock;  // x rows: words 0, 1; W rows: word 0 of rows 0-127, 128-255, word 1 of these
-constexpr int kAcc1Col = 192;               // the second accumulator's first column
-constexpr int kSfCol = 448, kSlotCols = 32;  // scale slots: x words at 0 and 8, W words at 16 and 24
+constexpr int kSlots = 4, kSlotCols = 32;
+constexpr int kSfCol = 512 - kSlots * kSlotCols;  // the scale slots' first column
+constexpr int kAcc1Col = kSfCol - kTileRows;      // the second accumulator's first column
+constexpr int kShared = kTileRows - kAcc1Col;     // columns that the accumulators share
+static_assert(kShared % 64 == 0, "the epilogue empties 64 columns at a time");
 constexpr int kEpiWarps = 8, kScaleWarps = 4;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
-static_assert(kAcc1Col + kTileRows <= kSfCol && kSfCol + 2 * kSlotCols <= 512, "TMEM columns");
+
 
 struct PairShared {
-    uint8_t scales[kStages][kScaleBytes];  // first: 16-byte aligned
+    uint8_t piece[kEpiWarps][32 * 64];  // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first: aligned)
+    uint4 scales[2][kTileRows];
     uint64_t full[kStages];    // leader only: both CTAs' codes and scales of the stage are in shared memory
     uint64_t empty[kStages];   // both: the MMAs (and copies) reading the stage are done
     uint64_t acc_full[2];      // both: accumulator holds a finished tile
@@ -122,7 +130,7 @@ __device__ __forceinline__ uint4 scale_bytes(const uint8_t *row, int s, int nb, 
 template <int W>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const uint8_t *__restrict__ xs, const uint8_t *__restrict__ ws,
+                      const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ ws,
                       const uint16_t *__restrict__ bias, uint16_t *__restrict__ out, int M, int N, int K, int group,
                       int32_t *status) {
     extern __shared__ uint8_t smem_raw[];
@@ -233,15 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint8_t *st = ring + s * kStageBytes;
                     const uint64_t adesc = smem_desc_sw128(smem_u32(st));
                     const uint64_t bdesc = smem_desc_sw128(smem_u32(st + kHalfBytes));
-                    const uint64_t sdesc = smem_desc_rows16(smem_u32(sh.scales[s]));
-                    const uint32_t sf = tmem + (uint32_t)(kSfCol + kSlotCols * (it & 1));
-                    constexpr uint64_t kStep = kScaleBlock >> 4;
-                    tmem_copy_scales_pair(sf, sdesc);
-                    tmem_copy_scales_pair(sf + 16, sdesc + 2 * kStep);
-                    tmem_copy_scales_pair(sf + 20, sdesc + 3 * kStep);
-                    tmem_copy_scales_pair(sf + 8, sdesc + kStep);
-                    tmem_copy_scales_pair(sf + 24, sdesc + 4 * kStep);
-                    tmem_copy_scales_pair(sf + 28, sdesc + 5 * kStep);
+                    const uint32_t sf = tmem + (uint32_t)(kSfCol + kSlotCols * (it % kSlots));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // 64 codes, two scale blocks
                         mma_mxf4_pair(acc, adesc + 2 * kk, bdesc + 2 * kk,
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- epilogue: TMEM lane quarter = warp % 4; four 32-column slices each, the shared columns first ----
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int row = quarter * 32 + lane;
-        const bool vec_ok = (N % 8) == 0;
+        const bool by_tma = N % 8 == 0;  // rows of out start on 16-byte boundaries
+        uint8_t *piece = sh.piece[warp - 2];
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t acc_shared = mapa_shared(smem_u32(&sh.acc_shared), 0);
         int tile = 0;
@@ -274,11 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_coords(u, p_tiles, q_tiles, group, p0, q0);
             const int m = p0 + (int)rank * kHalf + row;
             const int second = tile & 1;
-            // slice i of this warp: the shared one (columns 192-255 of the first accumulator, 0-63 of the second), then
-            // three of the other six
+            // the first column of this warp's slice i: the shared columns (128-255 of the first accumulator, 0-127 of the
+            // second) come first
             auto column = [&](int i) {
-                if (i == 0) return second ? 32 * half : 192 + 32 * half;
-                return (second ? 64 : 0) + 96 * half + 32 * (i - 1);
+                const int c = 32 * (2 * i + half);  // 0, 64, 128, 192 (+ 32)
+                return second ? c : (c + kAcc1Col) & 255;
             };
             float lb[4];  // the tile's bias, one value per lane and slice, read while the MMAs run
 #pragma unroll
@@ -304,41 +305,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[16 + j] = __uint_as_float(r1[j]);
                     }
                 }
-                if (i == 0) {
+                if (i == kShared / 64 - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(acc_shared);
                 }
-                if (!have) break;
+                if (!have) continue;
                 if (bias) bias_add32(v, lb[i]);  // warp-uniform condition
-                if (m < M && n < N) {
+                if (by_tma) {
+                    if (n >= N) continue;  // warp-uniform
+                    if (lane == 0) bulk_wait_read();  // the piece before has left shared memory
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
+                        *reinterpret_cast<uint4 *>(piece + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
+                            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m < M) tma_store_2d(&tm_out, piece, n, m);  // rows and columns past the end are cut off
+                } else if (m < M && n < N) {
                     uint16_t *o = out + (size_t)m * N + n;
-                    if (vec_ok && n + 32 <= N) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) OutStore<uint16_t>::eight(o + j, v + j);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (n + j < N) OutStore<uint16_t>::one(o + j, v[j]);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (n + j < N) OutStore<uint16_t>::one(o + j, v[j]);
                 }
             }
             tc_fence_before();
             if (!have) break;
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     } else {
         // ---- scales ----
         const int st = tid - 32 * (2 + kEpiWarps);
-        const int at = 16 * (st & 31) + 4 * (st >> 5);  // this row's word in a block
+        const int quarter = warp & 3;
+        const uint32_t slot0 = tmem + (uint32_t)kSfCol + ((uint32_t)(quarter * 32) << 16);
+        int step = 0;
         const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
         const uint8_t *xlo = xs, *xhi = xs + (size_t)M * nb, *wlo = ws, *whi = ws + (size_t)N * nb;
         const int D = (C + 1) / 2;  // steps of two chunks
         int it = 0;
         bool stop = false;
-        for (int u = cl; u < units && !stop; u += ncl) {
+        for (int u = cl; u < units; u += ncl) {
             int p0, q0;
             pair_coords(u, p_tiles, q_tiles, group, p0, q0);
-            const int ra = p0 + (int)rank * kHalf + st, rb0 = q0 + st, rb1 = rb0 + kHalf;
+            const int ra = p0 + (int)rank * kHalf + 32 * quarter + lane, rb0 = q0 + st, rb1 = rb0 + kHalf;
             const bool ia = ra < M, ib0 = rb0 < N, ib1 = rb1 < N;
             const uint8_t *pa = xs + (size_t)(ia ? ra : 0) * nb, *pb0 = ws + (size_t)(ib0 ? rb0 : 0) * nb,
                           *pb1 = ws + (size_t)(ib1 ? rb1 : 0) * nb;
@@ -350,32 +362,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vb0[d] = scale_bytes<W>(pb0, d, nb, ib0, wlo, whi);
                 vb1[d] = scale_bytes<W>(pb1, d, nb, ib1, wlo, whi);
             }
-            for (int s2 = 0; s2 < D && !stop; ++s2) {
-                const uint4 a = va[0], b0 = vb0[0], b1 = vb1[0];
+            // A warp that gave up goes on through the barriers, so that no other one waits for it there.
+            for (int s2 = 0; s2 < D; ++s2, ++step) {
+                const uint4 a = va[0];
+                uint4 *buf = sh.scales[step & 1];
+                buf[st] = vb0[0];
+                buf[kHalf + st] = vb1[0];
 #pragma unroll
                 for (int d = 0; d + 1 < PD; ++d) va[d] = va[d + 1], vb0[d] = vb0[d + 1], vb1[d] = vb1[d + 1];
                 va[PD - 1] = scale_bytes<W>(pa, s2 + PD, nb, ia, xlo, xhi);
                 vb0[PD - 1] = scale_bytes<W>(pb0, s2 + PD, nb, ib0, wlo, whi);
                 vb1[PD - 1] = scale_bytes<W>(pb1, s2 + PD, nb, ib1, wlo, whi);
+                // the buffer is whole; its last readers are past the barrier of the step before
+                named_barrier(1, 32 * kScaleWarps);
+                uint4 wb[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h, ++it) {  // the step's two chunks
-                    if (2 * s2 + h >= C) break;
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait(&sh.empty[s], ((it / kStages) - 1) & 1, status, kSiteScale))
+                for (int j = 0; j < 8; ++j) wb[j] = buf[32 * j + lane];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // the step's two chunks
+                    if (stop || 2 * s2 + h >= C) break;
+                    // the slot is free when the MMAs of the chunk kSlots before are done
+                    const int old = it - kSlots;
+                    if (old >= 0 && !mbar_wait(&sh.empty[old % kStages], (old / kStages) & 1, status, kSiteScale))
                         stop = true;
                     if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
                         atomicExch(&sh.aborted, 1);
                         stop = true;
                         break;
                     }
-                    uint8_t *blk = sh.scales[s] + at;
-                    const uint32_t w[6] = {h ? a.z : a.x,   h ? a.w : a.y,   h ? b0.z : b0.x,
-                                           h ? b1.z : b1.x, h ? b0.w : b0.y, h ? b1.w : b1.y};
+                    const uint32_t sf = slot0 + (uint32_t)(kSlotCols * (it % kSlots));
+                    const uint32_t a0 = h ? a.z : a.x, a1 = h ? a.w : a.y;
+                    tmem_st4(sf, a0, a0, a0, a0);  // column `quarter` of the four is the one read
+                    tmem_st4(sf + 8, a1, a1, a1, a1);
 #pragma unroll
-                    for (int k = 0; k < 6; ++k) *reinterpret_cast<uint32_t *>(blk + k * kScaleBlock) = w[k];
-                    fence_proxy_async_smem();  // the copies into TMEM read them through the async proxy
+                    for (int j = 0; j < 8; j += 4) {
+                        if (h) {
+                            tmem_st4(sf + 16 + j, wb[j].z, wb[j + 1].z, wb[j + 2].z, wb[j + 3].z);
+                            tmem_st4(sf + 24 + j, wb[j].w, wb[j + 1].w, wb[j + 2].w, wb[j + 3].w);
+                        } else {
+                            tmem_st4(sf + 16 + j, wb[j].x, wb[j + 1].x, wb[j + 2].x, wb[j + 3].x);
+                            tmem_st4(sf + 24 + j, wb[j].y, wb[j + 1].y, wb[j + 2].y, wb[j + 3].y);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)(s * sizeof(uint64_t)));
+                    if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)((it % kStages) * sizeof(uint64_t)));
+                    ++it;
                 }
             }
         }
@@ -405,7 +438,7 @@ constexpr int smem_bytes() { return 1024 + kStages * kStageBytes + (int)sizeof(P
 static_assert(smem_bytes() <= 232448, "shared memory");
 static_assert(smem_bytes() > 116 * 1024, "one CTA per SM: each allocates all 512 TMEM columns");
 
-using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *, const uint16_t *,
+using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *, const uint16_t *,
                         uint16_t *, int, int, int, int, int32_t *);
 
 PairFn pick_pair(uintptr_t align) {
@@ -465,6 +498,12 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
     r = make_tmap_u8_2d(&tw, wq, (uint64_t)N, (uint64_t)(K / 2), kHalf, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (r) return (int)cudaErrorInvalidValue;
+    CUtensorMap to = {};  // 32 x 32 pieces of out; not used where its rows are not 16-byte aligned
+    if (N % 8 == 0) {
+        r = make_tmap_bf16_2d(&to, out, (uint64_t)M, (uint64_t)N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE);
+        if (r) return (int)cudaErrorInvalidValue;
+    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
     // A cluster that cannot be resident with the others would run its tiles after them.
@@ -475,7 +514,7 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = pair_config((int)clusters, flags, stream, attr);
     const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
-    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a), tx, tw, static_cast<const uint8_t *>(xs),
+    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a), tx, tw, to, static_cast<const uint8_t *>(xs),
                                    static_cast<const uint8_t *>(ws), static_cast<const uint16_t *>(bias),
                                    static_cast<uint16_t *>(out), M, N, K, 8, status);
 }
