@@ -69,6 +69,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_mxfp4();
         if (!e) e = init_mxfp4_tile();
         if (!e) e = init_mxfp4_pair();
+        if (!e) e = init_mxfp4_split();
     }
     s.err = e;
 }

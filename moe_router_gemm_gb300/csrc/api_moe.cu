@@ -169,19 +169,15 @@ extern "C" int bf16_linear_mxfp4(const void *xq, const void *xs, const void *wq,
     int32_t *status = nullptr;
     st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    if (M > 16) {
-        const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
-        if (pairs >= 24)
-            return result(launch_mxfp4_pair(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
-        return result(
-            launch_mxfp4_tile(xq, xs, wq, ws, bias, out, M, N, K, 128, dev.num_sms, flags, stream, status));
-    }
-    return result(launch_mxfp4(xq, xs, wq, ws, bias, out, M, N, K, mxfp8_split(M, N, K, 128, dev.num_sms), 128, flags,
-                               stream, status));
+    const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
+    if (pairs >= 40)
+        return result(launch_mxfp4_pair(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
+    return result(launch_mxfp4_split(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
 }
 
 extern "C" size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K) {
     if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0) return 0;
+    if (mxfp4_split_quantises(M, N, K)) return 0;
     return up256((size_t)M * (size_t)(K / 2)) + up256((size_t)M * (size_t)(K / 32));
 }
 
@@ -198,6 +194,13 @@ extern "C" int bf16_linear_mxfp4_dynamic(const void *x, const void *wq, const vo
     const Span outs[2] = {{out, 2 * m * n}, {workspace, need}};
     const Span ins[4] = {{x, 2 * m * k}, {wq, n * k / 2}, {ws, n * k / 32}, {bias, 2 * n}};
     if (clash(outs, ins)) return BF16L_EINVAL;
+    if (need == 0) {  // the kernel quantises x itself
+        bf16l_device dev;
+        int32_t *status = nullptr;
+        st = current_device_status(&dev, &status);
+        if (st != BF16L_OK) return st;
+        return result(launch_mxfp4_split(x, nullptr, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
+    }
     uint8_t *xq = static_cast<uint8_t *>(workspace);
     uint8_t *xs = xq + up256((size_t)M * (size_t)(K / 2));
     st = bf16_quant_mxfp4(x, M, K, xq, xs, flags, stream);

@@ -30,6 +30,17 @@ int init_mxfp4_pair();
 int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                       int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
+// ... and with K over a cluster's CTAs, W on the MMA's M side (mxfp4_split.cu): xs null means that x is bf16 and is
+// quantised by the kernel (where mxfp4_split_quantises).
+struct Mxfp4SplitPlan {
+    int tokens, m_tiles, split, stages, smem;
+};
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, bool bf16, int num_sms);
+bool mxfp4_split_quantises(int M, int N, int K);
+int init_mxfp4_split();
+int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                       int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
+
 // Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
 int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,
                    void *codes, void *scales, const float *scale, int64_t rows, int H, float eps, int quant,

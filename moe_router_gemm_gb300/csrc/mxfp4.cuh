@@ -103,6 +103,71 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
+// 4 * NW scale bytes of one row (nb bytes at `row`) from byte b on; those past nb read as 1.0.  W: bytes that the rows'
+// start, their length and b are multiples of (16, 8, 4 or 1); [lo, hi): the whole array, which no read leaves.
+template <int W, int NW>
+__device__ __forceinline__ void scale_words(uint32_t (&w)[NW], const uint8_t *row, int b, int nb, bool in,
+                                            const uint8_t *lo, const uint8_t *hi) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0x7F7F7F7Fu;
+    if (!in || b >= nb) return;
+    const uint8_t *p = row + b;
+    if (W == 16 && NW == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = v.x, w[1] = v.y, w[NW - 2] = v.z, w[NW - 1] = v.w;
+    } else if (W >= 8) {
+#pragma unroll
+        for (int i = 0; i < NW / 2; ++i)
+            if (b + 8 * i < nb) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+                w[2 * i] = v.x, w[2 * i + 1] = v.y;
+            }
+    } else if (W == 4) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            if (b + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+    } else {
+        // the aligned words around the bytes, shifted together; a word that the array does not hold whole is read bytewise
+        const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u), left = nb - b;  // left: valid bytes
+        const uint8_t *q = p - sh;
+        uint32_t a[NW + 1];
+#pragma unroll
+        for (int i = 0; i <= NW; ++i) {
+            const uint8_t *c = q + 4 * i;
+            a[i] = 0;
+            if (4 * i - sh >= left) continue;
+            if (c >= lo && c + 4 <= hi) {
+                a[i] = __ldg(reinterpret_cast<const uint32_t *>(c));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c + j >= lo && c + j < hi) a[i] |= (uint32_t)__ldg(c + j) << (8 * j);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const uint32_t v = __funnelshift_r(a[i], a[i + 1], 8 * sh);
+            const int n = left - 4 * i;  // valid bytes of this word
+            const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+            w[i] = (v & keep) | (0x7F7F7F7Fu & ~keep);
+        }
+    }
+}
+template <int W>
+__device__ __forceinline__ uint4 scale_bytes16(const uint8_t *row, int b, int nb, bool in, const uint8_t *lo,
+                                               const uint8_t *hi) {
+    uint32_t w[4];
+    scale_words<W, 4>(w, row, b, nb, in, lo, hi);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int W>
+__device__ __forceinline__ uint2 scale_bytes8(const uint8_t *row, int b, int nb, bool in, const uint8_t *lo,
+                                              const uint8_t *hi) {
+    uint32_t w[2];
+    scale_words<W, 2>(w, row, b, nb, in, lo, hi);
+    return make_uint2(w[0], w[1]);
+}
+
 // Arrive on an mbarrier of a CTA of the cluster, ordering this thread's earlier
 // accesses for its own CTA only.  Enough where what the arrival announces is read
 // through the async proxy (a fence.proxy.async came before it) or by tcgen05: a

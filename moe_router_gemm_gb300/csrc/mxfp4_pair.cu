@@ -74,59 +74,6 @@ __device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int
     q0 = qi * kTileRows;
 }
 
-// Scale bytes 16s .. 16s + 15 of one row (nb bytes at `row`; those past nb read as 1.0), for two chunks.
-// W: bytes that the row's start and length are multiples of (16, 8, 4 or 1); lo, hi: the whole array's bounds.
-template <int W>
-__device__ __forceinline__ uint4 scale_bytes(const uint8_t *row, int s, int nb, bool in, const uint8_t *lo,
-                                             const uint8_t *hi) {
-    uint32_t w[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-    const int b = 16 * s;
-    if (in && b < nb) {
-        const uint8_t *p = row + b;
-        if (W == 16) return __ldg(reinterpret_cast<const uint4 *>(p));
-        if (W == 8) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (b + 8 * i < nb) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
-                    w[2 * i] = v.x;
-                    w[2 * i + 1] = v.y;
-                }
-        } else if (W == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (b + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
-        } else {
-            // aligned words around the bytes, shifted together; a word that the array does not hold whole is read bytewise
-            const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u);
-            const uint8_t *q = p - sh;
-            const int left = nb - b;  // valid bytes
-            uint32_t a[5];
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const uint8_t *c = q + 4 * i;
-                a[i] = 0;
-                if (4 * i - sh >= left) continue;
-                if (c >= lo && c + 4 <= hi) {
-                    a[i] = __ldg(reinterpret_cast<const uint32_t *>(c));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c + j >= lo && c + j < hi) a[i] |= (uint32_t)__ldg(c + j) << (8 * j);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t v = __funnelshift_r(a[i], a[i + 1], 8 * sh);
-                const int n = left - 4 * i;  // valid bytes of this word
-                const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-                w[i] = (v & keep) | (0x7F7F7F7Fu & ~keep);
-            }
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 template <int W>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -358,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 va[PD], vb0[PD], vb1[PD];
 #pragma unroll
             for (int d = 0; d < PD; ++d) {
-                va[d] = scale_bytes<W>(pa, d, nb, ia, xlo, xhi);
-                vb0[d] = scale_bytes<W>(pb0, d, nb, ib0, wlo, whi);
-                vb1[d] = scale_bytes<W>(pb1, d, nb, ib1, wlo, whi);
+                va[d] = scale_bytes16<W>(pa, 16 * d, nb, ia, xlo, xhi);
+                vb0[d] = scale_bytes16<W>(pb0, 16 * d, nb, ib0, wlo, whi);
+                vb1[d] = scale_bytes16<W>(pb1, 16 * d, nb, ib1, wlo, whi);
             }
             // A warp that gave up goes on through the barriers, so that no other one waits for it there.
             for (int s2 = 0; s2 < D; ++s2, ++step) {
@@ -370,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 buf[kHalf + st] = vb1[0];
 #pragma unroll
                 for (int d = 0; d + 1 < PD; ++d) va[d] = va[d + 1], vb0[d] = vb0[d + 1], vb1[d] = vb1[d + 1];
-                va[PD - 1] = scale_bytes<W>(pa, s2 + PD, nb, ia, xlo, xhi);
-                vb0[PD - 1] = scale_bytes<W>(pb0, s2 + PD, nb, ib0, wlo, whi);
-                vb1[PD - 1] = scale_bytes<W>(pb1, s2 + PD, nb, ib1, wlo, whi);
+                va[PD - 1] = scale_bytes16<W>(pa, 16 * (s2 + PD), nb, ia, xlo, xhi);
+                vb0[PD - 1] = scale_bytes16<W>(pb0, 16 * (s2 + PD), nb, ib0, wlo, whi);
+                vb1[PD - 1] = scale_bytes16<W>(pb1, 16 * (s2 + PD), nb, ib1, wlo, whi);
                 // the buffer is whole; its last readers are past the barrier of the step before
                 named_barrier(1, 32 * kScaleWarps);
                 uint4 wb[8];

@@ -1,0 +1,438 @@
+// mxfp4_split.cu — the MXFP4 linear where reading W, or filling the SMs, sets the
+// cost: from one token to a few hundred.
+//
+// W rows sit on the MMA's M side (tcgen05.mma.kind::mxf4.block_scale, 128 rows), NT
+// (16 to 128) tokens on its N side, and K is cut into runs for the S CTAs of a
+// cluster, so that a few thousand W rows still occupy every SM.  The weight goes from
+// HBM to the tensor core without passing a register: widening 4-bit codes for
+// mma.sync took 50 to 100 instructions for each 512 codes and left 1 x 14336 x 4096 at
+// 17 us and 16 x 14336 x 4096 at 31 us.
+//
+//   * a ring stage is one 256-code chunk (128-byte swizzle rows, TMA): 16 KB of W and
+//     NT * 128 bytes of x;
+//   * warp 0: TMA producer; warp 1: MMA issuer (four a chunk, two 32-code scale blocks
+//     each), TMEM; warps 2-5: scales, then the epilogue (TMEM lane quarter = warp % 4);
+//   * scales: thread i reads eight bytes (a chunk) of W row i, and each warp those of
+//     all NT tokens (every lane quarter needs them), kAhead chunks ahead, and writes
+//     the words to one of the TMEM slots: W words at columns 0 and 8 of the slot,
+//     token words at 16 and 24;
+//   * a bf16 x (M <= 16): all threads quantise the CTA's run of x into shared memory,
+//     in the layout that TMA would have written, while the first W chunks are on their
+//     way: no kernel and no memory before this one, and the same bits;
+//   * the CTAs of a cluster leave their fp32 sums [token][row] in shared memory, and
+//     after a cluster barrier each adds the S sums of its share of the tokens, in rank
+//     order, adds the bias and rounds: the order never changes;
+//   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
+#include <cuda_runtime.h>
+
+#include "moe.h"
+#include "mxfp4.cuh"
+
+namespace bf16l {
+
+namespace {
+
+constexpr int kRowsW = 128, kChunkBytes = 128, kChunkBlocks = 8;
+constexpr int kWBytes = kRowsW * kChunkBytes;
+constexpr int kThreads = 192;
+constexpr int kMaxSplit = 8, kMaxStages = 8;
+constexpr int kSlotCols = 32;
+constexpr int kAhead = 4;
+
+template <int NT>
+struct Split {
+    static constexpr int kSlots = NT <= 32 ? 3 : NT == 64 ? 2 : 4;
+    static constexpr int kCols = NT + kSlots * kSlotCols <= 128 ? 128 : 256;  // TMEM columns
+    static constexpr int kSfCol = kCols - kSlots * kSlotCols;
+    static constexpr int kXBytes = NT * kChunkBytes;
+    static_assert(kSfCol >= NT, "TMEM columns");
+};
+
+// The ring, which later holds the sums of NT tokens.
+__host__ __device__ constexpr int ring_bytes(int nt, int stages, int stage) {
+    return stages * stage > nt * kRowsW * 4 ? stages * stage : nt * kRowsW * 4;
+}
+
+struct SplitArgs {
+    const uint16_t *x;     // bf16 x (M <= 16), or null
+    const uint8_t *xs, *ws;
+    const uint16_t *bias;
+    uint16_t *out;
+    int M, N, K, S, m_tiles, stages;
+    int32_t *status;
+    int w_early;
+};
+
+struct SplitShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], sfull[kMaxStages], acc_full;
+    uint32_t tmem_base;
+    int32_t aborted, issued, consumed;
+};
+
+// NT: tokens of a tile.  BF16: x is bf16 and is quantised here.  W: alignment of the scale rows (scale_words).
+template <int NT, bool BF16, int W>
+__global__ void __launch_bounds__(kThreads)
+    mxfp4_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                       const SplitArgs a) {
+    using T = Split<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nb = a.K >> 5, C = (nb + kChunkBlocks - 1) / kChunkBlocks;
+    const int rank = a.S > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = (int)blockIdx.x / a.S;  // token tiles of one W tile follow each other
+    const int n0 = (tile / a.m_tiles) * kRowsW, m0 = (tile % a.m_tiles) * NT;
+    const int c0 = mul_div(C, rank, a.S), nc = mul_div(C, rank + 1, a.S) - c0;  // this CTA's chunks
+    const int tokens = a.M - m0 < NT ? a.M - m0 : NT;
+    // stages of W (and of x where TMA brings it); then, with a bf16 x, the whole run of x and its scale bytes
+    constexpr int kStage = kWBytes + (BF16 ? 0 : T::kXBytes);
+    const int stages = a.stages;
+    uint8_t *xrun = base + ring_bytes(NT, stages, kStage);  // [nc][NT][128], swizzled
+    const int nc_most = (C + a.S - 1) / a.S;
+    uint8_t *xscale = xrun + nc_most * T::kXBytes;          // [nc][NT][8]
+    SplitShared &sh = *reinterpret_cast<SplitShared *>(BF16 ? xscale + nc_most * NT * 8 : xrun);
+
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_w);
+        if (!BF16) tma_prefetch_desc(&tm_x);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int s = 0; s < T::kSlots; ++s) mbar_init(&sh.sfull[s], 4);  // one arrival per scale warp
+        mbar_init(&sh.acc_full, 1);
+        sh.aborted = 0;
+        sh.issued = 0;
+        sh.consumed = 0;
+        fence_barrier_init();
+    }
+    // the codes of chunk i into its stage
+    auto load = [&](int i) {
+        const int s = i % stages;
+        uint8_t *st = base + s * kStage;
+        mbar_arrive_expect_tx(&sh.full[s], kStage);
+        tma_load_2d(st, &tm_w, &sh.full[s], (c0 + i) * kChunkBytes, n0);
+        if (!BF16) tma_load_2d(st + kWBytes, &tm_x, &sh.full[s], (c0 + i) * kChunkBytes, m0);
+    };
+    int first = 0;  // chunks that the producer has already asked for
+    if (!BF16 || !a.w_early) pdl_wait();
+    if (tid == 0)
+        for (; first < stages && first < nc; ++first) load(first);
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem_base, T::kCols);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();  // x may be written, and out still read, by the previous kernel
+    if (BF16) {
+        // item: eight codes (a quad holds a block); the loads of kBatch items of a thread go out together
+        constexpr int kBatch = 4;
+        // (the tokens of the tile past M stay as they are: their columns of the accumulator are not read)
+        const int per = nc * kChunkBlocks * 4, items = tokens * per;  // multiples of 32: warps stay together
+        for (int i0 = tid; i0 < items; i0 += kBatch * kThreads) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads, tok = i / per, r = i - tok * per, b = c0 * kChunkBlocks + (r >> 2);
+                v[k] = (i < items && b < nb)
+                           ? __ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)(m0 + tok) * a.K + 32 * (size_t)b +
+                                                                   8 * (r & 3)))
+                           : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads, tok = i / per, r = i - tok * per;
+                if (i >= items) break;
+                uint32_t s;
+                const uint32_t w = mxfp4_quant_vec(v[k], 0xFu << (lane & 28), s);
+                const int c = r >> 5, u = (r >> 2) & 7;  // chunk, 16-byte unit of its row (a block)
+                *reinterpret_cast<uint32_t *>(xrun + c * T::kXBytes + tok * 128 + 16 * (u ^ (tok & 7)) + 4 * (r & 3)) = w;
+                if ((r & 3) == 0) xscale[(c * NT + tok) * 8 + u] = (uint8_t)s;
+            }
+        }
+        fence_proxy_async_smem();  // the MMAs read xrun through the async proxy
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {  // ---- TMA producer ----
+            int i = first;
+            for (; i < nc; ++i) {
+                if (i >= stages && !mbar_wait(&sh.empty[i % stages], ((i / stages) - 1) & 1, a.status, kSiteEmpty)) {
+                    atomicExch(&sh.aborted, 1);
+                    break;
+                }
+                if (*((volatile int32_t *)&sh.aborted)) break;
+                load(i);
+            }
+            sh.issued = i;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {  // ---- MMA issuer ----
+            int i = 0;
+            for (; i < nc; ++i) {
+                const int s = i % stages, f = i % T::kSlots;
+                if (!mbar_wait(&sh.full[s], (i / stages) & 1, a.status, kSiteFull) ||
+                    !mbar_wait(&sh.sfull[f], (i / T::kSlots) & 1, a.status, kSiteScale)) {
+                    atomicExch(&sh.aborted, 1);
+                    break;
+                }
+                tc_fence_after();
+                uint8_t *st = base + s * kStage;
+                const uint64_t wdesc = smem_desc_sw128(smem_u32(st));
+                const uint64_t xdesc = smem_desc_sw128(smem_u32(BF16 ? xrun + i * T::kXBytes : st + kWBytes));
+                const uint32_t sf = tmem + (uint32_t)(T::kSfCol + kSlotCols * f);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 64 codes, two scale blocks
+                    mma_mxf4(tmem, wdesc + 2 * kk, xdesc + 2 * kk, idesc_mxf4_f32(kRowsW, NT, 2 * (kk & 1)),
+                             sf + 8 * (kk >> 1), sf + 16 + 8 * (kk >> 1), (i > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(&sh.empty[s]);
+            }
+            sh.consumed = i;
+            if (i < nc)
+                mbar_arrive(&sh.acc_full);
+            else
+                mma_commit(&sh.acc_full);
+        }
+        __syncwarp();
+    } else {
+        // ---- scales ----
+        const int quarter = warp & 3;
+        const uint32_t slot0 = tmem + (uint32_t)T::kSfCol + ((uint32_t)(quarter * 32) << 16);
+        constexpr int kTw = (NT + 31) / 32;  // token words per lane
+        const int row = n0 + 32 * quarter + lane;
+        const uint8_t *wr = a.ws + (size_t)(row < a.N ? row : 0) * nb;
+        const uint8_t *xr = BF16 ? nullptr : a.xs + (size_t)m0 * nb;
+        auto w_words = [&](int i) {  // of this lane's W row, chunk i of the run
+            return scale_bytes8<W>(wr, 8 * (c0 + i), nb, row < a.N && i < nc, a.ws, a.ws + (size_t)a.N * nb);
+        };
+        auto token_words = [&](int j, int i) {  // of token 32 j + lane, chunk i of the run
+            const int tok = 32 * j + lane;
+            if (BF16) return tok < NT && i < nc ? *reinterpret_cast<const uint2 *>(xscale + (i * NT + tok) * 8)
+                                                : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            return scale_bytes8<W>(xr + (size_t)(tok < tokens ? tok : 0) * nb, 8 * (c0 + i), nb, tok < tokens && i < nc,
+                                   a.xs, a.xs + (size_t)a.M * nb);
+        };
+        uint2 vw[kAhead], vx[kAhead][kTw];
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            vw[d] = w_words(d);
+#pragma unroll
+            for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, d);
+        }
+        bool stop = false;
+        for (int i0 = 0; i0 < nc && !stop; i0 += kAhead) {
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+                const int i = i0 + d;
+                if (i >= nc) break;
+                const int f = i % T::kSlots, old = i - T::kSlots;  // the slot is free when the MMAs of chunk `old` are done
+                if (old >= 0 && !mbar_wait(&sh.empty[old % stages], (old / stages) & 1, a.status, kSiteScale)) stop = true;
+                if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
+                    atomicExch(&sh.aborted, 1);
+                    stop = true;
+                    break;
+                }
+                const uint32_t sf = slot0 + (uint32_t)(kSlotCols * f);
+                const uint2 w = vw[d];
+                tmem_st4(sf, w.x, w.x, w.x, w.x);  // column `quarter` of the four is the one read
+                tmem_st4(sf + 8, w.y, w.y, w.y, w.y);
+                constexpr int l = kTw - 1;
+                tmem_st4(sf + 16, vx[d][0].x, vx[d][l < 1 ? l : 1].x, vx[d][l < 2 ? l : 2].x, vx[d][l].x);
+                tmem_st4(sf + 24, vx[d][0].y, vx[d][l < 1 ? l : 1].y, vx[d][l < 2 ? l : 2].y, vx[d][l].y);
+                vw[d] = w_words(i + kAhead);
+#pragma unroll
+                for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, i + kAhead);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.sfull[f]);
+            }
+        }
+        // ---- epilogue: lane = W row, columns = tokens ----
+        const bool ok = mbar_wait(&sh.acc_full, 0, a.status, kSiteAccum);
+        tc_fence_after();
+        const bool have = __all_sync(0xFFFFFFFFu, ok && !*((volatile int32_t *)&sh.aborted));
+        if (have) {
+            float *sums = reinterpret_cast<float *>(base);  // [token][128 rows], over the ring: every chunk has been read
+            const float bias = a.bias && row < a.N ? bf16_to_f32(__ldg(a.bias + row)) : 0.0f;
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+            for (int c = 0; c < NT; c += 16) {
+                if (c >= tokens) break;
+                uint32_t r[16];
+                tmem_ld16(acc + (uint32_t)c, r);
+                tmem_ld_wait16(r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float v = __uint_as_float(r[j]);
+                    if (a.S > 1)
+                        sums[(c + j) * kRowsW + 32 * quarter + lane] = v;
+                    else if (c + j < tokens && row < a.N)
+                        a.out[(size_t)(m0 + c + j) * a.N + row] = f32_to_bf16(v + bias);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    if (a.S > 1) {
+        cluster_sync();  // every CTA's sums are in its shared memory
+        const bool have = *((volatile int32_t *)&sh.aborted) == 0;
+        const int row = n0 + 4 * lane;  // a warp takes a token at a time, a lane four rows of it
+        const bool vec = a.N % 4 == 0;
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (a.bias && row + j < a.N) bias[j] = bf16_to_f32(__ldg(a.bias + row + j));
+        for (int tok = rank + a.S * warp; have && tok < tokens; tok += a.S * (kThreads / 32)) {
+            const uint32_t at = smem_u32(base) + (uint32_t)(tok * kRowsW + 4 * lane) * 4u;
+            float4 v[kMaxSplit];
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                if (r < a.S) v[r] = ld_dsmem_f4(mapa_shared(at, (uint32_t)r));
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                if (r < a.S) s[0] += v[r].x, s[1] += v[r].y, s[2] += v[r].z, s[3] += v[r].w;  // ranks in order
+            uint16_t *o = a.out + (size_t)(m0 + tok) * a.N + row;
+            if (vec && row + 3 < a.N) {
+                OutStore<uint16_t>::four(o, s[0] + bias[0], s[1] + bias[1], s[2] + bias[2], s[3] + bias[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + j < a.N) o[j] = f32_to_bf16(s[j] + bias[j]);
+            }
+        }
+        cluster_sync();  // nobody exits while its sums are still read
+    } else {
+        __syncthreads();
+    }
+    if (tid == 0) {  // copies that were issued but never consumed (only after a timeout)
+        for (int i = sh.consumed; i < sh.issued; ++i)
+            if (!mbar_wait(&sh.full[i % stages], (i / stages) & 1, a.status, kSiteDrain)) break;
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, T::kCols);
+    }
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+using SplitFn = void (*)(const CUtensorMap, const CUtensorMap, const SplitArgs);
+
+template <int W>
+SplitFn pick_w(int nt, bool bf16) {
+    if (nt == 16) return bf16 ? mxfp4_split_kernel<16, true, W> : mxfp4_split_kernel<16, false, W>;
+    return nt == 32   ? mxfp4_split_kernel<32, false, W>
+           : nt == 64 ? mxfp4_split_kernel<64, false, W>
+                      : mxfp4_split_kernel<128, false, W>;
+}
+
+SplitFn pick_split(int nt, bool bf16, uintptr_t align) {
+    return align % 8 == 0 ? pick_w<8>(nt, bf16) : align % 4 == 0 ? pick_w<4>(nt, bf16) : pick_w<1>(nt, bf16);
+}
+
+constexpr int kMaxSmem = 227 * 1024;
+// Two CTAs to an SM, or one, and none beside a kernel that takes all of TMEM (those ask for 116 KB or more): the
+// CTAs of a cluster wait for one another, so none of them may wait for TMEM that another cluster's CTA holds.
+constexpr int kHalfSmem = 112 * 1024, kHalfSmemMost = 113 * 1024;
+
+int split_smem(int nt, int stages, int S, int K, bool bf16) {
+    const int nc = ceil_div(ceil_div(K, 256), S);
+    int n = 1024 + ring_bytes(nt, stages, kWBytes + (bf16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
+    if (bf16) n += nc * nt * (kChunkBytes + 8);
+    const int least = nt == 128 ? kHalfSmemMost + 2048 : kHalfSmem;  // 256 TMEM columns: one CTA per SM
+    return n > least ? n : least;
+}
+
+int split_slots(int nt) { return nt <= 32 ? Split<32>::kSlots : nt == 64 ? Split<64>::kSlots : Split<128>::kSlots; }
+
+}  // namespace
+
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, bool bf16, int num_sms) {
+    Mxfp4SplitPlan p;
+    const int C = ceil_div(K, 256), n_tiles = ceil_div(N, kRowsW);
+    p.tokens = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    p.m_tiles = ceil_div(M, p.tokens);
+    const long long tiles = (long long)n_tiles * p.m_tiles;
+    const int room = (p.tokens == 128 ? 1 : 2) * num_sms;  // CTAs that run at once
+    // K over twice the CTAs while they all run at once and each keeps two chunks
+    p.split = 1;
+    while (p.split < kMaxSplit && tiles * p.split * 2 <= room && 2 * p.split * 2 <= C) p.split *= 2;
+    const int nc = ceil_div(C, p.split), slots = split_slots(p.tokens);
+    const int most = p.tokens < 128 && tiles * p.split > num_sms ? kHalfSmemMost : kMaxSmem;
+    p.stages = nc < kMaxStages ? nc : kMaxStages;
+    // (with fewer stages than scale slots a slot's wait could miss a turn of the stage's barrier)
+    while (p.stages > slots && split_smem(p.tokens, p.stages, p.split, K, bf16) > most) --p.stages;
+    p.smem = split_smem(p.tokens, p.stages, p.split, K, bf16);
+    return p;
+}
+
+bool mxfp4_split_quantises(int M, int N, int K) {
+    return M <= 16 && mxfp4_split_plan(M, N, K, true, kGb300Sms).smem <= kMaxSmem;
+}
+
+int init_mxfp4_split() {
+    for (uintptr_t w : {8, 4, 1})
+        for (int nt : {16, 32, 64, 128})
+            for (bool b : {false, true}) {
+                if (b && nt > 16) continue;
+                const int e = (int)cudaFuncSetAttribute(pick_split(nt, b, w),
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+                if (e) return e;
+            }
+    return 0;
+}
+
+int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                       int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status) {
+    const bool bf16 = xs == nullptr;
+    const Mxfp4SplitPlan p = mxfp4_split_plan(M, N, K, bf16, num_sms);
+    CUtensorMap tx = {}, tw;  // 128-byte rows of 256 codes
+    int r = make_tmap_u8_2d(&tw, wq, (uint64_t)N, (uint64_t)(K / 2), kRowsW, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (r) return (int)cudaErrorInvalidValue;
+    if (!bf16) {
+        r = make_tmap_u8_2d(&tx, x, (uint64_t)M, (uint64_t)(K / 2), (uint32_t)p.tokens, kChunkBytes,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+        if (r) return (int)cudaErrorInvalidValue;
+    }
+    SplitArgs a = {bf16 ? static_cast<const uint16_t *>(x) : nullptr,
+                   static_cast<const uint8_t *>(xs),
+                   static_cast<const uint8_t *>(ws),
+                   static_cast<const uint16_t *>(bias),
+                   static_cast<uint16_t *>(out),
+                   M,
+                   N,
+                   K,
+                   p.split,
+                   p.m_tiles,
+                   p.stages,
+                   status,
+                   w_early_of(flags)};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ceil_div(N, kRowsW) * p.m_tiles * p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)p.smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    const uintptr_t al = (bf16 ? 0 : reinterpret_cast<uintptr_t>(xs)) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
+    return (int)cudaLaunchKernelEx(&cfg, pick_split(p.tokens, bf16, al), tx, tw, a);
+}
+
+}  // namespace bf16l
