@@ -66,8 +66,6 @@ void init_device(DeviceState &s) {
         if (!e) e = init_warpmma_ks();
         if (!e) e = init_dotmma();
         if (!e) e = init_mxfp8();
-        if (!e) e = init_mxfp4();
-        if (!e) e = init_mxfp4_tile();
         if (!e) e = init_mxfp4_pair();
         if (!e) e = init_mxfp4_split();
     }

@@ -10,36 +10,27 @@ namespace bf16l {
 // As current_device_checked, with the device's kernel status word.  Defined in api.cu.
 int current_device_status(bf16l_device *dev, int32_t **status);
 
-// MXFP4 (mxfp4.cu): quantisation and its inverse (n values, n % 32 == 0), and the block-scaled linear on
-// warp-level e4m3 MMAs (K % 32 == 0; grid.z covers any M in groups of 16 tokens; S: CTAs per cluster along K).
-int init_mxfp4();
+// MXFP4 (mxfp4.cu): quantisation and its inverse (n values, n % 32 == 0).
 int launch_quant_mxfp4(const void *x, void *q, void *scales, long long n, int num_sms, uint32_t flags, void *stream);
 int launch_dequant_mxfp4(const void *q, const void *scales, void *out, long long n, int num_sms, uint32_t flags,
                          void *stream);
-int launch_mxfp4(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out, int M,
-                 int N, int K, int S, int threads, uint32_t flags, void *stream, int32_t *status);
 
-// The MXFP4 tile form (mxfp4_tile.cu; tcgen05 block-scaled MMAs): 128 x rows by bq (128 or 256) W rows per tile.
-constexpr int kMxfp4TileThreads = 320;
-int init_mxfp4_tile();
-int launch_mxfp4_tile(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
-                      int M, int N, int K, int bq, int num_sms, uint32_t flags, void *stream, int32_t *status);
-
-// ... and by CTA pairs on 256 x 256 tiles (mxfp4_pair.cu).
-int init_mxfp4_pair();
-int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
-                      int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
-
-// ... and with K over a cluster's CTAs, W on the MMA's M side (mxfp4_split.cu): xs null means that x is bf16 and is
-// quantised by the kernel (where mxfp4_split_quantises).
+// The MXFP4 linear with K over a cluster's CTAs and W on the MMA's M side (mxfp4_split.cu): any M; xs null means that
+// x is bf16 and is quantised by the kernel (where mxfp4_split_quantises).
 struct Mxfp4SplitPlan {
-    int tokens, m_tiles, split, stages, smem;
+    int tokens, m_tiles, split, stages, smem;  // tokens and token tiles, CTAs along K, ring depth, dynamic shared memory
+    float estimate;                            // microseconds beside the fixed part, roughly
 };
-Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, bool bf16, int num_sms);
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms);
 bool mxfp4_split_quantises(int M, int N, int K);
 int init_mxfp4_split();
 int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                        int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
+// ... and by CTA pairs on 256 x 256 tiles (mxfp4_pair.cu).
+float mxfp4_pair_estimate(int M, int N, int K, int num_sms);  // as Mxfp4SplitPlan::estimate
+int init_mxfp4_pair();
+int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
+                      int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
 // Row norm (norm.cu) and routing (route.cu); arguments as in bf16_linear.h.
 int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void *weight, void *out, void *residual_out,

@@ -58,16 +58,6 @@ __device__ __forceinline__ uint32_t mxfp4_quant_vec(const uint4 &w, unsigned qua
     return nan ? 0u : e2m1x8(f);
 }
 
-// Eight e2m1 codes (one word) as e4m3 codes, the even elements in `even` and the
-// odd ones in `odd` (byte i: element 2i or 2i + 1).  The e2m1 fields land in the
-// low exponent and high mantissa bits of e4m3 (bias 7 instead of 1), so each
-// e4m3 value is the e2m1 value times 2^-6, exactly, e2m1's subnormal included.
-__device__ __forceinline__ void e2m1_to_e4m3(uint32_t w, uint32_t &even, uint32_t &odd) {
-    const uint32_t u = w << 4;
-    even = (u & 0x80808080u) | ((u >> 2) & 0x1C1C1C1Cu);
-    odd = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
-}
-
 // Instruction descriptor of the block-scaled e2m1 MMA (kind::mxf4): A and B e2m1
 // (format 1 at bits 7-9 and 10-12), K-major, N>>3 at bit 17, scale format E8M0
 // at bit 23, M>>4 at bit 24; the first of the two bytes of each 32-bit scale word
@@ -127,21 +117,19 @@ __device__ __forceinline__ void scale_words(uint32_t (&w)[NW], const uint8_t *ro
         for (int i = 0; i < NW; ++i)
             if (b + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
     } else {
-        // the aligned words around the bytes, shifted together; a word that the array does not hold whole is read bytewise
+        // the aligned words around the bytes, shifted together; at the array's ends byte by byte
         const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u), left = nb - b;  // left: valid bytes
         const uint8_t *q = p - sh;
         uint32_t a[NW + 1];
+        if (q >= lo && q + 4 * (NW + 1) <= hi) {
 #pragma unroll
-        for (int i = 0; i <= NW; ++i) {
-            const uint8_t *c = q + 4 * i;
-            a[i] = 0;
-            if (4 * i - sh >= left) continue;
-            if (c >= lo && c + 4 <= hi) {
-                a[i] = __ldg(reinterpret_cast<const uint32_t *>(c));
-            } else {
+            for (int i = 0; i <= NW; ++i) a[i] = __ldg(reinterpret_cast<const uint32_t *>(q) + i);
+        } else {
 #pragma unroll
+            for (int i = 0; i <= NW; ++i) {
+                a[i] = 0;
                 for (int j = 0; j < 4; ++j)
-                    if (c + j >= lo && c + j < hi) a[i] |= (uint32_t)__ldg(c + j) << (8 * j);
+                    if (q + 4 * i + j >= lo && q + 4 * i + j < hi) a[i] |= (uint32_t)__ldg(q + 4 * i + j) << (8 * j);
             }
         }
 #pragma unroll

@@ -2,7 +2,7 @@
 // cost: from one token to a few hundred.
 //
 // W rows sit on the MMA's M side (tcgen05.mma.kind::mxf4.block_scale, 128 rows), NT
-// (16 to 128) tokens on its N side, and K is cut into runs for the S CTAs of a
+// (16 to 64) tokens on its N side, and K is cut into runs for the S CTAs of a
 // cluster, so that a few thousand W rows still occupy every SM.  The weight goes from
 // HBM to the tensor core without passing a register: widening 4-bit codes for
 // mma.sync took 50 to 100 instructions for each 512 codes and left 1 x 14336 x 4096 at
@@ -16,9 +16,10 @@
 //     all NT tokens (every lane quarter needs them), kAhead chunks ahead, and writes
 //     the words to one of the TMEM slots: W words at columns 0 and 8 of the slot,
 //     token words at 16 and 24;
-//   * a bf16 x (M <= 16): all threads quantise the CTA's run of x into shared memory,
-//     in the layout that TMA would have written, while the first W chunks are on their
-//     way: no kernel and no memory before this one, and the same bits;
+//   * M <= 16: all threads put the CTA's whole run of x into shared memory, in the layout
+//     that TMA would have written, while the first W chunks are on their way: from codes
+//     (a TMA box that is mostly past M is slow: 1 x 14336 x 4096 16 us with it), or
+//     quantising a bf16 x: no kernel and no memory before this one, and the same bits;
 //   * the CTAs of a cluster leave their fp32 sums [token][row] in shared memory, and
 //     after a cluster barrier each adds the S sums of its share of the tokens, in rank
 //     order, adds the bias and rounds: the order never changes;
@@ -41,8 +42,8 @@ constexpr int kAhead = 4;
 
 template <int NT>
 struct Split {
-    static constexpr int kSlots = NT <= 32 ? 3 : NT == 64 ? 2 : 4;
-    static constexpr int kCols = NT + kSlots * kSlotCols <= 128 ? 128 : 256;  // TMEM columns
+    static constexpr int kSlots = NT <= 32 ? 3 : 2;
+    static constexpr int kCols = 128;  // TMEM columns
     static constexpr int kSfCol = kCols - kSlots * kSlotCols;
     static constexpr int kXBytes = NT * kChunkBytes;
     static_assert(kSfCol >= NT, "TMEM columns");
@@ -54,7 +55,7 @@ __host__ __device__ constexpr int ring_bytes(int nt, int stages, int stage) {
 }
 
 struct SplitArgs {
-    const uint16_t *x;     // bf16 x (M <= 16), or null
+    const void *x;         // bf16, or codes
     const uint8_t *xs, *ws;
     const uint16_t *bias;
     uint16_t *out;
@@ -69,12 +70,13 @@ struct SplitShared {
     int32_t aborted, issued, consumed;
 };
 
-// NT: tokens of a tile.  BF16: x is bf16 and is quantised here.  W: alignment of the scale rows (scale_words).
+// NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  W: alignment of the scale rows (scale_words).
 template <int NT, bool BF16, int W>
 __global__ void __launch_bounds__(kThreads)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const SplitArgs a) {
     using T = Split<NT>;
+    constexpr bool kStaged = NT == 16;  // x by the threads rather than by TMA
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -85,17 +87,17 @@ __global__ void __launch_bounds__(kThreads)
     const int n0 = (tile / a.m_tiles) * kRowsW, m0 = (tile % a.m_tiles) * NT;
     const int c0 = mul_div(C, rank, a.S), nc = mul_div(C, rank + 1, a.S) - c0;  // this CTA's chunks
     const int tokens = a.M - m0 < NT ? a.M - m0 : NT;
-    // stages of W (and of x where TMA brings it); then, with a bf16 x, the whole run of x and its scale bytes
-    constexpr int kStage = kWBytes + (BF16 ? 0 : T::kXBytes);
+    // stages of W (and of x where TMA brings it); then, where x is staged, its whole run and the scale bytes
+    constexpr int kStage = kWBytes + (kStaged ? 0 : T::kXBytes);
     const int stages = a.stages;
     uint8_t *xrun = base + ring_bytes(NT, stages, kStage);  // [nc][NT][128], swizzled
     const int nc_most = (C + a.S - 1) / a.S;
     uint8_t *xscale = xrun + nc_most * T::kXBytes;          // [nc][NT][8]
-    SplitShared &sh = *reinterpret_cast<SplitShared *>(BF16 ? xscale + nc_most * NT * 8 : xrun);
+    SplitShared &sh = *reinterpret_cast<SplitShared *>(kStaged ? xscale + nc_most * NT * 8 : xrun);
 
     if (tid == 0) {
         tma_prefetch_desc(&tm_w);
-        if (!BF16) tma_prefetch_desc(&tm_x);
+        if (!kStaged) tma_prefetch_desc(&tm_x);
         for (int s = 0; s < stages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
@@ -113,10 +115,10 @@ __global__ void __launch_bounds__(kThreads)
         uint8_t *st = base + s * kStage;
         mbar_arrive_expect_tx(&sh.full[s], kStage);
         tma_load_2d(st, &tm_w, &sh.full[s], (c0 + i) * kChunkBytes, n0);
-        if (!BF16) tma_load_2d(st + kWBytes, &tm_x, &sh.full[s], (c0 + i) * kChunkBytes, m0);
+        if (!kStaged) tma_load_2d(st + kWBytes, &tm_x, &sh.full[s], (c0 + i) * kChunkBytes, m0);
     };
     int first = 0;  // chunks that the producer has already asked for
-    if (!BF16 || !a.w_early) pdl_wait();
+    if (!kStaged || !a.w_early) pdl_wait();
     if (tid == 0)
         for (; first < stages && first < nc; ++first) load(first);
     if (warp == 1) {
@@ -125,9 +127,9 @@ __global__ void __launch_bounds__(kThreads)
     }
     pdl_launch_dependents();
     pdl_wait();  // x may be written, and out still read, by the previous kernel
-    if (BF16) {
+    if (kStaged && BF16) {
         // item: eight codes (a quad holds a block); the loads of kBatch items of a thread go out together
-        constexpr int kBatch = 4;
+        constexpr int kBatch = 8;
         // (the tokens of the tile past M stay as they are: their columns of the accumulator are not read)
         const int per = nc * kChunkBlocks * 4, items = tokens * per;  // multiples of 32: warps stay together
         for (int i0 = tid; i0 < items; i0 += kBatch * kThreads) {
@@ -136,8 +138,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k * kThreads, tok = i / per, r = i - tok * per, b = c0 * kChunkBlocks + (r >> 2);
                 v[k] = (i < items && b < nb)
-                           ? __ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)(m0 + tok) * a.K + 32 * (size_t)b +
-                                                                   8 * (r & 3)))
+                           ? __ldg(static_cast<const uint4 *>(a.x) + ((size_t)(m0 + tok) * nb + b) * 4 + (r & 3))
                            : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
@@ -151,8 +152,18 @@ __global__ void __launch_bounds__(kThreads)
                 if ((r & 3) == 0) xscale[(c * NT + tok) * 8 + u] = (uint8_t)s;
             }
         }
-        fence_proxy_async_smem();  // the MMAs read xrun through the async proxy
+    } else if (kStaged) {
+        const int per = nc * kChunkBlocks;  // item: a block, 16 bytes of codes and a scale byte
+        for (int i = tid; i < tokens * per; i += kThreads) {
+            const int tok = i / per, r = i - tok * per, b = c0 * kChunkBlocks + r, c = r >> 3, u = r & 7;
+            const bool in = b < nb;
+            const size_t at = (size_t)(m0 + tok) * nb + b;
+            *reinterpret_cast<uint4 *>(xrun + c * T::kXBytes + tok * 128 + 16 * (u ^ (tok & 7))) =
+                in ? __ldg(static_cast<const uint4 *>(a.x) + at) : make_uint4(0u, 0u, 0u, 0u);
+            xscale[(c * NT + tok) * 8 + u] = in ? __ldg(a.xs + at) : (uint8_t)127;
+        }
     }
+    if (kStaged) fence_proxy_async_smem();  // the MMAs read xrun through the async proxy
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(kThreads)
                 tc_fence_after();
                 uint8_t *st = base + s * kStage;
                 const uint64_t wdesc = smem_desc_sw128(smem_u32(st));
-                const uint64_t xdesc = smem_desc_sw128(smem_u32(BF16 ? xrun + i * T::kXBytes : st + kWBytes));
+                const uint64_t xdesc = smem_desc_sw128(smem_u32(kStaged ? xrun + i * T::kXBytes : st + kWBytes));
                 const uint32_t sf = tmem + (uint32_t)(T::kSfCol + kSlotCols * f);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // 64 codes, two scale blocks
@@ -207,13 +218,13 @@ __global__ void __launch_bounds__(kThreads)
         constexpr int kTw = (NT + 31) / 32;  // token words per lane
         const int row = n0 + 32 * quarter + lane;
         const uint8_t *wr = a.ws + (size_t)(row < a.N ? row : 0) * nb;
-        const uint8_t *xr = BF16 ? nullptr : a.xs + (size_t)m0 * nb;
+        const uint8_t *xr = kStaged ? nullptr : a.xs + (size_t)m0 * nb;
         auto w_words = [&](int i) {  // of this lane's W row, chunk i of the run
             return scale_bytes8<W>(wr, 8 * (c0 + i), nb, row < a.N && i < nc, a.ws, a.ws + (size_t)a.N * nb);
         };
         auto token_words = [&](int j, int i) {  // of token 32 j + lane, chunk i of the run
             const int tok = 32 * j + lane;
-            if (BF16) return tok < NT && i < nc ? *reinterpret_cast<const uint2 *>(xscale + (i * NT + tok) * 8)
+            if (kStaged) return tok < NT && i < nc ? *reinterpret_cast<const uint2 *>(xscale + (i * NT + tok) * 8)
                                                 : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
             return scale_bytes8<W>(xr + (size_t)(tok < tokens ? tok : 0) * nb, 8 * (c0 + i), nb, tok < tokens && i < nc,
                                    a.xs, a.xs + (size_t)a.M * nb);
@@ -330,9 +341,7 @@ using SplitFn = void (*)(const CUtensorMap, const CUtensorMap, const SplitArgs);
 template <int W>
 SplitFn pick_w(int nt, bool bf16) {
     if (nt == 16) return bf16 ? mxfp4_split_kernel<16, true, W> : mxfp4_split_kernel<16, false, W>;
-    return nt == 32   ? mxfp4_split_kernel<32, false, W>
-           : nt == 64 ? mxfp4_split_kernel<64, false, W>
-                      : mxfp4_split_kernel<128, false, W>;
+    return nt == 32 ? mxfp4_split_kernel<32, false, W> : mxfp4_split_kernel<64, false, W>;
 }
 
 SplitFn pick_split(int nt, bool bf16, uintptr_t align) {
@@ -344,44 +353,51 @@ constexpr int kMaxSmem = 227 * 1024;
 // CTAs of a cluster wait for one another, so none of them may wait for TMEM that another cluster's CTA holds.
 constexpr int kHalfSmem = 112 * 1024, kHalfSmemMost = 113 * 1024;
 
-int split_smem(int nt, int stages, int S, int K, bool bf16) {
+int split_smem(int nt, int stages, int S, int K) {
     const int nc = ceil_div(ceil_div(K, 256), S);
-    int n = 1024 + ring_bytes(nt, stages, kWBytes + (bf16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
-    if (bf16) n += nc * nt * (kChunkBytes + 8);
-    const int least = nt == 128 ? kHalfSmemMost + 2048 : kHalfSmem;  // 256 TMEM columns: one CTA per SM
-    return n > least ? n : least;
+    int n = 1024 + ring_bytes(nt, stages, kWBytes + (nt == 16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
+    if (nt == 16) n += nc * nt * (kChunkBytes + 8);
+    return n > kHalfSmem ? n : kHalfSmem;
 }
 
-int split_slots(int nt) { return nt <= 32 ? Split<32>::kSlots : nt == 64 ? Split<64>::kSlots : Split<128>::kSlots; }
+int split_slots(int nt) { return nt <= 32 ? Split<32>::kSlots : Split<64>::kSlots; }
 
 }  // namespace
 
-Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, bool bf16, int num_sms) {
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
     Mxfp4SplitPlan p;
     const int C = ceil_div(K, 256), n_tiles = ceil_div(N, kRowsW);
-    p.tokens = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    p.tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     p.m_tiles = ceil_div(M, p.tokens);
-    const long long tiles = (long long)n_tiles * p.m_tiles;
-    const int room = (p.tokens == 128 ? 1 : 2) * num_sms;  // CTAs that run at once
-    // K over twice the CTAs while they all run at once and each keeps two chunks
-    p.split = 1;
-    while (p.split < kMaxSplit && tiles * p.split * 2 <= room && 2 * p.split * 2 <= C) p.split *= 2;
+    // K over S CTAs: microseconds from timings of 40 shapes (1 to 512 tokens, 256 to 14336 rows).  A chunk takes about 0.4
+    // where every SM has at most one CTA, and as much longer as there are more; joining S sums costs more with S, and with
+    // the tokens where S is 8.  64 x 2112 x 7168: S = 1, 2, 4, 8 take 16.0, 10.7, 7.7, 8.6 us; 16 x 2112 x 7168: 16.7,
+    // 10.8, 8.0, 7.0; 1 x 14336 x 4096: 11.7, 9.9, 13.0, 19.0.
+    const float tiles = (float)n_tiles * (float)p.m_tiles;
+    float best = 0.0f;
+    for (int S = 1; S <= kMaxSplit && S <= C; S *= 2) {
+        const float load = tiles * (float)S / (float)num_sms;
+        const float join = S == 1 ? 0.0f : S == 2 ? 0.3f : S == 4 ? 0.7f : 0.7f + 0.03f * (float)p.tokens;
+        const float t = 0.4f * (float)ceil_div(C, S) * (load > 1.0f ? load : 1.0f) + join;
+        if (S == 1 || t < best) best = t, p.split = S;
+    }
+    p.estimate = best;
     const int nc = ceil_div(C, p.split), slots = split_slots(p.tokens);
-    const int most = p.tokens < 128 && tiles * p.split > num_sms ? kHalfSmemMost : kMaxSmem;
+    const int most = tiles * (float)p.split > (float)num_sms ? kHalfSmemMost : kMaxSmem;
     p.stages = nc < kMaxStages ? nc : kMaxStages;
     // (with fewer stages than scale slots a slot's wait could miss a turn of the stage's barrier)
-    while (p.stages > slots && split_smem(p.tokens, p.stages, p.split, K, bf16) > most) --p.stages;
-    p.smem = split_smem(p.tokens, p.stages, p.split, K, bf16);
+    while (p.stages > slots && split_smem(p.tokens, p.stages, p.split, K) > most) --p.stages;
+    p.smem = split_smem(p.tokens, p.stages, p.split, K);
     return p;
 }
 
 bool mxfp4_split_quantises(int M, int N, int K) {
-    return M <= 16 && mxfp4_split_plan(M, N, K, true, kGb300Sms).smem <= kMaxSmem;
+    return M <= 16 && mxfp4_split_plan(M, N, K, kGb300Sms).smem <= kMaxSmem;
 }
 
 int init_mxfp4_split() {
     for (uintptr_t w : {8, 4, 1})
-        for (int nt : {16, 32, 64, 128})
+        for (int nt : {16, 32, 64})
             for (bool b : {false, true}) {
                 if (b && nt > 16) continue;
                 const int e = (int)cudaFuncSetAttribute(pick_split(nt, b, w),
@@ -394,17 +410,17 @@ int init_mxfp4_split() {
 int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                        int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status) {
     const bool bf16 = xs == nullptr;
-    const Mxfp4SplitPlan p = mxfp4_split_plan(M, N, K, bf16, num_sms);
+    const Mxfp4SplitPlan p = mxfp4_split_plan(M, N, K, num_sms);
     CUtensorMap tx = {}, tw;  // 128-byte rows of 256 codes
     int r = make_tmap_u8_2d(&tw, wq, (uint64_t)N, (uint64_t)(K / 2), kRowsW, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (r) return (int)cudaErrorInvalidValue;
-    if (!bf16) {
+    if (p.tokens > 16) {
         r = make_tmap_u8_2d(&tx, x, (uint64_t)M, (uint64_t)(K / 2), (uint32_t)p.tokens, kChunkBytes,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
         if (r) return (int)cudaErrorInvalidValue;
     }
-    SplitArgs a = {bf16 ? static_cast<const uint16_t *>(x) : nullptr,
+    SplitArgs a = {x,
                    static_cast<const uint8_t *>(xs),
                    static_cast<const uint8_t *>(ws),
                    static_cast<const uint16_t *>(bias),
