@@ -2,10 +2,15 @@
 // logits: softmax or sigmoid scores, a bias for the choice alone, limited groups,
 // top-k, renormalised weights.
 //
-// One warp per token.  A key is an unsigned word whose order is the float's
-// (NaN and -inf at the bottom, -0 equal to +0, 0 for an expert that a group
-// limit or an earlier pick took out), so a pick is two warp reductions: the
-// largest key, then the lowest expert that has it.
+// One warp per token, each lane with a run of VPL neighbouring experts in registers.
+// A key is an unsigned word whose order is the float's (NaN and -inf at the bottom, -0
+// equal to +0, 0 for an expert that a group limit or an earlier pick took out).  A pick
+// is the largest of the lanes' largest keys (one warp reduction) and the first lane
+// that has it, which is the lowest expert as runs ascend; only that lane then looks for
+// its next key.  Groups that are whole lanes, a power of two of them, are ranked by a
+// butterfly and a count of the better ones; others by reductions over masked keys.
+// Some 600 instructions a token of 256 experts and 8 picks, two thirds of them in the
+// picks: issue, not the 1 KB of logits, is the bound.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -23,6 +28,9 @@ struct RouteArgs {
     long long tokens, ld;
     int E, k, groups, top_groups, group_best, softmax, renorm, bf16;
     float scale;
+    int by_logit;     // the logits are the keys
+    int vec;          // a lane's run may be read 16 bytes at a time
+    int group_lanes;  // lanes of a group, where that is a power of two; else 0
 };
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -48,21 +56,39 @@ __device__ __forceinline__ float load_logit(const RouteArgs &a, long long at) {
     return a.bf16 ? bf16_to_f32(static_cast<const uint16_t *>(a.logits)[at]) : static_cast<const float *>(a.logits)[at];
 }
 
-// VPL: experts per lane; expert e sits in slot e / 32 of lane e % 32.
+// VPL: experts per lane; expert e sits in slot e % VPL of lane e / VPL.
 template <int VPL>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    const int left = a.E - e0;  // experts from this lane's first on
     const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); tok < a.tokens; tok += warps) {
         const long long at = tok * a.ld;
         float l[VPL];
-        uint32_t key[VPL];
+        if (a.vec && left >= VPL) {  // rows and runs start on 16-byte boundaries
+            if (a.bf16) {
+                if constexpr (VPL % 8 == 0) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = 32 * j + lane;
-            l[j] = e < a.E ? load_logit(a, at + e) : -INFINITY;
+                    for (int j = 0; j < VPL / 8; ++j) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + at + e0) + j);
+                        l[8 * j] = bf16_lo(v.x), l[8 * j + 1] = bf16_hi(v.x), l[8 * j + 2] = bf16_lo(v.y), l[8 * j + 3] = bf16_hi(v.y);
+                        l[8 * j + 4] = bf16_lo(v.z), l[8 * j + 5] = bf16_hi(v.z), l[8 * j + 6] = bf16_lo(v.w), l[8 * j + 7] = bf16_hi(v.w);
+                    }
+                }
+            } else {
+                if constexpr (VPL % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < VPL / 4; ++j) {
+                        const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + at + e0) + j);
+                        l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) l[j] = j < left ? load_logit(a, at + e0 + j) : -INFINITY;
         }
         float mx = 0.0f, total = 0.0f;
         if (a.softmax) {
@@ -75,35 +101,59 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             for (int j = 0; j < VPL; ++j) total += expf(l[j] - mx);
             total = warp_sum(total);
         }
-        const bool by_logit = a.softmax && !a.bias && a.group_best == 1;
         auto score = [&](float v) {
             if (a.softmax) return total == 0.0f ? 0.0f : expf(v - mx) / total;
             return 1.0f / (1.0f + expf(-v));
         };
+        uint32_t key[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            const int e = 32 * j + lane;
             float v = l[j];
-            if (e < a.E && !by_logit && v != -INFINITY) v = score(v) + (a.bias ? __ldg(a.bias + e) : 0.0f);
-            key[j] = e < a.E ? order_key(v) : 0u;
+            if (!a.by_logit) {
+                const float s = score(v) + (a.bias && j < left ? __ldg(a.bias + e0 + j) : 0.0f);
+                v = v == -INFINITY ? v : s;
+            }
+            key[j] = j < left ? order_key(v) : 0u;
         }
-        if (a.groups > 1) {
+        if (a.group_lanes > 0) {
+            // groups of group_lanes lanes: the best two keys of this lane's group, in all its lanes
+            uint32_t m1 = 0, m2 = 0;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                m2 = max(m2, min(m1, key[j]));
+                m1 = max(m1, key[j]);
+            }
+            for (int o = 1; o < a.group_lanes; o <<= 1) {
+                const uint32_t n1 = __shfl_xor_sync(kAll, m1, o), n2 = __shfl_xor_sync(kAll, m2, o);
+                m2 = max(min(m1, n1), max(m2, n2));
+                m1 = max(m1, n1);
+            }
+            const uint32_t gkey = order_key(a.group_best == 1 ? key_value(m1) : key_value(m1) + key_value(m2));
+            const int mine = lane / a.group_lanes;
+            int better = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const uint32_t k = __shfl_sync(kAll, gkey, g * a.group_lanes);
+                better += k > gkey || (k == gkey && g < mine);
+            }
+            if (better >= a.top_groups) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) key[j] = 0;
+            }
+        } else if (a.groups > 1) {
             const int each = a.E / a.groups;
             uint32_t gkey = 0;  // lane g: the key of group g
             for (int g = 0; g < a.groups; ++g) {
-                const int e0 = g * each, e1 = e0 + each;
+                const int g0 = g * each - e0, g1 = g0 + each;
                 float sum = 0.0f;
-                uint32_t taken = ~0u;  // the expert that gave the largest key
+                int taken = -1;  // the expert that gave the largest key
                 for (int b = 0; b < a.group_best; ++b) {
                     uint32_t best = 0;
                     int who = INT_MAX;
 #pragma unroll
-                    for (int j = 0; j < VPL; ++j) {
-                        const int e = 32 * j + lane;
-                        if (e >= e0 && e < e1 && (uint32_t)e != taken && key[j] > best) best = key[j], who = e;
-                    }
+                    for (int j = 0; j < VPL; ++j)
+                        if (j >= g0 && j < g1 && e0 + j != taken && key[j] > best) best = key[j], who = e0 + j;
                     const uint32_t top = __reduce_max_sync(kAll, best);
-                    taken = (uint32_t)__reduce_min_sync(kAll, best == top ? who : INT_MAX);
+                    taken = __reduce_min_sync(kAll, best == top ? who : INT_MAX);
                     sum = b ? sum + key_value(top) : key_value(top);
                 }
                 if (lane == g) gkey = order_key(sum);
@@ -116,24 +166,29 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
                 if (lane == g) gkey = 0;
             }
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int e = 32 * j + lane;
-                if (e < a.E && !((keep >> (e / each)) & 1u)) key[j] = 0;
-            }
+            for (int j = 0; j < VPL; ++j)
+                if (j < left && !((keep >> ((e0 + j) / each)) & 1u)) key[j] = 0;
         }
-        int id = 0;  // lane i: the i-th pick
+        uint32_t best = key[0];  // this lane's largest key, in slot `slot` (the first that has it)
+        int slot = 0, id = 0;    // id, in lane i: the i-th pick
+#pragma unroll
+        for (int j = 1; j < VPL; ++j)
+            if (key[j] > best) best = key[j], slot = j;
         for (int i = 0; i < a.k; ++i) {
-            uint32_t best = 0;
-            int who = INT_MAX;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (key[j] > best) best = key[j], who = 32 * j + lane;
             const uint32_t top = __reduce_max_sync(kAll, best);
-            const int e = __reduce_min_sync(kAll, best == top ? who : INT_MAX);
+            const int win = __ffs(__ballot_sync(kAll, best == top)) - 1;
+            const int e = __shfl_sync(kAll, e0 + slot, win);
             if (lane == i) id = e;
+            if (lane == win) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (e == 32 * j + lane) key[j] = 0;
+                for (int j = 0; j < VPL; ++j)
+                    if (j == slot) key[j] = 0;
+                best = key[0];
+                slot = 0;
+#pragma unroll
+                for (int j = 1; j < VPL; ++j)
+                    if (key[j] > best) best = key[j], slot = j;
+            }
         }
         float w = 0.0f;
         if (lane < a.k) w = score(load_logit(a, at + id));
@@ -153,14 +208,18 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 int launch_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
                  int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
                  int logits_bf16, int num_sms, uint32_t flags, void *stream) {
+    const int need = (experts + 31) / 32, vpl = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : 32;
+    const int run = logits_bf16 ? 8 : 4, bytes = logits_bf16 ? 2 : 4, each = experts / groups, gl = each / vpl;
     RouteArgs a = {logits, bias,       weights,    ids,     tokens, ld,          experts, k,
                    groups, top_groups, group_best, softmax, renorm, logits_bf16, scale};
-    const int vpl = (experts + 31) / 32;
-    auto fn = vpl <= 1    ? route_kernel<1>
-              : vpl <= 2  ? route_kernel<2>
-              : vpl <= 4  ? route_kernel<4>
-              : vpl <= 8  ? route_kernel<8>
-              : vpl <= 16 ? route_kernel<16>
+    a.by_logit = softmax && !bias && group_best == 1;
+    a.vec = vpl % run == 0 && ld * bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
+    a.group_lanes = groups > 1 && each % vpl == 0 && (gl & (gl - 1)) == 0 ? gl : 0;
+    auto fn = vpl == 1    ? route_kernel<1>
+              : vpl == 2  ? route_kernel<2>
+              : vpl == 4  ? route_kernel<4>
+              : vpl == 8  ? route_kernel<8>
+              : vpl == 16 ? route_kernel<16>
                           : route_kernel<32>;
     const int threads = 128;
     const long long blocks = (tokens + 3) / 4, cap = 16LL * num_sms;
