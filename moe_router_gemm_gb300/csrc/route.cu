@@ -6,8 +6,8 @@
 // A key is an unsigned word whose order is the float's (NaN and -inf at the bottom, -0
 // equal to +0, 0 for an expert that a group limit or an earlier pick took out).  A pick
 // is the largest of the lanes' largest keys (one warp reduction) and the first lane
-// that has it, which is the lowest expert as runs ascend; only that lane then looks for
-// its next key.  Groups that are whole lanes, a power of two of them, are ranked by a
+// that has it, which is the lowest expert as runs ascend; a lane keeps its two largest
+// keys, so it has to look through its run again only after two picks.  Groups that are whole lanes, a power of two of them, are ranked by a
 // butterfly and a count of the better ones; others by reductions over masked keys.
 // Some 600 instructions a token of 256 experts and 8 picks, two thirds of them in the
 // picks: issue, not the 1 KB of logits, is the bound.
@@ -29,7 +29,8 @@ struct RouteArgs {
     int E, k, groups, top_groups, group_best, softmax, renorm, bf16;
     float scale;
     int by_logit;     // the logits are the keys
-    int vec;          // a lane's run may be read 16 bytes at a time
+    int vec;          // a lane's run of logits may be read 16 bytes at a time
+    int vec_bias;     // ... and of the bias
     int group_lanes;  // lanes of a group, where that is a power of two; else 0
 };
 
@@ -37,7 +38,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // Order-preserving key: a < b as floats <=> key(a) < key(b); -0 as +0; NaN as -inf.
 __device__ __forceinline__ uint32_t order_key(float v) {
-    v = (v != v) ? -INFINITY : v + 0.0f;
+    v = fmaxf(v, -INFINITY) + 0.0f;  // fmaxf gives the other operand for a NaN
     const uint32_t b = __float_as_uint(v);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
@@ -103,17 +104,34 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         }
         auto score = [&](float v) {
             if (a.softmax) return total == 0.0f ? 0.0f : expf(v - mx) / total;
-            return 1.0f / (1.0f + expf(-v));
+            return __frcp_rn(1.0f + expf(-v));  // the quotient, correctly rounded
         };
         uint32_t key[VPL];
+        if (a.by_logit) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            float v = l[j];
-            if (!a.by_logit) {
-                const float s = score(v) + (a.bias && j < left ? __ldg(a.bias + e0 + j) : 0.0f);
-                v = v == -INFINITY ? v : s;
+            for (int j = 0; j < VPL; ++j) key[j] = j < left ? order_key(l[j]) : 0u;
+        } else {
+            float b[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) b[j] = 0.0f;
+            if (a.bias && a.vec_bias && left >= VPL) {
+                if constexpr (VPL % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < VPL / 4; ++j) {
+                        const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0) + j);
+                        b[4 * j] = v.x, b[4 * j + 1] = v.y, b[4 * j + 2] = v.z, b[4 * j + 3] = v.w;
+                    }
+                }
+            } else if (a.bias) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (j < left) b[j] = __ldg(a.bias + e0 + j);
             }
-            key[j] = j < left ? order_key(v) : 0u;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const float s = score(l[j]) + b[j];
+                key[j] = j < left ? order_key(l[j] == -INFINITY ? l[j] : s) : 0u;
+            }
         }
         if (a.group_lanes > 0) {
             // groups of group_lanes lanes: the best two keys of this lane's group, in all its lanes
@@ -169,25 +187,33 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             for (int j = 0; j < VPL; ++j)
                 if (j < left && !((keep >> ((e0 + j) / each)) & 1u)) key[j] = 0;
         }
-        uint32_t best = key[0];  // this lane's largest key, in slot `slot` (the first that has it)
-        int slot = 0, id = 0;    // id, in lane i: the i-th pick
+        // This lane's largest key and the next, with their slots (equal keys: the lower slot first).
+        uint32_t best, next, gone = 0;  // gone: bit j, slot j has been picked
+        int slot, slot2, id = 0;        // id, in lane i: the i-th pick
+        auto scan = [&] {
+            best = gone & 1u ? 0u : key[0], next = 0, slot = 0, slot2 = 0;
 #pragma unroll
-        for (int j = 1; j < VPL; ++j)
-            if (key[j] > best) best = key[j], slot = j;
+            for (int j = 1; j < VPL; ++j) {
+                const uint32_t k = (gone >> j) & 1u ? 0u : key[j];
+                const bool over = k > best, over2 = k > next;
+                next = over ? best : over2 ? k : next;
+                slot2 = over ? slot : over2 ? j : slot2;
+                best = over ? k : best;
+                slot = over ? j : slot;
+            }
+        };
+        scan();
         for (int i = 0; i < a.k; ++i) {
             const uint32_t top = __reduce_max_sync(kAll, best);
             const int win = __ffs(__ballot_sync(kAll, best == top)) - 1;
             const int e = __shfl_sync(kAll, e0 + slot, win);
             if (lane == i) id = e;
             if (lane == win) {
-#pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (j == slot) key[j] = 0;
-                best = key[0];
-                slot = 0;
-#pragma unroll
-                for (int j = 1; j < VPL; ++j)
-                    if (key[j] > best) best = key[j], slot = j;
+                gone |= 1u << slot;
+                if (next != 0)  // steps up; its place is filled only if it is picked too
+                    best = next, slot = slot2, next = 0;
+                else
+                    scan();
             }
         }
         float w = 0.0f;
@@ -214,6 +240,7 @@ int launch_route(const void *logits, int64_t ld, const float *bias, float *weigh
                    groups, top_groups, group_best, softmax, renorm, logits_bf16, scale};
     a.by_logit = softmax && !bias && group_best == 1;
     a.vec = vpl % run == 0 && ld * bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
+    a.vec_bias = vpl % 4 == 0 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
     a.group_lanes = groups > 1 && each % vpl == 0 && (gl & (gl - 1)) == 0 ? gl : 0;
     auto fn = vpl == 1    ? route_kernel<1>
               : vpl == 2  ? route_kernel<2>
