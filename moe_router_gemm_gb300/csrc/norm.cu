@@ -3,17 +3,19 @@
 //
 //     h = x  or  RNE_bf16(x + residual);  y = h / sqrt(mean(h^2) + eps) * weight
 //
-// One pass: a block holds its row in registers between the sum of squares and
-// the output, so each input is read once and each output written once.  The sum
-// runs in fp32: each thread over its own values in order, then a shuffle tree,
-// then the warps in order, so it is the same from run to run.
+// One pass: a row stays in registers between the sum of squares and the output, so
+// each input is read once and each output written once: HBM is the bound.  The sum
+// runs in fp32: each thread over its own values in order, then a butterfly, then the
+// warps' sums by a butterfly, so it is the same from run to run.
 //
-//   * norm_vec_kernel: rows that start on 16-byte boundaries (H and ldx multiples
-//     of 8): thread i holds the 8-value vectors i, i + threads, ...; four
-//     neighbouring lanes hold a 32-element scale block.
-//   * norm_any_kernel: any H, stride and alignment, one value per lane and step;
-//     a warp's 32 lanes hold a scale block.  Reads the row twice (the second
-//     time from L1 or L2).
+//   * norm_vec_kernel: rows that start on 16-byte boundaries (H and ldx multiples of
+//     8): a row to a warp (H <= 1024) or to a block; thread i holds the 8-value vectors
+//     i, i + threads, ...; four neighbouring lanes hold a 32-element scale block.  The
+//     weight stays in registers from row to row, and the next row's loads go out
+//     before this row's sum, so memory is busy through the reduction.
+//   * norm_any_kernel: any H, stride and alignment, one value per lane and step; a
+//     warp's 32 lanes hold a scale block.  Rows of more than 16384 elements are read
+//     twice (the second time from L1 or L2).
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -43,74 +45,86 @@ __device__ __forceinline__ uint16_t e4m3x2_sat(float lo, float hi) {
     return r;
 }
 
-// Sum over the block, the same in every thread.  `red`: one float per warp.
-__device__ __forceinline__ float block_sum(float v, float *red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)blockDim.x >> 5;
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Sum over the block, the same in every thread.  `red`: 32 floats, alternating between two buffers from call to call
+// (one barrier a call: whoever writes a buffer again has passed the barrier after its last readers).
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)blockDim.x >> 5;
+    v = warp_sum(v);
     if (nw == 1) return v;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < nw; ++w) s += red[w];
-    __syncthreads();  // red is free again
-    return s;
+    return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
 // Magnitude bits of a value for a block's maximum: NaN above infinity, so it shows.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-template <int QUANT, int V>
-__global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
-    __shared__ float red[32];
+// V: vectors per thread.  WARP: a row to a warp, else to a block.
+template <int QUANT, int V, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormArgs a) {
+    __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();  // x, the residual, the weight and the scale may be written by the previous kernel
-    const int nvec = a.H >> 3, nt = (int)blockDim.x;
+    const int nvec = a.H >> 3, nt = WARP ? 32 : (int)blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const long long step = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+    long long r = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     const float inv_scale = QUANT == BF16L_QUANT_FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
     const unsigned quad = 0xFu << (threadIdx.x & 28u);
-    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + r * a.ldx);
-        uint4 h[V];
+    const uint4 kNone = make_uint4(0u, 0u, 0u, 0u);
+    uint4 w[V], h[V], q[V];
+    auto load = [&](long long row) {
+        const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + row * a.ldx);
+        const uint4 *rr = reinterpret_cast<const uint4 *>(a.residual + row * a.H);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = me + j * nt;
+            h[j] = i < nvec ? __ldg(xr + i) : kNone;
+            if (a.residual) q[j] = i < nvec ? rr[i] : kNone;  // (may be written in place: not __ldg)
+        }
+    };
+    if (r < a.rows) load(r);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = me + j * nt;
+        w[j] = i < nvec ? __ldg(reinterpret_cast<const uint4 *>(a.weight) + i) : kNone;
+    }
+    for (int par = 0; r < a.rows; r += step, par ^= 1) {
+        uint4 c[V];  // this row's h
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = (int)threadIdx.x + j * nt;
-            h[j] = i < nvec ? __ldg(xr + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (a.residual) {
-            const uint4 *rr = reinterpret_cast<const uint4 *>(a.residual + r * a.H);
-            uint4 q[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int i = (int)threadIdx.x + j * nt;
-                q[j] = i < nvec ? rr[i] : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                h[j].x = pack_bf16x2(bf16_lo(h[j].x) + bf16_lo(q[j].x), bf16_hi(h[j].x) + bf16_hi(q[j].x));
-                h[j].y = pack_bf16x2(bf16_lo(h[j].y) + bf16_lo(q[j].y), bf16_hi(h[j].y) + bf16_hi(q[j].y));
-                h[j].z = pack_bf16x2(bf16_lo(h[j].z) + bf16_lo(q[j].z), bf16_hi(h[j].z) + bf16_hi(q[j].z));
-                h[j].w = pack_bf16x2(bf16_lo(h[j].w) + bf16_lo(q[j].w), bf16_hi(h[j].w) + bf16_hi(q[j].w));
-                const int i = (int)threadIdx.x + j * nt;
-                if (i < nvec) reinterpret_cast<uint4 *>(a.residual_out + r * a.H)[i] = h[j];
+            c[j] = h[j];
+            if (a.residual) {
+                c[j].x = pack_bf16x2(bf16_lo(h[j].x) + bf16_lo(q[j].x), bf16_hi(h[j].x) + bf16_hi(q[j].x));
+                c[j].y = pack_bf16x2(bf16_lo(h[j].y) + bf16_lo(q[j].y), bf16_hi(h[j].y) + bf16_hi(q[j].y));
+                c[j].z = pack_bf16x2(bf16_lo(h[j].z) + bf16_lo(q[j].z), bf16_hi(h[j].z) + bf16_hi(q[j].z));
+                c[j].w = pack_bf16x2(bf16_lo(h[j].w) + bf16_lo(q[j].w), bf16_hi(h[j].w) + bf16_hi(q[j].w));
             }
         }
+        if (r + step < a.rows) load(r + step);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint32_t u[4] = {h[j].x, h[j].y, h[j].z, h[j].w};
+            const int i = me + j * nt;
+            if (a.residual && i < nvec) reinterpret_cast<uint4 *>(a.residual_out + r * a.H)[i] = c[j];
+            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 ss = fmaf(bf16_lo(u[e]), bf16_lo(u[e]), ss);
                 ss = fmaf(bf16_hi(u[e]), bf16_hi(u[e]), ss);
             }
         }
-        const float rstd = 1.0f / sqrtf(block_sum(ss, red) / (float)a.H + a.eps);
+        const float rstd = 1.0f / sqrtf((WARP ? warp_sum(ss) : block_sum(ss, red[par])) / (float)a.H + a.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = (int)threadIdx.x + j * nt;
+            const int i = me + j * nt;
             if (i >= nvec) break;  // nvec % 4 == 0 for the MX formats: a quad leaves together
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(a.weight) + i);
-            const uint32_t u[4] = {h[j].x, h[j].y, h[j].z, h[j].w}, g[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w}, g[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
             float y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -119,11 +133,11 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
             }
             if (a.out) OutStore<uint16_t>::eight(a.out + r * a.H + 8 * (long long)i, y);
             if (QUANT == BF16L_QUANT_FP8) {
-                uint16_t c[4];
+                uint16_t d[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = e4m3x2_sat(y[2 * e] * inv_scale, y[2 * e + 1] * inv_scale);
+                for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv_scale, y[2 * e + 1] * inv_scale);
                 reinterpret_cast<uint2 *>(a.codes + r * a.H)[i] =
-                    make_uint2((uint32_t)c[0] | ((uint32_t)c[1] << 16), (uint32_t)c[2] | ((uint32_t)c[3] << 16));
+                    make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
             } else if (QUANT != BF16L_QUANT_NONE) {
                 uint32_t m = 0;
 #pragma unroll
@@ -134,11 +148,11 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
                 const int s = mx_scale_exp(m, QUANT == BF16L_QUANT_MXFP8 ? 8 : 2);
                 const float inv = exp2_neg(nan ? 0 : s);
                 if (QUANT == BF16L_QUANT_MXFP8) {
-                    uint16_t c[4];
+                    uint16_t d[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e] = e4m3x2_sat(y[2 * e] * inv, y[2 * e + 1] * inv);
+                    for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv, y[2 * e + 1] * inv);
                     reinterpret_cast<uint2 *>(a.codes + r * a.H)[i] =
-                        make_uint2((uint32_t)c[0] | ((uint32_t)c[1] << 16), (uint32_t)c[2] | ((uint32_t)c[3] << 16));
+                        make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] *= inv;
@@ -150,48 +164,79 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
     }
 }
 
-template <int QUANT>
-__global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a) {
-    __shared__ float red[32];
+// N: values per thread that stay in registers (0: the row is read again).
+template <int QUANT, int N>
+__global__ void __launch_bounds__(1024) norm_any_kernel(const NormArgs a) {
+    __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
     const int nt = (int)blockDim.x, lane = threadIdx.x & 31;
     const float inv_scale = QUANT == BF16L_QUANT_FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
-    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    int par = 0;
+    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, par ^= 1) {
         const uint16_t *xr = a.x + r * a.ldx;
         const uint16_t *hr = a.residual ? a.residual_out + r * a.H : xr;  // where h is read from the second time
-        float ss = 0.0f;
-        for (int i = (int)threadIdx.x; i < a.H; i += nt) {
-            float h = bf16_to_f32(xr[i]);
+        float h[N ? N : 1], ss = 0.0f;
+        auto add = [&](uint16_t xv, uint16_t qv, int i) {
+            float v = bf16_to_f32(xv);
             if (a.residual) {
-                const uint16_t b = f32_to_bf16(h + bf16_to_f32(a.residual[r * a.H + i]));
-                a.residual_out[r * a.H + i] = b;  // read back below by this same thread
-                h = bf16_to_f32(b);
+                const uint16_t b = f32_to_bf16(v + bf16_to_f32(qv));
+                a.residual_out[r * a.H + i] = b;
+                v = bf16_to_f32(b);
             }
-            ss = fmaf(h, h, ss);
+            return v;
+        };
+        if constexpr (N > 0) {
+            uint16_t xv[N], qv[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int i = (int)threadIdx.x + j * nt;
+                xv[j] = i < a.H ? xr[i] : (uint16_t)0;
+                qv[j] = a.residual && i < a.H ? a.residual[r * a.H + i] : (uint16_t)0;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int i = (int)threadIdx.x + j * nt;
+                h[j] = i < a.H ? add(xv[j], qv[j], i) : 0.0f;
+                ss = fmaf(h[j], h[j], ss);
+            }
+        } else {
+            for (int i = (int)threadIdx.x; i < a.H; i += nt) {
+                const float v = add(xr[i], a.residual ? a.residual[r * a.H + i] : (uint16_t)0, i);
+                ss = fmaf(v, v, ss);
+            }
         }
-        const float rstd = 1.0f / sqrtf(block_sum(ss, red) / (float)a.H + a.eps);
-        for (int i = (int)threadIdx.x; i < a.H; i += nt) {
-            const float y = bf16_to_f32(hr[i]) * rstd * bf16_to_f32(__ldg(a.weight + i));
+        const float rstd = 1.0f / sqrtf(block_sum(ss, red[par]) / (float)a.H + a.eps);
+        auto put = [&](float v, int i) {
+            const float y = v * rstd * bf16_to_f32(__ldg(a.weight + i));
             if (a.out) a.out[r * a.H + i] = f32_to_bf16(y);
             if (QUANT == BF16L_QUANT_FP8) {
                 a.codes[r * a.H + i] = (uint8_t)(e4m3x2_sat(y * inv_scale, 0.0f) & 0xFFu);
-            } else if (QUANT != BF16L_QUANT_NONE) {  // H % 32 == 0: a warp's lanes are one block, together in the loop
+            } else if (QUANT != BF16L_QUANT_NONE) {  // H % 32 == 0: a warp's lanes are one block, together here
                 uint32_t m = mag_bits(y);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                 const bool nan = m > 0x7F800000u;
                 const int s = mx_scale_exp(m, QUANT == BF16L_QUANT_MXFP8 ? 8 : 2);
-                const float v = y * exp2_neg(nan ? 0 : s);
+                const float t = y * exp2_neg(nan ? 0 : s);
                 if (QUANT == BF16L_QUANT_MXFP8) {
-                    a.codes[r * a.H + i] = (uint8_t)(e4m3x2_sat(v, 0.0f) & 0xFFu);
+                    a.codes[r * a.H + i] = (uint8_t)(e4m3x2_sat(t, 0.0f) & 0xFFu);
                 } else {
-                    const float w[8] = {v, __shfl_down_sync(0xFFFFFFFFu, v, 1), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    const float w[8] = {t, __shfl_down_sync(0xFFFFFFFFu, t, 1), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     const uint32_t c = nan ? 0u : e2m1x8(w);
                     if ((lane & 1) == 0) a.codes[r * (a.H >> 1) + (i >> 1)] = (uint8_t)c;
                 }
                 if (lane == 0) a.scales[r * (a.H >> 5) + (i >> 5)] = nan ? 255 : (uint8_t)(s + 127);
             }
+        };
+        if constexpr (N > 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int i = (int)threadIdx.x + j * nt;
+                if (i < a.H) put(h[j], i);
+            }
+        } else {
+            for (int i = (int)threadIdx.x; i < a.H; i += nt) put(bf16_to_f32(hr[i]), i);  // h: written by this same thread
         }
     }
 }
@@ -199,8 +244,14 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormArgs a) {
 using NormFn = void (*)(const NormArgs);
 
 template <int QUANT>
-NormFn pick_vec(int v) {
-    return v == 1 ? norm_vec_kernel<QUANT, 1> : v == 2 ? norm_vec_kernel<QUANT, 2> : norm_vec_kernel<QUANT, 4>;
+NormFn pick_vec(int v, bool warp) {
+    if (warp) return v == 1 ? norm_vec_kernel<QUANT, 1, true> : v == 2 ? norm_vec_kernel<QUANT, 2, true> : norm_vec_kernel<QUANT, 4, true>;
+    return v == 1 ? norm_vec_kernel<QUANT, 1, false> : v == 2 ? norm_vec_kernel<QUANT, 2, false> : norm_vec_kernel<QUANT, 4, false>;
+}
+
+template <int QUANT>
+NormFn pick_any(int n) {
+    return n == 4 ? norm_any_kernel<QUANT, 4> : n == 8 ? norm_any_kernel<QUANT, 8> : n == 16 ? norm_any_kernel<QUANT, 16> : norm_any_kernel<QUANT, 0>;
 }
 
 }  // namespace
@@ -222,25 +273,31 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
                   eps};
     const bool vec = H % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H <= 8 * 4 * 1024;
     int threads;
+    long long blocks;
     NormFn fn;
     if (vec) {
         const int nvec = H / 8;
-        const int v = nvec <= 256 ? 1 : nvec <= 2048 ? 2 : 4;
-        threads = ((nvec + v - 1) / v + 31) / 32 * 32;
-        fn = quant == BF16L_QUANT_NONE    ? pick_vec<BF16L_QUANT_NONE>(v)
-             : quant == BF16L_QUANT_FP8   ? pick_vec<BF16L_QUANT_FP8>(v)
-             : quant == BF16L_QUANT_MXFP8 ? pick_vec<BF16L_QUANT_MXFP8>(v)
-                                          : pick_vec<BF16L_QUANT_MXFP4>(v);
+        const bool warp = nvec <= 128;
+        const int v = warp ? (nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4) : nvec <= 512 ? 1 : nvec <= 2048 ? 2 : 4;
+        threads = warp ? 256 : ((nvec + v - 1) / v + 31) / 32 * 32;
+        blocks = warp ? (rows + 7) / 8 : rows;
+        fn = quant == BF16L_QUANT_NONE    ? pick_vec<BF16L_QUANT_NONE>(v, warp)
+             : quant == BF16L_QUANT_FP8   ? pick_vec<BF16L_QUANT_FP8>(v, warp)
+             : quant == BF16L_QUANT_MXFP8 ? pick_vec<BF16L_QUANT_MXFP8>(v, warp)
+                                           : pick_vec<BF16L_QUANT_MXFP4>(v, warp);
     } else {
-        threads = H <= 512 ? (H + 31) / 32 * 32 : 512;
-        fn = quant == BF16L_QUANT_NONE    ? norm_any_kernel<BF16L_QUANT_NONE>
-             : quant == BF16L_QUANT_FP8   ? norm_any_kernel<BF16L_QUANT_FP8>
-             : quant == BF16L_QUANT_MXFP8 ? norm_any_kernel<BF16L_QUANT_MXFP8>
-                                          : norm_any_kernel<BF16L_QUANT_MXFP4>;
+        const int n = H <= 4 * 512 ? 4 : H <= 8 * 512 ? 8 : H <= 16 * 1024 ? 16 : 0;
+        threads = n ? ((H + n - 1) / n + 31) / 32 * 32 : 512;
+        blocks = rows;
+        fn = quant == BF16L_QUANT_NONE    ? pick_any<BF16L_QUANT_NONE>(n)
+             : quant == BF16L_QUANT_FP8   ? pick_any<BF16L_QUANT_FP8>(n)
+             : quant == BF16L_QUANT_MXFP8 ? pick_any<BF16L_QUANT_MXFP8>(n)
+                                           : pick_any<BF16L_QUANT_MXFP4>(n);
     }
     const long long cap = (long long)num_sms * (2048 / threads);
+    if (blocks > cap) blocks = cap;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows < cap ? rows : cap));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
