@@ -13,6 +13,11 @@
 //     i, i + threads, ...; four neighbouring lanes hold a 32-element scale block.  The
 //     weight stays in registers from row to row, and the next row's loads go out
 //     before this row's sum, so memory is busy through the reduction.
+//   * norm_shift_kernel: H not a multiple of 8, rows of x at the same place in a 16-byte
+//     line as the dense tensors' (ldx = H, or H plus a multiple of 8): a row is up to 7
+//     values, vectors on 16-byte boundaries, up to 7 values; the weight, which meets
+//     the vectors at a different place in every row, comes from shared memory.
+//     2000 x 2881 with a residual: 27 us a value at a time.
 //   * norm_any_kernel: any H, stride and alignment, one value per lane and step; a
 //     warp's 32 lanes hold a scale block.  Rows of more than 16384 elements are read
 //     twice (the second time from L1 or L2).
@@ -164,6 +169,118 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_vec_kernel(const NormA
     }
 }
 
+// Eight bf16 weights from element i on (any i), from a copy in shared memory that is two words longer than the weight.
+__device__ __forceinline__ uint4 weights_at(const uint32_t *w, int i) {
+    const uint32_t *p = w + (i >> 1);
+    if ((i & 1) == 0) return make_uint4(p[0], p[1], p[2], p[3]);
+    return make_uint4(__funnelshift_r(p[0], p[1], 16), __funnelshift_r(p[1], p[2], 16), __funnelshift_r(p[2], p[3], 16),
+                      __funnelshift_r(p[3], p[4], 16));
+}
+
+template <bool FP8, int V>
+__global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
+    extern __shared__ uint32_t sw[];  // the weight
+    __shared__ float red[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int nt = (int)blockDim.x, me = (int)threadIdx.x;
+    const float inv_scale = FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
+    const uint4 kNone = make_uint4(0u, 0u, 0u, 0u);
+    uint4 h[V], q[V];
+    uint16_t hs = 0, qs = 0;  // threads 0-7: the values before the first vector; 8-15: those after the last
+    int head, nv, edge;       // of the row that is loaded; edge: this thread's single value, or -1
+    auto load = [&](long long row) {
+        head = (int)(-(row * a.H) & 7);
+        if (head > a.H) head = a.H;
+        nv = (a.H - head) >> 3;
+        const int end = head + 8 * nv;
+        edge = me < head ? me : me >= 8 && me < 16 && end + me - 8 < a.H ? end + me - 8 : -1;
+        const uint16_t *x = a.x + row * a.ldx, *r = a.residual + row * a.H;
+        if (edge >= 0) {
+            hs = x[edge];
+            if (a.residual) qs = r[edge];
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = me + j * nt;
+            h[j] = i < nv ? __ldg(reinterpret_cast<const uint4 *>(x + head) + i) : kNone;
+            if (a.residual) q[j] = i < nv ? reinterpret_cast<const uint4 *>(r + head)[i] : kNone;
+        }
+    };
+    long long r = blockIdx.x;
+    if (r < a.rows) load(r);
+    for (int i = me; i < (a.H + 1) / 2 + 2; i += nt) {
+        const uint32_t lo = 2 * i < a.H ? __ldg(a.weight + 2 * i) : 0u, hi = 2 * i + 1 < a.H ? __ldg(a.weight + 2 * i + 1) : 0u;
+        sw[i] = lo | hi << 16;
+    }
+    __syncthreads();
+    for (int par = 0; r < a.rows; r += gridDim.x, par ^= 1) {
+        uint4 c[V];
+        float ss = 0.0f, cs = 0.0f;
+        const int chead = head, cnv = nv, cedge = edge;
+        const long long at = r * a.H;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            c[j] = h[j];
+            if (a.residual) {
+                c[j].x = pack_bf16x2(bf16_lo(h[j].x) + bf16_lo(q[j].x), bf16_hi(h[j].x) + bf16_hi(q[j].x));
+                c[j].y = pack_bf16x2(bf16_lo(h[j].y) + bf16_lo(q[j].y), bf16_hi(h[j].y) + bf16_hi(q[j].y));
+                c[j].z = pack_bf16x2(bf16_lo(h[j].z) + bf16_lo(q[j].z), bf16_hi(h[j].z) + bf16_hi(q[j].z));
+                c[j].w = pack_bf16x2(bf16_lo(h[j].w) + bf16_lo(q[j].w), bf16_hi(h[j].w) + bf16_hi(q[j].w));
+            }
+        }
+        if (cedge >= 0) {
+            uint16_t b = hs;
+            if (a.residual) {
+                b = f32_to_bf16(bf16_to_f32(hs) + bf16_to_f32(qs));
+                a.residual_out[at + cedge] = b;
+            }
+            cs = bf16_to_f32(b);
+            ss = cs * cs;
+        }
+        if (r + gridDim.x < a.rows) load(r + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = me + j * nt;
+            if (a.residual && i < cnv) reinterpret_cast<uint4 *>(a.residual_out + at + chead)[i] = c[j];
+            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ss = fmaf(bf16_lo(u[e]), bf16_lo(u[e]), ss);
+                ss = fmaf(bf16_hi(u[e]), bf16_hi(u[e]), ss);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(ss, red[par]) / (float)a.H + a.eps);
+        if (cedge >= 0) {
+            const uint32_t w = sw[cedge >> 1];
+            const float y = cs * rstd * (cedge & 1 ? bf16_hi(w) : bf16_lo(w));
+            if (a.out) a.out[at + cedge] = f32_to_bf16(y);
+            if (FP8) a.codes[at + cedge] = (uint8_t)(e4m3x2_sat(y * inv_scale, 0.0f) & 0xFFu);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = me + j * nt;
+            if (i >= cnv) break;
+            const uint4 w = weights_at(sw, chead + 8 * i);
+            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w}, g[4] = {w.x, w.y, w.z, w.w};
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[2 * e] = bf16_lo(u[e]) * rstd * bf16_lo(g[e]);
+                y[2 * e + 1] = bf16_hi(u[e]) * rstd * bf16_hi(g[e]);
+            }
+            if (a.out) OutStore<uint16_t>::eight(a.out + at + chead + 8 * (long long)i, y);
+            if (FP8) {
+                uint16_t d[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv_scale, y[2 * e + 1] * inv_scale);
+                reinterpret_cast<uint2 *>(a.codes + at + chead)[i] =
+                    make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
+            }
+        }
+    }
+}
+
 // N: values per thread that stay in registers (0: the row is read again).
 template <int QUANT, int N>
 __global__ void __launch_bounds__(1024) norm_any_kernel(const NormArgs a) {
@@ -274,6 +391,7 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
     const bool vec = H % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H <= 8 * 4 * 1024;
     int threads;
     long long blocks;
+    size_t smem = 0;
     NormFn fn;
     if (vec) {
         const int nvec = H / 8;
@@ -285,6 +403,16 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
              : quant == BF16L_QUANT_FP8   ? pick_vec<BF16L_QUANT_FP8>(v, warp)
              : quant == BF16L_QUANT_MXFP8 ? pick_vec<BF16L_QUANT_MXFP8>(v, warp)
                                            : pick_vec<BF16L_QUANT_MXFP4>(v, warp);
+    } else if (H % 8 != 0 && (ldx - H) % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H >= 64 && H <= 16384 &&
+               (quant == BF16L_QUANT_NONE || quant == BF16L_QUANT_FP8)) {
+        const int nvec = H / 8, v = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+        threads = ((nvec + v - 1) / v + 31) / 32 * 32;
+        blocks = rows;
+        smem = ((size_t)(H + 1) / 2 + 2) * 4;
+        const bool fp8 = quant == BF16L_QUANT_FP8;
+        fn = v == 1   ? (fp8 ? norm_shift_kernel<true, 1> : norm_shift_kernel<false, 1>)
+             : v == 2 ? (fp8 ? norm_shift_kernel<true, 2> : norm_shift_kernel<false, 2>)
+                      : (fp8 ? norm_shift_kernel<true, 4> : norm_shift_kernel<false, 4>);
     } else {
         const int n = H <= 4 * 512 ? 4 : H <= 8 * 512 ? 8 : H <= 16 * 1024 ? 16 : 0;
         threads = n ? ((H + n - 1) / n + 31) / 32 * 32 : 512;
@@ -299,6 +427,7 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -59,7 +59,7 @@ def _check(lib, x, r, w, eps, quant, res, scale=None):
 
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("rows,H", [(1, 1), (3, 7), (1, 33), (5, 64), (2, 1000), (1, 2048), (17, 2880), (4, 4097),
-                                    (33, 7168), (2, 16384), (1, 32768), (2, 33000), (1, 40009)])
+                                    (33, 7168), (700, 67), (1000, 1501), (2000, 2881), (300, 8189), (2, 16384), (9, 16383), (1, 32768), (2, 33000), (1, 40009)])
 def test_bf16(lib, rows, H, residual):
     x, r, w = _inputs(rows, H, rows + H, residual=residual)
     res = lib.rmsnorm(x, w, r)
@@ -80,6 +80,16 @@ def test_quantised(lib, rows, H, ld, quant, residual):
     assert alone.out is None and torch.equal(alone.codes, both.codes)
     if quant != "fp8":
         assert torch.equal(alone.scales, both.scales)
+
+
+@pytest.mark.parametrize("rows,H,ld", [(900, 188, 516), (5, 99, 107), (800, 2001, 2009), (3, 4099, 4099), (2000, 65, 65),
+                                       (5, 983, 1235)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_odd_rows_in_fp8(lib, rows, H, ld, residual):
+    x, r, w = _inputs(rows, H, rows + H, ld=ld, residual=residual)
+    scale = torch.full((1,), 0.03125, device=DEV)
+    res = lib.rmsnorm(x, w, r, quant="fp8", scale=scale)
+    _check(lib, x, r, w, 1e-6, "fp8", res, 0.03125)
 
 
 @pytest.mark.parametrize("start", [0, 1, 3, 8, 1536])
