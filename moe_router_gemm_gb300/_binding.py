@@ -1,7 +1,7 @@
 """ctypes binding of libbf16_linear.so — argument marshalling only.
 
 Every step of the computation runs in the library's CUDA kernels; this module
-turns torch tensors into (pointer, size, stream) arguments, checks dtype /
+(and csrc/torch_calls.cpp for the calls that a decode step makes most) turns torch tensors into (pointer, size, stream) arguments, checks dtype /
 contiguity / device on the Python side (the dtype guards the vLLM PR #42562
 review asked for: both x and W must be bfloat16), and raises on a nonzero
 status.  There is no fallback: if the library is missing the import-time
@@ -64,12 +64,33 @@ class BF16LinearError(RuntimeError):
 
 
 _lib = None
+_calls = None  # csrc/torch_calls.cpp, where it was built for this PyTorch: the usual calls without Python's share
 _lock = threading.Lock()
+
+
+def _load_calls(lib):
+    """The compiled marshalling module, bound to this library's entry points; None without one."""
+    import importlib.util
+
+    from . import build as _build
+    try:
+        path = _build.calls_path()
+        if not os.path.exists(path):
+            return None
+        spec = importlib.util.spec_from_file_location("_torch_calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError:
+        return None
+    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.bf16_rmsnorm, lib.bf16_route, lib.bf16_quant_mxfp4, lib.bf16_dequant_mxfp4, lib.bf16_linear_mxfp4,
+        lib.bf16_linear_mxfp4_dynamic, lib.bf16_linear_mxfp4_dynamic_workspace)))
+    return mod
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     with _lock:
@@ -155,6 +176,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.bf16_linear_cuda_error.restype = i32
         lib.bf16_linear_version.argtypes = []
         lib.bf16_linear_version.restype = i32
+        _calls = _load_calls(lib)
         _lib = lib
         return lib
 
@@ -577,6 +599,12 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, quant: str | None = 
     residual, and y's codes in `quant`: "fp8" (e4m3 with the one-element fp32 CUDA tensor `scale`), "mxfp8" or "mxfp4"
     (uint8 codes [rows, H] or [rows, H / 2], uint8 E8M0 scales [rows, H / 32]).  All bf16; x may be a column range of a
     wider matrix.  residual_out may be residual itself (in place)."""
+    if out is residual_out is codes is scales is stream is None and _calls is not None and quant in QUANT_FORMATS:
+        r = _calls.rmsnorm(x, weight, residual, eps, QUANT_FORMATS[quant], scale, bf16_out, flags)
+        if type(r) is tuple:
+            return tuple.__new__(Norm, r)
+        if r is not None:
+            _raise(r, f"bf16_rmsnorm(x{tuple(x.shape)}, quant={quant})")
     import torch
     bf16, u8 = torch.bfloat16, torch.uint8
     if x.dtype is not bf16:
@@ -640,6 +668,12 @@ def route(logits, k: int, *, scoring: str = "softmax", bias=None, groups: int = 
     the scores for the choice alone; with groups > 1 only the experts of the top_groups best of `groups` equal runs of
     experts stay, a group ranked by the sum of its group_best largest.  renormalize divides the weights by their sum; scale
     multiplies them.  Experts with a logit of -inf are out."""
+    if weights is ids is stream is None and _calls is not None and scoring in SCORES:
+        r = _calls.route(logits, k, SCORES[scoring], bias, groups, top_groups, group_best, renormalize, scale, flags)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _raise(r, f"bf16_route(logits{tuple(logits.shape)}, k={k}, groups={groups}, top_groups={top_groups})")
     import torch
     f32, dt = torch.float32, logits.dtype
     if dt is not f32 and dt is not torch.bfloat16:
@@ -663,6 +697,12 @@ def route(logits, k: int, *, scoring: str = "softmax", bias=None, groups: int = 
 def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
     """MXFP4 quantisation (bf16_quant_mxfp4) of a contiguous bf16 CUDA tensor x[rows, K], K % 32 == 0: returns (codes uint8
     [rows, K / 2], two to a byte, scales uint8 [rows, K / 32])."""
+    if out is scales is stream is None and _calls is not None:
+        r = _calls.quant_mxfp4(x, flags)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _raise(r, f"bf16_quant_mxfp4(x{tuple(x.shape)})")
     import torch
     dev, u8 = _cuda(x, "x"), torch.uint8
     rows, K = x.shape
@@ -680,6 +720,12 @@ def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
 
 def dequant_mxfp4(codes, scales, out=None, flags: int = 0, stream=None):
     """The bf16 values [rows, K] that MXFP4 codes [rows, K / 2] and scales [rows, K / 32] stand for (bf16_dequant_mxfp4)."""
+    if out is stream is None and _calls is not None:
+        r = _calls.dequant_mxfp4(codes, scales, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_dequant_mxfp4(codes{tuple(codes.shape)})")
+        if r is not None:
+            return r
     import torch
     dev, u8 = _cuda(codes, "codes"), torch.uint8
     rows, h = codes.shape
@@ -696,6 +742,12 @@ def dequant_mxfp4(codes, scales, out=None, flags: int = 0, stream=None):
 def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, stream=None):
     """MXFP4 linear (bf16_linear_mxfp4): packed e2m1 codes xq[M, K / 2], wq[N, K / 2] with E8M0 block scales xs[M, K / 32],
     ws[N, K / 32] (all uint8), optional bf16 bias[N]; bf16 out[M, N]."""
+    if out is stream is None and _calls is not None and xs is not None:
+        r = _calls.linear_mxfp4(xq, xs, wq, ws, bias, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_linear_mxfp4(xq{tuple(xq.shape)}, wq{tuple(wq.shape)})")
+        if r is not None:
+            return r
     import torch
     dev, u8, bf16 = _cuda(xq, "xq"), torch.uint8, torch.bfloat16
     (M, h), N = xq.shape, wq.shape[0]
@@ -719,6 +771,12 @@ def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, fl
     """MXFP4 linear with x[M, K] in bf16, quantised by the call (bf16_linear_mxfp4_dynamic): bit for bit quant_mxfp4 and
     then bf16_linear_mxfp4.  `workspace`: a contiguous CUDA tensor of at least mxfp4_dynamic_workspace(M, N, K) bytes to
     reuse from call to call on one stream; allocated for the call when None."""
+    if out is workspace is stream is None and _calls is not None:
+        r = _calls.linear_mxfp4(x, None, wq, ws, bias, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_linear_mxfp4_dynamic(x{tuple(x.shape)}, wq{tuple(wq.shape)})")
+        if r is not None:
+            return r
     import torch
     dev, u8, bf16 = _cuda(x, "x"), torch.uint8, torch.bfloat16
     (M, K), N = x.shape, wq.shape[0]

@@ -2,6 +2,9 @@
 
     python -m moe_router_gemm_gb300.build [--force]
 
+Beside it, a small module that marshals calls from PyTorch tensors in C++
+(csrc/torch_calls.cpp), where the installed PyTorch's headers allow.
+
 Each translation unit compiles in parallel to _build/*.o, then one link step
 produces moe_router_gemm_gb300/libbf16_linear.so (CUDA runtime linked
 statically, so the library needs only the driver at run time).
@@ -53,12 +56,52 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+# The compiled marshalling module (csrc/torch_calls.cpp): one file per PyTorch release, since it uses PyTorch's C++ types.
+def calls_path() -> str:
+    import torch
+    return os.path.join(PKG, "_torch_calls_" + "".join(c if c.isalnum() else "_" for c in torch.__version__) + ".so")
+
+
+def build_calls(force: bool = False) -> str | None:
+    """Compile the marshalling module for the installed PyTorch; None where it cannot be (the binding then calls the library
+    through ctypes alone)."""
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    try:
+        import sysconfig
+
+        import torch
+        out = calls_path()
+        inputs = (src, os.path.join(INCLUDE, "bf16_linear.h"), os.path.abspath(__file__))
+        if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in inputs):
+            return out
+        root = os.path.dirname(torch.__file__)
+        cuda = os.environ.get("CUDA_HOME") or "/usr/local/cuda"
+        inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+        libs = os.path.join(root, "lib")
+        tmp = out + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *("-I" + i for i in inc), src, "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs,
+               "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            print(f"torch_calls.cpp does not build, calls go through ctypes:\n{r.stderr[-2000:]}", file=sys.stderr)
+            return None
+        os.replace(tmp, out)
+        return out
+    except (ImportError, OSError) as e:
+        print(f"torch_calls.cpp is not built, calls go through ctypes: {e}", file=sys.stderr)
+        return None
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
+        build_calls()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ex.submit(build_calls, force)
         objs = list(ex.map(lambda s: _compile(os.path.join(CSRC, s), extra), SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
