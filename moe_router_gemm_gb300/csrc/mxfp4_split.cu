@@ -12,6 +12,7 @@
 //     NT * 128 bytes of x;
 //   * warp 0: TMA producer; warp 1: MMA issuer (four a chunk, two 32-code scale blocks
 //     each), TMEM; warps 2-5: scales, then the epilogue (TMEM lane quarter = warp % 4);
+//     warps 6 and 7 help to stage x and to join the sums;
 //   * scales: thread i reads eight bytes (a chunk) of W row i, and each warp those of
 //     all NT tokens (every lane quarter needs them), kAhead chunks ahead, and writes
 //     the words to one of the TMEM slots: W words at columns 0 and 8 of the slot,
@@ -24,6 +25,14 @@
 //     after a cluster barrier each adds the S sums of its share of the tokens, in rank
 //     order, adds the bias and rounds: the order never changes;
 //   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
+//
+// Bound by latency: launch, TMEM and barriers 2.0 us, cold codes 1 to 1.5, scales 1.2,
+// the join 0.5 (16 tokens) to 2 (64).  From codes / from bf16: 1 x 2112 x 7168 6.0 /
+// 6.2 us, 16 x 2112 x 7168 6.7 / 8.3, 1 x 14336 x 4096 9.6 / 9.8 (3.3 TB/s), 64 x 14336
+// x 4096 11.3.  Measured and not taken: W's rows asked into L2 before the wait for the
+// previous kernel (0 to 1 us slower), TMA boxes issued by a lane per stage (no change),
+// scale words asked for before x is staged (-0.4 to +0.3 us), 128-token tiles (128 x
+// 2112 x 7168 9.9 us, 8.4 with 64).
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -35,7 +44,7 @@ namespace {
 
 constexpr int kRowsW = 128, kChunkBytes = 128, kChunkBlocks = 8;
 constexpr int kWBytes = kRowsW * kChunkBytes;
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8, kMaxStages = 8;
 constexpr int kSlotCols = 32;
 constexpr int kAhead = 4;
@@ -72,7 +81,7 @@ struct SplitShared {
 
 // NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  W: alignment of the scale rows (scale_words).
 template <int NT, bool BF16, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const SplitArgs a) {
     using T = Split<NT>;
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kThreads)
                 mma_commit(&sh.acc_full);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 6) {
         // ---- scales ----
         const int quarter = warp & 3;
         const uint32_t slot0 = tmem + (uint32_t)T::kSfCol + ((uint32_t)(quarter * 32) << 16);
