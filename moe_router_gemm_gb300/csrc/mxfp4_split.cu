@@ -371,12 +371,10 @@ int split_smem(int nt, int stages, int S, int K) {
 
 int split_slots(int nt) { return nt <= 32 ? Split<32>::kSlots : Split<64>::kSlots; }
 
-}  // namespace
-
-Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
+Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms) {
     Mxfp4SplitPlan p;
     const int C = ceil_div(K, 256), n_tiles = ceil_div(N, kRowsW);
-    p.tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    p.tokens = tokens;
     p.m_tiles = ceil_div(M, p.tokens);
     // K over S CTAs: microseconds from timings of 40 shapes (1 to 512 tokens, 256 to 14336 rows).  A chunk takes about 0.4
     // where every SM has at most one CTA, and as much longer as there are more; joining S sums costs more with S, and with
@@ -400,9 +398,17 @@ Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
     return p;
 }
 
-bool mxfp4_split_quantises(int M, int N, int K) {
-    return M <= 16 && mxfp4_split_plan(M, N, K, kGb300Sms).smem <= kMaxSmem;
+}  // namespace
+
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
+    if (M <= 16) {
+        const Mxfp4SplitPlan p = plan_for(16, M, N, K, num_sms);
+        if (p.smem <= kMaxSmem) return p;  // else (K of 200000 and more) a run of x does not fit: by TMA, stage by stage
+    }
+    return plan_for(M <= 32 ? 32 : 64, M, N, K, num_sms);
 }
+
+bool mxfp4_split_quantises(int M, int N, int K) { return mxfp4_split_plan(M, N, K, kGb300Sms).tokens == 16; }
 
 int init_mxfp4_split() {
     for (uintptr_t w : {8, 4, 1})

@@ -173,6 +173,31 @@ def test_linear_offsets_past_32_bits(lib, M):
     ref.check_linear(got, xv, wv, None, K)
 
 
+def test_linear_output_past_32_bits(lib):
+    """An output of more than 2^32 elements: its corners."""
+    M, N, K = 66000, 65536, 32
+    assert M * N > 2 ** 32
+    x = torch.randn(M, K, device=DEV).to(torch.bfloat16)
+    wq = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    ws = torch.randint(124, 130, (N, K // 32), dtype=torch.uint8, device=DEV)
+    got = lib.bf16_linear_mxfp4_dynamic(x, wq, ws)
+    for r, c in ((slice(0, 5), slice(0, 7)), (slice(-5, None), slice(-9, None)), (slice(33000, 33003), slice(40000, 40050))):
+        q, s = ref.quant_mxfp4(ref.f64(x[r]))
+        ref.check_linear(got[r, c], ref.values_mxfp4(q, s), ref.values_mxfp4(wq[c].cpu().numpy(), ws[c].cpu().numpy()), None, K)
+
+
+@pytest.mark.parametrize("K", [65536, 262144, 200032])
+def test_linear_long_k(lib, K):
+    """K so long that a run of x for 16 tokens does not fit shared memory."""
+    for M in (2, 16, 20):
+        x, wq, ws, _ = _operands(M, 40, K, K + M, False)
+        xq, xs = lib.quant_mxfp4(x)
+        got = lib.bf16_linear_mxfp4(xq, xs, wq, ws)
+        ref.check_linear(got, ref.values_mxfp4(xq.cpu().numpy(), xs.cpu().numpy()),
+                         ref.values_mxfp4(wq.cpu().numpy(), ws.cpu().numpy()), None, K, f"M={M}")
+        assert torch.equal(lib.bf16_linear_mxfp4_dynamic(x, wq, ws), got)
+
+
 def test_quant_offsets_past_32_bits(lib):
     rows, K = 600000, 7200
     assert rows * K > 2 ** 32
