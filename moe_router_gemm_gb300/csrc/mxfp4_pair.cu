@@ -45,7 +45,8 @@ constexpr int kChunkBytes = 128;            // code bytes of a row per chunk (25
 constexpr int kHalfBytes = kHalf * kChunkBytes;
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kStages = 6;
-constexpr int kGroup = 4;                   // W tiles of a raster group: 8192 x 7168 x 7168 takes 135.6 us with 4, 136.7 with 2, 138 with 8
+// W tiles of a raster group: 8192 x 7168 x 7168 takes 135.6 us with 4, 136.7 with 2, 138 with 8
+constexpr int kGroup = 4;
 constexpr int kSlots = 4, kSlotCols = 32;
 constexpr int kSfCol = 512 - kSlots * kSlotCols;  // the scale slots' first column
 constexpr int kAcc1Col = kSfCol - kTileRows;      // the second accumulator's first column
@@ -54,9 +55,9 @@ static_assert(kShared % 64 == 0, "the epilogue empties 64 columns at a time");
 constexpr int kEpiWarps = 8, kScaleWarps = 4;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 
-
 struct PairShared {
-    uint8_t piece[kEpiWarps][32 * 64];  // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first: aligned)
+    // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first, so aligned)
+    uint8_t piece[kEpiWarps][32 * 64];
     uint4 scales[2][kTileRows];
     uint64_t full[kStages];    // leader only: both CTAs' codes and scales of the stage are in shared memory
     uint64_t empty[kStages];   // both: the MMAs (and copies) reading the stage are done
@@ -66,11 +67,11 @@ struct PairShared {
     int32_t bad_pair, aborted, issued, consumed;
 };
 
-__device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int group, int &p0, int &q0) {
-    const int per_group = group * p_tiles;
+__device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int &p0, int &q0) {
+    const int per_group = kGroup * p_tiles;
     const int g = u / per_group, r = u - g * per_group;
-    const int gq = (q_tiles - g * group) < group ? (q_tiles - g * group) : group;
-    const int pi = r / gq, qi = g * group + (r - pi * gq);
+    const int gq = (q_tiles - g * kGroup) < kGroup ? (q_tiles - g * kGroup) : kGroup;
+    const int pi = r / gq, qi = g * kGroup + (r - pi * gq);
     p0 = pi * kTileRows;
     q0 = qi * kTileRows;
 }
@@ -78,9 +79,9 @@ __device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int
 template <int W>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ ws,
-                      const uint16_t *__restrict__ bias, uint16_t *__restrict__ out, int M, int N, int K, int group,
-                      int32_t *status) {
+                      const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ xs,
+                      const uint8_t *__restrict__ ws, const uint16_t *__restrict__ bias, uint16_t *__restrict__ out,
+                      int M, int N, int K, int32_t *status) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0;
             for (int u = cl; u < units; u += ncl) {
                 int p0, q0;
-                pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+                pair_coords(u, p_tiles, q_tiles, p0, q0);
                 const int ap = p0 + (int)rank * kHalf, bq = q0 + (int)rank * kHalf;
                 for (int c = 0; c < C; ++c, ++it) {
                     const int s = it % kStages;
@@ -220,11 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tile = 0;
         for (int u = cl; u < units; u += ncl, ++tile) {
             int p0, q0;
-            pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+            pair_coords(u, p_tiles, q_tiles, p0, q0);
             const int m = p0 + (int)rank * kHalf + row;
             const int second = tile & 1;
-            // the first column of this warp's slice i: the shared columns (128-255 of the first accumulator, 0-127 of the
-            // second) come first
+            // the first column of this warp's slice i: the shared columns (128-255 of the first accumulator,
+            // 0-127 of the second) come first
             auto column = [&](int i) {
                 const int c = 32 * (2 * i + half);  // 0, 64, 128, 192 (+ 32)
                 return second ? c : (c + kAcc1Col) & 255;
@@ -268,10 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
                         *reinterpret_cast<uint4 *>(piece + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
                             make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                       pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && m < M) tma_store_2d(&tm_out, piece, n, m);  // rows and columns past the end are cut off
+                    // (rows and columns past the end are cut off)
+                    if (lane == 0 && m < M) tma_store_2d(&tm_out, piece, n, m);
                 } else if (m < M && n < N) {
                     uint16_t *o = out + (size_t)m * N + n;
 #pragma unroll
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool stop = false;
         for (int u = cl; u < units; u += ncl) {
             int p0, q0;
-            pair_coords(u, p_tiles, q_tiles, group, p0, q0);
+            pair_coords(u, p_tiles, q_tiles, p0, q0);
             const int ra = p0 + (int)rank * kHalf + 32 * quarter + lane, rb0 = q0 + st, rb1 = rb0 + kHalf;
             const bool ia = ra < M, ib0 = rb0 < N, ib1 = rb1 < N;
             const uint8_t *pa = xs + (size_t)(ia ? ra : 0) * nb, *pb0 = ws + (size_t)(ib0 ? rb0 : 0) * nb,
@@ -386,8 +389,8 @@ constexpr int smem_bytes() { return 1024 + kStages * kStageBytes + (int)sizeof(P
 static_assert(smem_bytes() <= 232448, "shared memory");
 static_assert(smem_bytes() > 116 * 1024, "one CTA per SM: each allocates all 512 TMEM columns");
 
-using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *, const uint16_t *,
-                        uint16_t *, int, int, int, int, int32_t *);
+using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *,
+                        const uint16_t *, uint16_t *, int, int, int, int32_t *);
 
 PairFn pick_pair(uintptr_t align) {
     return align % 16 == 0  ? mxfp4_pair_kernel<16>
@@ -471,7 +474,7 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
     const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
     return (int)cudaLaunchKernelEx(&cfg, pick_pair(a), tx, tw, to, static_cast<const uint8_t *>(xs),
                                    static_cast<const uint8_t *>(ws), static_cast<const uint16_t *>(bias),
-                                   static_cast<uint16_t *>(out), M, N, K, kGroup, status);
+                                   static_cast<uint16_t *>(out), M, N, K, status);
 }
 
 }  // namespace bf16l

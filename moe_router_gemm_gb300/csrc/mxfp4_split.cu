@@ -79,7 +79,8 @@ struct SplitShared {
     int32_t aborted, issued, consumed;
 };
 
-// NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  W: alignment of the scale rows (scale_words).
+// NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  W: alignment of the scale rows, as for
+// scale_words.
 template <int NT, bool BF16, int W>
 __global__ void __launch_bounds__(kThreads, 2)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint32_t s;
                 const uint32_t w = mxfp4_quant_vec(v[k], 0xFu << (lane & 28), s);
                 const int c = r >> 5, u = (r >> 2) & 7;  // chunk, 16-byte unit of its row (a block)
-                *reinterpret_cast<uint32_t *>(xrun + c * T::kXBytes + tok * 128 + 16 * (u ^ (tok & 7)) + 4 * (r & 3)) = w;
+                uint8_t *to = xrun + c * T::kXBytes + tok * 128 + 16 * (u ^ (tok & 7)) + 4 * (r & 3);
+                *reinterpret_cast<uint32_t *>(to) = w;
                 if ((r & 3) == 0) xscale[(c * NT + tok) * 8 + u] = (uint8_t)s;
             }
         }
@@ -251,8 +253,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int d = 0; d < kAhead; ++d) {
                 const int i = i0 + d;
                 if (i >= nc) break;
-                const int f = i % T::kSlots, old = i - T::kSlots;  // the slot is free when the MMAs of chunk `old` are done
-                if (old >= 0 && !mbar_wait(&sh.empty[old % stages], (old / stages) & 1, a.status, kSiteScale)) stop = true;
+                // the slot is free when the MMAs of chunk `old` are done
+                const int f = i % T::kSlots, old = i - T::kSlots;
+                if (old >= 0 && !mbar_wait(&sh.empty[old % stages], (old / stages) & 1, a.status, kSiteScale))
+                    stop = true;
                 if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
                     atomicExch(&sh.aborted, 1);
                     stop = true;
@@ -279,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         const bool have = __all_sync(0xFFFFFFFFu, ok && !*((volatile int32_t *)&sh.aborted));
         if (have) {
-            float *sums = reinterpret_cast<float *>(base);  // [token][128 rows], over the ring: every chunk has been read
+            // [token][128 rows], over the ring: every chunk has been read
+            float *sums = reinterpret_cast<float *>(base);
             const float bias = a.bias && row < a.N ? bf16_to_f32(__ldg(a.bias + row)) : 0.0f;
             const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
@@ -376,9 +381,9 @@ Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms) {
     const int C = ceil_div(K, 256), n_tiles = ceil_div(N, kRowsW);
     p.tokens = tokens;
     p.m_tiles = ceil_div(M, p.tokens);
-    // K over S CTAs: microseconds from timings of 40 shapes (1 to 512 tokens, 256 to 14336 rows).  A chunk takes about 0.4
-    // where every SM has at most one CTA, and as much longer as there are more; joining S sums costs more with S, and with
-    // the tokens where S is 8.  64 x 2112 x 7168: S = 1, 2, 4, 8 take 16.0, 10.7, 7.7, 8.6 us; 16 x 2112 x 7168: 16.7,
+    // K over S CTAs: microseconds from timings of 40 shapes (1 to 512 tokens, 256 to 14336 rows).  A chunk takes
+    // about 0.4 where every SM has at most one CTA, and as much longer as there are more; joining S sums costs more
+    // with S, and with the tokens where S is 8.  64 x 2112 x 7168: S = 1, 2, 4, 8 take 16.0, 10.7, 7.7, 8.6 us; 16 x 2112 x 7168: 16.7,
     // 10.8, 8.0, 7.0; 1 x 14336 x 4096: 11.7, 9.9, 13.0, 19.0.
     const float tiles = (float)n_tiles * (float)p.m_tiles;
     float best = 0.0f;
@@ -403,7 +408,8 @@ Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms) {
 Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
     if (M <= 16) {
         const Mxfp4SplitPlan p = plan_for(16, M, N, K, num_sms);
-        if (p.smem <= kMaxSmem) return p;  // else (K of 200000 and more) a run of x does not fit: by TMA, stage by stage
+        // else (K of 200000 and more) a run of x does not fit: by TMA, stage by stage
+        if (p.smem <= kMaxSmem) return p;
     }
     return plan_for(M <= 32 ? 32 : 64, M, N, K, num_sms);
 }
@@ -462,7 +468,8 @@ int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    const uintptr_t al = (bf16 ? 0 : reinterpret_cast<uintptr_t>(xs)) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
+    const uintptr_t al =
+        (bf16 ? 0 : reinterpret_cast<uintptr_t>(xs)) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
     return (int)cudaLaunchKernelEx(&cfg, pick_split(p.tokens, bf16, al), tx, tw, a);
 }
 

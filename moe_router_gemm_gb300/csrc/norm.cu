@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
     long long r = blockIdx.x;
     if (r < a.rows) load(r);
     for (int i = me; i < (a.H + 1) / 2 + 2; i += nt) {
-        const uint32_t lo = 2 * i < a.H ? __ldg(a.weight + 2 * i) : 0u, hi = 2 * i + 1 < a.H ? __ldg(a.weight + 2 * i + 1) : 0u;
+        const uint32_t lo = 2 * i < a.H ? __ldg(a.weight + 2 * i) : 0u;
+        const uint32_t hi = 2 * i + 1 < a.H ? __ldg(a.weight + 2 * i + 1) : 0u;
         sw[i] = lo | hi << 16;
     }
     __syncthreads();
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const NormArgs a) {
                 if (i < a.H) put(h[j], i);
             }
         } else {
-            for (int i = (int)threadIdx.x; i < a.H; i += nt) put(bf16_to_f32(hr[i]), i);  // h: written by this same thread
+            // (h was written by this same thread)
+            for (int i = (int)threadIdx.x; i < a.H; i += nt) put(bf16_to_f32(hr[i]), i);
         }
     }
 }
@@ -374,7 +376,10 @@ NormFn pick_vec(int v, bool warp, int threads) {
 
 template <int QUANT>
 NormFn pick_any(int n) {
-    return n == 4 ? norm_any_kernel<QUANT, 4> : n == 8 ? norm_any_kernel<QUANT, 8> : n == 16 ? norm_any_kernel<QUANT, 16> : norm_any_kernel<QUANT, 0>;
+    return n == 4    ? norm_any_kernel<QUANT, 4>
+           : n == 8  ? norm_any_kernel<QUANT, 8>
+           : n == 16 ? norm_any_kernel<QUANT, 16>
+                     : norm_any_kernel<QUANT, 0>;
 }
 
 }  // namespace
@@ -413,8 +418,8 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
              : quant == BF16L_QUANT_FP8   ? pick_vec<BF16L_QUANT_FP8>(v, warp, threads)
              : quant == BF16L_QUANT_MXFP8 ? pick_vec<BF16L_QUANT_MXFP8>(v, warp, threads)
                                            : pick_vec<BF16L_QUANT_MXFP4>(v, warp, threads);
-    } else if (H % 8 != 0 && (ldx - H) % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H >= 64 && H <= 16384 &&
-               (quant == BF16L_QUANT_NONE || quant == BF16L_QUANT_FP8)) {
+    } else if (H % 8 != 0 && (ldx - H) % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H >= 64 &&
+               H <= 16384 && (quant == BF16L_QUANT_NONE || quant == BF16L_QUANT_FP8)) {
         const int nvec = H / 8, v = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
         threads = ((nvec + v - 1) / v + 31) / 32 * 32;
         blocks = rows;

@@ -7,10 +7,14 @@
 // equal to +0, 0 for an expert that a group limit or an earlier pick took out).  A pick
 // is the largest of the lanes' largest keys (one warp reduction) and the first lane
 // that has it, which is the lowest expert as runs ascend; a lane keeps its two largest
-// keys, so it has to look through its run again only after two picks.  Groups that are whole lanes, a power of two of them, are ranked by a
-// butterfly and a count of the better ones; others by reductions over masked keys.
-// Some 600 instructions a token of 256 experts and 8 picks, two thirds of them in the
-// picks: issue, not the 1 KB of logits, is the bound.
+// keys, so it has to look through its run again only after two picks.  Groups that are
+// whole lanes, a power of two of them, are ranked by a butterfly and a count of the
+// better ones; others by reductions over masked keys.
+//
+// About 1000 instructions a token of 256 experts in groups and 8 picks, a quarter of
+// them the exact exponentials and quotients of the scores: issue, not the 1 KB of
+// logits, is the bound.  8192 x 256: 10.9 us (28 with experts strided over the lanes
+// and two reductions a pick, 12.6 with one key per lane); softmax without groups 8.0.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -73,16 +77,19 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
                 if constexpr (VPL % 8 == 0) {
 #pragma unroll
                     for (int j = 0; j < VPL / 8; ++j) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + at + e0) + j);
-                        l[8 * j] = bf16_lo(v.x), l[8 * j + 1] = bf16_hi(v.x), l[8 * j + 2] = bf16_lo(v.y), l[8 * j + 3] = bf16_hi(v.y);
-                        l[8 * j + 4] = bf16_lo(v.z), l[8 * j + 5] = bf16_hi(v.z), l[8 * j + 6] = bf16_lo(v.w), l[8 * j + 7] = bf16_hi(v.w);
+                        const uint16_t *p = static_cast<const uint16_t *>(a.logits) + at + e0 + 8 * j;
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[8 * j + 2 * i] = bf16_lo(u[i]), l[8 * j + 2 * i + 1] = bf16_hi(u[i]);
                     }
                 }
             } else {
                 if constexpr (VPL % 4 == 0) {
 #pragma unroll
                     for (int j = 0; j < VPL / 4; ++j) {
-                        const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + at + e0) + j);
+                        const float *p = static_cast<const float *>(a.logits) + at + e0 + 4 * j;
+                        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
                         l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
                     }
                 }
@@ -234,7 +241,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 int launch_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
                  int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
                  int logits_bf16, int num_sms, uint32_t flags, void *stream) {
-    const int need = (experts + 31) / 32, vpl = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : need <= 16 ? 16 : 32;
+    int vpl = 1;  // a power of two
+    while (32 * vpl < experts) vpl *= 2;
     const int run = logits_bf16 ? 8 : 4, bytes = logits_bf16 ? 2 : 4, each = experts / groups, gl = each / vpl;
     RouteArgs a = {logits, bias,       weights,    ids,     tokens, ld,          experts, k,
                    groups, top_groups, group_best, softmax, renorm, logits_bf16, scale};
