@@ -56,7 +56,7 @@ def _logits(T, E, seed, dtype=torch.float32, ld=None):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (5, 8, 2), (7, 33, 5), (16, 128, 4), (31, 100, 32),
-                                   (65, 384, 6), (3, 512, 10), (2, 1000, 16), (2, 1024, 1), (1, 32, 32), (9, 160, 6)])
+                                   (65, 384, 6), (3, 512, 10), (2, 1000, 16), (2, 1024, 1), (1, 32, 32), (9, 160, 6), (5, 96, 3), (6, 192, 7), (40, 384, 8), (3, 700, 12), (8, 383, 8)])
 def test_softmax(lib, T, E, k, dtype):
     _check(lib, _logits(T, E, T + E, dtype), k, exact_ids=True)
     _check(lib, _logits(T, E, T + E + 1, dtype, ld=E + 3), k, exact_ids=True, renormalize=False, scale=2.5)
@@ -73,7 +73,8 @@ def test_bias_ranks_but_does_not_weigh(lib, T, E, k, scoring):
 
 @pytest.mark.parametrize("scoring,best", [("softmax", 1), ("softmax", 2), ("sigmoid", 1), ("sigmoid", 2)])
 @pytest.mark.parametrize("T,E,k,groups,top", [(33, 256, 8, 8, 4), (5, 64, 6, 4, 1), (3, 160, 6, 8, 3), (9, 96, 5, 32, 3),
-                                              (4, 15, 2, 5, 2), (2, 1024, 8, 8, 2), (6, 24, 12, 2, 1), (7, 14, 4, 7, 2)])
+                                              (4, 15, 2, 5, 2), (2, 1024, 8, 8, 2), (70, 384, 8, 8, 3), (9, 384, 6, 4, 2), (5, 192, 4, 2, 1),
+                                              (8, 96, 4, 3, 2), (11, 768, 9, 16, 5), (3, 160, 5, 4, 2), (6, 24, 12, 2, 1), (7, 14, 4, 7, 2)])
 def test_groups(lib, T, E, k, groups, top, scoring, best):
     g = torch.Generator().manual_seed(E + groups)
     bias = (0.2 * torch.randn(E, generator=g)).to(DEV) if scoring == "sigmoid" else None
