@@ -15,14 +15,18 @@
 //     before this row's sum, so memory is busy through the reduction.  8192 x 7168
 //     with a residual: 70.5 us to bf16 (98% of the copy bandwidth), 83 us to bf16 and
 //     MXFP8 (94%); without one 40.5 us (85%).
-//   * norm_shift_kernel: H not a multiple of 8, rows of x at the same place in a 16-byte
-//     line as the dense tensors' (ldx = H, or H plus a multiple of 8): a row is up to 7
-//     values, vectors on 16-byte boundaries, up to 7 values; the weight, which meets
-//     the vectors at a different place in every row, comes from shared memory.
-//     2000 x 2881 with a residual: 27 us a value at a time.
-//   * norm_any_kernel: any H, stride and alignment, one value per lane and step; a
-//     warp's 32 lanes hold a scale block.  Rows of more than 16384 elements are read
-//     twice (the second time from L1 or L2).
+//   * norm_shift_kernel: odd lengths and strides.  The dense tensors' vectors start on
+//     16-byte boundaries, so a row is up to 7 values, vectors, up to 7 values; a
+//     vector of x that lies across two 16-byte blocks is shifted out of both; the
+//     weight, which meets the vectors at a different place in every row, comes from
+//     shared memory.  A value at a time these took two to seven times as long:
+//     2000 x 2881 with a residual 27 us (10.9 here), 8192 x 7168 of 7300 columns 114
+//     (78), 8192 x 7168 of 7169 columns with MXFP8 295 (100).  (The second block from
+//     the next lane instead of a load of its own: 2048 x 1536 of 2113 columns 11.5 us,
+//     6.3 with the load.)
+//   * norm_any_kernel: what is left (H below 64, or above 16384 and odd in some way): one
+//     value per lane and step; a warp's 32 lanes hold a scale block.  Rows of more than
+//     16384 elements are read twice (the second time from L1 or L2).
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -72,6 +76,65 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 // Magnitude bits of a value for a block's maximum: NaN above infinity, so it shows.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// The outputs of eight values from element `at` of the dense tensors on (a multiple of 8).  For the MX formats the
+// four lanes of a quad hold a block and call it together.
+template <int QUANT>
+__device__ __forceinline__ void put8(const NormArgs &a, long long at, float (&y)[8], float inv_scale) {
+    if (a.out) OutStore<uint16_t>::eight(a.out + at, y);
+    if (QUANT == BF16L_QUANT_NONE) return;
+    float f = inv_scale;
+    bool nan = false;
+    if (QUANT != BF16L_QUANT_FP8) {
+        const unsigned quad = 0xFu << (threadIdx.x & 28u);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, mag_bits(y[e]));
+        m = max(m, __shfl_xor_sync(quad, m, 1));
+        m = max(m, __shfl_xor_sync(quad, m, 2));
+        nan = m > 0x7F800000u;
+        const int s = mx_scale_exp(m, QUANT == BF16L_QUANT_MXFP8 ? 8 : 2);
+        f = exp2_neg(nan ? 0 : s);
+        if ((threadIdx.x & 3) == 0) a.scales[at >> 5] = nan ? 255 : (uint8_t)(s + 127);
+    }
+    if (QUANT == BF16L_QUANT_MXFP4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= f;
+        *reinterpret_cast<uint32_t *>(a.codes + (at >> 1)) = nan ? 0u : e2m1x8(y);
+    } else {
+        uint16_t d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * f, y[2 * e + 1] * f);
+        *reinterpret_cast<uint2 *>(a.codes + at) =
+            make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
+    }
+}
+
+__device__ __forceinline__ uint4 add_bf16x8(const uint4 &h, const uint4 &q) {
+    return make_uint4(pack_bf16x2(bf16_lo(h.x) + bf16_lo(q.x), bf16_hi(h.x) + bf16_hi(q.x)),
+                      pack_bf16x2(bf16_lo(h.y) + bf16_lo(q.y), bf16_hi(h.y) + bf16_hi(q.y)),
+                      pack_bf16x2(bf16_lo(h.z) + bf16_lo(q.z), bf16_hi(h.z) + bf16_hi(q.z)),
+                      pack_bf16x2(bf16_lo(h.w) + bf16_lo(q.w), bf16_hi(h.w) + bf16_hi(q.w)));
+}
+
+__device__ __forceinline__ float squares(const uint4 &v, float ss) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        ss = fmaf(bf16_lo(u[e]), bf16_lo(u[e]), ss);
+        ss = fmaf(bf16_hi(u[e]), bf16_hi(u[e]), ss);
+    }
+    return ss;
+}
+
+__device__ __forceinline__ void scaled(float (&y)[8], const uint4 &v, float rstd, const uint4 &w) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w}, g[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        y[2 * e] = bf16_lo(u[e]) * rstd * bf16_lo(g[e]);
+        y[2 * e + 1] = bf16_hi(u[e]) * rstd * bf16_hi(g[e]);
+    }
+}
+
 // V: vectors per thread.  WARP: a row to a warp, else to a block.  T: at most this many threads.
 template <int QUANT, int V, bool WARP, int T>
 __global__ void __launch_bounds__(T) norm_vec_kernel(const NormArgs a) {
@@ -82,7 +145,6 @@ __global__ void __launch_bounds__(T) norm_vec_kernel(const NormArgs a) {
     const long long step = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
     long long r = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     const float inv_scale = QUANT == BF16L_QUANT_FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
-    const unsigned quad = 0xFu << (threadIdx.x & 28u);
     const uint4 kNone = make_uint4(0u, 0u, 0u, 0u);
     uint4 w[V], h[V], q[V];
     auto load = [&](long long row) {
@@ -105,68 +167,22 @@ __global__ void __launch_bounds__(T) norm_vec_kernel(const NormArgs a) {
         uint4 c[V];  // this row's h
         float ss = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            c[j] = h[j];
-            if (a.residual) {
-                c[j].x = pack_bf16x2(bf16_lo(h[j].x) + bf16_lo(q[j].x), bf16_hi(h[j].x) + bf16_hi(q[j].x));
-                c[j].y = pack_bf16x2(bf16_lo(h[j].y) + bf16_lo(q[j].y), bf16_hi(h[j].y) + bf16_hi(q[j].y));
-                c[j].z = pack_bf16x2(bf16_lo(h[j].z) + bf16_lo(q[j].z), bf16_hi(h[j].z) + bf16_hi(q[j].z));
-                c[j].w = pack_bf16x2(bf16_lo(h[j].w) + bf16_lo(q[j].w), bf16_hi(h[j].w) + bf16_hi(q[j].w));
-            }
-        }
+        for (int j = 0; j < V; ++j) c[j] = a.residual ? add_bf16x8(h[j], q[j]) : h[j];
         if (r + step < a.rows) load(r + step);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = me + j * nt;
             if (a.residual && i < nvec) reinterpret_cast<uint4 *>(a.residual_out + r * a.H)[i] = c[j];
-            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ss = fmaf(bf16_lo(u[e]), bf16_lo(u[e]), ss);
-                ss = fmaf(bf16_hi(u[e]), bf16_hi(u[e]), ss);
-            }
+            ss = squares(c[j], ss);
         }
         const float rstd = 1.0f / sqrtf((WARP ? warp_sum(ss) : block_sum(ss, red[par])) / (float)a.H + a.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = me + j * nt;
             if (i >= nvec) break;  // nvec % 4 == 0 for the MX formats: a quad leaves together
-            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w}, g[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
             float y[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = bf16_lo(u[e]) * rstd * bf16_lo(g[e]);
-                y[2 * e + 1] = bf16_hi(u[e]) * rstd * bf16_hi(g[e]);
-            }
-            if (a.out) OutStore<uint16_t>::eight(a.out + r * a.H + 8 * (long long)i, y);
-            if (QUANT == BF16L_QUANT_FP8) {
-                uint16_t d[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv_scale, y[2 * e + 1] * inv_scale);
-                reinterpret_cast<uint2 *>(a.codes + r * a.H)[i] =
-                    make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
-            } else if (QUANT != BF16L_QUANT_NONE) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = max(m, mag_bits(y[e]));
-                m = max(m, __shfl_xor_sync(quad, m, 1));
-                m = max(m, __shfl_xor_sync(quad, m, 2));
-                const bool nan = m > 0x7F800000u;
-                const int s = mx_scale_exp(m, QUANT == BF16L_QUANT_MXFP8 ? 8 : 2);
-                const float inv = exp2_neg(nan ? 0 : s);
-                if (QUANT == BF16L_QUANT_MXFP8) {
-                    uint16_t d[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv, y[2 * e + 1] * inv);
-                    reinterpret_cast<uint2 *>(a.codes + r * a.H)[i] =
-                        make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] *= inv;
-                    reinterpret_cast<uint32_t *>(a.codes + r * (a.H >> 1))[i] = nan ? 0u : e2m1x8(y);
-                }
-                if ((threadIdx.x & 3) == 0) a.scales[r * (a.H >> 5) + (i >> 2)] = nan ? 255 : (uint8_t)(s + 127);
-            }
+            scaled(y, c[j], rstd, w[j]);
+            put8<QUANT>(a, r * a.H + 8 * (long long)i, y, inv_scale);
         }
     }
 }
@@ -179,18 +195,43 @@ __device__ __forceinline__ uint4 weights_at(const uint32_t *w, int i) {
                       __funnelshift_r(p[3], p[4], 16));
 }
 
-template <bool FP8, int V>
-__global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
+// The 16-byte block at p (16-byte aligned), of which only the part inside [lo, hi) is read.
+__device__ __forceinline__ uint4 load_block(const uint16_t *p, const uint16_t *lo, const uint16_t *hi) {
+    if (p >= lo && p + 8 <= hi) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i)
+        if (p + i >= lo && p + i < hi) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sixteen bytes from byte m (even, below 16) of two neighbouring blocks on.
+__device__ __forceinline__ uint4 shift_blocks(const uint4 &a, const uint4 &b, int m) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t v[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {  // words m / 4 + k
+        const uint32_t lo = m & 4 ? w[k + 1] : w[k], hi = m & 4 ? w[k + 3 < 8 ? k + 3 : 7] : w[k + 2];
+        v[k] = m & 8 ? hi : lo;
+    }
+    if ((m & 2) == 0) return make_uint4(v[0], v[1], v[2], v[3]);
+    return make_uint4(__funnelshift_r(v[0], v[1], 16), __funnelshift_r(v[1], v[2], 16), __funnelshift_r(v[2], v[3], 16),
+                      __funnelshift_r(v[3], v[4], 16));
+}
+
+// V: vectors per thread.  XS: the vectors of x are not all on 16-byte boundaries.
+template <int QUANT, int V, bool XS>
+__global__ void __launch_bounds__(1024) norm_shift_kernel(const NormArgs a) {
     extern __shared__ uint32_t sw[];  // the weight
     __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
     const int nt = (int)blockDim.x, me = (int)threadIdx.x;
-    const float inv_scale = FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
+    const float inv_scale = QUANT == BF16L_QUANT_FP8 ? 1.0f / __ldg(a.scale) : 0.0f;
     const uint4 kNone = make_uint4(0u, 0u, 0u, 0u);
-    uint4 h[V], q[V];
-    uint16_t hs = 0, qs = 0;  // threads 0-7: the values before the first vector; 8-15: those after the last
-    int head, nv, edge;       // of the row that is loaded; edge: this thread's single value, or -1
+    const uint16_t *xend = a.x + (a.rows - 1) * a.ldx + a.H;
+    uint4 h[V], h2[XS ? V : 1], q[V];
+    uint16_t hs = 0, qs = 0;     // threads 0-7: the values before the first vector; 8-15: those after the last
+    int head, nv, edge, xm = 0;  // of the row that is loaded; edge: this thread's single value, or -1
     auto load = [&](long long row) {
         head = (int)(-(row * a.H) & 7);
         if (head > a.H) head = a.H;
@@ -202,10 +243,17 @@ __global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
             hs = x[edge];
             if (a.residual) qs = r[edge];
         }
+        if (XS) xm = (int)(reinterpret_cast<uintptr_t>(x + head) & 15u);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = me + j * nt;
-            h[j] = i < nv ? __ldg(reinterpret_cast<const uint4 *>(x + head) + i) : kNone;
+            if (XS) {
+                const uint16_t *b = x + head + 8 * i - (xm >> 1);
+                h[j] = i < nv ? load_block(b, a.x, xend) : kNone;
+                h2[j] = i < nv && xm ? load_block(b + 8, a.x, xend) : kNone;
+            } else {
+                h[j] = i < nv ? __ldg(reinterpret_cast<const uint4 *>(x + head) + i) : kNone;
+            }
             if (a.residual) q[j] = i < nv ? reinterpret_cast<const uint4 *>(r + head)[i] : kNone;
         }
     };
@@ -224,13 +272,8 @@ __global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
         const long long at = r * a.H;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            c[j] = h[j];
-            if (a.residual) {
-                c[j].x = pack_bf16x2(bf16_lo(h[j].x) + bf16_lo(q[j].x), bf16_hi(h[j].x) + bf16_hi(q[j].x));
-                c[j].y = pack_bf16x2(bf16_lo(h[j].y) + bf16_lo(q[j].y), bf16_hi(h[j].y) + bf16_hi(q[j].y));
-                c[j].z = pack_bf16x2(bf16_lo(h[j].z) + bf16_lo(q[j].z), bf16_hi(h[j].z) + bf16_hi(q[j].z));
-                c[j].w = pack_bf16x2(bf16_lo(h[j].w) + bf16_lo(q[j].w), bf16_hi(h[j].w) + bf16_hi(q[j].w));
-            }
+            c[j] = XS ? shift_blocks(h[j], h2[XS ? j : 0], xm) : h[j];
+            if (a.residual) c[j] = add_bf16x8(c[j], q[j]);
         }
         if (cedge >= 0) {
             uint16_t b = hs;
@@ -245,41 +288,24 @@ __global__ void __launch_bounds__(512) norm_shift_kernel(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = me + j * nt;
-            if (a.residual && i < cnv) reinterpret_cast<uint4 *>(a.residual_out + at + chead)[i] = c[j];
-            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ss = fmaf(bf16_lo(u[e]), bf16_lo(u[e]), ss);
-                ss = fmaf(bf16_hi(u[e]), bf16_hi(u[e]), ss);
-            }
+            if (i >= cnv) break;  // (what lies there of x is not this row's)
+            if (a.residual) reinterpret_cast<uint4 *>(a.residual_out + at + chead)[i] = c[j];
+            ss = squares(c[j], ss);
         }
         const float rstd = 1.0f / sqrtf(block_sum(ss, red[par]) / (float)a.H + a.eps);
-        if (cedge >= 0) {
+        if (cedge >= 0) {  // (never for the MX formats: their rows are whole vectors)
             const uint32_t w = sw[cedge >> 1];
             const float y = cs * rstd * (cedge & 1 ? bf16_hi(w) : bf16_lo(w));
             if (a.out) a.out[at + cedge] = f32_to_bf16(y);
-            if (FP8) a.codes[at + cedge] = (uint8_t)(e4m3x2_sat(y * inv_scale, 0.0f) & 0xFFu);
+            if (QUANT == BF16L_QUANT_FP8) a.codes[at + cedge] = (uint8_t)(e4m3x2_sat(y * inv_scale, 0.0f) & 0xFFu);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = me + j * nt;
-            if (i >= cnv) break;
-            const uint4 w = weights_at(sw, chead + 8 * i);
-            const uint32_t u[4] = {c[j].x, c[j].y, c[j].z, c[j].w}, g[4] = {w.x, w.y, w.z, w.w};
+            if (i >= cnv) break;  // a quad leaves together, as in norm_vec_kernel
             float y[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = bf16_lo(u[e]) * rstd * bf16_lo(g[e]);
-                y[2 * e + 1] = bf16_hi(u[e]) * rstd * bf16_hi(g[e]);
-            }
-            if (a.out) OutStore<uint16_t>::eight(a.out + at + chead + 8 * (long long)i, y);
-            if (FP8) {
-                uint16_t d[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = e4m3x2_sat(y[2 * e] * inv_scale, y[2 * e + 1] * inv_scale);
-                reinterpret_cast<uint2 *>(a.codes + at + chead)[i] =
-                    make_uint2((uint32_t)d[0] | ((uint32_t)d[1] << 16), (uint32_t)d[2] | ((uint32_t)d[3] << 16));
-            }
+            scaled(y, c[j], rstd, weights_at(sw, chead + 8 * i));
+            put8<QUANT>(a, at + chead + 8 * (long long)i, y, inv_scale);
         }
     }
 }
@@ -375,11 +401,14 @@ NormFn pick_vec(int v, bool warp, int threads) {
 }
 
 template <int QUANT>
+NormFn pick_shift(int v, bool xs) {
+    if (xs) return v == 1 ? norm_shift_kernel<QUANT, 1, true> : norm_shift_kernel<QUANT, 2, true>;
+    return v == 1 ? norm_shift_kernel<QUANT, 1, false> : norm_shift_kernel<QUANT, 2, false>;
+}
+
+template <int QUANT>
 NormFn pick_any(int n) {
-    return n == 4    ? norm_any_kernel<QUANT, 4>
-           : n == 8  ? norm_any_kernel<QUANT, 8>
-           : n == 16 ? norm_any_kernel<QUANT, 16>
-                     : norm_any_kernel<QUANT, 0>;
+    return n == 4 ? norm_any_kernel<QUANT, 4> : norm_any_kernel<QUANT, 0>;
 }
 
 }  // namespace
@@ -418,19 +447,19 @@ int launch_rmsnorm(const void *x, int64_t ldx, const void *residual, const void 
              : quant == BF16L_QUANT_FP8   ? pick_vec<BF16L_QUANT_FP8>(v, warp, threads)
              : quant == BF16L_QUANT_MXFP8 ? pick_vec<BF16L_QUANT_MXFP8>(v, warp, threads)
                                            : pick_vec<BF16L_QUANT_MXFP4>(v, warp, threads);
-    } else if (H % 8 != 0 && (ldx - H) % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && H >= 64 &&
-               H <= 16384 && (quant == BF16L_QUANT_NONE || quant == BF16L_QUANT_FP8)) {
-        const int nvec = H / 8, v = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+    } else if (H >= 64 && H <= 16384) {
+        const bool xs = (ldx - H) % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15u) != 0;
+        const int nvec = (H + 7) / 8, v = nvec <= (xs ? 1024 : 256) ? 1 : 2;
         threads = ((nvec + v - 1) / v + 31) / 32 * 32;
         blocks = rows;
         smem = ((size_t)(H + 1) / 2 + 2) * 4;
-        const bool fp8 = quant == BF16L_QUANT_FP8;
-        fn = v == 1   ? (fp8 ? norm_shift_kernel<true, 1> : norm_shift_kernel<false, 1>)
-             : v == 2 ? (fp8 ? norm_shift_kernel<true, 2> : norm_shift_kernel<false, 2>)
-                      : (fp8 ? norm_shift_kernel<true, 4> : norm_shift_kernel<false, 4>);
+        fn = quant == BF16L_QUANT_NONE    ? pick_shift<BF16L_QUANT_NONE>(v, xs)
+             : quant == BF16L_QUANT_FP8   ? pick_shift<BF16L_QUANT_FP8>(v, xs)
+             : quant == BF16L_QUANT_MXFP8 ? pick_shift<BF16L_QUANT_MXFP8>(v, xs)
+                                          : pick_shift<BF16L_QUANT_MXFP4>(v, xs);
     } else {
-        const int n = H <= 4 * 512 ? 4 : H <= 8 * 512 ? 8 : H <= 16 * 1024 ? 16 : 0;
-        threads = n ? ((H + n - 1) / n + 31) / 32 * 32 : 512;
+        const int n = H <= 64 ? 4 : 0;
+        threads = n ? 32 : 512;
         blocks = rows;
         fn = quant == BF16L_QUANT_NONE    ? pick_any<BF16L_QUANT_NONE>(n)
              : quant == BF16L_QUANT_FP8   ? pick_any<BF16L_QUANT_FP8>(n)

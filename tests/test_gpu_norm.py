@@ -68,7 +68,8 @@ def test_bf16(lib, rows, H, residual):
 
 
 @pytest.mark.parametrize("quant", ["fp8", "mxfp8", "mxfp4"])
-@pytest.mark.parametrize("rows,H,ld", [(1, 32, 32), (3, 96, 96), (7, 1536, 2112), (5, 2880, 2881), (16, 7168, 7168),
+@pytest.mark.parametrize("rows,H,ld", [(1, 32, 32), (3, 96, 96), (700, 7168, 7169), (300, 1536, 2113), (9, 64, 70),
+                                       (40, 16384, 16390), (3, 16416, 16417), (7, 1536, 2112), (5, 2880, 2881), (16, 7168, 7168),
                                        (2, 512, 515)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_quantised(lib, rows, H, ld, quant, residual):
@@ -83,7 +84,7 @@ def test_quantised(lib, rows, H, ld, quant, residual):
 
 
 @pytest.mark.parametrize("rows,H,ld", [(900, 188, 516), (5, 99, 107), (800, 2001, 2009), (3, 4099, 4099), (2000, 65, 65),
-                                       (5, 983, 1235)])
+                                       (5, 983, 1235), (900, 1501, 1800), (400, 7168, 7300), (3, 64, 67), (77, 8191, 8195)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_odd_rows_in_fp8(lib, rows, H, ld, residual):
     x, r, w = _inputs(rows, H, rows + H, ld=ld, residual=residual)
