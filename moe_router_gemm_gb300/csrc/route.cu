@@ -7,9 +7,9 @@
 // equal to +0, 0 for an expert that a group limit or an earlier pick took out).  A pick
 // is the largest of the lanes' largest keys (one warp reduction) and the first lane
 // that has it, which is the lowest expert as runs ascend; a lane keeps its two largest
-// keys, so it has to look through its run again only after two picks.  Groups that are
-// whole lanes, a power of two of them, are ranked by a butterfly and a count of the
-// better ones; others by reductions over masked keys.
+// keys, so it has to look through its run again only after two picks.  Each group has a
+// power of two of lanes to itself and is ranked by a butterfly and a count of the better
+// ones; groups too long for that (1023 experts in 3) by reductions over masked keys.
 //
 // About 1000 instructions a token of 256 experts in groups and 8 picks, a quarter of
 // them the exact exponentials and quotients of the scores: issue, not the 1 KB of
@@ -35,7 +35,9 @@ struct RouteArgs {
     int by_logit;     // the logits are the keys
     int vec;          // a lane's run of logits may be read four at a time
     int vec_bias;     // ... and of the bias
-    int group_lanes;  // lanes of a group, where that is a power of two; else 0
+    int group_lanes;  // lanes of a group, a power of two; 0 where there are none or a group's run would be too long
+    int lane_bits;    // log2 of it
+    int each, run;    // experts of a group, and of a lane within it
 };
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -66,31 +68,31 @@ template <int VPL>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, e0 = lane * VPL;
-    const int left = a.E - e0;  // experts from this lane's first on
+    const int lane = threadIdx.x & 31;
+    int e0 = lane * VPL, left = a.E - e0;  // this lane's first expert, and how many there are from it on
+    if (a.group_lanes > 0) {
+        const int g = lane >> a.lane_bits, at = (lane & (a.group_lanes - 1)) * a.run;
+        e0 = g * a.each + at;
+        left = g < a.groups ? min(a.run, a.each - at) : 0;
+    }
     const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long tok = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); tok < a.tokens; tok += warps) {
         const long long at = tok * a.ld;
         float l[VPL];
-        if (a.vec && left >= VPL) {  // four logits at a time
-            if (a.bf16) {
-                if constexpr (VPL % 4 == 0) {
+        if (VPL % 4 == 0 && a.vec) {  // four logits at a time
 #pragma unroll
-                    for (int j = 0; j < VPL / 4; ++j) {
-                        const uint16_t *p = static_cast<const uint16_t *>(a.logits) + at + e0 + 4 * j;
-                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-                        l[4 * j] = bf16_lo(v.x), l[4 * j + 1] = bf16_hi(v.x);
-                        l[4 * j + 2] = bf16_lo(v.y), l[4 * j + 3] = bf16_hi(v.y);
-                    }
-                }
-            } else {
-                if constexpr (VPL % 4 == 0) {
+            for (int j = 0; j + 4 <= VPL; j += 4) {
+                if (j + 4 > left) {
 #pragma unroll
-                    for (int j = 0; j < VPL / 4; ++j) {
-                        const float *p = static_cast<const float *>(a.logits) + at + e0 + 4 * j;
-                        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-                        l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
-                    }
+                    for (int i = j; i < j + 4; ++i) l[i] = i < left ? load_logit(a, at + e0 + i) : -INFINITY;
+                } else if (a.bf16) {
+                    const uint16_t *p = static_cast<const uint16_t *>(a.logits) + at + e0 + j;
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+                    l[j] = bf16_lo(v.x), l[j + 1] = bf16_hi(v.x), l[j + 2] = bf16_lo(v.y), l[j + 3] = bf16_hi(v.y);
+                } else {
+                    const float *p = static_cast<const float *>(a.logits) + at + e0 + j;
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+                    l[j] = v.x, l[j + 1] = v.y, l[j + 2] = v.z, l[j + 3] = v.w;
                 }
             }
         } else {
@@ -120,12 +122,16 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             float b[VPL];
 #pragma unroll
             for (int j = 0; j < VPL; ++j) b[j] = 0.0f;
-            if (a.bias && a.vec_bias && left >= VPL) {
-                if constexpr (VPL % 4 == 0) {
+            if (VPL % 4 == 0 && a.bias && a.vec_bias) {
 #pragma unroll
-                    for (int j = 0; j < VPL / 4; ++j) {
-                        const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0) + j);
-                        b[4 * j] = v.x, b[4 * j + 1] = v.y, b[4 * j + 2] = v.z, b[4 * j + 3] = v.w;
+                for (int j = 0; j + 4 <= VPL; j += 4) {
+                    if (j + 4 > left) {
+#pragma unroll
+                        for (int i = j; i < j + 4; ++i)
+                            if (i < left) b[i] = __ldg(a.bias + e0 + i);
+                    } else {
+                        const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0 + j));
+                        b[j] = v.x, b[j + 1] = v.y, b[j + 2] = v.z, b[j + 3] = v.w;
                     }
                 }
             } else if (a.bias) {
@@ -153,10 +159,10 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
                 m1 = max(m1, n1);
             }
             const uint32_t gkey = order_key(a.group_best == 1 ? key_value(m1) : key_value(m1) + key_value(m2));
-            const int mine = lane / a.group_lanes;
+            const int mine = lane >> a.lane_bits;
             int better = 0;
             for (int g = 0; g < a.groups; ++g) {
-                const uint32_t k = __shfl_sync(kAll, gkey, g * a.group_lanes);
+                const uint32_t k = __shfl_sync(kAll, gkey, g << a.lane_bits);
                 better += k > gkey || (k == gkey && g < mine);
             }
             if (better >= a.top_groups) {
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
                 for (int j = 0; j < VPL; ++j) key[j] = 0;
             }
         } else if (a.groups > 1) {
-            const int each = a.E / a.groups;
+            const int each = a.each;
             uint32_t gkey = 0;  // lane g: the key of group g
             for (int g = 0; g < a.groups; ++g) {
                 const int g0 = g * each - e0, g1 = g0 + each;
@@ -240,36 +246,38 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 int launch_route(const void *logits, int64_t ld, const float *bias, float *weights, int32_t *ids, int64_t tokens,
                  int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
                  int logits_bf16, int num_sms, uint32_t flags, void *stream) {
-    // The shortest run that reaches every expert (8192 x 384 takes 12.4 us with 12 to a lane, 19.8 with 16), or the next
-    // ones up to twice as long where groups are whole lanes with them only (8192 x 96 in 3 groups: 6.6 us with 4, 8.4
-    // with 3).
+    // Forms by the length of a lane's run, the shortest that is long enough (8192 x 384: 12 12.4 us, 16 19.8).
     static const struct {
         int vpl;
         void (*fn)(const RouteArgs);
     } kForms[] = {{1, route_kernel<1>},   {2, route_kernel<2>},   {3, route_kernel<3>},   {4, route_kernel<4>},
                   {6, route_kernel<6>},   {8, route_kernel<8>},   {12, route_kernel<12>}, {16, route_kernel<16>},
                   {24, route_kernel<24>}, {32, route_kernel<32>}};
-    int form = 0;
-    while (32 * kForms[form].vpl < experts) ++form;
+    // Each group has a power of two of lanes, unless its runs would be longer than a lane can hold: 7175 x 240 in 16
+    // groups 13.6 us (by reductions over masked keys 38.9), 7642 x 272 in 8 12.1 (34.4).
     const int each = experts / groups;
-    auto lanes_of = [&](int v) {  // lanes of a group, where that is a power of two; else 0
-        const int n = each / v;
-        return groups > 1 && each % v == 0 && (n & (n - 1)) == 0 ? n : 0;
-    };
-    if (groups > 1)
-        for (int f = form; f < 10 && kForms[f].vpl <= 2 * kForms[form].vpl; ++f)
-            if (lanes_of(kForms[f].vpl)) {
-                form = f;
-                break;
-            }
+    int group_lanes = 0, lane_bits = 0, run = 0;
+    if (groups > 1) {
+        while (2 * groups << lane_bits <= 32) ++lane_bits;
+        group_lanes = 1 << lane_bits;
+        run = (each + group_lanes - 1) / group_lanes;
+        if (each % 4 == 0 && run > 3) run = (run + 3) / 4 * 4;  // four at a time
+        if (run > 32) group_lanes = 0;
+    }
+    int form = 0;
+    while (kForms[form].vpl < (group_lanes ? run : (experts + 31) / 32)) ++form;
     const int vpl = kForms[form].vpl;
+    const bool fours = vpl % 4 == 0 && (group_lanes == 0 || (each % 4 == 0 && run % 4 == 0));
     const uintptr_t bytes = logits_bf16 ? 8 : 16;  // four logits
     RouteArgs a = {logits, bias,       weights,    ids,     tokens, ld,          experts, k,
                    groups, top_groups, group_best, softmax, renorm, logits_bf16, scale};
     a.by_logit = softmax && !bias && group_best == 1;
-    a.vec = vpl % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % bytes == 0;
-    a.vec_bias = vpl % 4 == 0 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
-    a.group_lanes = lanes_of(vpl);
+    a.vec = fours && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % bytes == 0;
+    a.vec_bias = fours && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
+    a.group_lanes = group_lanes;
+    a.lane_bits = lane_bits;
+    a.each = each;
+    a.run = run;
     auto fn = kForms[form].fn;
     const int threads = 128;
     const long long blocks = (tokens + 3) / 4, cap = 16LL * num_sms;

@@ -82,6 +82,18 @@ def test_groups(lib, T, E, k, groups, top, scoring, best):
            exact_ids=scoring == "softmax" and best == 1)
 
 
+@pytest.mark.parametrize("scoring,best", [("softmax", 1), ("sigmoid", 2)])
+@pytest.mark.parametrize("T,E,k,groups,top", [(50, 240, 14, 16, 9), (7, 336, 10, 16, 1), (9, 272, 4, 8, 5), (6, 288, 11, 8, 1),
+                                              (5, 382, 8, 2, 1), (8, 300, 8, 12, 4), (4, 1023, 9, 3, 2), (3, 1000, 9, 20, 7),
+                                              (9, 34, 3, 17, 4), (5, 62, 30, 31, 29), (3, 1023, 31, 31, 30), (6, 40, 6, 4, 3)])
+@pytest.mark.parametrize("dtype,pad", [(torch.float32, 0), (torch.bfloat16, 4), (torch.float32, 1)])
+def test_groups_of_any_size(lib, T, E, k, groups, top, scoring, best, dtype, pad):
+    g = torch.Generator().manual_seed(E + groups)
+    bias = (0.2 * torch.randn(E, generator=g)).to(DEV) if scoring == "sigmoid" else None
+    _check(lib, _logits(T, E, E + T, dtype, ld=E + pad), k, scoring=scoring, bias=bias, groups=groups, top_groups=top,
+           group_best=best, exact_ids=scoring == "softmax" and best == 1)
+
+
 def test_ties_go_to_the_lowest_index(lib):
     g = torch.Generator().manual_seed(0)
     for E, groups, top in [(256, 1, 1), (256, 8, 3), (100, 1, 1), (60, 5, 2), (1024, 1, 1)]:
