@@ -17,9 +17,14 @@
 //     share columns 128-255, which the epilogue empties first, so the next tile's
 //     MMAs start when half of this one is out; four scale slots of 32 columns (x words
 //     at 0 and 8, W words at 16 and 24: every address a multiple of 8) from 384;
-//   * epilogue: 32 x 32 pieces through shared memory and TMA stores (N % 8 == 0); each
+//   * epilogue, N % 8 == 0: 32 x 32 pieces through shared memory and TMA stores (each
 //     lane storing its own row's 16-byte pieces takes a line per lane and held
-//     8192 x 7168 x 7168 at 174 us;
+//     8192 x 7168 x 7168 at 174 us).  Other N, whose rows start on no 16-byte boundary:
+//     rows of 64 columns through shared memory, a warp's store taking whole rows.
+//     6152 x N x 32: N = 12064 42 us; 12060 (8-byte stores) 53, 12062 (4-byte) 56, 12061
+//     70, where a lane storing its own row took 680.  Rows shifted in shared memory to
+//     their place in out's 16-byte lines, 16-byte stores and the rest by elements: 84, 85
+//     and 89: the shifts and single elements cost more instructions than they save;
 //   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
 //
 // Measured and not taken (8192 x 7168 x 7168): arrivals released at cluster scope (they
@@ -51,13 +56,15 @@ constexpr int kSlots = 4, kSlotCols = 32;
 constexpr int kSfCol = 512 - kSlots * kSlotCols;  // the scale slots' first column
 constexpr int kAcc1Col = kSfCol - kTileRows;      // the second accumulator's first column
 constexpr int kShared = kTileRows - kAcc1Col;     // columns that the accumulators share
-static_assert(kShared % 64 == 0, "the epilogue empties 64 columns at a time");
+static_assert(kShared == 128, "the epilogue empties 128 columns first");
 constexpr int kEpiWarps = 8, kScaleWarps = 4;
+constexpr int kPitch = 144;  // bytes of a shifted row of 64 columns: nine units; eight neighbouring rows' never collide
+constexpr int kPieceBytes = 2560;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 
 struct PairShared {
-    // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first, so aligned)
-    uint8_t piece[kEpiWarps][32 * 64];
+    // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first, so aligned), or 16 rows of kPitch bytes
+    uint8_t piece[kEpiWarps][kPieceBytes];
     uint4 scales[2][kTileRows];
     uint64_t full[kStages];    // leader only: both CTAs' codes and scales of the stage are in shared memory
     uint64_t empty[kStages];   // both: the MMAs (and copies) reading the stage are done
@@ -76,7 +83,57 @@ __device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int
     q0 = qi * kTileRows;
 }
 
-template <int W>
+// 32 rows (one a lane) x 64 columns (p) to rows of out that start on no 16-byte boundary: sixteen rows at a time
+// through shared memory, then T at a time, a store taking whole rows.  N, and so `cols` (64, or what is left of out), is a
+// multiple of T's elements, or odd: then T is a word, every other row starts within one and goes to shared memory an
+// element further on, and single elements at a row's ends are stored by themselves.
+template <class T, bool ODD>
+__device__ __forceinline__ void store_rows(uint16_t *o, uint8_t *piece, const uint32_t (&p)[32], int rows, int cols,
+                                           int N, int lane) {
+    constexpr int lanes = 128 / sizeof(T), at_once = 32 / lanes, each = sizeof(T) / 2;  // lanes: of a row
+    const int s0 = ODD ? (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1 : 0;  // (row r: s0 ^ r & 1)
+    const bool mine = ODD && ((s0 ^ lane) & 1);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 && r0 < rows; r0 += 16, o += (size_t)16 * N) {
+        __syncwarp();  // the rows before have been read
+        if ((lane & 16) == r0) {
+            uint32_t *q = reinterpret_cast<uint32_t *>(piece + kPitch * (lane & 15));
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                uint32_t t[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    t[j] = mine ? __funnelshift_l(k + j > 0 ? p[k + j - 1] : 0u, p[k + j], 16) : p[k + j];
+                *reinterpret_cast<uint4 *>(q + k) = make_uint4(t[0], t[1], t[2], t[3]);
+            }
+            if (mine) q[32] = p[31] >> 16;
+        }
+        __syncwarp();
+        const int have = min(rows - r0, 16);
+        const int r1 = lane / lanes, u = lane % lanes;
+        const uint8_t *from = piece + kPitch * r1 + (int)sizeof(T) * u;
+        T v[16 / at_once];  // read before the first store, which they would have to wait for
+#pragma unroll
+        for (int i = 0; i < 16; i += at_once)
+            v[i / at_once] = *reinterpret_cast<const T *>(from + kPitch * i + 4 * ((s0 ^ i) & ODD));
+        // Odd N: what row lane / 2 has outside its words, its first element (even lanes) or its last (odd lanes).
+        const int er = lane >> 1, es = (s0 ^ er) & 1;
+        const int e = lane & 1 ? (es == (cols == 64) ? cols - 1 : -1) : es ? 0 : -1;
+        uint16_t edge = 0;
+        if (ODD && e >= 0) edge = *reinterpret_cast<const uint16_t *>(piece + kPitch * er + 2 * (e + es));
+        uint16_t *to = o + (size_t)r1 * N + each * u;
+#pragma unroll
+        for (int i = 0; i < 16; i += at_once, to += (size_t)at_once * N) {
+            const int sr = (s0 ^ i) & ODD;
+            if (i + r1 < have && sr + each * u + each <= cols) *reinterpret_cast<T *>(to + sr) = v[i / at_once];
+        }
+        if (ODD && er < have && e >= 0) o[(size_t)er * N + e] = edge;
+    }
+}
+
+// W: alignment of the scale rows.  ALIGNED: rows of out start on 16-byte boundaries (N % 8 == 0); a kernel of its own,
+// since the other rows' code costs it 2% (8192 x 7168 x 7168: 135.3 us, together 138.4).
+template <int W, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ xs,
@@ -214,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- epilogue: TMEM lane quarter = warp % 4; four 32-column slices each, the shared columns first ----
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int row = quarter * 32 + lane;
-        const bool by_tma = N % 8 == 0;  // rows of out start on 16-byte boundaries
         uint8_t *piece = sh.piece[warp - 2];
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t acc_shared = mapa_shared(smem_u32(&sh.acc_shared), 0);
@@ -225,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m = p0 + (int)rank * kHalf + row;
             const int second = tile & 1;
             // the first column of this warp's slice i: the shared columns (128-255 of the first accumulator,
-            // 0-127 of the second) come first
+            // 0-127 of the second) come first; slices 2i and 2i + 1 are neighbours
             auto column = [&](int i) {
-                const int c = 32 * (2 * i + half);  // 0, 64, 128, 192 (+ 32)
+                const int c = 128 * (i >> 1) + 64 * half + 32 * (i & 1);
                 return second ? c : (c + kAcc1Col) & 255;
             };
             float lb[4];  // the tile's bias, one value per lane and slice, read while the MMAs run
@@ -238,48 +294,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             // warp-uniform, so that the bias shuffles below run on all 32 lanes
             const bool have = __all_sync(0xFFFFFFFFu, ok && !*((volatile int32_t *)&sh.aborted));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = q0 + column(i);
-                float v[32];
-                if (have) {
-                    uint32_t r0[16], r1[16];
-                    const uint32_t at = lanes + (uint32_t)(second * kAcc1Col + column(i));
-                    tmem_ld16(at, r0);
-                    tmem_ld16(at + 16, r1);
-                    tmem_ld_wait16(r0);
-                    tmem_ld_wait16(r1);
+            for (int pair = 0; pair < 2; ++pair) {
+                uint32_t p[32];  // 64 columns of this lane's row, in bf16
+                const int n0 = q0 + column(2 * pair);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[j] = __uint_as_float(r0[j]);
-                        v[16 + j] = __uint_as_float(r1[j]);
+                for (int i = 0; i < 2; ++i) {
+                    float v[32];
+                    if (have) {
+                        uint32_t r0[16], r1[16];
+                        const uint32_t at = lanes + (uint32_t)(second * kAcc1Col + n0 - q0 + 32 * i);
+                        tmem_ld16(at, r0);
+                        tmem_ld16(at + 16, r1);
+                        tmem_ld_wait16(r0);
+                        tmem_ld_wait16(r1);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            v[j] = __uint_as_float(r0[j]);
+                            v[16 + j] = __uint_as_float(r1[j]);
+                        }
+                    }
+                    if (pair == 0 && i == 1) {  // the shared columns are out
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(acc_shared);
+                    }
+                    if (!have) continue;
+                    if (bias) bias_add32(v, pair ? lb[2 + i] : lb[i]);  // warp-uniform condition
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[16 * i + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    if (ALIGNED && n0 + 32 * i < N) {  // warp-uniform
+                        if (lane == 0) bulk_wait_read();  // the piece before has left shared memory
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
+                            *reinterpret_cast<uint4 *>(piece + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
+                                make_uint4(p[16 * i + 4 * j], p[16 * i + 4 * j + 1], p[16 * i + 4 * j + 2],
+                                           p[16 * i + 4 * j + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        // (rows and columns past the end are cut off)
+                        if (lane == 0 && m < M) tma_store_2d(&tm_out, piece, n0 + 32 * i, m);
                     }
                 }
-                if (i == kShared / 64 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(acc_shared);
-                }
-                if (!have) continue;
-                if (bias) bias_add32(v, lb[i]);  // warp-uniform condition
-                if (by_tma) {
-                    if (n >= N) continue;  // warp-uniform
-                    if (lane == 0) bulk_wait_read();  // the piece before has left shared memory
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
-                        *reinterpret_cast<uint4 *>(piece + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
-                            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                       pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    // (rows and columns past the end are cut off)
-                    if (lane == 0 && m < M) tma_store_2d(&tm_out, piece, n, m);
-                } else if (m < M && n < N) {
-                    uint16_t *o = out + (size_t)m * N + n;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (n + j < N) OutStore<uint16_t>::one(o + j, v[j]);
+                if (!ALIGNED && have && n0 < N) {
+                    uint16_t *o = out + (size_t)(m - lane) * N + n0;
+                    const int rows = M - (m - lane), cols = min(N - n0, 64);
+                    if (N % 4 == 0)
+                        store_rows<uint2, false>(o, piece, p, rows, cols, N, lane);
+                    else if (N % 2 == 0)
+                        store_rows<uint32_t, false>(o, piece, p, rows, cols, N, lane);
+                    else
+                        store_rows<uint32_t, true>(o, piece, p, rows, cols, N, lane);
                 }
             }
             tc_fence_before();
@@ -392,12 +457,15 @@ static_assert(smem_bytes() > 116 * 1024, "one CTA per SM: each allocates all 512
 using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *,
                         const uint16_t *, uint16_t *, int, int, int, int32_t *);
 
-PairFn pick_pair(uintptr_t align) {
-    return align % 16 == 0  ? mxfp4_pair_kernel<16>
-           : align % 8 == 0 ? mxfp4_pair_kernel<8>
-           : align % 4 == 0 ? mxfp4_pair_kernel<4>
-                            : mxfp4_pair_kernel<1>;
+template <bool ALIGNED>
+PairFn pick_w(uintptr_t align) {
+    return align % 16 == 0  ? mxfp4_pair_kernel<16, ALIGNED>
+           : align % 8 == 0 ? mxfp4_pair_kernel<8, ALIGNED>
+           : align % 4 == 0 ? mxfp4_pair_kernel<4, ALIGNED>
+                            : mxfp4_pair_kernel<1, ALIGNED>;
 }
+
+PairFn pick_pair(uintptr_t align, bool aligned) { return aligned ? pick_w<true>(align) : pick_w<false>(align); }
 
 cudaLaunchConfig_t pair_config(int clusters, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
@@ -419,11 +487,12 @@ cudaLaunchConfig_t pair_config(int clusters, uint32_t flags, void *stream, cudaL
 }  // namespace
 
 int init_mxfp4_pair() {
-    for (uintptr_t a : {16, 8, 4, 1}) {
-        const int e =
-            (int)cudaFuncSetAttribute(pick_pair(a), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes());
-        if (e) return e;
-    }
+    for (uintptr_t a : {16, 8, 4, 1})
+        for (bool aligned : {false, true}) {
+            const int e = (int)cudaFuncSetAttribute(pick_pair(a, aligned), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    smem_bytes());
+            if (e) return e;
+        }
     int dev = 0;
     const int e = (int)cudaGetDevice(&dev);
     if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
@@ -432,7 +501,7 @@ int init_mxfp4_pair() {
     cfg.numAttrs = 1;
     int n = 0;
     // A failed query only loses the clamp (launches then use half the SMs' number).
-    if (cudaOccupancyMaxActiveClusters(&n, pick_pair(16), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, pick_pair(16, true), &cfg) != cudaSuccess) {
         n = 0;
         (void)cudaGetLastError();
     }
@@ -472,7 +541,7 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = pair_config((int)clusters, flags, stream, attr);
     const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
-    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a), tx, tw, to, static_cast<const uint8_t *>(xs),
+    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a, N % 8 == 0), tx, tw, to, static_cast<const uint8_t *>(xs),
                                    static_cast<const uint8_t *>(ws), static_cast<const uint16_t *>(bias),
                                    static_cast<uint16_t *>(out), M, N, K, status);
 }

@@ -236,3 +236,16 @@ def test_empty_and_refusals(lib):
         with pytest.raises(lib.BF16LinearError) as e:
             lib.bf16_linear_mxfp4_dynamic(big, wq, ws, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
         assert e.value.status == -1
+
+
+@pytest.mark.parametrize("N", [2049, 2050, 2051, 2052, 2053, 2054, 2055, 2079, 2337])
+@pytest.mark.parametrize("M,K", [(1300, 32), (1025, 544)])
+def test_linear_rows_off_16_byte_boundaries(lib, M, N, K):
+    """Every place of a row of out in its 16-byte line, ragged last rows and columns, and nothing written outside."""
+    x, wq, ws, b = _operands(M, N, K, M + N, True)
+    xq, xs = lib.quant_mxfp4(x)
+    whole = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+    got = lib.bf16_linear_mxfp4(xq, xs, wq, ws, b, out=whole[32:32 + M * N].view(M, N))
+    xv, wv = ref.values_mxfp4(xq.cpu().numpy(), xs.cpu().numpy()), ref.values_mxfp4(wq.cpu().numpy(), ws.cpu().numpy())
+    ref.check_linear(got, xv, wv, ref.f64(b), K, f"{M} {N} {K}")
+    assert bool((whole[:32] == 7).all()) and bool((whole[32 + M * N:] == 7).all())
