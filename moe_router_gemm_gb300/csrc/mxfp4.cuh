@@ -142,18 +142,44 @@ __device__ __forceinline__ void scale_words(uint32_t (&w)[NW], const uint8_t *ro
     }
 }
 template <int W>
-__device__ __forceinline__ uint4 scale_bytes16(const uint8_t *row, int b, int nb, bool in, const uint8_t *lo,
-                                               const uint8_t *hi) {
-    uint32_t w[4];
-    scale_words<W, 4>(w, row, b, nb, in, lo, hi);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <int W>
 __device__ __forceinline__ uint2 scale_bytes8(const uint8_t *row, int b, int nb, bool in, const uint8_t *lo,
                                               const uint8_t *hi) {
     uint32_t w[2];
     scale_words<W, 2>(w, row, b, nb, in, lo, hi);
     return make_uint2(w[0], w[1]);
+}
+
+// Asks for the 16-byte block at p (16-byte aligned) in shared memory at `to`, of which only the part inside [lo, hi) is
+// read.  The array's first block, where it starts within one, is there on return.
+__device__ __forceinline__ void copy_block(uint4 *to, const uint8_t *p, const uint8_t *lo, const uint8_t *hi) {
+    if (p >= lo) {
+        const long long left = hi - p;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(p),
+                     "r"(left < 16 ? (int)left : 16)
+                     : "memory");
+        return;
+    }
+#pragma unroll 1
+    for (int i = (int)(lo - p); i < 16 && p + i < hi; ++i) reinterpret_cast<uint8_t *>(to)[i] = __ldg(p + i);
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's newest N groups of copies are complete.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sixteen bytes from byte m (below 16) of two neighbouring blocks on.
+__device__ __forceinline__ uint4 shift_blocks(const uint4 &a, const uint4 &b, int m) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t[7], v[5];  // words (m / 4) & 1 on, then m / 4 on
+#pragma unroll
+    for (int k = 0; k < 7; ++k) t[k] = m & 4 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) v[k] = m & 8 ? t[k + 2] : t[k];
+    const int s = 8 * (m & 3);
+    return make_uint4(__funnelshift_r(v[0], v[1], s), __funnelshift_r(v[1], v[2], s), __funnelshift_r(v[2], v[3], s),
+                      __funnelshift_r(v[3], v[4], s));
 }
 
 // Arrive on an mbarrier of a CTA of the cluster, ordering this thread's earlier

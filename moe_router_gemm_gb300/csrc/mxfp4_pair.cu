@@ -10,9 +10,13 @@
 //   * scales: thread i of the scale warps reads 16 scale bytes (two chunks) of x row
 //     i and of W rows i and i + 128 of the tile, two steps ahead.  The W bytes go
 //     through shared memory, since every TMEM lane quarter needs all 256 rows'; each
-//     warp writes its quarter of a chunk's slot with tcgen05.st.  Reading each row
-//     once per CTA, 16 bytes at a time, matters: a row's bytes are a cache line of
-//     their own;
+//     warp writes its quarter of a step's two slots with tcgen05.st (one wait and one
+//     arrival for both: 8192 x 7168 x 7168 135.3 us a chunk at a time, 133 so).  Reading
+//     each row once per CTA, 16 bytes at a time, matters: a row's bytes are a cache line
+//     of their own.  Rows that do not start on 16-byte boundaries (K % 512) go by
+//     cp.async, whole blocks, and are shifted on the way out of shared memory: 8192 x
+//     7168 x 2880 81 us, x 6176 158 (117 and 259 by words from the row's first byte on;
+//     blocks in registers 87 and 170, which are too few to keep loads in flight);
 //   * TMEM: accumulators at columns 0 and 128, 256 columns each, taken in turn: they
 //     share columns 128-255, which the epilogue empties first, so the next tile's
 //     MMAs start when half of this one is out; four scale slots of 32 columns (x words
@@ -49,7 +53,8 @@ constexpr int kTileRows = 256;              // x rows, and W rows, of a pair til
 constexpr int kChunkBytes = 128;            // code bytes of a row per chunk (256 codes)
 constexpr int kHalfBytes = kHalf * kChunkBytes;
 constexpr int kStageBytes = 2 * kHalfBytes;
-constexpr int kStages = 6;
+constexpr int kStages = 6;  // (five where scale rows are shifted: the memory of their blocks)
+constexpr int kRaw = 4;     // blocks of a shifted scale row in shared memory
 // W tiles of a raster group: 8192 x 7168 x 7168 takes 135.6 us with 4, 136.7 with 2, 138 with 8
 constexpr int kGroup = 4;
 constexpr int kSlots = 4, kSlotCols = 32;
@@ -62,10 +67,13 @@ constexpr int kPitch = 144;  // bytes of a shifted row of 64 columns: nine units
 constexpr int kPieceBytes = 2560;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 
+template <bool SHIFTED>
 struct PairShared {
+    static constexpr int kStages = SHIFTED ? bf16l::kStages - 1 : bf16l::kStages;
     // an epilogue warp's 32 rows x 32 columns in bf16, 64-byte swizzle (first, so aligned), or 16 rows of kPitch bytes
     uint8_t piece[kEpiWarps][kPieceBytes];
     uint4 scales[2][kTileRows];
+    uint4 raw[SHIFTED ? kRaw : 1][SHIFTED ? 3 : 1][kHalf];  // blocks of each scale thread's x row and two W rows
     uint64_t full[kStages];    // leader only: both CTAs' codes and scales of the stage are in shared memory
     uint64_t empty[kStages];   // both: the MMAs (and copies) reading the stage are done
     uint64_t acc_full[2];      // both: accumulator holds a finished tile
@@ -84,9 +92,9 @@ __device__ __forceinline__ void pair_coords(int u, int p_tiles, int q_tiles, int
 }
 
 // 32 rows (one a lane) x 64 columns (p) to rows of out that start on no 16-byte boundary: sixteen rows at a time
-// through shared memory, then T at a time, a store taking whole rows.  N, and so `cols` (64, or what is left of out), is a
-// multiple of T's elements, or odd: then T is a word, every other row starts within one and goes to shared memory an
-// element further on, and single elements at a row's ends are stored by themselves.
+// through shared memory, then T at a time, a store taking whole rows.  N, and so `cols` (64, or what is left of out),
+// is a multiple of T's elements, or odd: then T is a word, every other row starts within one and goes to shared memory
+// an element further on, and single elements at a row's ends are stored by themselves.
 template <class T, bool ODD>
 __device__ __forceinline__ void store_rows(uint16_t *o, uint8_t *piece, const uint32_t (&p)[32], int rows, int cols,
                                            int N, int lane) {
@@ -131,18 +139,21 @@ __device__ __forceinline__ void store_rows(uint16_t *o, uint8_t *piece, const ui
     }
 }
 
-// W: alignment of the scale rows.  ALIGNED: rows of out start on 16-byte boundaries (N % 8 == 0); a kernel of its own,
-// since the other rows' code costs it 2% (8192 x 7168 x 7168: 135.3 us, together 138.4).
-template <int W, bool ALIGNED>
+// SHIFTED: scale rows do not all start on 16-byte boundaries (K % 512, or the tensors' start).  ALIGNED: rows of out do
+// (N % 8 == 0); a kernel of its own, since the other rows' code costs it 2% (8192 x 7168 x 7168: 135.3 us, together
+// 138.4).
+template <bool SHIFTED, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ xs,
                       const uint8_t *__restrict__ ws, const uint16_t *__restrict__ bias, uint16_t *__restrict__ out,
                       int M, int N, int K, int32_t *status) {
+    using Shared = PairShared<SHIFTED>;
+    constexpr int kStages = Shared::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    PairShared &sh = *reinterpret_cast<PairShared *>(ring + kStages * kStageBytes);
+    Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStageBytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
@@ -370,63 +381,95 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ia = ra < M, ib0 = rb0 < N, ib1 = rb1 < N;
             const uint8_t *pa = xs + (size_t)(ia ? ra : 0) * nb, *pb0 = ws + (size_t)(ib0 ? rb0 : 0) * nb,
                           *pb1 = ws + (size_t)(ib1 ? rb1 : 0) * nb;
-            constexpr int PD = 2;
-            uint4 va[PD], vb0[PD], vb1[PD];
+            // !SHIFTED: the 16-byte blocks of the next two steps, in registers
+            const uint4 one = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            auto block = [&](const uint8_t *p, int k, bool in) {
+                return in && 16 * k < nb ? __ldg(reinterpret_cast<const uint4 *>(p) + k) : one;
+            };
+            uint4 va[2], vb0[2], vb1[2];
+            // SHIFTED: block k, counted from the 16-byte boundary before the row, on its way to shared memory.  A
+            // step's bytes lie across two blocks; the three after its first are asked for before it starts.
+            const int ma = (int)(reinterpret_cast<uintptr_t>(pa) & 15u), na = ia ? nb : 0;
+            const int mb0 = (int)(reinterpret_cast<uintptr_t>(pb0) & 15u), nb0 = ib0 ? nb : 0;
+            const int mb1 = (int)(reinterpret_cast<uintptr_t>(pb1) & 15u), nb1 = ib1 ? nb : 0;
+            auto ask = [&](int k) {
+                uint4(*to)[kHalf] = sh.raw[k % kRaw];
+                if (16 * k - ma < na) copy_block(&to[0][st], pa - ma + 16 * k, xlo, xhi);
+                if (16 * k - mb0 < nb0) copy_block(&to[1][st], pb0 - mb0 + 16 * k, wlo, whi);
+                if (16 * k - mb1 < nb1) copy_block(&to[2][st], pb1 - mb1 + 16 * k, wlo, whi);
+                cp_async_commit();
+            };
+            auto take = [&](int r, int m, int n, int s) {  // the bytes of step s, 1.0 from byte n of the row on
+                const uint4 q = shift_blocks(sh.raw[s % kRaw][r][st], sh.raw[(s + 1) % kRaw][r][st], m);
+                if (16 * s + 16 <= n) return q;
+                uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int d = 0; d < PD; ++d) {
-                va[d] = scale_bytes16<W>(pa, 16 * d, nb, ia, xlo, xhi);
-                vb0[d] = scale_bytes16<W>(pb0, 16 * d, nb, ib0, wlo, whi);
-                vb1[d] = scale_bytes16<W>(pb1, 16 * d, nb, ib1, wlo, whi);
+                for (int j = 0; j < 4; ++j) {
+                    const int left = n - 16 * s - 4 * j;  // valid bytes of this word
+                    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                    w[j] = (w[j] & keep) | (0x7F7F7F7Fu & ~keep);
+                }
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            if constexpr (SHIFTED) {
+                for (int k = 0; k < kRaw - 1; ++k) ask(k);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                    va[d] = block(pa, d, ia), vb0[d] = block(pb0, d, ib0), vb1[d] = block(pb1, d, ib1);
             }
             // A warp that gave up goes on through the barriers, so that no other one waits for it there.
             for (int s2 = 0; s2 < D; ++s2, ++step) {
-                const uint4 a = va[0];
-                uint4 *buf = sh.scales[step & 1];
-                buf[st] = vb0[0];
-                buf[kHalf + st] = vb1[0];
-#pragma unroll
-                for (int d = 0; d + 1 < PD; ++d) va[d] = va[d + 1], vb0[d] = vb0[d + 1], vb1[d] = vb1[d + 1];
-                va[PD - 1] = scale_bytes16<W>(pa, 16 * (s2 + PD), nb, ia, xlo, xhi);
-                vb0[PD - 1] = scale_bytes16<W>(pb0, 16 * (s2 + PD), nb, ib0, wlo, whi);
-                vb1[PD - 1] = scale_bytes16<W>(pb1, 16 * (s2 + PD), nb, ib1, wlo, whi);
+                uint4 *buf = sh.scales[step & 1], a;
+                if constexpr (SHIFTED) {
+                    ask(s2 + kRaw - 1);
+                    cp_async_wait<kRaw - 2>();  // block s2 + 1 and those before it are there
+                    a = take(0, ma, na, s2);
+                    buf[st] = take(1, mb0, nb0, s2);
+                    buf[kHalf + st] = take(2, mb1, nb1, s2);
+                } else {
+                    a = va[0];
+                    buf[st] = vb0[0];
+                    buf[kHalf + st] = vb1[0];
+                    va[0] = va[1], vb0[0] = vb0[1], vb1[0] = vb1[1];
+                    va[1] = block(pa, s2 + 2, ia), vb0[1] = block(pb0, s2 + 2, ib0), vb1[1] = block(pb1, s2 + 2, ib1);
+                }
                 // the buffer is whole; its last readers are past the barrier of the step before
                 named_barrier(1, 32 * kScaleWarps);
-                uint4 wb[8];
+                if (stop) continue;
+                const int n = C - 2 * s2 < 2 ? 1 : 2;  // the step's chunks
+                // their slots are free when the MMAs of the chunk kSlots before the last of them are done
+                const int old = it + n - 1 - kSlots;
+                if (old >= 0 && !mbar_wait(&sh.empty[old % kStages], (old / kStages) & 1, status, kSiteScale))
+                    stop = true;
+                if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
+                    atomicExch(&sh.aborted, 1);
+                    stop = true;
+                    continue;
+                }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) wb[j] = buf[32 * j + lane];
+                for (int h = 0; h < 2; ++h) {
+                    if (h == n) break;
+                    uint2 wb[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // the step's two chunks
-                    if (stop || 2 * s2 + h >= C) break;
-                    // the slot is free when the MMAs of the chunk kSlots before are done
-                    const int old = it - kSlots;
-                    if (old >= 0 && !mbar_wait(&sh.empty[old % kStages], (old / kStages) & 1, status, kSiteScale))
-                        stop = true;
-                    if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
-                        atomicExch(&sh.aborted, 1);
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t sf = slot0 + (uint32_t)(kSlotCols * (it % kSlots));
+                    for (int j = 0; j < 8; ++j) wb[j] = reinterpret_cast<const uint2 *>(&buf[32 * j + lane])[h];
+                    const uint32_t sf = slot0 + (uint32_t)(kSlotCols * ((it + h) % kSlots));
                     const uint32_t a0 = h ? a.z : a.x, a1 = h ? a.w : a.y;
                     tmem_st4(sf, a0, a0, a0, a0);  // column `quarter` of the four is the one read
                     tmem_st4(sf + 8, a1, a1, a1, a1);
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
-                        if (h) {
-                            tmem_st4(sf + 16 + j, wb[j].z, wb[j + 1].z, wb[j + 2].z, wb[j + 3].z);
-                            tmem_st4(sf + 24 + j, wb[j].w, wb[j + 1].w, wb[j + 2].w, wb[j + 3].w);
-                        } else {
-                            tmem_st4(sf + 16 + j, wb[j].x, wb[j + 1].x, wb[j + 2].x, wb[j + 3].x);
-                            tmem_st4(sf + 24 + j, wb[j].y, wb[j + 1].y, wb[j + 2].y, wb[j + 3].y);
-                        }
+                        tmem_st4(sf + 16 + j, wb[j].x, wb[j + 1].x, wb[j + 2].x, wb[j + 3].x);
+                        tmem_st4(sf + 24 + j, wb[j].y, wb[j + 1].y, wb[j + 2].y, wb[j + 3].y);
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)((it % kStages) * sizeof(uint64_t)));
-                    ++it;
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane < n) mbar_arrive_remote(full0 + (uint32_t)(((it + lane) % kStages) * sizeof(uint64_t)));
+                it += n;
             }
+            if (SHIFTED) cp_async_wait<0>();  // the next tile's blocks go to the same places
         }
         __syncwarp();
     }
@@ -450,28 +493,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMaxDevices = 64;
 int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
 
-constexpr int smem_bytes() { return 1024 + kStages * kStageBytes + (int)sizeof(PairShared); }
-static_assert(smem_bytes() <= 232448, "shared memory");
-static_assert(smem_bytes() > 116 * 1024, "one CTA per SM: each allocates all 512 TMEM columns");
+template <bool SHIFTED>
+constexpr int smem_bytes() {
+    return 1024 + PairShared<SHIFTED>::kStages * kStageBytes + (int)sizeof(PairShared<SHIFTED>);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory");
+static_assert(smem_bytes<false>() > 116 * 1024 && smem_bytes<true>() > 116 * 1024,
+              "one CTA per SM: each allocates all 512 TMEM columns");
+int smem_of(bool shifted) { return shifted ? smem_bytes<true>() : smem_bytes<false>(); }
 
 using PairFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const uint8_t *, const uint8_t *,
                         const uint16_t *, uint16_t *, int, int, int, int32_t *);
 
-template <bool ALIGNED>
-PairFn pick_w(uintptr_t align) {
-    return align % 16 == 0  ? mxfp4_pair_kernel<16, ALIGNED>
-           : align % 8 == 0 ? mxfp4_pair_kernel<8, ALIGNED>
-           : align % 4 == 0 ? mxfp4_pair_kernel<4, ALIGNED>
-                            : mxfp4_pair_kernel<1, ALIGNED>;
+PairFn pick_pair(bool shifted, bool aligned) {
+    if (shifted) return aligned ? mxfp4_pair_kernel<true, true> : mxfp4_pair_kernel<true, false>;
+    return aligned ? mxfp4_pair_kernel<false, true> : mxfp4_pair_kernel<false, false>;
 }
 
-PairFn pick_pair(uintptr_t align, bool aligned) { return aligned ? pick_w<true>(align) : pick_w<false>(align); }
-
-cudaLaunchConfig_t pair_config(int clusters, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t pair_config(int clusters, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem_bytes();
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = (cudaStream_t)stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -487,21 +530,21 @@ cudaLaunchConfig_t pair_config(int clusters, uint32_t flags, void *stream, cudaL
 }  // namespace
 
 int init_mxfp4_pair() {
-    for (uintptr_t a : {16, 8, 4, 1})
+    for (bool shifted : {false, true})
         for (bool aligned : {false, true}) {
-            const int e = (int)cudaFuncSetAttribute(pick_pair(a, aligned), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    smem_bytes());
+            const int e = (int)cudaFuncSetAttribute(pick_pair(shifted, aligned),
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(shifted));
             if (e) return e;
         }
     int dev = 0;
     const int e = (int)cudaGetDevice(&dev);
     if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config(kGb300Sms, 0, nullptr, attr);
+    cudaLaunchConfig_t cfg = pair_config(kGb300Sms, smem_of(false), 0, nullptr, attr);
     cfg.numAttrs = 1;
     int n = 0;
     // A failed query only loses the clamp (launches then use half the SMs' number).
-    if (cudaOccupancyMaxActiveClusters(&n, pick_pair(16, true), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, pick_pair(false, true), &cfg) != cudaSuccess) {
         n = 0;
         (void)cudaGetLastError();
     }
@@ -538,10 +581,11 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
         (long long)((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
     long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
     if (units < clusters) clusters = units;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = pair_config((int)clusters, flags, stream, attr);
     const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
-    return (int)cudaLaunchKernelEx(&cfg, pick_pair(a, N % 8 == 0), tx, tw, to, static_cast<const uint8_t *>(xs),
+    const bool shifted = a % 16 != 0;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = pair_config((int)clusters, smem_of(shifted), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick_pair(shifted, N % 8 == 0), tx, tw, to, static_cast<const uint8_t *>(xs),
                                    static_cast<const uint8_t *>(ws), static_cast<const uint16_t *>(bias),
                                    static_cast<uint16_t *>(out), M, N, K, status);
 }

@@ -249,3 +249,22 @@ def test_linear_rows_off_16_byte_boundaries(lib, M, N, K):
     xv, wv = ref.values_mxfp4(xq.cpu().numpy(), xs.cpu().numpy()), ref.values_mxfp4(wq.cpu().numpy(), ws.cpu().numpy())
     ref.check_linear(got, xv, wv, ref.f64(b), K, f"{M} {N} {K}")
     assert bool((whole[:32] == 7).all()) and bool((whole[32 + M * N:] == 7).all())
+
+
+@pytest.mark.parametrize("M,N", [(1281, 1283), (40, 300), (5, 300)])
+@pytest.mark.parametrize("blocks,off", [(97, 0), (98, 1), (99, 2), (100, 4), (101, 7), (102, 8), (104, 8), (107, 15), (96, 5), (111, 3),
+                                        (17, 9), (1, 1)])
+def test_linear_scale_rows_off_16_byte_boundaries(lib, M, N, blocks, off):
+    """Scale rows at every place in their 16-byte lines, between bytes that read as NaN, random codes and scales."""
+    K = 32 * blocks
+    rng = np.random.default_rng(M + blocks)
+    xq, wq = (rng.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    xs, ws = (rng.integers(110, 145, (r, blocks)).astype(np.uint8) for r in (M, N))
+
+    def between(s):
+        whole = torch.full((s.size + 64,), 255, dtype=torch.uint8, device=DEV)
+        part = whole[off:off + s.size].view(s.shape)
+        part.copy_(_u8(s))
+        return part
+    got = lib.bf16_linear_mxfp4(_u8(xq), between(xs), _u8(wq), between(ws))
+    ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K)
