@@ -172,7 +172,7 @@ extern "C" int bf16_linear_mxfp4(const void *xq, const void *xs, const void *wq,
     // Few tokens, or few tiles for their K: the split form.  512 x 2112 x 7168: split 14.4 us, pairs 15.4; 1024 x 2112 x
     // 7168: 21.9 and 15.1; 1000 x 256 x 7168: 8.0 and 13.7; 128 x 14336 x 4096: 15.3 and 11.3.
     if (M > 16 &&
-        mxfp4_pair_estimate(M, N, K, dev.num_sms) < mxfp4_split_plan(M, N, K, dev.num_sms).estimate)
+        mxfp4_pair_estimate(M, N, K, dev.num_sms) < mxfp4_split_plan(M, N, K, dev.num_sms, false).estimate)
         return result(launch_mxfp4_pair(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
     return result(launch_mxfp4_split(xq, xs, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
 }

@@ -21,7 +21,7 @@ struct Mxfp4SplitPlan {
     int tokens, m_tiles, split, stages, smem;  // tokens and token tiles, CTAs along K, ring depth, dynamic shared memory
     float estimate;                            // microseconds beside the fixed part, roughly
 };
-Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms);
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms, bool shifted);
 bool mxfp4_split_quantises(int M, int N, int K);
 int init_mxfp4_split();
 int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,

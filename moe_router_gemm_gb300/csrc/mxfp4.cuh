@@ -93,62 +93,6 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
-// 4 * NW scale bytes of one row (nb bytes at `row`) from byte b on; those past nb read as 1.0.  W: bytes that the rows'
-// start, their length and b are multiples of (16, 8, 4 or 1); [lo, hi): the whole array, which no read leaves.
-template <int W, int NW>
-__device__ __forceinline__ void scale_words(uint32_t (&w)[NW], const uint8_t *row, int b, int nb, bool in,
-                                            const uint8_t *lo, const uint8_t *hi) {
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = 0x7F7F7F7Fu;
-    if (!in || b >= nb) return;
-    const uint8_t *p = row + b;
-    if (W == 16 && NW == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x, w[1] = v.y, w[NW - 2] = v.z, w[NW - 1] = v.w;
-    } else if (W >= 8) {
-#pragma unroll
-        for (int i = 0; i < NW / 2; ++i)
-            if (b + 8 * i < nb) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
-                w[2 * i] = v.x, w[2 * i + 1] = v.y;
-            }
-    } else if (W == 4) {
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-            if (b + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
-    } else {
-        // the aligned words around the bytes, shifted together; at the array's ends byte by byte
-        const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u), left = nb - b;  // left: valid bytes
-        const uint8_t *q = p - sh;
-        uint32_t a[NW + 1];
-        if (q >= lo && q + 4 * (NW + 1) <= hi) {
-#pragma unroll
-            for (int i = 0; i <= NW; ++i) a[i] = __ldg(reinterpret_cast<const uint32_t *>(q) + i);
-        } else {
-#pragma unroll
-            for (int i = 0; i <= NW; ++i) {
-                a[i] = 0;
-                for (int j = 0; j < 4; ++j)
-                    if (q + 4 * i + j >= lo && q + 4 * i + j < hi) a[i] |= (uint32_t)__ldg(q + 4 * i + j) << (8 * j);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const uint32_t v = __funnelshift_r(a[i], a[i + 1], 8 * sh);
-            const int n = left - 4 * i;  // valid bytes of this word
-            const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-            w[i] = (v & keep) | (0x7F7F7F7Fu & ~keep);
-        }
-    }
-}
-template <int W>
-__device__ __forceinline__ uint2 scale_bytes8(const uint8_t *row, int b, int nb, bool in, const uint8_t *lo,
-                                              const uint8_t *hi) {
-    uint32_t w[2];
-    scale_words<W, 2>(w, row, b, nb, in, lo, hi);
-    return make_uint2(w[0], w[1]);
-}
-
 // Asks for the 16-byte block at p (16-byte aligned) in shared memory at `to`, of which only the part inside [lo, hi) is
 // read.  The array's first block, where it starts within one, is there on return.
 __device__ __forceinline__ void copy_block(uint4 *to, const uint8_t *p, const uint8_t *lo, const uint8_t *hi) {
@@ -161,6 +105,18 @@ __device__ __forceinline__ void copy_block(uint4 *to, const uint8_t *p, const ui
     }
 #pragma unroll 1
     for (int i = (int)(lo - p); i < 16 && p + i < hi; ++i) reinterpret_cast<uint8_t *>(to)[i] = __ldg(p + i);
+}
+// Sixteen scale bytes, 1.0 from byte n on.
+__device__ __forceinline__ uint4 scales_until(const uint4 &q, int n) {
+    if (n >= 16) return q;
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int left = n - 4 * j;  // valid bytes of this word
+        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        w[j] = (w[j] & keep) | (0x7F7F7F7Fu & ~keep);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but this thread's newest N groups of copies are complete.

@@ -389,27 +389,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 va[2], vb0[2], vb1[2];
             // SHIFTED: block k, counted from the 16-byte boundary before the row, on its way to shared memory.  A
             // step's bytes lie across two blocks; the three after its first are asked for before it starts.
-            const int ma = (int)(reinterpret_cast<uintptr_t>(pa) & 15u), na = ia ? nb : 0;
-            const int mb0 = (int)(reinterpret_cast<uintptr_t>(pb0) & 15u), nb0 = ib0 ? nb : 0;
-            const int mb1 = (int)(reinterpret_cast<uintptr_t>(pb1) & 15u), nb1 = ib1 ? nb : 0;
+            auto off = [](const uint8_t *p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15u); };
+            const int ma = off(pa), na = ia ? nb : 0, ka = ia ? (ma + nb + 15) / 16 : 0;  // place, bytes, blocks
+            const int mb0 = off(pb0), nb0 = ib0 ? nb : 0, kb0 = ib0 ? (mb0 + nb + 15) / 16 : 0;
+            const int mb1 = off(pb1), nb1 = ib1 ? nb : 0, kb1 = ib1 ? (mb1 + nb + 15) / 16 : 0;
             auto ask = [&](int k) {
                 uint4(*to)[kHalf] = sh.raw[k % kRaw];
-                if (16 * k - ma < na) copy_block(&to[0][st], pa - ma + 16 * k, xlo, xhi);
-                if (16 * k - mb0 < nb0) copy_block(&to[1][st], pb0 - mb0 + 16 * k, wlo, whi);
-                if (16 * k - mb1 < nb1) copy_block(&to[2][st], pb1 - mb1 + 16 * k, wlo, whi);
+                if (k < ka) copy_block(&to[0][st], pa - ma + 16 * k, xlo, xhi);
+                if (k < kb0) copy_block(&to[1][st], pb0 - mb0 + 16 * k, wlo, whi);
+                if (k < kb1) copy_block(&to[2][st], pb1 - mb1 + 16 * k, wlo, whi);
                 cp_async_commit();
             };
             auto take = [&](int r, int m, int n, int s) {  // the bytes of step s, 1.0 from byte n of the row on
-                const uint4 q = shift_blocks(sh.raw[s % kRaw][r][st], sh.raw[(s + 1) % kRaw][r][st], m);
-                if (16 * s + 16 <= n) return q;
-                uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int left = n - 16 * s - 4 * j;  // valid bytes of this word
-                    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-                    w[j] = (w[j] & keep) | (0x7F7F7F7Fu & ~keep);
-                }
-                return make_uint4(w[0], w[1], w[2], w[3]);
+                return scales_until(shift_blocks(sh.raw[s % kRaw][r][st], sh.raw[(s + 1) % kRaw][r][st], m),
+                                    n - 16 * s);
             };
             if constexpr (SHIFTED) {
                 for (int k = 0; k < kRaw - 1; ++k) ask(k);

@@ -16,7 +16,11 @@
 //   * scales: thread i reads eight bytes (a chunk) of W row i, and each warp those of
 //     all NT tokens (every lane quarter needs them), kAhead chunks ahead, and writes
 //     the words to one of the TMEM slots: W words at columns 0 and 8 of the slot,
-//     token words at 16 and 24;
+//     token words at 16 and 24.  Rows that do not start on 8-byte boundaries (K % 256) go
+//     by cp.async in 16-byte blocks, each row's once for the CTA, and are shifted on the
+//     way out of shared memory: 558 x 2112 x 6176 16.8 us, 13 x 5760 x 2880 6.7 (33.6 and
+//     7.2 by words from the row's first byte on: three loads for a chunk and row, each a
+//     cache line per lane);
 //   * M <= 16: all threads put the CTA's whole run of x into shared memory, in the layout
 //     that TMA would have written, while the first W chunks are on their way: from codes
 //     (a TMA box that is mostly past M is slow: 1 x 14336 x 4096 16 us with it), or
@@ -48,6 +52,11 @@ constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8, kMaxStages = 8;
 constexpr int kSlotCols = 32;
 constexpr int kAhead = 4;
+constexpr int kRaw = 4;  // blocks of a shifted scale row in shared memory
+
+// ... and their bytes: of 128 W rows, and of the tokens where no staging has brought them.
+__host__ __device__ constexpr int raw_rows(int nt) { return nt == 16 ? kRowsW : kRowsW + nt; }
+__host__ __device__ constexpr int raw_bytes(int nt) { return kRaw * 16 * raw_rows(nt); }
 
 template <int NT>
 struct Split {
@@ -79,9 +88,9 @@ struct SplitShared {
     int32_t aborted, issued, consumed;
 };
 
-// NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  W: alignment of the scale rows, as for
-// scale_words.
-template <int NT, bool BF16, int W>
+// NT: tokens of a tile.  BF16: x is bf16 and is quantised here (NT == 16).  SHIFTED: scale rows do not all start on
+// 8-byte boundaries (K % 256, or the tensors' start).
+template <int NT, bool BF16, bool SHIFTED>
 __global__ void __launch_bounds__(kThreads, 2)
     mxfp4_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const SplitArgs a) {
@@ -103,7 +112,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t *xrun = base + ring_bytes(NT, stages, kStage);  // [nc][NT][128], swizzled
     const int nc_most = (C + a.S - 1) / a.S;
     uint8_t *xscale = xrun + nc_most * T::kXBytes;          // [nc][NT][8]
-    SplitShared &sh = *reinterpret_cast<SplitShared *>(kStaged ? xscale + nc_most * NT * 8 : xrun);
+    uint8_t *after = kStaged ? xscale + nc_most * NT * 8 : xrun;
+    uint4(*raw_scales)[raw_rows(NT)] = reinterpret_cast<uint4(*)[raw_rows(NT)]>(after);  // SHIFTED: [kRaw][row]
+    SplitShared &sh = *reinterpret_cast<SplitShared *>(after + (SHIFTED ? raw_bytes(NT) : 0));
 
     if (tid == 0) {
         tma_prefetch_desc(&tm_w);
@@ -228,54 +239,128 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t slot0 = tmem + (uint32_t)T::kSfCol + ((uint32_t)(quarter * 32) << 16);
         constexpr int kTw = (NT + 31) / 32;  // token words per lane
         const int row = n0 + 32 * quarter + lane;
-        const uint8_t *wr = a.ws + (size_t)(row < a.N ? row : 0) * nb;
-        const uint8_t *xr = kStaged ? nullptr : a.xs + (size_t)m0 * nb;
-        auto w_words = [&](int i) {  // of this lane's W row, chunk i of the run
-            return scale_bytes8<W>(wr, 8 * (c0 + i), nb, row < a.N && i < nc, a.ws, a.ws + (size_t)a.N * nb);
+        const uint2 one = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        // the slot of chunk i is free when the MMAs of the chunk kSlots before are done
+        auto slot_free = [&](int i) {
+            const int old = i - T::kSlots;
+            const bool ok =
+                old < 0 || mbar_wait(&sh.empty[old % stages], (old / stages) & 1, a.status, kSiteScale);
+            if (!__any_sync(0xFFFFFFFFu, !ok || *((volatile int32_t *)&sh.aborted))) return true;
+            atomicExch(&sh.aborted, 1);
+            return false;
         };
-        auto token_words = [&](int j, int i) {  // of token 32 j + lane, chunk i of the run
-            const int tok = 32 * j + lane;
-            if (kStaged) return tok < NT && i < nc ? *reinterpret_cast<const uint2 *>(xscale + (i * NT + tok) * 8)
-                                                : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            return scale_bytes8<W>(xr + (size_t)(tok < tokens ? tok : 0) * nb, 8 * (c0 + i), nb, tok < tokens && i < nc,
-                                   a.xs, a.xs + (size_t)a.M * nb);
+        auto put = [&](int i, const uint2 &w, const uint2 (&x)[kTw]) {
+            const uint32_t sf = slot0 + (uint32_t)(kSlotCols * (i % T::kSlots));
+            tmem_st4(sf, w.x, w.x, w.x, w.x);  // column `quarter` of the four is the one read
+            tmem_st4(sf + 8, w.y, w.y, w.y, w.y);
+            constexpr int l = kTw - 1;
+            tmem_st4(sf + 16, x[0].x, x[l < 1 ? l : 1].x, x[l < 2 ? l : 2].x, x[l].x);
+            tmem_st4(sf + 24, x[0].y, x[l < 1 ? l : 1].y, x[l < 2 ? l : 2].y, x[l].y);
         };
-        uint2 vw[kAhead], vx[kAhead][kTw];
+        auto arrive = [&](int i) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.sfull[i % T::kSlots]);
+        };
+        auto staged_words = [&](int i) {  // of token `lane`, chunk i of the run
+            return lane < NT && i < nc ? *reinterpret_cast<const uint2 *>(xscale + (i * NT + lane) * 8) : one;
+        };
+        if constexpr (SHIFTED) {
+            // The rows' bytes from this run's first on, in 16-byte blocks counted from the boundary before: thread t
+            // asks for those of W row t and of token t, three blocks ahead.
+            const int t = tid - 64, most = min(nb - kChunkBlocks * c0, kChunkBlocks * nc);
+            const uint8_t *whi = a.ws + (size_t)a.N * nb, *xhi = a.xs + (size_t)a.M * nb;
+            const uint8_t *pw = a.ws + (size_t)(n0 + t) * nb + kChunkBlocks * c0;  // (read where the row exists)
+            const uint8_t *px = a.xs + (size_t)(m0 + t) * nb + kChunkBlocks * c0;
+            auto off = [](const uint8_t *p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15u); };
+            // how many blocks the rows have (none where there is no such row)
+            const int kw = n0 + t < a.N ? (off(pw) + most + 15) / 16 : 0;
+            const int kx = !kStaged && t < tokens ? (off(px) + most + 15) / 16 : 0;
+            auto ask = [&](int k) {
+                uint4 *to = raw_scales[k % kRaw];
+                if (k < kw) copy_block(&to[t], pw - off(pw) + 16 * k, a.ws, whi);
+                if (k < kx) copy_block(&to[kRowsW + t], px - off(px) + 16 * k, a.xs, xhi);
+                cp_async_commit();
+            };
+            // what this lane takes of them: W row 32 quarter + lane, tokens 32 j + lane
+            constexpr int kTake = kStaged ? 1 : 1 + kTw;
+            int at[kTake], m[kTake], n[kTake];
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-            vw[d] = w_words(d);
+            for (int r = 0; r < kTake; ++r) {
+                const int i = r == 0 ? 32 * quarter + lane : 32 * (r - 1) + lane;
+                at[r] = r == 0 ? i : kRowsW + i;
+                m[r] = off((r == 0 ? a.ws + (size_t)(n0 + i) * nb : a.xs + (size_t)(m0 + i) * nb) + kChunkBlocks * c0);
+                n[r] = (r == 0 ? n0 + i < a.N : i < tokens) ? most : 0;
+            }
+            for (int k = 0; k < kRaw - 1; ++k) ask(k);
+            // A warp that gave up goes on through the barriers, so that no other one waits for it there.
+            bool stop = false;
+            for (int i0 = 0; i0 < nc; i0 += 2) {
+                const int k = i0 / 2;
+                cp_async_wait<kRaw - 3>();  // this thread's block k + 1 and those before it are there,
+                named_barrier(1, 4 * 32);   // and the others' too; block k - 1 has been read
+                ask(k + kRaw - 1);
+                if (stop) continue;
+                uint4 q[kTake];
 #pragma unroll
-            for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, d);
-        }
-        bool stop = false;
-        for (int i0 = 0; i0 < nc && !stop; i0 += kAhead) {
+                for (int r = 0; r < kTake; ++r)
+                    q[r] = scales_until(
+                        shift_blocks(raw_scales[k % kRaw][at[r]], raw_scales[(k + 1) % kRaw][at[r]], m[r]),
+                        n[r] - 16 * k);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (i0 + h >= nc || stop) break;
+                    if (!slot_free(i0 + h)) {
+                        stop = true;
+                        break;
+                    }
+                    uint2 x[kTw];
+#pragma unroll
+                    for (int j = 0; j < kTw; ++j) {
+                        const uint4 &v = q[kStaged ? 0 : 1 + j];
+                        x[j] = kStaged ? staged_words(i0 + h) : h ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+                    }
+                    put(i0 + h, h ? make_uint2(q[0].z, q[0].w) : make_uint2(q[0].x, q[0].y), x);
+                    arrive(i0 + h);
+                }
+            }
+            cp_async_wait<0>();
+        } else {
+            const uint8_t *wr = a.ws + (size_t)(row < a.N ? row : 0) * nb;
+            const uint8_t *xr = kStaged ? nullptr : a.xs + (size_t)m0 * nb;
+            auto w_words = [&](int i) {  // of this lane's W row, chunk i of the run
+                return row < a.N && i < nc ? __ldg(reinterpret_cast<const uint2 *>(wr) + c0 + i) : one;
+            };
+            auto token_words = [&](int j, int i) {  // of token 32 j + lane, chunk i of the run
+                if (kStaged) return staged_words(i);
+                const int tok = 32 * j + lane;
+                if (tok >= tokens || i >= nc) return one;
+                return __ldg(reinterpret_cast<const uint2 *>(xr + (size_t)tok * nb) + c0 + i);
+            };
+            uint2 vw[kAhead], vx[kAhead][kTw];
 #pragma unroll
             for (int d = 0; d < kAhead; ++d) {
-                const int i = i0 + d;
-                if (i >= nc) break;
-                // the slot is free when the MMAs of chunk `old` are done
-                const int f = i % T::kSlots, old = i - T::kSlots;
-                if (old >= 0 && !mbar_wait(&sh.empty[old % stages], (old / stages) & 1, a.status, kSiteScale))
-                    stop = true;
-                if (__any_sync(0xFFFFFFFFu, stop || *((volatile int32_t *)&sh.aborted))) {
-                    atomicExch(&sh.aborted, 1);
-                    stop = true;
-                    break;
-                }
-                const uint32_t sf = slot0 + (uint32_t)(kSlotCols * f);
-                const uint2 w = vw[d];
-                tmem_st4(sf, w.x, w.x, w.x, w.x);  // column `quarter` of the four is the one read
-                tmem_st4(sf + 8, w.y, w.y, w.y, w.y);
-                constexpr int l = kTw - 1;
-                tmem_st4(sf + 16, vx[d][0].x, vx[d][l < 1 ? l : 1].x, vx[d][l < 2 ? l : 2].x, vx[d][l].x);
-                tmem_st4(sf + 24, vx[d][0].y, vx[d][l < 1 ? l : 1].y, vx[d][l < 2 ? l : 2].y, vx[d][l].y);
-                vw[d] = w_words(i + kAhead);
+                vw[d] = w_words(d);
 #pragma unroll
-                for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, i + kAhead);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.sfull[f]);
+                for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, d);
+            }
+            bool stop = false;
+            for (int i0 = 0; i0 < nc && !stop; i0 += kAhead) {
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    const int i = i0 + d;
+                    if (i >= nc) break;
+                    if (!slot_free(i)) {
+                        stop = true;
+                        break;
+                    }
+                    put(i, vw[d], vx[d]);
+                    vw[d] = w_words(i + kAhead);
+#pragma unroll
+                    for (int j = 0; j < kTw; ++j) vx[d][j] = token_words(j, i + kAhead);
+                    arrive(i);
+                }
             }
         }
         // ---- epilogue: lane = W row, columns = tokens ----
@@ -352,14 +437,14 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 using SplitFn = void (*)(const CUtensorMap, const CUtensorMap, const SplitArgs);
 
-template <int W>
-SplitFn pick_w(int nt, bool bf16) {
-    if (nt == 16) return bf16 ? mxfp4_split_kernel<16, true, W> : mxfp4_split_kernel<16, false, W>;
-    return nt == 32 ? mxfp4_split_kernel<32, false, W> : mxfp4_split_kernel<64, false, W>;
+template <bool SHIFTED>
+SplitFn pick_by(int nt, bool bf16) {
+    if (nt == 16) return bf16 ? mxfp4_split_kernel<16, true, SHIFTED> : mxfp4_split_kernel<16, false, SHIFTED>;
+    return nt == 32 ? mxfp4_split_kernel<32, false, SHIFTED> : mxfp4_split_kernel<64, false, SHIFTED>;
 }
 
-SplitFn pick_split(int nt, bool bf16, uintptr_t align) {
-    return align % 8 == 0 ? pick_w<8>(nt, bf16) : align % 4 == 0 ? pick_w<4>(nt, bf16) : pick_w<1>(nt, bf16);
+SplitFn pick_split(int nt, bool bf16, bool shifted) {
+    return shifted ? pick_by<true>(nt, bf16) : pick_by<false>(nt, bf16);
 }
 
 constexpr int kMaxSmem = 227 * 1024;
@@ -367,61 +452,61 @@ constexpr int kMaxSmem = 227 * 1024;
 // CTAs of a cluster wait for one another, so none of them may wait for TMEM that another cluster's CTA holds.
 constexpr int kHalfSmem = 112 * 1024, kHalfSmemMost = 113 * 1024;
 
-int split_smem(int nt, int stages, int S, int K) {
+int split_smem(int nt, int stages, int S, int K, bool shifted) {
     const int nc = ceil_div(ceil_div(K, 256), S);
     int n = 1024 + ring_bytes(nt, stages, kWBytes + (nt == 16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
     if (nt == 16) n += nc * nt * (kChunkBytes + 8);
+    if (shifted) n += raw_bytes(nt);
     return n > kHalfSmem ? n : kHalfSmem;
 }
 
 int split_slots(int nt) { return nt <= 32 ? Split<32>::kSlots : Split<64>::kSlots; }
 
-Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms) {
+Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms, bool shifted) {
     Mxfp4SplitPlan p;
     const int C = ceil_div(K, 256), n_tiles = ceil_div(N, kRowsW);
     p.tokens = tokens;
     p.m_tiles = ceil_div(M, p.tokens);
     // K over S CTAs: microseconds from timings of 40 shapes (1 to 512 tokens, 256 to 14336 rows).  A chunk takes
     // about 0.4 where every SM has at most one CTA, and as much longer as there are more; joining S sums costs more
-    // with S, and with the tokens where S is 8.  64 x 2112 x 7168: S = 1, 2, 4, 8 take 16.0, 10.7, 7.7, 8.6 us; 16 x 2112 x 7168: 16.7,
-    // 10.8, 8.0, 7.0; 1 x 14336 x 4096: 11.7, 9.9, 13.0, 19.0.
+    // with S, and with the tokens where S is 8.  64 x 2112 x 7168: S = 1, 2, 4, 8 take 16.0, 10.7, 7.7, 8.6 us; 16 x
+    // 2112 x 7168: 16.7, 10.8, 8.0, 7.0; 1 x 14336 x 4096: 11.7, 9.9, 13.0, 19.0.
     const float tiles = (float)n_tiles * (float)p.m_tiles;
     float best = 0.0f;
     for (int S = 1; S <= kMaxSplit && S <= C; S *= 2) {
         const float load = tiles * (float)S / (float)num_sms;
         const float join = S == 1 ? 0.0f : S == 2 ? 0.3f : S == 4 ? 0.7f : 0.7f + 0.03f * (float)p.tokens;
         const float t = 0.4f * (float)ceil_div(C, S) * (load > 1.0f ? load : 1.0f) + join;
-        if (S == 1 || t < best) best = t, p.split = S;
+        // (to compare with the pair form: just above one CTA to an SM the slowest SM has two; 558 x 2112 x 6144, 153
+        // tiles: 15.5 us here, 12.8 in pairs)
+        if (S == 1 || t < best) best = t, p.split = S, p.estimate = load > 1.0f && load < 1.4f ? t * 1.4f / load : t;
     }
-    p.estimate = best;
     const int nc = ceil_div(C, p.split), slots = split_slots(p.tokens);
     const int most = tiles * (float)p.split > (float)num_sms ? kHalfSmemMost : kMaxSmem;
     p.stages = nc < kMaxStages ? nc : kMaxStages;
     // (with fewer stages than scale slots a slot's wait could miss a turn of the stage's barrier)
-    while (p.stages > slots && split_smem(p.tokens, p.stages, p.split, K) > most) --p.stages;
-    p.smem = split_smem(p.tokens, p.stages, p.split, K);
+    while (p.stages > slots && split_smem(p.tokens, p.stages, p.split, K, shifted) > most) --p.stages;
+    p.smem = split_smem(p.tokens, p.stages, p.split, K, shifted);
     return p;
 }
 
 }  // namespace
 
-Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms) {
-    if (M <= 16) {
-        const Mxfp4SplitPlan p = plan_for(16, M, N, K, num_sms);
-        // else (K of 200000 and more) a run of x does not fit: by TMA, stage by stage
-        if (p.smem <= kMaxSmem) return p;
-    }
-    return plan_for(M <= 32 ? 32 : 64, M, N, K, num_sms);
+Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms, bool shifted) {
+    // Where a run of x does not fit (K of 200000 and more): by TMA, stage by stage, whatever the scales' alignment.
+    if (M <= 16 && plan_for(16, M, N, K, num_sms, true).smem <= kMaxSmem)
+        return plan_for(16, M, N, K, num_sms, shifted);
+    return plan_for(M <= 32 ? 32 : 64, M, N, K, num_sms, shifted);
 }
 
-bool mxfp4_split_quantises(int M, int N, int K) { return mxfp4_split_plan(M, N, K, kGb300Sms).tokens == 16; }
+bool mxfp4_split_quantises(int M, int N, int K) { return mxfp4_split_plan(M, N, K, kGb300Sms, true).tokens == 16; }
 
 int init_mxfp4_split() {
-    for (uintptr_t w : {8, 4, 1})
+    for (bool shifted : {false, true})
         for (int nt : {16, 32, 64})
             for (bool b : {false, true}) {
                 if (b && nt > 16) continue;
-                const int e = (int)cudaFuncSetAttribute(pick_split(nt, b, w),
+                const int e = (int)cudaFuncSetAttribute(pick_split(nt, b, shifted),
                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
                 if (e) return e;
             }
@@ -431,7 +516,10 @@ int init_mxfp4_split() {
 int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void *ws, const void *bias, void *out,
                        int M, int N, int K, int num_sms, uint32_t flags, void *stream, int32_t *status) {
     const bool bf16 = xs == nullptr;
-    const Mxfp4SplitPlan p = mxfp4_split_plan(M, N, K, num_sms);
+    const uintptr_t al =
+        (bf16 ? 0 : reinterpret_cast<uintptr_t>(xs)) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
+    const bool shifted = al % 8 != 0;
+    const Mxfp4SplitPlan p = mxfp4_split_plan(M, N, K, num_sms, shifted);
     CUtensorMap tx = {}, tw;  // 128-byte rows of 256 codes
     int r = make_tmap_u8_2d(&tw, wq, (uint64_t)N, (uint64_t)(K / 2), kRowsW, kChunkBytes, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
@@ -468,9 +556,7 @@ int launch_mxfp4_split(const void *x, const void *xs, const void *wq, const void
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    const uintptr_t al =
-        (bf16 ? 0 : reinterpret_cast<uintptr_t>(xs)) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);
-    return (int)cudaLaunchKernelEx(&cfg, pick_split(p.tokens, bf16, al), tx, tw, a);
+    return (int)cudaLaunchKernelEx(&cfg, pick_split(p.tokens, bf16, shifted), tx, tw, a);
 }
 
 }  // namespace bf16l
