@@ -66,3 +66,8 @@ def test_chain(lib, T, H):
             assert all(torch.equal(a, b) for a, b in zip(want, got)), f"flags {flags}"
     assert all(torch.equal(a, b) for a, b in zip(want, run(0, lambda: None, graph=True)))
     assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("T,H", [(16, 1440), (40, 1440), (1300, 2080)])
+def test_chain_with_scale_rows_off_16_byte_boundaries(lib, T, H):
+    test_chain(lib, T, H)
