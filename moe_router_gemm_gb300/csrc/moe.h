@@ -18,8 +18,9 @@ int launch_dequant_mxfp4(const void *q, const void *scales, void *out, long long
 // The MXFP4 linear with K over a cluster's CTAs and W on the MMA's M side (mxfp4_split.cu): any M; xs null means that
 // x is bf16 and is quantised by the kernel (where mxfp4_split_quantises).
 struct Mxfp4SplitPlan {
-    int tokens, m_tiles, split, stages, smem;  // tokens and token tiles, CTAs along K, ring depth, dynamic shared memory
-    float estimate;                            // microseconds beside the fixed part, roughly
+    int tokens, m_tiles, split, stages;  // tokens and token tiles, CTAs along K, ring depth
+    long long smem;                      // dynamic shared memory (more than there is, where a run of x does not fit)
+    float estimate;                      // microseconds beside the fixed part, roughly
 };
 Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms, bool shifted);
 bool mxfp4_split_quantises(int M, int N, int K);

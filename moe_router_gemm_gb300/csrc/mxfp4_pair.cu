@@ -67,6 +67,10 @@ constexpr int kPitch = 144;  // bytes of a shifted row of 64 columns: nine units
 constexpr int kPieceBytes = 2560;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 
+// K % 32 == 0 (K + 255 may not fit an int).
+__host__ __device__ constexpr int chunks_of(int K) { return K / 256 + (K % 256 != 0); }
+static_assert(2 * kChunkBytes == 256, "two codes to a byte");
+
 template <bool SHIFTED>
 struct PairShared {
     static constexpr int kStages = SHIFTED ? bf16l::kStages - 1 : bf16l::kStages;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_tiles = (M + kTileRows - 1) / kTileRows, q_tiles = (N + kTileRows - 1) / kTileRows;
     const int units = p_tiles * q_tiles;
     const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
-    const int C = (K + 2 * kChunkBytes - 1) / (2 * kChunkBytes);
+    const int C = chunks_of(K);
     const int nb = K >> 5;
 
     if (tid == 0) {
@@ -549,7 +553,7 @@ float mxfp4_pair_estimate(int M, int N, int K, int num_sms) {
     // 0.42 us a chunk and round of tiles (K = 7168: 15.4 us for one round, 4096: 11, 1024: 5.4)
     const long long units = (long long)((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
     const long long rounds = (units + num_sms / 2 - 1) / (num_sms / 2);
-    return 0.42f * (float)((K + 2 * kChunkBytes - 1) / (2 * kChunkBytes)) * (float)rounds;
+    return 0.42f * (float)chunks_of(K) * (float)rounds;
 }
 
 int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void *ws, const void *bias, void *out,

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }  // (a + b - 1 may not fit)
 
 using SplitFn = void (*)(const CUtensorMap, const CUtensorMap, const SplitArgs);
 
@@ -454,10 +454,10 @@ constexpr int kMaxSmem = 227 * 1024;
 // CTAs of a cluster wait for one another, so none of them may wait for TMEM that another cluster's CTA holds.
 constexpr int kHalfSmem = 112 * 1024, kHalfSmemMost = 113 * 1024;
 
-int split_smem(int nt, int stages, int S, int K, bool shifted) {
+long long split_smem(int nt, int stages, int S, int K, bool shifted) {
     const int nc = ceil_div(ceil_div(K, 256), S);
-    int n = 1024 + ring_bytes(nt, stages, kWBytes + (nt == 16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
-    if (nt == 16) n += nc * nt * (kChunkBytes + 8);
+    long long n = 1024 + ring_bytes(nt, stages, kWBytes + (nt == 16 ? 0 : nt * kChunkBytes)) + (int)sizeof(SplitShared);
+    if (nt == 16) n += (long long)nc * nt * (kChunkBytes + 8);  // (a run of x: past 32 bits where K is two billion)
     if (shifted) n += raw_bytes(nt);
     return n > kHalfSmem ? n : kHalfSmem;
 }

@@ -110,3 +110,12 @@ def test_the_reference_forms_of_norm_and_route():
     key, score, allowed = ref.route(np.log(np.array([[1.0, 2.0, 3.0, 2.0]])), 2, "softmax", None, 2, 1, 1, True, 1.0)
     assert np.allclose(score, [[0.125, 0.25, 0.375, 0.25]]) and allowed.tolist() == [[False, False, True, True]]
 
+
+
+def test_mxfp4_workspace_at_long_k(lib):
+    """Up to the largest K there is, a call whose x does not fit shared memory asks for room for its codes and scales."""
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    for M in (1, 16, 17, 300):
+        for K in (262144, 1 << 26, 1 << 28, 2_000_000_000, 2_021_027_872, 2_147_483_392, (1 << 31) - 32):
+            for N in (128, 2112):
+                assert lib.mxfp4_dynamic_workspace(M, N, K) == up(M * K // 2) + up(M * K // 32), (M, N, K)
