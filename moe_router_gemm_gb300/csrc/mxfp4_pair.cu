@@ -70,6 +70,7 @@ constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 // K % 32 == 0 (K + 255 may not fit an int).
 __host__ __device__ constexpr int chunks_of(int K) { return K / 256 + (K % 256 != 0); }
 static_assert(2 * kChunkBytes == 256, "two codes to a byte");
+__host__ __device__ constexpr int tiles_of(int rows) { return rows / kTileRows + (rows % kTileRows != 0); }
 
 template <bool SHIFTED>
 struct PairShared {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const int p_tiles = (M + kTileRows - 1) / kTileRows, q_tiles = (N + kTileRows - 1) / kTileRows;
+    const int p_tiles = tiles_of(M), q_tiles = tiles_of(N);
     const int units = p_tiles * q_tiles;
     const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
     const int C = chunks_of(K);
@@ -551,7 +552,7 @@ int init_mxfp4_pair() {
 
 float mxfp4_pair_estimate(int M, int N, int K, int num_sms) {
     // 0.42 us a chunk and round of tiles (K = 7168: 15.4 us for one round, 4096: 11, 1024: 5.4)
-    const long long units = (long long)((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
+    const long long units = (long long)tiles_of(M) * tiles_of(N);
     const long long rounds = (units + num_sms / 2 - 1) / (num_sms / 2);
     return 0.42f * (float)chunks_of(K) * (float)rounds;
 }
@@ -574,8 +575,7 @@ int launch_mxfp4_pair(const void *xq, const void *xs, const void *wq, const void
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
     // A cluster that cannot be resident with the others would run its tiles after them.
-    const long long units =
-        (long long)((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
+    const long long units = (long long)tiles_of(M) * tiles_of(N);
     long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
     if (units < clusters) clusters = units;
     const uintptr_t a = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | (uintptr_t)(K / 32);

@@ -268,3 +268,19 @@ def test_linear_scale_rows_off_16_byte_boundaries(lib, M, N, blocks, off):
         return part
     got = lib.bf16_linear_mxfp4(_u8(xq), between(xs), _u8(wq), between(ws))
     ref.check_linear(got, ref.values_mxfp4(xq, xs), ref.values_mxfp4(wq, ws), None, K)
+
+
+@pytest.mark.parametrize("M,N", [((1 << 31) - 7, 1), (3, (1 << 31) - 7)])
+def test_linear_rows_near_the_largest_count(lib, M, N):
+    """Almost 2^31 rows of x (the pair form) or of W (the split form): the last rows, and rows that were zero."""
+    K = 32
+    xq, wq = (torch.zeros(r, K // 2, dtype=torch.uint8, device=DEV) for r in (M, N))
+    xs, ws = (torch.full((r, 1), 127, dtype=torch.uint8, device=DEV) for r in (M, N))
+    for q in (xq, wq):
+        q[-40:] = torch.randint(0, 256, (min(40, len(q)), K // 2), dtype=torch.uint8, device=DEV)
+    got = lib.bf16_linear_mxfp4(xq, xs, wq, ws)
+    assert lib.device_status() == 0
+    xv, wv = (ref.values_mxfp4(q[-300:].cpu().numpy(), s[-300:].cpu().numpy()) for q, s in ((xq, xs), (wq, ws)))
+    ref.check_linear(got[-300:, -300:], xv, wv, None, K)
+    middle = got[1 << 30:(1 << 30) + 600] if M > N else got[:, 1 << 30:(1 << 30) + 600]
+    assert middle.numel() == 600 * min(M, N) and not middle.any()
