@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const NormArgs a) {
                 ss = fmaf(h[j], h[j], ss);
             }
         } else {
-            for (int i = (int)threadIdx.x; i < a.H; i += nt) {
-                const float v = add(xr[i], a.residual ? a.residual[r * a.H + i] : (uint16_t)0, i);
+            for (unsigned i = threadIdx.x; i < (unsigned)a.H; i += nt) {  // (H may be within a block of 2^31)
+                const float v = add(xr[i], a.residual ? a.residual[r * a.H + i] : (uint16_t)0, (int)i);
                 ss = fmaf(v, v, ss);
             }
         }
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const NormArgs a) {
             }
         } else {
             // (h was written by this same thread)
-            for (int i = (int)threadIdx.x; i < a.H; i += nt) put(bf16_to_f32(hr[i]), i);
+            for (unsigned i = threadIdx.x; i < (unsigned)a.H; i += nt) put(bf16_to_f32(hr[i]), (int)i);
         }
     }
 }

@@ -193,3 +193,13 @@ def test_refusals(lib):
     with pytest.raises(lib.BF16LinearError) as e:
         lib.rmsnorm(x, w, out=x)  # an output over an input
     assert e.value.status == -1
+
+
+def test_the_longest_rows(lib):
+    """H within a block's threads of 2^31.  Ones have a norm of one exactly, so y is the weight, which bf16 holds."""
+    H = (1 << 31) - 40
+    x = torch.ones(1, H, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    w[-700:] = (1 + torch.rand(700, device=DEV)).to(torch.bfloat16)
+    w[1 << 30] = 3.0
+    assert torch.equal(lib.rmsnorm(x, w, eps=0.0).out[0], w)
