@@ -581,6 +581,12 @@ def _pitch(t, name):
     return ld if ld > cols else cols
 
 
+def _fits(what, flags, *sizes):
+    """Refuse what the C ABI's 32 bits do not hold (ctypes would pass the low ones)."""
+    if not 0 <= flags < 1 << 32 or any(not -(1 << 31) <= v < 1 << 31 for v in sizes):
+        _raise(EINVAL, f"{what}: sizes {sizes}, flags {flags}")
+
+
 QUANT_FORMATS = {None: 0, "fp8": 1, "mxfp8": 2, "mxfp4": 3}
 
 
@@ -613,6 +619,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, *, quant: str | None = 
         raise ValueError(f"quant must be one of {list(QUANT_FORMATS)}, got {quant!r}")
     dev, shape, ld = _cuda(x, "x"), x.shape, _pitch(x, "x")
     rows, H = shape
+    _fits("bf16_rmsnorm", flags, H)
     w = _need(weight, "weight", bf16, (H,), dev)
     r = ro = o = c = sc = s1 = None
     if residual is not None:
@@ -681,6 +688,7 @@ def route(logits, k: int, *, scoring: str = "softmax", bias=None, groups: int = 
     if scoring not in SCORES:
         raise ValueError(f"scoring must be one of {list(SCORES)}, got {scoring!r}")
     dev, (T, E), ld = _cuda(logits, "logits"), logits.shape, _pitch(logits, "logits")
+    _fits("bf16_route", flags, E, k, groups, top_groups, group_best)
     b = None if bias is None else _need(bias, "bias", f32, (E,), dev)
     if weights is None:
         weights = _empty((T, k if k > 0 else 0), f32, dev, stream)
@@ -707,6 +715,7 @@ def quant_mxfp4(x, out=None, scales=None, flags: int = 0, stream=None):
     dev, u8 = _cuda(x, "x"), torch.uint8
     rows, K = x.shape
     p = _need(x, "x", torch.bfloat16, (rows, K), dev)
+    _fits("bf16_quant_mxfp4", flags, K)
     if out is None:
         out = _empty((rows, K // 2), u8, dev, stream)
     if scales is None:
@@ -730,6 +739,7 @@ def dequant_mxfp4(codes, scales, out=None, flags: int = 0, stream=None):
     dev, u8 = _cuda(codes, "codes"), torch.uint8
     rows, h = codes.shape
     q, s = _need(codes, "codes", u8, (rows, h), dev), _need(scales, "scales", u8, (rows, h // 16), dev)
+    _fits("bf16_dequant_mxfp4", flags, 2 * h)
     if out is None:
         out = _empty((rows, 2 * h), torch.bfloat16, dev, stream)
     st = _call(load().bf16_dequant_mxfp4, dev, stream, q, s, rows, 2 * h,
@@ -753,6 +763,7 @@ def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, strea
     (M, h), N = xq.shape, wq.shape[0]
     a, b = _need(xq, "xq", u8, (M, h), dev), _need(xs, "xs", u8, (M, h // 16), dev)
     c, d = _need(wq, "wq", u8, (N, h), dev), _need(ws, "ws", u8, (N, h // 16), dev)
+    _fits("bf16_linear_mxfp4", flags, M, N, 2 * h)
     e = None if bias is None else _need(bias, "bias", bf16, (N,), dev)
     if out is None:
         out = _empty((M, N), bf16, dev, stream)
@@ -763,8 +774,8 @@ def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, strea
 
 
 def mxfp4_dynamic_workspace(M: int, N: int, K: int) -> int:
-    """Workspace bytes of bf16_linear_mxfp4_dynamic (0 where the product quantises x itself)."""
-    return int(load().bf16_linear_mxfp4_dynamic_workspace(M, N, K))
+    """Workspace bytes of bf16_linear_mxfp4_dynamic (0 where the product quantises x itself, and for sizes that it refuses)."""
+    return int(load().bf16_linear_mxfp4_dynamic_workspace(M, N, K)) if max(M, N, K) < 1 << 31 else 0
 
 
 def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, flags: int = 0, stream=None):
@@ -782,6 +793,7 @@ def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, fl
     (M, K), N = x.shape, wq.shape[0]
     a = _need(x, "x", bf16, (M, K), dev)
     c, d = _need(wq, "wq", u8, (N, K // 2), dev), _need(ws, "ws", u8, (N, K // 32), dev)
+    _fits("bf16_linear_mxfp4_dynamic", flags, M, N, K)
     e = None if bias is None else _need(bias, "bias", bf16, (N,), dev)
     if out is None:
         out = _empty((M, N), bf16, dev, stream)

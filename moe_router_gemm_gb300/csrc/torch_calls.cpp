@@ -88,6 +88,20 @@ PyObject *pack(std::initializer_list<Tensor> list) {
     return r;
 }
 
+// The C ABI's int and flags of a Python number; `wide` where it does not fit (the wrapper then refuses it).
+int as_int(PyObject *o, bool &wide) {
+    int over = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &over);
+    if (over || v < INT32_MIN || v > INT32_MAX) wide = true;
+    return (int)v;
+}
+uint32_t as_flags(PyObject *o, bool &wide) {
+    int over = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &over);
+    if (over || v < 0 || v > (long)UINT32_MAX) wide = true;
+    return (uint32_t)v;
+}
+
 bool wrong_count(Py_ssize_t got, Py_ssize_t want) {
     if (got == want) return false;
     PyErr_Format(PyExc_TypeError, "%zd arguments, %zd are wanted", got, want);
@@ -99,9 +113,11 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (wrong_count(n, 8)) return nullptr;
     const double eps = PyFloat_AsDouble(args[3]);
-    const long quant = PyLong_AsLong(args[4]), flags = PyLong_AsLong(args[7]);
-    const int want = PyObject_IsTrue(args[6]);
+    bool wide = false;
+    const int quant = as_int(args[4], wide), want = PyObject_IsTrue(args[6]);
+    const uint32_t flags = as_flags(args[7], wide);
     if (PyErr_Occurred() || want < 0) return nullptr;
+    if (wide) return none();
     const Tensor *x = cuda_tensor(args[0]);
     if (!x || x->scalar_type() != at::kBFloat16 || x->dim() != 2) return none();
     const int64_t rows = x->size(0), H = x->size(1), ld = pitch(*x);
@@ -119,7 +135,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
                              out.defined() ? out.data_ptr() : nullptr, sum.defined() ? sum.data_ptr() : nullptr,
                              codes.defined() ? codes.data_ptr() : nullptr, scales.defined() ? scales.data_ptr() : nullptr,
                              s ? static_cast<const float *>(s->const_data_ptr()) : nullptr, rows, (int)H, (float)eps,
-                             (int)quant, (uint32_t)flags, stream_of(*x));
+                             quant, flags, stream_of(*x));
     return st ? PyLong_FromLong(st) : pack({out, sum, codes, scales});
     END_HANDLE_TH_ERRORS
 }
@@ -128,11 +144,14 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *route(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (wrong_count(n, 10)) return nullptr;
-    const long k = PyLong_AsLong(args[1]), scoring = PyLong_AsLong(args[2]), groups = PyLong_AsLong(args[4]),
-               top = PyLong_AsLong(args[5]), best = PyLong_AsLong(args[6]), flags = PyLong_AsLong(args[9]);
+    bool wide = false;
+    const int k = as_int(args[1], wide), scoring = as_int(args[2], wide), groups = as_int(args[4], wide),
+              top = as_int(args[5], wide), best = as_int(args[6], wide);
+    const uint32_t flags = as_flags(args[9], wide);
     const int renorm = PyObject_IsTrue(args[7]);
     const double scale = PyFloat_AsDouble(args[8]);
     if (PyErr_Occurred() || renorm < 0) return nullptr;
+    if (wide) return none();
     const Tensor *l = cuda_tensor(args[0]), *b = nullptr;
     if (!l || l->dim() != 2 || (l->scalar_type() != at::kFloat && l->scalar_type() != at::kBFloat16)) return none();
     const int64_t T = l->size(0), E = l->size(1), ld = pitch(*l);
@@ -140,9 +159,9 @@ PyObject *route(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (args[3] != Py_None && !(b = dense(args[3], at::kFloat, E))) return none();
     Tensor w = make(*l, at::kFloat, {T, k}), ids = make(*l, at::kInt, {T, k});
     const int st = g_route(l->const_data_ptr(), ld, b ? static_cast<const float *>(b->const_data_ptr()) : nullptr,
-                           static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(ids.data_ptr()), T, (int)E, (int)k,
-                           (int)scoring, (int)groups, (int)top, (int)best, renorm, (float)scale,
-                           l->scalar_type() == at::kBFloat16, (uint32_t)flags, stream_of(*l));
+                           static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(ids.data_ptr()), T, (int)E, k,
+                           scoring, groups, top, best, renorm, (float)scale, l->scalar_type() == at::kBFloat16, flags,
+                           stream_of(*l));
     return st ? PyLong_FromLong(st) : pack({w, ids});
     END_HANDLE_TH_ERRORS
 }
@@ -151,14 +170,16 @@ PyObject *route(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *quant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (wrong_count(n, 2)) return nullptr;
-    const long flags = PyLong_AsLong(args[1]);
+    bool wide = false;
+    const uint32_t flags = as_flags(args[1], wide);
     if (PyErr_Occurred()) return nullptr;
+    if (wide) return none();
     const Tensor *x = cuda_tensor(args[0]);
     if (!x || x->dim() != 2 || x->scalar_type() != at::kBFloat16 || !x->is_contiguous()) return none();
     const int64_t rows = x->size(0), K = x->size(1);
     if (K > INT32_MAX) return none();
     Tensor q = make(*x, at::kByte, {rows, K / 2}), s = make(*x, at::kByte, {rows, K / 32});
-    const int st = g_quant(x->const_data_ptr(), rows, (int)K, q.data_ptr(), s.data_ptr(), (uint32_t)flags, stream_of(*x));
+    const int st = g_quant(x->const_data_ptr(), rows, (int)K, q.data_ptr(), s.data_ptr(), flags, stream_of(*x));
     return st ? PyLong_FromLong(st) : pack({q, s});
     END_HANDLE_TH_ERRORS
 }
@@ -167,8 +188,10 @@ PyObject *quant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *dequant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (wrong_count(n, 3)) return nullptr;
-    const long flags = PyLong_AsLong(args[2]);
+    bool wide = false;
+    const uint32_t flags = as_flags(args[2], wide);
     if (PyErr_Occurred()) return nullptr;
+    if (wide) return none();
     const Tensor *q = cuda_tensor(args[0]);
     if (!q || q->dim() != 2 || q->scalar_type() != at::kByte || !q->is_contiguous()) return none();
     const int64_t rows = q->size(0), h = q->size(1);
@@ -176,7 +199,7 @@ PyObject *dequant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!s || 2 * h > INT32_MAX) return none();
     Tensor out = make(*q, at::kBFloat16, {rows, 2 * h});
     const int st = g_dequant(q->const_data_ptr(), s->const_data_ptr(), rows, (int)(2 * h), out.data_ptr(),
-                             (uint32_t)flags, stream_of(*q));
+                             flags, stream_of(*q));
     return st ? PyLong_FromLong(st) : item(out);
     END_HANDLE_TH_ERRORS
 }
@@ -185,8 +208,10 @@ PyObject *dequant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *linear_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (wrong_count(n, 6)) return nullptr;
-    const long flags = PyLong_AsLong(args[5]);
+    bool wide = false;
+    const uint32_t flags = as_flags(args[5], wide);
     if (PyErr_Occurred()) return nullptr;
+    if (wide) return none();
     const bool dynamic = args[1] == Py_None;
     const Tensor *x = cuda_tensor(args[0]), *wq = cuda_tensor(args[2]), *xs = nullptr, *b = nullptr;
     if (!x || !wq || x->dim() != 2 || wq->dim() != 2 || !x->is_contiguous() ||
@@ -204,10 +229,10 @@ PyObject *linear_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const size_t need = g_workspace((int)M, (int)N, (int)K);
         if (need) space = make(*x, at::kByte, {(int64_t)need});  // freed on return, to this stream's own memory
         st = g_dynamic(x->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias, out.data_ptr(), (int)M,
-                       (int)N, (int)K, need ? space.data_ptr() : nullptr, need, (uint32_t)flags, stream_of(*x));
+                       (int)N, (int)K, need ? space.data_ptr() : nullptr, need, flags, stream_of(*x));
     } else {
         st = g_linear(x->const_data_ptr(), xs->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias,
-                      out.data_ptr(), (int)M, (int)N, (int)K, (uint32_t)flags, stream_of(*x));
+                      out.data_ptr(), (int)M, (int)N, (int)K, flags, stream_of(*x));
     }
     return st ? PyLong_FromLong(st) : item(out);
     END_HANDLE_TH_ERRORS

@@ -81,3 +81,29 @@ def test_refusals(path):
         with pytest.raises(m.BF16LinearError) as e:
             f()
         assert e.value.status == status
+
+
+def test_sizes_past_32_bits_are_refused(path):
+    """Arguments that no C int holds are errors and not what their low 32 bits say."""
+    m, wide = path, (1 << 32) + 64
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device=DEV)
+    w, (q, s) = torch.ones(64, dtype=torch.bfloat16, device=DEV), m.quant_mxfp4(x)
+    row, codes = torch.zeros(1, wide, dtype=torch.bfloat16, device=DEV), torch.zeros(1, wide // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(1, wide // 32, dtype=torch.uint8, device=DEV)
+    calls = [lambda: m.rmsnorm(row, row[0]), lambda: m.rmsnorm(row, row[0], quant="mxfp4", bf16_out=False),
+             lambda: m.quant_mxfp4(row), lambda: m.dequant_mxfp4(codes, scales),
+             lambda: m.bf16_linear_mxfp4(codes, scales, codes, scales),
+             lambda: m.bf16_linear_mxfp4_dynamic(row, codes, scales),
+             lambda: m.route(row, 2), lambda: m.route(x, (1 << 32) + 2)]
+    for over in (1 << 32, 1 << 70):
+        calls += [lambda o=o: m.route(x, 2, **o) for o in (dict(groups=over + 1), dict(top_groups=over + 1), dict(group_best=over + 1))]
+        calls += [lambda f=f: m.rmsnorm(x, w, flags=f) for f in (over, -over)]
+        calls += [lambda f=f: f(over) for f in (lambda v: m.quant_mxfp4(x, flags=v), lambda v: m.dequant_mxfp4(q, s, flags=v),
+                                                lambda v: m.bf16_linear_mxfp4(q, s, q, s, flags=v),
+                                                lambda v: m.bf16_linear_mxfp4_dynamic(x, q, s, flags=v),
+                                                lambda v: m.route(x, 2, flags=v))]
+    for f in calls:
+        with pytest.raises(m.BF16LinearError) as e:
+            f()
+        assert e.value.status in (-1, -6)
+    assert m.mxfp4_dynamic_workspace(17, 64, wide) == 0
