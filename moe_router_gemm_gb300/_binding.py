@@ -80,7 +80,7 @@ def _load_calls(lib):
         spec = importlib.util.spec_from_file_location("_torch_calls", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
-    except ImportError:
+    except (ImportError, OSError):
         return None
     mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.bf16_rmsnorm, lib.bf16_route, lib.bf16_quant_mxfp4, lib.bf16_dequant_mxfp4, lib.bf16_linear_mxfp4,

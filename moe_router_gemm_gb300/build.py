@@ -12,6 +12,8 @@ statically, so the library needs only the driver at run time).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import hashlib
 import os
 import subprocess
 import sys
@@ -56,23 +58,36 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-# The compiled marshalling module (csrc/torch_calls.cpp): one file per PyTorch release, since it uses PyTorch's C++ types.
-def calls_path() -> str:
+CALLS_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared"]
+
+
+def _calls_stem() -> str:
+    import sysconfig
+
     import torch
-    return os.path.join(PKG, "_torch_calls_" + "".join(c if c.isalnum() else "_" for c in torch.__version__) + ".so")
+    return "_torch_calls_" + "".join(c if c.isalnum() else "_" for c in f"{torch.__version__}_{sysconfig.get_config_var('SOABI')}") + "_"
+
+
+def calls_path() -> str:
+    """The compiled marshalling module (csrc/torch_calls.cpp).  It uses PyTorch's and Python's C++ types and the library's
+    argument lists, so its name says which release, which Python and which sources it was built from: a file that stands
+    there is never one of another."""
+    h = hashlib.sha256(" ".join(CALLS_FLAGS).encode())
+    for path in (os.path.join(CSRC, "torch_calls.cpp"), os.path.join(INCLUDE, "bf16_linear.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return os.path.join(PKG, f"{_calls_stem()}{h.hexdigest()[:16]}.so")
 
 
 def build_calls(force: bool = False) -> str | None:
     """Compile the marshalling module for the installed PyTorch; None where it cannot be (the binding then calls the library
     through ctypes alone)."""
-    src = os.path.join(CSRC, "torch_calls.cpp")
     try:
         import sysconfig
 
         import torch
         out = calls_path()
-        inputs = (src, os.path.join(INCLUDE, "bf16_linear.h"), os.path.abspath(__file__))
-        if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in inputs):
+        if not force and os.path.exists(out):
             return out
         root = os.path.dirname(torch.__file__)
         cuda = os.environ.get("CUDA_HOME") or "/usr/local/cuda"
@@ -80,14 +95,18 @@ def build_calls(force: bool = False) -> str | None:
                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
         libs = os.path.join(root, "lib")
         tmp = out + f".tmp{os.getpid()}"
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               *("-I" + i for i in inc), src, "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs,
+        cmd = ["g++", *CALLS_FLAGS, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *("-I" + i for i in inc), os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs,
                "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             print(f"torch_calls.cpp does not build, calls go through ctypes:\n{r.stderr[-2000:]}", file=sys.stderr)
             return None
         os.replace(tmp, out)
+        for name in os.listdir(PKG):  # of earlier sources
+            if name.startswith(_calls_stem()) and name.endswith(".so") and name != os.path.basename(out):
+                with contextlib.suppress(FileNotFoundError):  # (another build took it)
+                    os.remove(os.path.join(PKG, name))
         return out
     except (ImportError, OSError) as e:
         print(f"torch_calls.cpp is not built, calls go through ctypes: {e}", file=sys.stderr)
