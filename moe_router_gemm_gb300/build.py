@@ -120,8 +120,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ex.submit(build_calls, force)
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(lambda s: _compile(os.path.join(CSRC, s), extra), SOURCES))
+        calls.result()  # (raises what build_calls did not handle)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -72,3 +72,20 @@ def test_forcing_builds_again(tree):
 
 def test_the_binding_loads_what_the_build_names(tree):
     assert _binding._load_calls(None) is None  # nothing was built here
+
+
+def test_what_the_module_build_raises_is_raised(tree, monkeypatch):
+    """Only what build_calls itself handles turns into calls through ctypes."""
+    root, compiler = tree
+    monkeypatch.setattr(build, "LIB", str(root / "pkg" / "lib.so"))
+    monkeypatch.setattr(build, "BUILD", str(root / "objects"))
+    monkeypatch.setattr(build, "up_to_date", lambda: False)
+
+    def broken(force=False):
+        raise ValueError("a mistake in build_calls")
+
+    monkeypatch.setattr(build, "build_calls", broken)
+    with pytest.raises(ValueError, match="a mistake"):
+        build.build()
+    monkeypatch.setattr(build, "build_calls", lambda force=False: None)
+    assert build.build() == build.LIB
