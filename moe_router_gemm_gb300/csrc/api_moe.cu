@@ -201,8 +201,7 @@ extern "C" int bf16_linear_mxfp4_dynamic(const void *x, const void *wq, const vo
         int32_t *status = nullptr;
         st = current_device_status(&dev, &status);
         if (st != BF16L_OK) return st;
-        // (planned for the same number of SMs as the workspace was)
-        return result(launch_mxfp4_split(x, nullptr, wq, ws, bias, out, M, N, K, kGb300Sms, flags, stream, status));
+        return result(launch_mxfp4_split(x, nullptr, wq, ws, bias, out, M, N, K, dev.num_sms, flags, stream, status));
     }
     uint8_t *xq = static_cast<uint8_t *>(workspace);
     uint8_t *xs = xq + up256((size_t)M * (size_t)(K / 2));

@@ -495,6 +495,9 @@ Mxfp4SplitPlan plan_for(int tokens, int M, int N, int K, int num_sms, bool shift
 }  // namespace
 
 Mxfp4SplitPlan mxfp4_split_plan(int M, int N, int K, int num_sms, bool shifted) {
+    // One plan whatever the device's SMs: codes, a bf16 x and the workspace's size are asked for apart, and the first two
+    // have to sum in one order.
+    if (M <= 16) num_sms = kGb300Sms;
     // Where a run of x does not fit (K of 200000 and more): by TMA, stage by stage, whatever the scales' alignment.
     if (M <= 16 && plan_for(16, M, N, K, num_sms, true).smem <= kMaxSmem)
         return plan_for(16, M, N, K, num_sms, shifted);
