@@ -102,6 +102,13 @@ uint32_t as_flags(PyObject *o, bool &wide) {
     return (uint32_t)v;
 }
 
+// The interpreter is free while this lives: an allocation may wait for the device, and a launch waits where the stream has
+// as many as it takes, maybe behind a host function that needs the interpreter.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 bool wrong_count(Py_ssize_t got, Py_ssize_t want) {
     if (got == want) return false;
     PyErr_Format(PyExc_TypeError, "%zd arguments, %zd are wanted", got, want);
@@ -127,15 +134,19 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (args[2] != Py_None && !(r = dense(args[2], at::kBFloat16, rows, H))) return none();
     if (quant == BF16L_QUANT_FP8 ? !(s = dense(args[5], at::kFloat, 1)) : args[5] != Py_None) return none();
     Tensor out, sum, codes, scales;
-    if (r) sum = make(*x, at::kBFloat16, {rows, H});
-    if (want) out = make(*x, at::kBFloat16, {rows, H});
-    if (quant != BF16L_QUANT_NONE) codes = make(*x, at::kByte, {rows, quant == BF16L_QUANT_MXFP4 ? H / 2 : H});
-    if (mx) scales = make(*x, at::kByte, {rows, H / 32});
-    const int st = g_rmsnorm(x->const_data_ptr(), ld, r ? r->const_data_ptr() : nullptr, w->const_data_ptr(),
-                             out.defined() ? out.data_ptr() : nullptr, sum.defined() ? sum.data_ptr() : nullptr,
-                             codes.defined() ? codes.data_ptr() : nullptr, scales.defined() ? scales.data_ptr() : nullptr,
-                             s ? static_cast<const float *>(s->const_data_ptr()) : nullptr, rows, (int)H, (float)eps,
-                             quant, flags, stream_of(*x));
+    int st;
+    {
+        const Unlocked unlocked;
+        if (r) sum = make(*x, at::kBFloat16, {rows, H});
+        if (want) out = make(*x, at::kBFloat16, {rows, H});
+        if (quant != BF16L_QUANT_NONE) codes = make(*x, at::kByte, {rows, quant == BF16L_QUANT_MXFP4 ? H / 2 : H});
+        if (mx) scales = make(*x, at::kByte, {rows, H / 32});
+        st = g_rmsnorm(x->const_data_ptr(), ld, r ? r->const_data_ptr() : nullptr, w->const_data_ptr(),
+                       out.defined() ? out.data_ptr() : nullptr, sum.defined() ? sum.data_ptr() : nullptr,
+                       codes.defined() ? codes.data_ptr() : nullptr, scales.defined() ? scales.data_ptr() : nullptr,
+                       s ? static_cast<const float *>(s->const_data_ptr()) : nullptr, rows, (int)H, (float)eps, quant,
+                       flags, stream_of(*x));
+    }
     return st ? PyLong_FromLong(st) : pack({out, sum, codes, scales});
     END_HANDLE_TH_ERRORS
 }
@@ -157,11 +168,16 @@ PyObject *route(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t T = l->size(0), E = l->size(1), ld = pitch(*l);
     if (ld < 0 || E > INT32_MAX || k < 1 || k > 1024) return none();
     if (args[3] != Py_None && !(b = dense(args[3], at::kFloat, E))) return none();
-    Tensor w = make(*l, at::kFloat, {T, k}), ids = make(*l, at::kInt, {T, k});
-    const int st = g_route(l->const_data_ptr(), ld, b ? static_cast<const float *>(b->const_data_ptr()) : nullptr,
-                           static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(ids.data_ptr()), T, (int)E, k,
-                           scoring, groups, top, best, renorm, (float)scale, l->scalar_type() == at::kBFloat16, flags,
-                           stream_of(*l));
+    Tensor w, ids;
+    int st;
+    {
+        const Unlocked unlocked;
+        w = make(*l, at::kFloat, {T, k});
+        ids = make(*l, at::kInt, {T, k});
+        st = g_route(l->const_data_ptr(), ld, b ? static_cast<const float *>(b->const_data_ptr()) : nullptr,
+                     static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(ids.data_ptr()), T, (int)E, k, scoring,
+                     groups, top, best, renorm, (float)scale, l->scalar_type() == at::kBFloat16, flags, stream_of(*l));
+    }
     return st ? PyLong_FromLong(st) : pack({w, ids});
     END_HANDLE_TH_ERRORS
 }
@@ -178,8 +194,14 @@ PyObject *quant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!x || x->dim() != 2 || x->scalar_type() != at::kBFloat16 || !x->is_contiguous()) return none();
     const int64_t rows = x->size(0), K = x->size(1);
     if (K > INT32_MAX) return none();
-    Tensor q = make(*x, at::kByte, {rows, K / 2}), s = make(*x, at::kByte, {rows, K / 32});
-    const int st = g_quant(x->const_data_ptr(), rows, (int)K, q.data_ptr(), s.data_ptr(), flags, stream_of(*x));
+    Tensor q, s;
+    int st;
+    {
+        const Unlocked unlocked;
+        q = make(*x, at::kByte, {rows, K / 2});
+        s = make(*x, at::kByte, {rows, K / 32});
+        st = g_quant(x->const_data_ptr(), rows, (int)K, q.data_ptr(), s.data_ptr(), flags, stream_of(*x));
+    }
     return st ? PyLong_FromLong(st) : pack({q, s});
     END_HANDLE_TH_ERRORS
 }
@@ -197,9 +219,13 @@ PyObject *dequant_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t rows = q->size(0), h = q->size(1);
     const Tensor *s = dense(args[1], at::kByte, rows, h / 16);
     if (!s || 2 * h > INT32_MAX) return none();
-    Tensor out = make(*q, at::kBFloat16, {rows, 2 * h});
-    const int st = g_dequant(q->const_data_ptr(), s->const_data_ptr(), rows, (int)(2 * h), out.data_ptr(),
-                             flags, stream_of(*q));
+    Tensor out;
+    int st;
+    {
+        const Unlocked unlocked;
+        out = make(*q, at::kBFloat16, {rows, 2 * h});
+        st = g_dequant(q->const_data_ptr(), s->const_data_ptr(), rows, (int)(2 * h), out.data_ptr(), flags, stream_of(*q));
+    }
     return st ? PyLong_FromLong(st) : item(out);
     END_HANDLE_TH_ERRORS
 }
@@ -222,17 +248,22 @@ PyObject *linear_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!ws || !dense(args[2], at::kByte, N, K / 2) || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return none();
     if (!dynamic && !(xs = dense(args[1], at::kByte, M, K / 32))) return none();
     if (args[4] != Py_None && !(b = dense(args[4], at::kBFloat16, N))) return none();
-    Tensor out = make(*x, at::kBFloat16, {M, N}), space;
+    Tensor out;
     const void *bias = b ? b->const_data_ptr() : nullptr;
     int st;
-    if (dynamic) {
-        const size_t need = g_workspace((int)M, (int)N, (int)K);
-        if (need) space = make(*x, at::kByte, {(int64_t)need});  // freed on return, to this stream's own memory
-        st = g_dynamic(x->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias, out.data_ptr(), (int)M,
-                       (int)N, (int)K, need ? space.data_ptr() : nullptr, need, flags, stream_of(*x));
-    } else {
-        st = g_linear(x->const_data_ptr(), xs->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias,
-                      out.data_ptr(), (int)M, (int)N, (int)K, flags, stream_of(*x));
+    {
+        const Unlocked unlocked;
+        out = make(*x, at::kBFloat16, {M, N});
+        if (dynamic) {
+            Tensor space;  // freed on return, to this stream's own memory
+            const size_t need = g_workspace((int)M, (int)N, (int)K);
+            if (need) space = make(*x, at::kByte, {(int64_t)need});
+            st = g_dynamic(x->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias, out.data_ptr(), (int)M,
+                           (int)N, (int)K, need ? space.data_ptr() : nullptr, need, flags, stream_of(*x));
+        } else {
+            st = g_linear(x->const_data_ptr(), xs->const_data_ptr(), wq->const_data_ptr(), ws->const_data_ptr(), bias,
+                          out.data_ptr(), (int)M, (int)N, (int)K, flags, stream_of(*x));
+        }
     }
     return st ? PyLong_FromLong(st) : item(out);
     END_HANDLE_TH_ERRORS

@@ -1,4 +1,7 @@
 """The calls that csrc/torch_calls.cpp marshals give what the ctypes path gives, and leave the same errors."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -107,3 +110,37 @@ def test_sizes_past_32_bits_are_refused(path):
             f()
         assert e.value.status in (-1, -6)
     assert m.mxfp4_dynamic_workspace(17, 64, wide) == 0
+
+
+def test_other_threads_run_while_a_launch_waits(path):
+    """A launch waits when the stream has as many as it takes; the interpreter is free meanwhile."""
+    x = torch.ones(4, 256, dtype=torch.bfloat16, device=DEV)
+    w, logits = x[0].contiguous(), torch.zeros(4, 64, device=DEV)
+    q, sc = path.quant_mxfp4(x)
+    calls = [lambda: path.rmsnorm(x, w), lambda: path.route(logits, 2), lambda: path.quant_mxfp4(x),
+             lambda: path.dequant_mxfp4(q, sc), lambda: path.bf16_linear_mxfp4(q, sc, q, sc),
+             lambda: path.bf16_linear_mxfp4_dynamic(x, q, sc)]
+    stream = torch.cuda.Stream()
+    for call in calls:
+        took = []
+
+        def work():
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(1_200_000_000)  # most of a second
+                for _ in range(3000):
+                    t = time.perf_counter()
+                    call()
+                    took.append(time.perf_counter() - t)
+
+        torch.cuda.synchronize()
+        worker = threading.Thread(target=work)
+        worker.start()
+        gap, last = 0.0, time.perf_counter()
+        while worker.is_alive():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap, last = max(gap, now - last), now
+        worker.join()
+        torch.cuda.synchronize()
+        assert len(took) == 3000 and max(took) > 0.1, "no launch had to wait"
+        assert gap < max(took) / 2, f"{gap:.3f} s without the interpreter, in a call of {max(took):.3f} s"
