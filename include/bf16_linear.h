@@ -526,8 +526,12 @@ typedef enum {
  * (FP8, MXFP8) or [rows][H / 2] (MXFP4), scales[rows][H / 32] (MXFP8, MXFP4);
  * `scale` is the per-tensor scale of FP8 (device, fp32).  out may be NULL when
  * quant is not NONE.  residual_out may be residual itself (in place), and
- * nothing else may overlap an output.  A NaN or an infinity in a row makes that
- * row's y NaN (as the formula does) and touches no other row.
+ * nothing else may overlap an output.  As the formula has it, a NaN in a row
+ * makes all of that row's y NaN, and an infinity makes y NaN at its own place and
+ * 0 at the finite ones; no other row is touched.  The sum of squares is fp32 too:
+ * a finite row whose squares sum to 2^128 or more (magnitudes of about 2^64 /
+ * sqrt(H)) gives zeros, and with eps == 0 a row whose squares are all below
+ * 2^-150 gives infinities (NaN where h is 0).
  * Any H >= 1; H % 32 == 0 for the MX formats (else BF16L_EUNSUPPORTED).
  * x needs 2-byte, scale 4-byte, scales 1-byte alignment, the rest 16-byte.
  */

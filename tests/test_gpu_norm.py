@@ -203,3 +203,19 @@ def test_the_longest_rows(lib):
     w[-700:] = (1 + torch.rand(700, device=DEV)).to(torch.bfloat16)
     w[1 << 30] = 3.0
     assert torch.equal(lib.rmsnorm(x, w, eps=0.0).out[0], w)
+
+
+@pytest.mark.parametrize("H", [40, 512, 2001, 40000])
+def test_squares_past_fp32(lib, H):
+    """Rows whose squares fp32 does not hold: zeros above, infinities below where eps is 0, and only in those rows."""
+    x, _, w = _inputs(4, H, 8, residual=False)
+    x = x.sign() + (x == 0)
+    clean = lib.rmsnorm(x, w, eps=0.0).out
+    x[1] *= 2.0 ** 64
+    x[2] *= 2.0 ** -76
+    y = lib.rmsnorm(x, w, eps=0.0).out
+    assert (y[1] == 0).all() and torch.equal(y[2], torch.inf * (x[2].float() * w.float()).sign().to(y.dtype))
+    assert torch.equal(y[[0, 3]], clean[[0, 3]])
+    y = lib.rmsnorm(x, w).out
+    assert (y[1] == 0).all()
+    _check(lib, x[2:3], None, w, 1e-6, None, lib.rmsnorm(x[2:3], w))
