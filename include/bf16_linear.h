@@ -558,8 +558,9 @@ typedef enum { BF16L_SCORE_SOFTMAX = 0, BF16L_SCORE_SIGMOID = 1 } bf16l_score;
  *           when renormalize is nonzero, times `scale`.
  * A logit of -inf takes its expert out: score 0, and chosen only when too few
  * others are left (lowest index first).  A row of -inf alone has weights 0.  A
- * NaN logit ranks with -inf; it makes every weight of a softmax row NaN.  The
- * ids are always k different experts.
+ * NaN key ranks with -inf.  A NaN logit is one; in a softmax row it, or a logit of
+ * +inf, makes every score NaN, and so every weight, and where the scores are the
+ * keys every finite logit's key too.  The ids are always k different experts.
  * 1 <= k <= 32, experts <= 1024, groups <= 32 dividing experts, k <= top_groups *
  * experts / groups, group_best <= experts / groups (else BF16L_EINVAL or, above
  * the limits, BF16L_EUNSUPPORTED).  Element alignment for every pointer.

@@ -195,3 +195,16 @@ def test_empty_and_refusals(lib):
         lib.route(x, 2, bias=torch.zeros(63, device=DEV))
     with pytest.raises(TypeError):
         lib.route(x.double(), 2)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scores_without_a_value(lib, bad):
+    """A NaN or +inf logit leaves a softmax row no scores: ranked by logits the choice stands, ranked by scores it is the lowest."""
+    logits = _logits(3, 64, 2)
+    logits[1, 20] = bad
+    best = torch.where(torch.isnan(logits[1]), -float("inf"), logits[1]).sort(descending=True, stable=True).indices[:4]
+    w, ids = lib.route(logits, 4)
+    assert w[1].isnan().all() and ids[1].tolist() == best.tolist() and not w[[0, 2]].isnan().any()
+    for kw in (dict(bias=torch.rand(64, device=DEV)), dict(groups=8, top_groups=2, group_best=2)):
+        w, ids = lib.route(logits, 4, **kw)
+        assert w[1].isnan().all() and ids[1].tolist() == [0, 1, 2, 3] and not w[[0, 2]].isnan().any()
