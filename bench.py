@@ -2,6 +2,7 @@
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--workload router|smallest|decode|mlp|prefill] [--pdl]
+    python bench.py --operators    (the norm, routing and MXFP4 cases of perf/operators.py)
 
 Default workload: the MoE router sweep, M = 1..16 x (K, N) in {(4096,256),
 (6144,256), (7168,256), (7168,384), (2880,128)} (80 shapes), seeded synthetic
@@ -1109,6 +1110,78 @@ def mxfp8_arm(args, points):
                       "workload": workload_desc(args.workload), "shapes": res}))
 
 
+def operator_floor_us(work, peaks):
+    """The least time of a pass (perf/operators.py: work) at the measured copy and bf16 rates, and which of them sets it."""
+    by = {"hbm": work["bytes"] / peaks["hbm_gbs"] / 1e3, "bf16 tensor": work["flops"] / peaks["bf16_tflops"] / 1e6}
+    bound = max(by, key=by.get)
+    return by[bound], bound
+
+
+def operators_arm(args):
+    """The cases of perf/operators.py (norm, routing, MXFP4), one JSON line each.
+
+    device_us: a CUDA graph of calls on three sets of inputs in turn (those of a few megabytes stay in L2), the median of
+    --steps replays by events.  call_us: a pass among others from Python, host work included.  plain_us: the plain form's,
+    likewise (its calls cannot all be captured)."""
+    import importlib.util
+
+    import moe_router_gemm_gb300 as lib
+    from moe_router_gemm_gb300 import build as _build
+    _build.build()
+    lib.load()
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    peaks = load_peaks()
+    steps, sets, calls = max(args.steps, 1), 3, 24
+
+    def events(f):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) * 1e3
+
+    def passes(states, n):
+        for i in range(n):
+            mod.run(states[i % sets])
+
+    for case in mod.listed():
+        work = mod.work(case)
+        states = [mod.prepare(case, seed) for seed in range(sets)]
+        sampler = ClockSampler(torch.cuda.current_device())
+        sampler.start()
+        mod.own = True
+        passes(states, args.warmup * sets)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            passes(states, calls)
+        for _ in range(args.warmup):
+            graph.replay()
+        device_us = statistics.median(events(graph.replay) for _ in range(steps)) / calls
+        call_us = []
+        for _ in range(steps):
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            passes(states, 10 * calls)
+            torch.cuda.synchronize()
+            call_us.append((time.perf_counter() - t) * 1e6 / (10 * calls))
+        clocks = sampler.stop()
+        del graph
+        mod.own = False
+        passes(states, args.warmup)
+        torch.cuda.synchronize()
+        plain_us = statistics.median(events(lambda: passes(states, sets)) for _ in range(steps)) / sets
+        floor, bound = operator_floor_us(work, peaks)
+        print(json.dumps({"mode": "operators", "case": case["name"], "floor_us": round(floor, 3), "floor_by": bound,
+                          "plain_us": round(plain_us, 1), "device_us": round(device_us, 2),
+                          "call_us": round(statistics.median(call_us), 2), "steps": steps, "clocks": clocks}), flush=True)
+        del states
+        torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------
 # main
 # ---------------------------------------------------------------------------
@@ -1128,6 +1201,8 @@ def main():
                     help="time the per-tensor FP8 linear (bf16_linear_fp8) on the workload's shapes instead")
     ap.add_argument("--mxfp8", action="store_true",
                     help="time the MXFP8 linear (bf16_linear_mxfp8) on the workload's shapes instead")
+    ap.add_argument("--operators", action="store_true",
+                    help="time the norm, routing and MXFP4 cases of perf/operators.py instead")
     ap.add_argument("--pdl", action="store_true",
                     help="launch with programmatic dependent launch (BF16L_FLAG_PDL): back-to-back calls overlap")
     ap.add_argument("--no-pdl-variant", action="store_true",
@@ -1217,6 +1292,9 @@ def main():
         return
     if args.mxfp8:
         mxfp8_arm(args, points)
+        return
+    if args.operators:
+        operators_arm(args)
         return
     r = gpu_arm(args, points, rank, world)
     shapes, per_us = r["shapes"], r["per_shape_us"]

@@ -121,3 +121,12 @@ def test_clock_record_and_slowdown_retime_rule():
     assert c["reasons"] == ["hw_slowdown", "sw_power_cap", "sw_thermal_slowdown"]
     assert bench.slowdowns(c) == ["hw_slowdown", "sw_thermal_slowdown"]
     assert bench.slowdowns({"sm_mhz": None, "reasons": ["nvidia-smi unavailable"]}) == []
+
+
+def test_operator_floor():
+    """The larger of the two times, with its name."""
+    peaks = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0}
+    us, by = bench.operator_floor_us({"bytes": 6_800_000, "flops": 1_000}, peaks)
+    assert by == "hbm" and abs(us - 1.0) < 1e-9
+    us, by = bench.operator_floor_us({"bytes": 1_000, "flops": 3_800_000_000}, peaks)
+    assert by == "bf16 tensor" and abs(us - 2.0) < 1e-9
