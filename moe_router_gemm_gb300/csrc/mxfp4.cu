@@ -4,8 +4,8 @@
 // magnitude by a quad shuffle on the bf16 bits, the scale exponent from its exponent
 // field, one exact multiplication by 2^-s and the hardware's e2m1 conversion (nearest
 // even, saturating) per value.  2 bytes in and 0.53 out per element, and the reverse:
-// bound by HBM.  7168 x 7168: 19.5 us quantised (98% of the copy bandwidth; 22.7 with
-// loads that also fill L1), 22.2 us back (86%).
+// bound by HBM.  7168 x 7168: 19.4 us quantised (98% of the copy bandwidth; 22.7 with
+// loads that also fill L1), 22.3 us back (86%).
 #include <cuda_runtime.h>
 
 #include "moe.h"

@@ -18,9 +18,9 @@
 //     the words to one of the TMEM slots: W words at columns 0 and 8 of the slot,
 //     token words at 16 and 24.  Rows that do not start on 8-byte boundaries (K % 256) go
 //     by cp.async in 16-byte blocks, each row's once for the CTA, and are shifted on the
-//     way out of shared memory: 558 x 2112 x 6176 16.8 us, 13 x 5760 x 2880 6.7 (33.6 and
-//     7.2 by words from the row's first byte on: three loads for a chunk and row, each a
-//     cache line per lane);
+//     way out of shared memory: from codes 558 x 2112 x 6176 16.8 us, 13 x 5760 x 2880 6.7
+//     (33.6 and 7.2 by words from the row's first byte on: three loads for a chunk and row,
+//     each a cache line per lane);
 //   * M <= 16: all threads put the CTA's whole run of x into shared memory, in the layout
 //     that TMA would have written, while the first W chunks are on their way: from codes
 //     (a TMA box that is mostly past M is slow: 1 x 14336 x 4096 16 us with it), or
@@ -30,13 +30,15 @@
 //     order, adds the bias and rounds: the order never changes;
 //   * K past its end: codes are zero (TMA fill), scale bytes 1.0.
 //
-// Bound by latency: launch, TMEM and barriers 2.0 us, cold codes 1 to 1.5, scales 1.2,
-// the join 0.5 (16 tokens) to 2 (64).  From codes / from bf16: 1 x 2112 x 7168 6.0 /
-// 6.2 us, 16 x 2112 x 7168 6.7 / 8.3, 1 x 14336 x 4096 9.6 / 9.8 (3.3 TB/s), 64 x 14336
-// x 4096 11.3.  Measured and not taken: W's rows asked into L2 before the wait for the
-// previous kernel (0 to 1 us slower), TMA boxes issued by a lane per stage (no change),
-// scale words asked for before x is staged (-0.4 to +0.3 us), 128-token tiles (128 x
-// 2112 x 7168 9.9 us, 8.4 with 64).
+// This form is bound by its latencies in series: launch, TMEM and barriers 2.0 us, cold
+// codes 1 to 1.5, scales 1.2, the join 0.5 (16 tokens) to 2 (64).  From codes / from bf16,
+// weights not in L2: 1 x 2112 x 7168 6.0 / 6.2 us, 16 x 2112 x 7168 6.8 / 8.3, 1 x 14336 x
+// 4096 10.0 / 9.8 (3.2 TB/s), 64 x 14336 x 4096 11.4 / 13.4.  They are not the product's
+// own bound: the bf16 linear, on nearly four times the bytes, takes 5.3, 7.4, 18.3 and 24.0.
+// Measured and not taken: W's rows asked into L2 before the wait for the previous kernel (0
+// to 1 us slower), TMA boxes issued by a lane per stage (no change), scale words asked for
+// before x is staged (-0.4 to +0.3 us), 128-token tiles (128 x 2112 x 7168 9.9 us, 8.4 with
+// 64).
 #include <cuda_runtime.h>
 
 #include "moe.h"

@@ -3,8 +3,8 @@
 //
 //     h = x  or  RNE_bf16(x + residual);  y = h / sqrt(mean(h^2) + eps) * weight
 //
-// One pass: a row stays in registers between the sum of squares and the output, so
-// each input is read once and each output written once: HBM is the bound.  The sum
+// One pass: a row stays on the SM between the sum of squares and the output, so each
+// input is read from memory once and each output written once: HBM is the bound.  The sum
 // runs in fp32: each thread over its own values in order, then a butterfly, then the
 // warps' sums by a butterfly, so it is the same from run to run.
 //
@@ -13,20 +13,26 @@
 //     i, i + threads, ...; four neighbouring lanes hold a 32-element scale block.  The
 //     weight stays in registers from row to row, and the next row's loads go out
 //     before this row's sum, so memory is busy through the reduction.  8192 x 7168
-//     with a residual: 70.5 us to bf16 (98% of the copy bandwidth), 83 us to bf16 and
-//     MXFP8 (94%); without one 40.5 us (85%).
+//     with a residual: 71 us to bf16 (97% of the copy bandwidth), 83 us to bf16 and
+//     MXFP8 (94%); without one 40.4 us (86%), and 59 to bf16 and MXFP8 (74%) or MXFP4
+//     (66%).  Not all of a row is in registers everywhere: blocks of up to 1024 threads
+//     have 64 a thread, of which two vectors with MX output spill 32 to 36 bytes, and four
+//     (H above 16384) 188 to 288: 8192 x 20000 212 us (45%).
 //   * norm_shift_kernel: odd lengths and strides.  The dense tensors' vectors start on
 //     16-byte boundaries, so a row is up to 7 values, vectors, up to 7 values; a
 //     vector of x that lies across two 16-byte blocks is shifted out of both; the
 //     weight, which meets the vectors at a different place in every row, comes from
-//     shared memory.  A value at a time these took two to seven times as long:
-//     2000 x 2881 with a residual 27 us (10.9 here), 8192 x 7168 of 7300 columns 114
-//     (78), 8192 x 7168 of 7169 columns with MXFP8 295 (100).  (The second block from
-//     the next lane instead of a load of its own: 2048 x 1536 of 2113 columns 11.5 us,
-//     6.3 with the load.)
-//   * norm_any_kernel: what is left (H below 64, or above 16384 and odd in some way): one
-//     value per lane and step; a warp's 32 lanes hold a scale block.  Rows of more than
-//     16384 elements are read twice (the second time from L1 or L2).
+//     shared memory.  A value at a time these took 1.5 to 3 times as long: 2000 x 2881
+//     with a residual 27 us (10.2 here; floor 6.8), 8192 x 7168 of 7300 columns 114 (78;
+//     34.6), 8192 x 7168 of 7169 columns with MXFP8 295 (100; 43.5).  8192 x 5001 of 5200
+//     takes 71 (24.1).  So 29 to 67% of the floor's rate is reached, and not HBM but this
+//     kernel's own work bounds it: the weight comes in 4-byte reads, four lanes to a bank,
+//     even where H % 8 == 0 and registers could keep it, and two shifted vectors a thread
+//     spill 36 to 204 bytes.  (The second block from the next lane instead of a load of
+//     its own: 2048 x 1536 of 2113 columns 11.5 us, 6.3 with the load.)
+//   * norm_any_kernel: what is left (off 16-byte boundaries: H below 64 or above 16384; on
+//     them: H above 32768): one value per lane and step; a warp's 32 lanes hold a scale
+//     block.  Long rows are read twice (the second time from L1 or L2).
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -204,8 +210,8 @@ __device__ __forceinline__ uint4 load_block(const uint16_t *p, const uint16_t *l
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Sixteen bytes from byte m (even, below 16) of two neighbouring blocks on.
-__device__ __forceinline__ uint4 shift_blocks(const uint4 &a, const uint4 &b, int m) {
+// Sixteen bytes from byte m (even, below 16) of two neighbouring blocks on (shift_blocks, less the odd places).
+__device__ __forceinline__ uint4 shift_blocks_even(const uint4 &a, const uint4 &b, int m) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t v[5];
 #pragma unroll
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(1024) norm_shift_kernel(const NormArgs a) {
         const long long at = r * a.H;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            c[j] = XS ? shift_blocks(h[j], h2[XS ? j : 0], xm) : h[j];
+            c[j] = XS ? shift_blocks_even(h[j], h2[XS ? j : 0], xm) : h[j];
             if (a.residual) c[j] = add_bf16x8(c[j], q[j]);
         }
         if (cedge >= 0) {

@@ -11,10 +11,13 @@
 // power of two of lanes to itself and is ranked by a butterfly and a count of the better
 // ones; groups too long for that (1023 experts in 3) by reductions over masked keys.
 //
-// About 1000 instructions a token of 256 experts in groups and 8 picks, a quarter of
-// them the exact exponentials and quotients of the scores: issue, not the 1 KB of
-// logits, is the bound.  8192 x 256: 10.9 us (28 with experts strided over the lanes
-// and two reductions a pick, 12.6 with one key per lane); softmax without groups 8.0.
+// Instructions, not the 1 KB of logits, are the bound of a long batch: a token of 256
+// experts takes 1040 with sigmoid, bias, groups and 8 picks, 570 of them up to the keys
+// and for the weights, 165 for the groups, 35 to 40 a pick (730 with softmax alone).
+// 8192 tokens then are 6.8 us of issue on all SMs, and take 11.0 us (28 with experts
+// strided over the lanes and two reductions a pick, 12.6 with one key per lane); softmax
+// without groups 7.8.  A short batch is one token's chain: 2.7 us for 1 to 16 tokens of
+// 384 and 6 picks, launch included, 3.2 for 1216, 5.1 for 2047 (1.3 of them issue).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
