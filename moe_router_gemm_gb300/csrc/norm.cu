@@ -25,11 +25,11 @@
 //     shared memory.  A value at a time these took 1.5 to 3 times as long: 2000 x 2881
 //     with a residual 27 us (10.2 here; floor 6.8), 8192 x 7168 of 7300 columns 114 (78;
 //     34.6), 8192 x 7168 of 7169 columns with MXFP8 295 (100; 43.5).  8192 x 5001 of 5200
-//     takes 71 (24.1).  So 29 to 67% of the floor's rate is reached, and not HBM but this
-//     kernel's own work bounds it: the weight comes in 4-byte reads, four lanes to a bank,
-//     even where H % 8 == 0 and registers could keep it, and two shifted vectors a thread
-//     spill 36 to 204 bytes.  (The second block from the next lane instead of a load of
-//     its own: 2048 x 1536 of 2113 columns 11.5 us, 6.3 with the load.)
+//     takes 71 (24.1).  So 29 to 67% of the floor's rate is reached and HBM is not the
+//     bound; the weight comes in 4-byte reads, four lanes to a bank, even where H % 8 == 0
+//     and registers could keep it, and two shifted vectors a thread spill 36 to 204 bytes.
+//     (The second block from the next lane instead of a load of its own: 2048 x 1536 of
+//     2113 columns 11.5 us, 6.3 with the load.)
 //   * norm_any_kernel: what is left (off 16-byte boundaries: H below 64 or above 16384; on
 //     them: H above 32768): one value per lane and step; a warp's 32 lanes hold a scale
 //     block.  Long rows are read twice (the second time from L1 or L2).
