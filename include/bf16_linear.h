@@ -610,6 +610,67 @@ int bf16_linear_mxfp4_dynamic(const void *x, const void *wq, const void *ws, con
                               int K, void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream);
 size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
 
+/*
+ * Rows whose weight depends on the row: a routing's experts, requests' adapters.
+ *
+ * bf16_group_rows — the pairs (token t, choice j) of ids[tokens][k], ordered by
+ * group: a stable counting sort, the same on every run.
+ *   offsets[groups + 1]: the pairs of group e have the positions
+ *       offsets[e] .. offsets[e + 1] - 1; offsets[0] = 0;
+ *   rows[tokens * k]: the token of the pair at each position, -1 from
+ *       offsets[groups] on;
+ *   place[tokens][k] (may be NULL): the pair's position, -1 where its id lies
+ *       outside 0 .. groups - 1 (such a pair is left out).
+ * groups <= 1024 (else BF16L_EUNSUPPORTED), tokens * k < 2^31 - 65536.  With no
+ * tokens the offsets are still written.  Launches one kernel.
+ *
+ * bf16_linear_grouped — a linear for each group's rows: for offsets[e] <= p <
+ *   offsets[e + 1]
+ *     y = x[rows[p]] @ w[e]^T (+ bias[e])        (x[p] when rows is NULL)
+ *     out[p] = RNE_bf16(y), or with swiglu RNE_bf16(g / (1 + exp(-g)) * u), g the
+ *     first N and u the last N columns of y, in fp32.
+ * x[x_rows][K], w[groups][N][K] (2 N rows a group with swiglu, the N gate rows
+ * first), bias[groups][N] (or 2 N; may be NULL), out[P][N], all bf16, dense.
+ * offsets and rows are read on the device: offsets rise, from 0 or more to at most P;
+ * where they do not, no position outside 0 .. P - 1 is read or written, and which group
+ * a position inside belongs to is not defined.  Rows of out that belong to no group are
+ * left as they were.  A value of rows outside
+ * 0 .. x_rows - 1 is taken as the nearest row.  rows NULL needs x_rows == P.
+ * K % 8 == 0, groups <= 1024, N and K <= 2^24 (else BF16L_EUNSUPPORTED).  A group's
+ * rows give the same bits whatever the other groups hold.  Pointers of bf16 data
+ * 16-byte aligned.  BF16L_FLAG_PDL has no effect: which weights are read follows from
+ * the offsets.  Launches one kernel.
+ *
+ * bf16_combine_rows — out[t] = RNE_bf16( sum over j of weights[t][j] *
+ *   y[place[t][j]] (+ addend[t]) ), in fp32, in the order of j, the addend last.
+ * y[y_rows][H], addend and out [tokens][H] (bf16, 16-byte aligned), place and
+ * weights [tokens][k]; weights NULL counts every row once, addend may be NULL or out
+ * itself.  A place outside 0 .. y_rows - 1 adds nothing.
+ *
+ * bf16_linear_lora — a linear with a low-rank adapter for each row:
+ *     out[t] = RNE_bf16( x[t] @ w^T (+ bias) + s * (x[t] @ a[id]^T) @ b[id]^T ),
+ *     id = ids[t], s = scale[id] (1 when scale is NULL);
+ * a row whose id lies outside 0 .. L - 1 has no adapter.  x[M][K], w[N][K], bias[N],
+ * a[L][R][K], b[L][N][R], out[M][N] bf16, scale[L] fp32, ids[M].  The inner values
+ * and all sums are held in 32 bits, rounded once.  K % 8 == 0, R % 8 == 0, R <= 128, L <= 1024, N
+ * and K <= 2^24 (else BF16L_EUNSUPPORTED).  `workspace` (256-byte aligned, needs no
+ * initialisation; one call at a time): bf16_linear_lora_workspace(M, N, K, R, L)
+ * bytes; a smaller one is BF16L_EINVAL.
+ *
+ * No output may overlap an input or another output, but as said.
+ */
+int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int groups, int32_t *offsets, int32_t *rows,
+                    int32_t *place, uint32_t flags, bf16l_stream_t stream);
+int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
+                        const int32_t *rows, void *out, int64_t P, int groups, int N, int K, int swiglu,
+                        uint32_t flags, bf16l_stream_t stream);
+int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
+                      void *out, int64_t tokens, int k, int H, uint32_t flags, bf16l_stream_t stream);
+int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b, const float *scale,
+                     const int32_t *ids, void *out, int M, int N, int K, int R, int L, void *workspace,
+                     size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream);
+size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *bf16_linear_strerror(int status);
 

@@ -84,7 +84,8 @@ def _load_calls(lib):
         return None
     mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.bf16_rmsnorm, lib.bf16_route, lib.bf16_quant_mxfp4, lib.bf16_dequant_mxfp4, lib.bf16_linear_mxfp4,
-        lib.bf16_linear_mxfp4_dynamic, lib.bf16_linear_mxfp4_dynamic_workspace)))
+        lib.bf16_linear_mxfp4_dynamic, lib.bf16_linear_mxfp4_dynamic_workspace, lib.bf16_group_rows,
+        lib.bf16_linear_grouped, lib.bf16_combine_rows, lib.bf16_linear_lora, lib.bf16_linear_lora_workspace)))
     return mod
 
 
@@ -162,6 +163,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.bf16_linear_mxfp4_dynamic.restype = i32
         lib.bf16_linear_mxfp4_dynamic_workspace.argtypes = [i32, i32, i32]
         lib.bf16_linear_mxfp4_dynamic_workspace.restype = ctypes.c_size_t
+        lib.bf16_group_rows.argtypes = [vp, i64, i32, i32, vp, vp, vp, u32, vp]
+        lib.bf16_group_rows.restype = i32
+        lib.bf16_linear_grouped.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, u32, vp]
+        lib.bf16_linear_grouped.restype = i32
+        lib.bf16_combine_rows.argtypes = [vp, i64, vp, vp, vp, vp, i64, i32, i32, u32, vp]
+        lib.bf16_combine_rows.restype = i32
+        lib.bf16_linear_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, ctypes.c_size_t, u32, vp]
+        lib.bf16_linear_lora.restype = i32
+        lib.bf16_linear_lora_workspace.argtypes = [i32, i32, i32, i32, i32]
+        lib.bf16_linear_lora_workspace.restype = ctypes.c_size_t
         lib.bf16_linear_probe_read.argtypes = [vp, ctypes.c_size_t, i32, i32, vp, ctypes.c_uint32, vp]
         lib.bf16_linear_probe_read.restype = i32
         lib.bf16_linear_noalloc_scratch_bytes.argtypes = []
@@ -812,6 +823,159 @@ def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, fl
                flags)
     if st != OK:
         _raise(st, f"bf16_linear_mxfp4_dynamic(M={M}, N={N}, K={K})")
+    return out
+
+
+class Groups(NamedTuple):
+    """What group_rows gives: the groups' first positions, the token of each position, and each pair's position."""
+    offsets: object
+    rows: object
+    place: object
+
+
+def group_rows(ids, groups: int, *, offsets=None, rows=None, place=None, flags: int = 0, stream=None) -> Groups:
+    """The pairs of ids[tokens, k] or ids[tokens] (int32) ordered by id, equal ids in their own order (bf16_group_rows):
+    offsets int32 [groups + 1], where each group's positions start; rows int32 [tokens * k], the token of each position, -1
+    past offsets[groups]; place int32 like ids, each pair's position, -1 for an id outside 0 .. groups - 1, which is left
+    out."""
+    if offsets is rows is place is stream is None and _calls is not None:
+        r = _calls.group_rows(ids, groups, flags)
+        if type(r) is tuple:
+            return tuple.__new__(Groups, r)
+        if r is not None:
+            _raise(r, f"bf16_group_rows(ids{tuple(ids.shape)}, groups={groups})")
+    import torch
+    i32 = torch.int32
+    if ids.dtype is not i32:
+        raise TypeError(f"ids must be torch.int32 (got {ids.dtype})")
+    if not ids.is_cuda or ids.dim() not in (1, 2):
+        raise ValueError(f"ids must be a 1-D or 2-D CUDA tensor, got {tuple(ids.shape)} on {ids.device}")
+    dev, shape = ids.device, ids.shape
+    T, k = shape[0], shape[1] if len(shape) == 2 else 1
+    p = _need(ids, "ids", i32, shape, dev)
+    _fits("bf16_group_rows", flags, k, groups)
+    if groups < 1:
+        _raise(EINVAL, f"bf16_group_rows(ids{tuple(shape)}, groups={groups})")
+    if offsets is None:
+        offsets = _empty((groups + 1,), i32, dev, stream)
+    if rows is None:
+        rows = _empty((T * k,), i32, dev, stream)
+    if place is None:
+        place = _empty(shape, i32, dev, stream)
+    st = _call(load().bf16_group_rows, dev, stream, p, T, k, groups, _need(offsets, "offsets", i32, (groups + 1,), dev),
+               _need(rows, "rows", i32, (T * k,), dev), _need(place, "place", i32, shape, dev), flags)
+    if st != OK:
+        _raise(st, f"bf16_group_rows(ids{tuple(shape)}, groups={groups})")
+    return Groups(offsets, rows, place)
+
+
+def bf16_linear_grouped(x, w, offsets, bias=None, *, rows=None, swiglu: bool = False, out=None, flags: int = 0, stream=None):
+    """A linear for each group's rows (bf16_linear_grouped): out[p] = x[p] @ w[e]^T (+ bias[e]) for the positions p from
+    offsets[e] to offsets[e + 1], x[rows[p]] where rows (int32) is given.  x[x_rows, K], w[groups, N, K], bias[groups, N] bf16,
+    offsets int32 [groups + 1]; out bf16 [len(rows) or x_rows, N], in which rows of no group are not written.  swiglu: w and
+    bias hold N gate rows and N up rows a group, out = silu(gate) * up."""
+    if out is stream is None and _calls is not None:
+        r = _calls.linear_grouped(x, w, offsets, bias, rows, swiglu, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_linear_grouped(x{tuple(x.shape)}, w{tuple(w.shape)}, swiglu={bool(swiglu)})")
+        if r is not None:
+            return r
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    if x.dtype is not bf16 or w.dtype is not bf16:
+        raise TypeError(f"x and w must be torch.bfloat16 (got {x.dtype}, {w.dtype})")
+    dev, (xr, K) = _cuda(x, "x"), x.shape
+    if w.dim() != 3 or (swiglu and w.shape[1] % 2):
+        raise ValueError(f"w must be [groups, N, K], with swiglu [groups, 2 N, K], got {tuple(w.shape)}")
+    G, W = w.shape[:2]
+    P, N = xr if rows is None else rows.numel(), W // 2 if swiglu else W
+    a, b = _need(x, "x", bf16, (xr, K), dev), _need(w, "w", bf16, (G, W, K), dev)
+    c = _need(offsets, "offsets", i32, (G + 1,), dev)
+    d = None if rows is None else _need(rows, "rows", i32, (P,), dev)
+    e = None if bias is None else _need(bias, "bias", bf16, (G, W), dev)
+    _fits("bf16_linear_grouped", flags, G, W, K)
+    if out is None:
+        out = _empty((P, N), bf16, dev, stream)
+    st = _call(load().bf16_linear_grouped, dev, stream, a, xr, b, e, c, d, _need(out, "out", bf16, (P, N), dev), P, G, N, K,
+               bool(swiglu), flags)
+    if st != OK:
+        _raise(st, f"bf16_linear_grouped(x{tuple(x.shape)}, w{tuple(w.shape)}, swiglu={bool(swiglu)})")
+    return out
+
+
+def combine_rows(y, place, weights=None, addend=None, *, out=None, flags: int = 0, stream=None):
+    """out[t] = sum over j of weights[t, j] * y[place[t, j]] (+ addend[t]) in bf16, summed in fp32 (bf16_combine_rows).
+    y[y_rows, H] and addend[tokens, H] bf16, place[tokens, k] int32, weights[tokens, k] fp32 (None: all 1).  A place outside y
+    adds nothing.  out may be addend itself (in place)."""
+    if out is stream is None and _calls is not None:
+        r = _calls.combine_rows(y, place, weights, addend, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_combine_rows(y{tuple(y.shape)}, place{tuple(place.shape)})")
+        if r is not None:
+            return r
+    import torch
+    bf16 = torch.bfloat16
+    dev, (yr, H) = _cuda(y, "y"), y.shape
+    if place.dim() != 2:
+        raise ValueError(f"place must be [tokens, k], got {tuple(place.shape)}")
+    T, k = place.shape
+    a, b = _need(y, "y", bf16, (yr, H), dev), _need(place, "place", torch.int32, (T, k), dev)
+    c = None if weights is None else _need(weights, "weights", torch.float32, (T, k), dev)
+    d = None if addend is None else _need(addend, "addend", bf16, (T, H), dev)
+    _fits("bf16_combine_rows", flags, k, H)
+    if out is None:
+        out = _empty((T, H), bf16, dev, stream)
+    st = _call(load().bf16_combine_rows, dev, stream, a, yr, b, c, d, _need(out, "out", bf16, (T, H), dev), T, k, H, flags)
+    if st != OK:
+        _raise(st, f"bf16_combine_rows(y{tuple(y.shape)}, place{tuple(place.shape)})")
+    return out
+
+
+def lora_workspace(M: int, N: int, K: int, R: int, L: int) -> int:
+    """Workspace bytes of bf16_linear_lora (0 for sizes that it refuses)."""
+    return int(load().bf16_linear_lora_workspace(M, N, K, R, L)) if max(M, N, K, R, L) < 1 << 31 else 0
+
+
+def bf16_linear_lora(x, w, a, b, ids, bias=None, *, scale=None, out=None, workspace=None, flags: int = 0, stream=None):
+    """A linear with a low-rank adapter for each row (bf16_linear_lora): out[t] = x[t] @ w^T (+ bias) +
+    scale[id] * (x[t] @ a[id]^T) @ b[id]^T, id = ids[t]; rows whose id lies outside 0 .. L - 1 have none.  x[M, K], w[N, K],
+    a[L, R, K], b[L, N, R], bias[N] bf16, ids[M] int32, scale[L] fp32 (None: 1).  `workspace`: a contiguous CUDA tensor of at
+    least lora_workspace(M, N, K, R, L) bytes to reuse from call to call on one stream; allocated for the call when None."""
+    if out is workspace is stream is None and _calls is not None:
+        r = _calls.linear_lora(x, w, a, b, ids, bias, scale, flags)
+        if type(r) is int:
+            _raise(r, f"bf16_linear_lora(x{tuple(x.shape)}, w{tuple(w.shape)}, a{tuple(a.shape)})")
+        if r is not None:
+            return r
+    import torch
+    bf16 = torch.bfloat16
+    if x.dtype is not bf16 or w.dtype is not bf16:
+        raise TypeError(f"x and w must be torch.bfloat16 (got {x.dtype}, {w.dtype})")
+    dev, (M, K) = _cuda(x, "x"), x.shape
+    if w.dim() != 2 or a.dim() != 3:
+        raise ValueError(f"need w[N, K] and a[L, R, K], got {tuple(w.shape)} and {tuple(a.shape)}")
+    N, (L, R) = w.shape[0], a.shape[:2]
+    args = [_need(x, "x", bf16, (M, K), dev), _need(w, "w", bf16, (N, K), dev),
+            None if bias is None else _need(bias, "bias", bf16, (N,), dev), _need(a, "a", bf16, (L, R, K), dev),
+            _need(b, "b", bf16, (L, N, R), dev), None if scale is None else _need(scale, "scale", torch.float32, (L,), dev),
+            _need(ids, "ids", torch.int32, (M,), dev)]
+    _fits("bf16_linear_lora", flags, M, N, K, R, L)
+    if out is None:
+        out = _empty((M, N), bf16, dev, stream)
+    lib = load()
+    wp, wn = None, 0
+    if workspace is None:
+        wn = lib.bf16_linear_lora_workspace(M, N, K, R, L)
+        if wn:
+            workspace = _empty((wn,), torch.uint8, dev, stream)
+            wp = workspace.data_ptr()
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on x's device")
+    else:
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _call(lib.bf16_linear_lora, dev, stream, *args, _need(out, "out", bf16, (M, N), dev), M, N, K, R, L, wp, wn, flags)
+    if st != OK:
+        _raise(st, f"bf16_linear_lora(M={M}, N={N}, K={K}, R={R}, L={L})")
     return out
 
 

@@ -68,6 +68,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_mxfp8();
         if (!e) e = init_mxfp4_pair();
         if (!e) e = init_mxfp4_split();
+        if (!e) e = init_group();
     }
     s.err = e;
 }

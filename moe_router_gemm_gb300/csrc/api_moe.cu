@@ -42,6 +42,8 @@ int result(int cuda_err) {
 }
 
 constexpr uint64_t kMaxElements = 1ull << 40;
+constexpr int64_t kMaxRows = 0x7FFFFFFF - 65536;  // rows of a group's matrix, so that a tile past the last fits an int
+constexpr int kMaxWidth = 1 << 24;                // ... and their length
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -208,4 +210,97 @@ extern "C" int bf16_linear_mxfp4_dynamic(const void *x, const void *wq, const vo
     st = bf16_quant_mxfp4(x, M, K, xq, xs, flags, stream);
     if (st != BF16L_OK) return st;
     return bf16_linear_mxfp4(xq, xs, wq, ws, bias, out, M, N, K, flags, stream);
+}
+
+extern "C" int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int groups, int32_t *offsets, int32_t *rows,
+                               int32_t *place, uint32_t flags, bf16l_stream_t stream) {
+    if (tokens < 0 || k <= 0 || groups <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
+    if (groups > kMaxGroups) return BF16L_EUNSUPPORTED;
+    if (tokens > kMaxRows / k) return BF16L_EINVAL;
+    const uint64_t n = (uint64_t)tokens * (uint64_t)k;
+    if (!offsets || (n && (!ids || !rows))) return BF16L_EINVAL;
+    if (off(ids, 4) || off(offsets, 4) || off(rows, 4) || off(place, 4)) return BF16L_EALIGN;
+    const Span outs[3] = {{offsets, 4ull * ((uint64_t)groups + 1)}, {rows, 4 * n}, {place, 4 * n}};
+    const Span ins[1] = {{ids, 4 * n}};
+    if (clash(outs, ins)) return BF16L_EINVAL;
+    bf16l_device dev;
+    const int st = current_device_checked(&dev);
+    if (st != BF16L_OK) return st;
+    return result(launch_group_rows(ids, (int)n, k, groups, offsets, rows, place, flags, stream));
+}
+
+extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
+                                   const int32_t *rows, void *out, int64_t P, int groups, int N, int K, int swiglu,
+                                   uint32_t flags, bf16l_stream_t stream) {
+    if (P < 0 || x_rows < 0 || groups <= 0 || N <= 0 || K <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
+    if (K % 8 != 0 || groups > kMaxGroups || N > kMaxWidth || K > kMaxWidth) return BF16L_EUNSUPPORTED;
+    if (P > kMaxRows || x_rows > kMaxRows) return BF16L_EINVAL;
+    if (P == 0) return BF16L_OK;  // (an empty `rows` may be NULL)
+    if (!rows && x_rows != P) return BF16L_EINVAL;
+    if (!x || !w || !offsets || !out || x_rows == 0) return BF16L_EINVAL;
+    if (off(x, 16) || off(w, 16) || off(bias, 16) || off(out, 16) || off(offsets, 4) || off(rows, 4)) return BF16L_EALIGN;
+    const uint64_t k = (uint64_t)K, wide = (uint64_t)N * (swiglu ? 2 : 1), g = (uint64_t)groups;
+    if ((uint64_t)P * wide > kMaxElements || g * wide > kMaxElements / k) return BF16L_EINVAL;
+    const Span outs[1] = {{out, 2ull * (uint64_t)P * (uint64_t)N}};
+    const Span ins[5] = {{x, 2ull * (uint64_t)x_rows * k}, {w, 2 * g * wide * k}, {bias, 2 * g * wide},
+                         {offsets, 4 * (g + 1)}, {rows, 4ull * (uint64_t)P}};
+    if (clash(outs, ins)) return BF16L_EINVAL;
+    bf16l_device dev;
+    const int st = current_device_checked(&dev);
+    if (st != BF16L_OK) return st;
+    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0};
+    return result(launch_grouped(a, flags, stream));
+}
+
+extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights,
+                                 const void *addend, void *out, int64_t tokens, int k, int H, uint32_t flags,
+                                 bf16l_stream_t stream) {
+    if (tokens < 0 || y_rows < 0 || k <= 0 || H <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
+    if (tokens == 0) return BF16L_OK;
+    if ((y_rows && !y) || !place || !out) return BF16L_EINVAL;
+    if (off(y, 16) || off(addend, 16) || off(out, 16) || off(place, 4) || off(weights, 4)) return BF16L_EALIGN;
+    const uint64_t h = (uint64_t)H, t = (uint64_t)tokens;
+    if (t > kMaxElements / h || (uint64_t)y_rows > kMaxElements / h || t > kMaxElements / (uint64_t)k) return BF16L_EINVAL;
+    const Span outs[1] = {{out, 2 * t * h}};
+    const Span ins[4] = {{y, 2ull * (uint64_t)y_rows * h}, {place, 4 * t * (uint64_t)k}, {weights, 4 * t * (uint64_t)k},
+                         {addend == out ? nullptr : addend, 2 * t * h}};
+    if (clash(outs, ins)) return BF16L_EINVAL;
+    bf16l_device dev;
+    const int st = current_device_checked(&dev);
+    if (st != BF16L_OK) return st;
+    return result(launch_combine_rows(y, y_rows, place, weights, addend, out, tokens, k, H, dev.num_sms, flags, stream));
+}
+
+extern "C" size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L) {
+    if (M <= 0 || N <= 0 || K <= 0 || K % 8 != 0 || R <= 0 || R % 8 != 0 || R > kLoraMaxRank || L <= 0) return 0;
+    return up256(4ull * (size_t)M * (size_t)R) + up256(4ull * (size_t)M * (size_t)N);
+}
+
+extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b,
+                                const float *scale, const int32_t *ids, void *out, int M, int N, int K, int R, int L,
+                                void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream) {
+    if (M < 0 || N <= 0 || K <= 0 || R <= 0 || L <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
+    if (K % 8 != 0 || R % 8 != 0 || R > kLoraMaxRank || L > kMaxGroups || N > kMaxWidth || K > kMaxWidth)
+        return BF16L_EUNSUPPORTED;
+    if (M == 0) return BF16L_OK;
+    if (!x || !w || !a || !b || !ids || !out) return BF16L_EINVAL;
+    if (off(x, 16) || off(w, 16) || off(bias, 16) || off(a, 16) || off(b, 16) || off(out, 16) || off(scale, 4) ||
+        off(ids, 4) || off(workspace, 256))
+        return BF16L_EALIGN;
+    const uint64_t m = (uint64_t)M, n = (uint64_t)N, k = (uint64_t)K, r = (uint64_t)R, l = (uint64_t)L;
+    if (m * n > kMaxElements || l * r * (n > k ? n : k) > kMaxElements) return BF16L_EINVAL;
+    const size_t need = bf16_linear_lora_workspace(M, N, K, R, L);
+    if (!workspace || workspace_bytes < need) return BF16L_EINVAL;
+    const Span outs[2] = {{out, 2 * m * n}, {workspace, need}};
+    const Span ins[7] = {{x, 2 * m * k}, {w, 2 * n * k}, {bias, 2 * n}, {a, 2 * l * r * k}, {b, 2 * l * r * n},
+                         {scale, 4 * l}, {ids, 4 * m}};
+    if (clash(outs, ins)) return BF16L_EINVAL;
+    float *h = static_cast<float *>(workspace);
+    float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(4ull * (size_t)M * (size_t)R));
+    const LoraArgs args = {x, a, b, scale, ids, h, y, out, M, N, K, R, L};
+    bf16l_device dev;
+    int st = current_device_checked(&dev);
+    if (st == BF16L_OK) st = result(launch_lora_inner(args, flags, stream));
+    if (st == BF16L_OK) st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
+    return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
 }

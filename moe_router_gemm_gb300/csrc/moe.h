@@ -42,4 +42,35 @@ int launch_route(const void *logits, int64_t ld, const float *bias, float *weigh
                  int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
                  int logits_bf16, int num_sms, uint32_t flags, void *stream);
 
+// Rows by group (group.cu): n keys, n + 1024 <= 2^31; and a token's rows summed.
+constexpr int kMaxGroups = 1024;
+int init_group();
+int launch_group_rows(const int32_t *ids, int n, int k, int groups, int32_t *offsets, int32_t *rows, int32_t *place,
+                      uint32_t flags, void *stream);
+int launch_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
+                        void *out, int64_t tokens, int k, int H, int num_sms, uint32_t flags, void *stream);
+
+// The linear of grouped rows (grouped.cu); N: columns of out, W has 2 N rows a group with swiglu.
+struct GroupedArgs {
+    const void *x, *w, *bias;
+    const int32_t *offsets, *rows;  // rows null: row p of x is row p of out
+    void *out;
+    int x_rows, P, groups, N, K, swiglu;
+};
+int launch_grouped(const GroupedArgs &a, uint32_t flags, void *stream);
+
+// The adapters of a linear (lora.cu): the inner values h[M][R] in fp32, and out from them and the shared product y[M][N].
+constexpr int kLoraMaxRank = 128;
+struct LoraArgs {
+    const void *x, *a, *b;
+    const float *scale;
+    const int32_t *ids;
+    float *h;
+    const float *y;
+    void *out;
+    int M, N, K, R, L;
+};
+int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
+int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
+
 }  // namespace bf16l

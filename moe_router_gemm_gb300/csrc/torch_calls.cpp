@@ -28,6 +28,11 @@ decltype(&bf16_dequant_mxfp4) g_dequant;
 decltype(&bf16_linear_mxfp4) g_linear;
 decltype(&bf16_linear_mxfp4_dynamic) g_dynamic;
 decltype(&bf16_linear_mxfp4_dynamic_workspace) g_workspace;
+decltype(&bf16_group_rows) g_group;
+decltype(&bf16_linear_grouped) g_grouped;
+decltype(&bf16_combine_rows) g_combine;
+decltype(&bf16_linear_lora) g_lora;
+decltype(&bf16_linear_lora_workspace) g_lora_workspace;
 
 using at::Tensor;
 
@@ -44,6 +49,13 @@ const Tensor *cuda_tensor(PyObject *o) {
 const Tensor *dense(PyObject *o, at::ScalarType type, int64_t rows, int64_t cols) {
     const Tensor *t = cuda_tensor(o);
     if (!t || t->scalar_type() != type || t->dim() != 2 || t->size(0) != rows || t->size(1) != cols || !t->is_contiguous())
+        return nullptr;
+    return t;
+}
+const Tensor *dense(PyObject *o, at::ScalarType type, int64_t planes, int64_t rows, int64_t cols) {
+    const Tensor *t = cuda_tensor(o);
+    if (!t || t->scalar_type() != type || t->dim() != 3 || t->size(0) != planes || t->size(1) != rows ||
+        t->size(2) != cols || !t->is_contiguous())
         return nullptr;
     return t;
 }
@@ -269,11 +281,141 @@ PyObject *linear_mxfp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// group_rows(ids, groups, flags)
+PyObject *group_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (wrong_count(n, 3)) return nullptr;
+    bool wide = false;
+    const int groups = as_int(args[1], wide);
+    const uint32_t flags = as_flags(args[2], wide);
+    if (PyErr_Occurred()) return nullptr;
+    if (wide || groups < 1 || groups > 65536) return none();
+    const Tensor *ids = cuda_tensor(args[0]);
+    if (!ids || ids->scalar_type() != at::kInt || ids->dim() < 1 || ids->dim() > 2 || !ids->is_contiguous()) return none();
+    const int64_t T = ids->size(0), k = ids->dim() == 2 ? ids->size(1) : 1;
+    if (k < 1 || k > INT32_MAX) return none();
+    Tensor offsets, rows, place;
+    int st;
+    {
+        const Unlocked unlocked;
+        offsets = make(*ids, at::kInt, {groups + 1});
+        rows = make(*ids, at::kInt, {T * k});
+        place = make(*ids, at::kInt, ids->sizes());
+        st = g_group(static_cast<const int32_t *>(ids->const_data_ptr()), T, (int)k, groups,
+                     static_cast<int32_t *>(offsets.data_ptr()), static_cast<int32_t *>(rows.data_ptr()),
+                     static_cast<int32_t *>(place.data_ptr()), flags, stream_of(*ids));
+    }
+    return st ? PyLong_FromLong(st) : pack({offsets, rows, place});
+    END_HANDLE_TH_ERRORS
+}
+
+// linear_grouped(x, w, offsets, bias, rows, swiglu, flags)
+PyObject *linear_grouped(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (wrong_count(n, 7)) return nullptr;
+    bool wide = false;
+    const int swiglu = PyObject_IsTrue(args[5]);
+    const uint32_t flags = as_flags(args[6], wide);
+    if (PyErr_Occurred() || swiglu < 0) return nullptr;
+    if (wide) return none();
+    const Tensor *x = cuda_tensor(args[0]), *w = cuda_tensor(args[1]), *rows = nullptr, *bias = nullptr;
+    if (!x || !w || x->scalar_type() != at::kBFloat16 || w->scalar_type() != at::kBFloat16 || x->dim() != 2 ||
+        w->dim() != 3 || !x->is_contiguous() || !w->is_contiguous() || w->size(2) != x->size(1))
+        return none();
+    const int64_t G = w->size(0), W = w->size(1), K = x->size(1), N = swiglu ? W / 2 : W;
+    if (G > INT32_MAX || W > INT32_MAX || K > INT32_MAX || (swiglu && W % 2)) return none();
+    const Tensor *offsets = dense(args[2], at::kInt, G + 1);
+    if (!offsets || (args[3] != Py_None && !(bias = dense(args[3], at::kBFloat16, G, W)))) return none();
+    if (args[4] != Py_None) {
+        rows = cuda_tensor(args[4]);
+        if (!rows || rows->scalar_type() != at::kInt || rows->dim() != 1 || !rows->is_contiguous()) return none();
+    }
+    const int64_t P = rows ? rows->size(0) : x->size(0);
+    Tensor out;
+    int st;
+    {
+        const Unlocked unlocked;
+        out = make(*x, at::kBFloat16, {P, N});
+        st = g_grouped(x->const_data_ptr(), x->size(0), w->const_data_ptr(), bias ? bias->const_data_ptr() : nullptr,
+                       static_cast<const int32_t *>(offsets->const_data_ptr()),
+                       rows ? static_cast<const int32_t *>(rows->const_data_ptr()) : nullptr, out.data_ptr(), P, (int)G,
+                       (int)N, (int)K, swiglu, flags, stream_of(*x));
+    }
+    return st ? PyLong_FromLong(st) : item(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// combine_rows(y, place, weights, addend, flags)
+PyObject *combine_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (wrong_count(n, 5)) return nullptr;
+    bool wide = false;
+    const uint32_t flags = as_flags(args[4], wide);
+    if (PyErr_Occurred()) return nullptr;
+    if (wide) return none();
+    const Tensor *y = cuda_tensor(args[0]), *place = cuda_tensor(args[1]), *weights = nullptr, *addend = nullptr;
+    if (!y || !place || y->scalar_type() != at::kBFloat16 || y->dim() != 2 || !y->is_contiguous() ||
+        place->scalar_type() != at::kInt || place->dim() != 2 || !place->is_contiguous())
+        return none();
+    const int64_t T = place->size(0), k = place->size(1), H = y->size(1);
+    if (k > INT32_MAX || H > INT32_MAX) return none();
+    if (args[2] != Py_None && !(weights = dense(args[2], at::kFloat, T, k))) return none();
+    if (args[3] != Py_None && !(addend = dense(args[3], at::kBFloat16, T, H))) return none();
+    Tensor out;
+    int st;
+    {
+        const Unlocked unlocked;
+        out = make(*y, at::kBFloat16, {T, H});
+        st = g_combine(y->const_data_ptr(), y->size(0), static_cast<const int32_t *>(place->const_data_ptr()),
+                       weights ? static_cast<const float *>(weights->const_data_ptr()) : nullptr,
+                       addend ? addend->const_data_ptr() : nullptr, out.data_ptr(), T, (int)k, (int)H, flags,
+                       stream_of(*y));
+    }
+    return st ? PyLong_FromLong(st) : item(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// linear_lora(x, w, a, b, ids, bias, scale, flags)
+PyObject *linear_lora(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (wrong_count(n, 8)) return nullptr;
+    bool wide = false;
+    const uint32_t flags = as_flags(args[7], wide);
+    if (PyErr_Occurred()) return nullptr;
+    if (wide) return none();
+    const Tensor *x = cuda_tensor(args[0]), *w = cuda_tensor(args[1]), *a = cuda_tensor(args[2]), *bias = nullptr,
+                 *scale = nullptr;
+    if (!x || !w || !a || x->dim() != 2 || w->dim() != 2 || a->dim() != 3) return none();
+    const int64_t M = x->size(0), K = x->size(1), N = w->size(0), L = a->size(0), R = a->size(1);
+    const Tensor *b = dense(args[3], at::kBFloat16, L, N, R), *ids = dense(args[4], at::kInt, M);
+    if (!dense(args[0], at::kBFloat16, M, K) || !dense(args[1], at::kBFloat16, N, K) ||
+        !dense(args[2], at::kBFloat16, L, R, K) || !b || !ids || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX ||
+        L > INT32_MAX || R > INT32_MAX)
+        return none();
+    if (args[5] != Py_None && !(bias = dense(args[5], at::kBFloat16, N))) return none();
+    if (args[6] != Py_None && !(scale = dense(args[6], at::kFloat, L))) return none();
+    Tensor out;
+    int st;
+    {
+        const Unlocked unlocked;
+        out = make(*x, at::kBFloat16, {M, N});
+        Tensor space;  // freed on return, to this stream's own memory
+        const size_t need = g_lora_workspace((int)M, (int)N, (int)K, (int)R, (int)L);
+        if (need) space = make(*x, at::kByte, {(int64_t)need});
+        st = g_lora(x->const_data_ptr(), w->const_data_ptr(), bias ? bias->const_data_ptr() : nullptr, a->const_data_ptr(),
+                    b->const_data_ptr(), scale ? static_cast<const float *>(scale->const_data_ptr()) : nullptr,
+                    static_cast<const int32_t *>(ids->const_data_ptr()), out.data_ptr(), (int)M, (int)N, (int)K, (int)R,
+                    (int)L, need ? space.data_ptr() : nullptr, need, flags, stream_of(*x));
+    }
+    return st ? PyLong_FromLong(st) : item(out);
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points, in the order of the declarations above)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (wrong_count(n, 7)) return nullptr;
-    void *p[7];
-    for (int i = 0; i < 7; ++i) {
+    if (wrong_count(n, 12)) return nullptr;
+    void *p[12];
+    for (int i = 0; i < 12; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -284,12 +426,18 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     g_linear = reinterpret_cast<decltype(g_linear)>(p[4]);
     g_dynamic = reinterpret_cast<decltype(g_dynamic)>(p[5]);
     g_workspace = reinterpret_cast<decltype(g_workspace)>(p[6]);
+    g_group = reinterpret_cast<decltype(g_group)>(p[7]);
+    g_grouped = reinterpret_cast<decltype(g_grouped)>(p[8]);
+    g_combine = reinterpret_cast<decltype(g_combine)>(p[9]);
+    g_lora = reinterpret_cast<decltype(g_lora)>(p[10]);
+    g_lora_workspace = reinterpret_cast<decltype(g_lora_workspace)>(p[11]);
     Py_RETURN_NONE;
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CALL(rmsnorm),       CALL(route),        CALL(quant_mxfp4),
-                           CALL(dequant_mxfp4), CALL(linear_mxfp4), CALL(bind),
+                           CALL(dequant_mxfp4), CALL(linear_mxfp4), CALL(group_rows),
+                           CALL(linear_grouped), CALL(combine_rows), CALL(linear_lora), CALL(bind),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
