@@ -27,7 +27,7 @@ LIB = os.path.join(PKG, "libbf16_linear.so")
 
 SOURCES = ["api.cu", "plan.cpp", "dotprod.cu", "dotprod_f32.cu", "splitk.cu", "tile.cu", "tile_t.cu", "stream.cu", "noalloc.cu", "tile2.cu", "warprow.cu", "warpmma.cu", "warpmma_ks.cu", "dotmma.cu", "fp8.cu", "mxfp8.cu", "probe.cu", "mxfp4.cu", "mxfp4_pair.cu", "mxfp4_split.cu",
            "norm.cu", "route.cu", "group.cu", "grouped.cu", "lora.cu", "api_moe.cu"]
-HEADERS = ["common.cuh", "kernels.h", "moe.h", "dotprod.cuh", "tile.cuh", "mxfp4.cuh", "dispatch_table.inc"]
+HEADERS = ["common.cuh", "kernels.h", "moe.h", "dotprod.cuh", "tile.cuh", "mxfp4.cuh", "grouped.cuh", "dispatch_table.inc"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE, "-I" + CSRC]

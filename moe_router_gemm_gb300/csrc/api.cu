@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "grouped.cuh"
 #include "moe.h"
 
 namespace bf16l {
@@ -69,6 +70,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_mxfp4_pair();
         if (!e) e = init_mxfp4_split();
         if (!e) e = init_group();
+        if (!e) e = init_grouped();
     }
     s.err = e;
 }
@@ -256,6 +258,19 @@ int make_tmap_bf16_chunks(CUtensorMap *map, const void *base, uint64_t rows, uin
     const cuuint32_t box[3] = {(cuuint32_t)kChunkK, box_rows, kc};
     const cuuint32_t estr[3] = {1, 1, 1};
     return (int)enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
+                         uint32_t box_halves, uint32_t box_rows, uint32_t box_cols) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return (int)CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t dims[4] = {cols, rows, halves, planes};
+    const cuuint64_t strides[3] = {cols * 2, rows * cols * 2, halves * rows * cols * 2};  // bytes
+    const cuuint32_t box[4] = {box_cols, box_rows, box_halves, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return (int)enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }

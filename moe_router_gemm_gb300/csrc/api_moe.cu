@@ -246,10 +246,11 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
                          {offsets, 4 * (g + 1)}, {rows, 4ull * (uint64_t)P}};
     if (clash(outs, ins)) return BF16L_EINVAL;
     bf16l_device dev;
-    const int st = current_device_checked(&dev);
+    int32_t *status = nullptr;
+    const int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
     const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0};
-    return result(launch_grouped(a, flags, stream));
+    return result(launch_grouped(a, dev.num_sms, flags, stream, status));
 }
 
 extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights,

@@ -1,82 +1,434 @@
 // grouped.cu — out[p] = x[row of p] @ W[e]^T (+ bias[e]) for the rows p of each group e, their numbers known on the
 // device alone; with SwiGLU, W[e] holds N gate rows and then N up rows and out = silu(gate) * up.
 //
-// The simple form: 32 x 32 tiles on CUDA cores.  Block y finds its group and rows by walking the offsets.
+// W rows on the MMA's M side and rows of x on its N side, by CTA pairs (cta_group::2): a tile is 256 W rows (128 of each
+// CTA) by up to `bt` rows of one group.  A group has few rows or many, and an MMA's time goes with its N: so a group's rows
+// are split evenly over as few tiles as hold them, and each tile's MMAs take its own N, a multiple of 32.  A weight is read
+// for each of its group's row tiles, one after the other, so once from HBM.
+//
+//   * every CTA turns the offsets into the first tile of each group (a scan in shared memory) and each role finds a tile's
+//     group by bisection;
+//   * warp 0: TMA producer, all its lanes: 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
+//     group's weight is zero, not the next group's) and of its half of the tile's rows of x, 16 rows a box, or four rows
+//     an instruction where `rows` gives them (tile::gather4), so that no sorted copy of x is made;
+//   * warp 1 of the even CTA: MMA issuer; warps 2-9: epilogue, two for each quarter of the TMEM lanes;
+//   * fp32 accumulators double-buffered in TMEM;
+//   * SwiGLU: boxes of 16 gate rows and their 16 up rows, so that a warp's 32 lanes hold both: one shuffle for two rows
+//     of x brings them together in fp32, and out is written without the wide product's way through memory.
+// Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any remote arrival or copy) and one
+// before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>
 
-#include "common.cuh"
+#include "grouped.cuh"
 #include "moe.h"
+#include "mxfp4.cuh"
 
 namespace bf16l {
 
 namespace {
 
-constexpr int kTile = 32;
+constexpr int kHalf = 128;                        // W rows per CTA
+constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
+constexpr int kMaxRowsTile = 256, kMaxStages = 12;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr unsigned kAll = 0xFFFFFFFFu;
 
-template <bool SWIGLU>
-__global__ void __launch_bounds__(kTile * 8) grouped_kernel(const GroupedArgs a) {
-    __shared__ float sx[kTile][kTile + 1], sw[SWIGLU ? 2 : 1][kTile][kTile + 1];
+struct GroupedShared {
+    uint64_t full[kMaxStages];   // leader only: both CTAs' copies of the stage have landed
+    uint64_t empty[kMaxStages];  // both: the MMAs reading the stage are done
+    uint64_t acc_full[2];        // both: the accumulator holds a finished tile
+    uint64_t acc_empty[2];       // leader only: both CTAs' epilogues have read it
+    uint32_t tmem_base;
+    int32_t bad_pair, aborted, issued, consumed;
+    int32_t part[kThreads / 32];
+    int32_t tiles[kMaxGroups + 1];  // row tiles before each group
+    int32_t first[kMaxGroups];      // first row of each group
+    int32_t count[kMaxGroups];      // its rows
+};
+
+// Unit u: a row tile of a group and 256 W rows (128 outputs with SwiGLU); row tiles vary fastest.
+struct Unit {
+    int e, p0, rows, m;  // group, first position, rows, W tile
+    int cols;            // rows rounded up for the MMA
+};
+__device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int groups, long long u, int m_tiles) {
+    const int q = (int)(u / m_tiles);
+    int lo = 0, hi = groups;  // tiles[lo] <= q < tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.tiles[mid] <= q)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int nt = sh.tiles[lo + 1] - sh.tiles[lo], count = sh.count[lo];
+    const long long local = u - (long long)sh.tiles[lo] * m_tiles;
+    const int m = (int)(local / nt), t = (int)(local - (long long)m * nt);
+    const int each = count / nt, more = count - each * nt;
+    Unit r;
+    r.e = lo;
+    r.m = m;
+    r.rows = each + (t < more);
+    r.p0 = sh.first[lo] + t * each + min(t, more);
+    r.cols = (r.rows + 31) & ~31;
+    return r;
+}
+
+template <bool SWIGLU, bool GATHER>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                   const GroupedArgs a, int bt, int stages, int32_t *status) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int stage_bytes = kWBytes + bt * kChunkK;  // bt / 2 rows of 128 bytes
+    GroupedShared &sh = *reinterpret_cast<GroupedShared *>(ring + stages * stage_bytes);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    constexpr int kOuts = SWIGLU ? 128 : 256;  // outputs of a W tile
+    const int m_tiles = (a.N + kOuts - 1) / kOuts;
+    const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
+    const int C = (a.K + kChunkK - 1) / kChunkK;
+    const uint32_t tmem_cols = 2u * (uint32_t)bt;
+
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_x);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&sh.full[s], 1);   // the leader producer's arrive.expect_tx
+            mbar_init(&sh.empty[s], 1);  // the leader's multicast commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sh.acc_full[b], 1);
+            mbar_init(&sh.acc_empty[b], 2 * kEpiWarps);
+        }
+        sh.aborted = 0;
+        sh.issued = 0;
+        sh.consumed = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&sh.tmem_base, tmem_cols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    // Both CTAs' barriers and TMEM exist before any cross-CTA arrival or copy.
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    // The pair MMA writes the same TMEM address in both CTAs: check that the joint
+    // allocation gave both the same columns (each CTA reads the other's).
+    if (tid == 0) {
+        uint32_t other;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(other)
+                     : "r"(mapa_shared(smem_u32(&sh.tmem_base), rank ^ 1u))
+                     : "memory");
+        sh.bad_pair = other != tmem;
+        if (other != tmem) record_timeout(status, kSitePairTmem);
+    }
     pdl_launch_dependents();
-    pdl_wait();
-    int left = (int)blockIdx.y, lo = 0, hi = 0, e = 0;
-    for (; e < a.groups; ++e) {
-        lo = min(max(a.offsets[e], 0), a.P);
-        hi = min(max(a.offsets[e + 1], lo), a.P);
-        const int tiles = (hi - lo + kTile - 1) / kTile;
-        if (left < tiles) break;
-        left -= tiles;
+    pdl_wait();  // nothing is read before the previous kernel has finished
+
+    // The row tiles before each group: `per` consecutive groups a thread, summed over the block.
+    const int per = (a.groups + kThreads - 1) / kThreads, e0 = tid * per;
+    int mine = 0;
+    for (int e = e0; e < min(e0 + per, a.groups); ++e) {
+        const int lo = min(max(__ldg(a.offsets + e), 0), a.P), hi = min(max(__ldg(a.offsets + e + 1), lo), a.P);
+        sh.first[e] = lo;
+        sh.count[e] = hi - lo;
+        mine += (hi - lo + bt - 1) / bt;
     }
-    if (e == a.groups) return;
-    const int p0 = lo + left * kTile, n0 = (int)blockIdx.x * kTile;
-    const int wide = SWIGLU ? 2 * a.N : a.N;
-    const int c = threadIdx.x % kTile, r0 = threadIdx.x / kTile;
-    const uint16_t *w = static_cast<const uint16_t *>(a.w) + (size_t)e * wide * a.K;
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
-    float acc[SWIGLU ? 2 : 1][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kTile) {
-        __syncthreads();
-        for (int r = r0; r < kTile; r += 8) {
-            const bool in = k0 + c < a.K;
-            const int p = min(p0 + r, hi - 1);
-            const long long row = min(max(a.rows ? a.rows[p] : p, 0), a.x_rows - 1);
-            sx[r][c] = in ? bf16_to_f32(x[row * a.K + k0 + c]) : 0.0f;
-            for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-                sw[h][r][c] = in && n0 + r < a.N ? bf16_to_f32(w[(size_t)(h * a.N + n0 + r) * a.K + k0 + c]) : 0.0f;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) sh.part[warp] = upto;
+    __syncthreads();
+    int before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += sh.part[w];
+    for (int e = e0; e < min(e0 + per, a.groups); ++e) {
+        sh.tiles[e] = before;
+        before += (sh.count[e] + bt - 1) / bt;
+    }
+    if (e0 < a.groups && e0 + per >= a.groups) sh.tiles[a.groups] = before;
+    __syncthreads();
+    const bool bad_pair = sh.bad_pair != 0;  // the same verdict in both CTAs
+    const long long units = (long long)sh.tiles[a.groups] * m_tiles;
+
+    if (bad_pair) {
+        // nothing issued: fall through to the exit barrier
+    } else if (warp == 0) {
+        // ---- TMA producer (both CTAs), the whole warp ----
+        const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // leader's full[0]
+        int it = 0;
+        bool ok = true;
+        for (long long u = cl; ok && u < units; u += ncl) {
+            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
+            const int n0 = t.m * kOuts + (int)rank * (kOuts / 2);
+            int32_t row[4] = {0, 0, 0, 0};
+            if (GATHER) {  // rows past the tile's: its last one again
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    row[j] = min(max(__ldg(a.rows + min(q0 + 4 * lane + j, t.p0 + t.rows - 1)), 0), a.x_rows - 1);
+            }
+            for (int c = 0; c < C; ++c, ++it) {
+                const int s = it % stages;
+                ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
+                ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
+                if (!ok) {
+                    if (lane == 0) atomicExch(&sh.aborted, 1);
+                    break;
+                }
+                uint8_t *st = ring + s * stage_bytes;
+                const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
+                if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * kWBytes + t.cols * kChunkK * 2));
+                if (SWIGLU) {
+                    if (lane < 4) tma_load_4d_pair(st + lane * (kWBytes / 4), &tm_w, fb, c * kChunkK, n0 + 16 * lane, 0, t.e);
+                } else {
+                    if (lane == 0) tma_load_4d_pair(st, &tm_w, fb, c * kChunkK, n0, 0, t.e);
+                }
+                if (GATHER) {
+                    if (4 * lane < half) tma_gather4_pair(st + kWBytes + 512 * lane, &tm_x, fb, c * kChunkK, row);
+                } else {
+                    if (16 * lane < half) tma_load_2d_pair(st + kWBytes + 2048 * lane, &tm_x, fb, c * kChunkK, q0 + 16 * lane);
+                }
+            }
         }
-        __syncthreads();
-        for (int k = 0; k < kTile; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) acc[h][i] = fmaf(sx[r0 + 8 * i][k], sw[h][c][k], acc[h][i]);
-    }
-    const uint16_t *bias = static_cast<const uint16_t *>(a.bias);
-    if (n0 + c >= a.N) return;
-    for (int i = 0; i < 4; ++i) {
-        const int p = p0 + r0 + 8 * i;
-        if (p >= hi) continue;
-        float v = acc[0][i] + (bias ? bf16_to_f32(bias[(size_t)e * wide + n0 + c]) : 0.0f);
-        if constexpr (SWIGLU) {
-            const float up = acc[1][i] + (bias ? bf16_to_f32(bias[(size_t)e * wide + a.N + n0 + c]) : 0.0f);
-            v = v / (1.0f + expf(-v)) * up;
+        if (lane == 0) sh.issued = it;
+        // Every commit that arrives on this CTA's `empty` barriers has landed before the exit barrier.
+        if (ok) {
+            for (int i = (it > stages ? it - stages : 0); i < it; ++i)
+                if (!mbar_wait(&sh.empty[i % stages], (i / stages) & 1, status, kSiteDrain)) break;
         }
-        static_cast<uint16_t *>(a.out)[(size_t)p * a.N + n0 + c] = f32_to_bf16(v);
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {  // ---- MMA issuer (leader only) ----
+            int it = 0, tile = 0;
+            for (long long u = cl; u < units; u += ncl, ++tile) {
+                sh.consumed = it;
+                const Unit t = unit_of(sh, a.groups, u, m_tiles);
+                const uint32_t idesc = idesc_bf16_f32(2 * kHalf, t.cols);
+                const int b = tile & 1;
+                const uint32_t acc = tmem + (uint32_t)(b * bt);
+                // Both CTAs' epilogues have read this buffer (used two tiles ago).
+                bool ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
+                tc_fence_after();
+                for (int c = 0; ok && c < C; ++c, ++it) {
+                    const int s = it % stages;
+                    if (!mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t *st = ring + s * stage_bytes;
+                    const uint64_t adesc = smem_desc_sw128(smem_u32(st));
+                    const uint64_t bdesc = smem_desc_sw128(smem_u32(st + kWBytes));
+#pragma unroll
+                    for (int kk = 0; kk < kChunkK / 16; ++kk)
+                        mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
+                }
+                if (!ok) {  // release both epilogues at once
+                    atomicExch(&sh.aborted, 1);
+                    sh.consumed = it;
+                    mbar_arrive(&sh.acc_full[b]);
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&sh.acc_full[b]), 1));
+                    break;
+                }
+                mma_commit_pair(&sh.acc_full[b], (uint16_t)0x3);
+            }
+            sh.consumed = it;
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: TMEM lane quarter = warp % 4; the quarter's two warps take 16 rows of x in turn ----
+        const int quarter = warp & 3, h = (warp - 2) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t acc_empty0 = mapa_shared(smem_u32(&sh.acc_empty[0]), 0);
+        uint16_t *out = static_cast<uint16_t *>(a.out);
+        const uint16_t *bias = static_cast<const uint16_t *>(a.bias);
+        int tile = 0;
+        for (long long u = cl; u < units; u += ncl, ++tile) {
+            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const int b = tile & 1;
+            // this lane's output, and the W row that it is of
+            const int n = t.m * kOuts + (int)rank * (kOuts / 2) +
+                          (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
+            const int wide = SWIGLU ? 2 * a.N : a.N, wrow = SWIGLU && lane >= 16 ? a.N + n : n;
+            const float lb = bias && n < a.N ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
+            const bool ok = mbar_wait(&sh.acc_full[b], (tile >> 1) & 1, status, kSiteAccum);
+            tc_fence_after();
+            const bool have = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
+            const uint32_t acc = lanes + (uint32_t)(b * bt);
+            const bool pairs = (a.N & 1) == 0;
+            for (int c0 = 16 * h; have && c0 < t.rows; c0 += 32) {
+                uint32_t r[16];
+                tmem_ld16(acc + (uint32_t)c0, r);
+                tmem_ld_wait16(r);
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) + lb;
+                // (row of x: c0 + j)
+                uint16_t *o = out + (size_t)(t.p0 + c0) * a.N + n;
+                const int left = t.rows - c0;
+                if constexpr (SWIGLU) {
+                    float f[8];  // row 2 i (gate lanes) or 2 i + 1 (up lanes) of output n
+                    const bool up = lane >= 16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 16);
+                        const float g = up ? got : v[2 * i], w = up ? v[2 * i + 1] : got;
+                        f[i] = g / (1.0f + expf(-g)) * w;
+                    }
+                    o += up ? a.N : 0;
+                    if (pairs) {  // two outputs a store: even lanes take f[i] of their neighbour's output too, odd ones f[i + 1]
+                        const bool odd = lane & 1;
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const float got = __shfl_xor_sync(kAll, odd ? f[i] : f[i + 1], 1);
+                            const int j = 2 * i + (odd ? 2 : 0);
+                            if (n < a.N && j + up < left)
+                                *reinterpret_cast<uint32_t *>(o + (size_t)j * a.N - odd) =
+                                    odd ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n < a.N && 2 * i + up < left) o[(size_t)(2 * i) * a.N] = f32_to_bf16(f[i]);
+                    }
+                } else if (pairs) {
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float got = __shfl_xor_sync(kAll, odd ? v[j] : v[j + 1], 1);
+                        if (n < a.N && j + odd < left)
+                            *reinterpret_cast<uint32_t *>(o + (size_t)(j + odd) * a.N - odd) =
+                                odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n < a.N && j < left) o[(size_t)j * a.N] = f32_to_bf16(v[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(&sh.acc_empty[b]);
+                else
+                    mbar_arrive_cluster(acc_empty0 + (uint32_t)(b * sizeof(uint64_t)));
+            }
+            if (!have) break;
+        }
     }
+
+    tc_fence_before();
+    __syncthreads();
+    // Drain TMA copies that were issued but never consumed (only after a timeout).
+    if (tid == 0 && leader) {
+        for (int i = sh.consumed; i < sh.issued; ++i)
+            if (!mbar_wait(&sh.full[i % stages], (i / stages) & 1, status, kSiteDrain)) break;
+    }
+    // No remote arrival, copy or MMA operand read is left in flight past here.
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, tmem_cols);
+    }
+}
+
+constexpr int kMaxDevices = 64;
+int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
+
+constexpr int kSmem = 232448;
+int stages_of(int bt) {
+    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kWBytes + bt * kChunkK);
+    return n < kMaxStages ? n : kMaxStages;
+}
+// One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
+int smem_of(int bt) { return 1024 + stages_of(bt) * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
+static_assert(kSmem - 1024 - (int)sizeof(GroupedShared) >= 6 * (kWBytes + kMaxRowsTile * kChunkK), "six stages of the widest");
+
+using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const GroupedArgs, int, int, int32_t *);
+
+GroupedFn pick(bool swiglu, bool gather) {
+    if (swiglu) return gather ? grouped_kernel<true, true> : grouped_kernel<true, false>;
+    return gather ? grouped_kernel<false, true> : grouped_kernel<false, false>;
+}
+
+cudaLaunchConfig_t config(int clusters, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = (cudaStream_t)stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
 }
 
 }  // namespace
 
-int launch_grouped(const GroupedArgs &a, uint32_t flags, void *stream) {
-    const long long tiles = (long long)a.P / kTile + (a.P < a.groups ? a.P : a.groups);
-    if (tiles > 65535) return (int)cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.N + kTile - 1) / kTile), (unsigned)tiles);
-    cfg.blockDim = dim3(kTile * 8);
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
-    cfg.attrs = attr;
+int init_grouped() {
+    for (bool swiglu : {false, true})
+        for (bool gather : {false, true}) {
+            const int e = (int)cudaFuncSetAttribute(pick(swiglu, gather), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            if (e) return e;
+        }
+    int dev = 0;
+    const int e = (int)cudaGetDevice(&dev);
+    if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(kGb300Sms, kSmem, 0, nullptr, attr);
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, a.swiglu ? grouped_kernel<true> : grouped_kernel<false>, a);
+    int n = 0;
+    // A failed query only loses the clamp (launches then use half the SMs' number).
+    if (cudaOccupancyMaxActiveClusters(&n, pick(false, true), &cfg) != cudaSuccess) {
+        n = 0;
+        (void)cudaGetLastError();
+    }
+    g_clusters[dev] = n;
+    return 0;
+}
+
+int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status) {
+    // Rows of a tile: groups of the average size, and of twice that, fit one.
+    const int full = a.P < a.groups ? a.P : a.groups;  // groups that may have rows
+    const long long twice = 2ll * a.P / full;
+    const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
+    CUtensorMap tw, tx;
+    int r = make_tmap_bf16_stack(&tw, a.w, (uint64_t)a.groups, a.swiglu ? 2 : 1, (uint64_t)a.N, (uint64_t)a.K,
+                                 a.swiglu ? 2 : 1, a.swiglu ? 16 : kHalf, kChunkK);
+    if (r) return (int)cudaErrorInvalidValue;
+    r = make_tmap_bf16_2d(&tx, a.x, (uint64_t)a.x_rows, (uint64_t)a.K, a.rows ? 1 : 16, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (r) return (int)cudaErrorInvalidValue;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
+    // A cluster that cannot be resident with the others would run its tiles after them.
+    const int outs = a.swiglu ? 128 : 256;
+    const long long units = ((long long)a.P / bt + full) * ((a.N + outs - 1) / outs);  // at most
+    long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
+    if (units < clusters) clusters = units;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config((int)clusters, smem_of(bt), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, bt, stages_of(bt), status);
 }
 
 }  // namespace bf16l

@@ -1,0 +1,35 @@
+// grouped.cuh — device helpers of the kernels whose weight depends on the row: TMA loads for a CTA pair from a stack of
+// matrices and from rows given by index, and the tiles of groups whose sizes the device alone knows.
+#pragma once
+
+#include "common.cuh"
+
+namespace bf16l {
+
+// As tma_load_2d_pair, from a stack of matrices: c0 innermost (K), c1 row, c2 half, c3 matrix.
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t c0,
+                                                 int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Four rows of a matrix (a map whose box is one row high), 128 bytes of each from column c0 on, to 512 bytes at dst.
+__device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t c0,
+                                                 const int32_t (&row)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(row[0]), "r"(row[1]),
+        "r"(row[2]), "r"(row[3])
+        : "memory");
+}
+
+// Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
+// box_halves x 1 elements and 128-byte swizzle.  Defined in api.cu.  Returns a CUresult value (0 on success).
+int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
+                         uint32_t box_halves, uint32_t box_rows, uint32_t box_cols);
+
+}  // namespace bf16l

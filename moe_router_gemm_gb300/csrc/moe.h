@@ -57,7 +57,8 @@ struct GroupedArgs {
     void *out;
     int x_rows, P, groups, N, K, swiglu;
 };
-int launch_grouped(const GroupedArgs &a, uint32_t flags, void *stream);
+int init_grouped();
+int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
 // The adapters of a linear (lora.cu): the inner values h[M][R] in fp32, and out from them and the shared product y[M][N].
 constexpr int kLoraMaxRank = 128;
