@@ -275,6 +275,20 @@ int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, ui
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+int make_tmap_bf16_blocks(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
+                          uint32_t block_rows, uint32_t box_blocks, uint32_t box_cols) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return (int)CUDA_ERROR_NOT_FOUND;
+    if (rows % block_rows != 0) return (int)CUDA_ERROR_INVALID_VALUE;
+    const cuuint64_t dims[5] = {cols, block_rows, halves, rows / block_rows, planes};
+    const cuuint64_t strides[4] = {cols * 2, rows * cols * 2, block_rows * cols * 2, halves * rows * cols * 2};  // bytes
+    const cuuint32_t box[5] = {box_cols, block_rows, (cuuint32_t)halves, box_blocks, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return (int)enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 int make_tmap_u8_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                     uint32_t box_cols, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
     return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, box_rows, box_cols, swizzle, promo);

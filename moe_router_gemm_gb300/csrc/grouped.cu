@@ -9,8 +9,10 @@
 //   * every CTA turns the offsets into the first tile of each group (a scan in shared memory) and each role finds a tile's
 //     group by bisection;
 //   * warp 0: TMA producer, all its lanes: 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
-//     group's weight is zero, not the next group's) and of its half of the tile's rows of x, 16 rows a box, or four rows
-//     an instruction where `rows` gives them (tile::gather4), so that no sorted copy of x is made;
+//     group's weight is zero, not the next group's) and of its half of the tile's rows of x, by boxes of 16 to 128 rows;
+//   * warps 10-13, where `rows` gives the rows of x: 16-byte asynchronous copies from where they are, so that no sorted copy
+//     of x is made.  (TMA's gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs
+//     leaves: 8192 rows of 8 choices, 128 groups, 2 x 2048 x 7168: 9.05 ms.);
 //   * warp 1 of the even CTA: MMA issuer; warps 2-9: epilogue, two for each quarter of the TMEM lanes;
 //   * fp32 accumulators double-buffered in TMEM;
 //   * SwiGLU: boxes of 16 gate rows and their 16 up rows, so that a warp's 32 lanes hold both: one shuffle for two rows
@@ -31,7 +33,8 @@ constexpr int kHalf = 128;                        // W rows per CTA
 constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
 constexpr int kMaxRowsTile = 256, kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kGatherWarps = 4, kGatherAhead = 4;  // stages whose copies are on their way when one is handed over
+__host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps : 0)); }
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 struct GroupedShared {
@@ -41,7 +44,7 @@ struct GroupedShared {
     uint64_t acc_empty[2];       // leader only: both CTAs' epilogues have read it
     uint32_t tmem_base;
     int32_t bad_pair, aborted, issued, consumed;
-    int32_t part[kThreads / 32];
+    int32_t part[threads_of(true) / 32];
     int32_t tiles[kMaxGroups + 1];  // row tiles before each group
     int32_t first[kMaxGroups];      // first row of each group
     int32_t count[kMaxGroups];      // its rows
@@ -75,10 +78,16 @@ __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int groups, lon
     return r;
 }
 
+// Maps of x with boxes of 16, 32, 64 and 128 rows.
+struct RowMaps {
+    CUtensorMap of[4];
+};
+
 template <bool SWIGLU, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                   const GroupedArgs a, int bt, int stages, int32_t *status) {
+__global__ void __launch_bounds__(threads_of(GATHER), 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ RowMaps tm_x,
+                   const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
+    constexpr int kThreads = threads_of(GATHER);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -96,9 +105,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
+        if (!GATHER)
+            for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm_x.of[i]);
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&sh.full[s], 1);   // the leader producer's arrive.expect_tx
+            mbar_init(&sh.full[s], 1 + (GATHER ? 2 * kGatherWarps : 0));  // the leader producer's arrive.expect_tx, the copies of x
             mbar_init(&sh.empty[s], 1);  // the leader's multicast commit
         }
         for (int b = 0; b < 2; ++b) {
@@ -173,12 +183,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit t = unit_of(sh, a.groups, u, m_tiles);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
             const int n0 = t.m * kOuts + (int)rank * (kOuts / 2);
-            int32_t row[4] = {0, 0, 0, 0};
-            if (GATHER) {  // rows past the tile's: its last one again
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    row[j] = min(max(__ldg(a.rows + min(q0 + 4 * lane + j, t.p0 + t.rows - 1)), 0), a.x_rows - 1);
-            }
             for (int c = 0; c < C; ++c, ++it) {
                 const int s = it % stages;
                 ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
@@ -189,16 +193,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
-                if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * kWBytes + t.cols * kChunkK * 2));
+                if (leader && lane == 0)
+                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2)));
                 if (SWIGLU) {
-                    if (lane < 4) tma_load_4d_pair(st + lane * (kWBytes / 4), &tm_w, fb, c * kChunkK, n0 + 16 * lane, 0, t.e);
+                    if (w_boxes == 1) {
+                        if (lane == 0) tma_load_5d_pair(st, &tm_w, fb, c * kChunkK, 0, 0, n0 >> 4, t.e);
+                    } else if (lane < 4) {
+                        tma_load_4d_pair(st + lane * (kWBytes / 4), &tm_w, fb, c * kChunkK, n0 + 16 * lane, 0, t.e);
+                    }
                 } else {
                     if (lane == 0) tma_load_4d_pair(st, &tm_w, fb, c * kChunkK, n0, 0, t.e);
                 }
-                if (GATHER) {
-                    if (4 * lane < half) tma_gather4_pair(st + kWBytes + 512 * lane, &tm_x, fb, c * kChunkK, row);
-                } else {
-                    if (16 * lane < half) tma_load_2d_pair(st + kWBytes + 2048 * lane, &tm_x, fb, c * kChunkK, q0 + 16 * lane);
+                // this CTA's rows, a multiple of 16, by boxes of falling sizes: lane 4 + i takes 16 << i of them
+                if (!GATHER && lane >= 4 && lane < 8 && (half & (1 << lane))) {
+                    const int r = half & ~((2 << lane) - 1);
+                    tma_load_2d_pair(st + kWBytes + r * 128, &tm_x.of[lane - 4], fb, c * kChunkK, q0 + r);
                 }
             }
         }
@@ -247,6 +256,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sh.consumed = it;
         }
+        __syncwarp();
+    } else if (warp >= 2 + kEpiWarps) {
+        // ---- x by index (both CTAs): eight lanes a row, 16 rows at a time over the four warps ----
+        const int gt = tid - 32 * (2 + kEpiWarps), r0 = gt >> 3, v = gt & 7;
+        const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
+        const uint16_t *x = static_cast<const uint16_t *>(a.x) + 8 * v;
+        const uint32_t to0 = smem_u32(ring) + kWBytes + (uint32_t)(r0 * 128 + ((v ^ (r0 & 7)) << 4));
+        int it = 0, handed = 0;  // stages asked for, handed over
+        bool ok = true;
+        auto hand = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)((handed % stages) * sizeof(uint64_t)));
+            ++handed;
+        };
+        for (long long u = cl; ok && u < units; u += ncl) {
+            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;
+            const uint16_t *row[kHalf / 16];  // rows past the tile's: its last one again
+#pragma unroll
+            for (int i = 0; i < kHalf / 16; ++i) {
+                const int p = min(q0 + r0 + 16 * i, t.p0 + t.rows - 1);
+                row[i] = x + (size_t)min(max(__ldg(a.rows + p), 0), a.x_rows - 1) * a.K;
+            }
+            for (int c = 0; c < C; ++c, ++it) {
+                const int s = it % stages;
+                ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
+                ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
+                if (!ok) {
+                    if (lane == 0) atomicExch(&sh.aborted, 1);
+                    break;
+                }
+                const uint32_t to = to0 + (uint32_t)(s * stage_bytes);
+                const uint32_t bytes = c * kChunkK + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
+#pragma unroll
+                for (int i = 0; i < kHalf / 16; ++i)
+                    if (16 * i < half) cp_async_16(to + 2048 * i, row[i] + (bytes ? c * kChunkK : 0), bytes);
+                cp_async_commit();
+                if (it - handed >= kGatherAhead) {
+                    cp_async_wait<kGatherAhead>();
+                    hand();
+                }
+            }
+        }
+        cp_async_wait<0>();
+        while (ok && handed < it) hand();
         __syncwarp();
     } else {
         // ---- epilogue: TMEM lane quarter = warp % 4; the quarter's two warps take 16 rows of x in turn ----
@@ -357,19 +412,20 @@ int stages_of(int bt) {
 }
 // One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
 int smem_of(int bt) { return 1024 + stages_of(bt) * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
+static_assert(kGatherAhead < 6, "a stage is handed over before its next use is waited for");
 static_assert(kSmem - 1024 - (int)sizeof(GroupedShared) >= 6 * (kWBytes + kMaxRowsTile * kChunkK), "six stages of the widest");
 
-using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const GroupedArgs, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
 
 GroupedFn pick(bool swiglu, bool gather) {
     if (swiglu) return gather ? grouped_kernel<true, true> : grouped_kernel<true, false>;
     return gather ? grouped_kernel<false, true> : grouped_kernel<false, false>;
 }
 
-cudaLaunchConfig_t config(int clusters, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t config(int clusters, bool gather, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads_of(gather));
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = (cudaStream_t)stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -395,7 +451,7 @@ int init_grouped() {
     const int e = (int)cudaGetDevice(&dev);
     if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config(kGb300Sms, kSmem, 0, nullptr, attr);
+    cudaLaunchConfig_t cfg = config(kGb300Sms, true, kSmem, 0, nullptr, attr);
     cfg.numAttrs = 1;
     int n = 0;
     // A failed query only loses the clamp (launches then use half the SMs' number).
@@ -412,12 +468,17 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     const int full = a.P < a.groups ? a.P : a.groups;  // groups that may have rows
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
-    CUtensorMap tw, tx;
-    int r = make_tmap_bf16_stack(&tw, a.w, (uint64_t)a.groups, a.swiglu ? 2 : 1, (uint64_t)a.N, (uint64_t)a.K,
-                                 a.swiglu ? 2 : 1, a.swiglu ? 16 : kHalf, kChunkK);
-    if (r) return (int)cudaErrorInvalidValue;
-    r = make_tmap_bf16_2d(&tx, a.x, (uint64_t)a.x_rows, (uint64_t)a.K, a.rows ? 1 : 16, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    CUtensorMap tw;
+    RowMaps tx = {};
+    // SwiGLU: blocks of 16 gate rows and their 16 up rows, all of a stage's in one box where no block runs past N
+    const int w_boxes = a.swiglu && a.N % 16 ? 4 : 1;
+    int r = a.swiglu && w_boxes == 1
+                ? make_tmap_bf16_blocks(&tw, a.w, (uint64_t)a.groups, 2, (uint64_t)a.N, (uint64_t)a.K, 16, 4, kChunkK)
+                : make_tmap_bf16_stack(&tw, a.w, (uint64_t)a.groups, a.swiglu ? 2 : 1, (uint64_t)a.N, (uint64_t)a.K,
+                                       a.swiglu ? 2 : 1, a.swiglu ? 16 : kHalf, kChunkK);
+    for (int i = 0; i < 4 && !r && !a.rows; ++i)
+        r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, (uint64_t)a.K, 16u << i, kChunkK,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (r) return (int)cudaErrorInvalidValue;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
@@ -427,8 +488,9 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config((int)clusters, smem_of(bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, bt, stages_of(bt), status);
+    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, stages_of(bt),
+                                   status);
 }
 
 }  // namespace bf16l

@@ -1,5 +1,5 @@
 // grouped.cuh — device helpers of the kernels whose weight depends on the row: TMA loads for a CTA pair from a stack of
-// matrices and from rows given by index, and the tiles of groups whose sizes the device alone knows.
+// matrices, and copies of rows given by index.
 #pragma once
 
 #include "common.cuh"
@@ -16,20 +16,29 @@ __device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
-// Four rows of a matrix (a map whose box is one row high), 128 bytes of each from column c0 on, to 512 bytes at dst.
-__device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t c0,
-                                                 const int32_t (&row)[4]) {
+// ... c0 innermost (K), c1 row of a block, c2 half, c3 block, c4 matrix.
+__device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t c0,
+                                                 int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(row[0]), "r"(row[1]),
-        "r"(row[2]), "r"(row[3])
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(c4)
         : "memory");
+}
+
+// Sixteen bytes to shared memory, asynchronously: those from `bytes` (0 or 16) on are zero and not read.
+__device__ __forceinline__ void cp_async_16(uint32_t to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
 // Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
 // box_halves x 1 elements and 128-byte swizzle.  Defined in api.cu.  Returns a CUresult value (0 on success).
 int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
                          uint32_t box_halves, uint32_t box_rows, uint32_t box_cols);
+// The same with the rows in blocks of block_rows (a divisor of rows): a box is box_blocks blocks of every half, in shared
+// memory block by block, a block's halves one after the other.
+int make_tmap_bf16_blocks(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
+                          uint32_t block_rows, uint32_t box_blocks, uint32_t box_cols);
 
 }  // namespace bf16l
