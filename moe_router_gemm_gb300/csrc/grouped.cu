@@ -11,7 +11,7 @@
 //   * warp 0: TMA producer, all its lanes: 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
 //     group's weight is zero, not the next group's) and of its half of the tile's rows of x, by boxes of 16 to 128 rows;
 //   * warps 10-13, where `rows` gives the rows of x: 16-byte asynchronous copies from where they are, so that no sorted copy
-//     of x is made.  (TMA's gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs
+//     of x is made; they arrive by themselves on a barrier of the CTA, and warp 14 passes that on to the leader's.  (TMA's gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs
 //     leaves: 8192 rows of 8 choices, 128 groups, 2 x 2048 x 7168: 9.05 ms.);
 //   * warp 1 of the even CTA: MMA issuer; warps 2-9: epilogue, two for each quarter of the TMEM lanes;
 //   * fp32 accumulators double-buffered in TMEM;
@@ -31,15 +31,16 @@ namespace {
 
 constexpr int kHalf = 128;                        // W rows per CTA
 constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
-constexpr int kMaxRowsTile = 256, kMaxStages = 12;
+constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kGatherWarps = 4, kGatherAhead = 4;  // stages whose copies are on their way when one is handed over
-__host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps : 0)); }
+constexpr int kGatherWarps = 2, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
+__host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps + 1 : 0)); }
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 struct GroupedShared {
     uint64_t full[kMaxStages];   // leader only: both CTAs' copies of the stage have landed
     uint64_t empty[kMaxStages];  // both: the MMAs reading the stage are done
+    uint64_t copied[kMaxStages]; // this CTA's rows of x by index are in shared memory
     uint64_t acc_full[2];        // both: the accumulator holds a finished tile
     uint64_t acc_empty[2];       // leader only: both CTAs' epilogues have read it
     uint32_t tmem_base;
@@ -86,12 +87,13 @@ struct RowMaps {
 template <bool SWIGLU, bool GATHER>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ RowMaps tm_x,
-                   const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
+                   const GroupedArgs a, int w_boxes, int bt, int kc, int stages, int32_t *status) {
     constexpr int kThreads = threads_of(GATHER);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    const int stage_bytes = kWBytes + bt * kChunkK;  // bt / 2 rows of 128 bytes
+    const int chunk_bytes = kWBytes + bt * kChunkK;  // W rows, and bt / 2 rows of x, of 128 bytes
+    const int stage_bytes = kc * chunk_bytes;        // kc consecutive chunks of K
     GroupedShared &sh = *reinterpret_cast<GroupedShared *>(ring + stages * stage_bytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     constexpr int kOuts = SWIGLU ? 128 : 256;  // outputs of a W tile
     const int m_tiles = (a.N + kOuts - 1) / kOuts;
     const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
-    const int C = (a.K + kChunkK - 1) / kChunkK;
+    const int C = (a.K + kChunkK * kc - 1) / (kChunkK * kc);  // stages of a tile (zeros past K)
     const uint32_t tmem_cols = 2u * (uint32_t)bt;
 
     if (tid == 0) {
@@ -108,7 +110,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         if (!GATHER)
             for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm_x.of[i]);
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&sh.full[s], 1 + (GATHER ? 2 * kGatherWarps : 0));  // the leader producer's arrive.expect_tx, the copies of x
+            mbar_init(&sh.full[s], GATHER ? 3 : 1);  // the leader producer's arrive.expect_tx, each CTA's copies of x
+            mbar_init(&sh.copied[s], 32 * kGatherWarps);
             mbar_init(&sh.empty[s], 1);  // the leader's multicast commit
         }
         for (int b = 0; b < 2; ++b) {
@@ -194,20 +197,23 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
                 if (leader && lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2)));
-                if (SWIGLU) {
-                    if (w_boxes == 1) {
-                        if (lane == 0) tma_load_5d_pair(st, &tm_w, fb, c * kChunkK, 0, 0, n0 >> 4, t.e);
-                    } else if (lane < 4) {
-                        tma_load_4d_pair(st + lane * (kWBytes / 4), &tm_w, fb, c * kChunkK, n0 + 16 * lane, 0, t.e);
+                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(kc * (2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2))));
+                // eight lanes a chunk: the first (with four boxes, the first four) bring W ...
+                const int i = lane & 7, k0 = (c * kc + (lane >> 3)) * kChunkK;
+                uint8_t *ch = st + (lane >> 3) * chunk_bytes;
+                if (lane >> 3 < kc) {
+                    if (!SWIGLU) {
+                        if (i == 0) tma_load_4d_pair(ch, &tm_w, fb, k0, n0, 0, t.e);
+                    } else if (w_boxes == 1) {
+                        if (i == 0) tma_load_5d_pair(ch, &tm_w, fb, k0, 0, 0, n0 >> 4, t.e);
+                    } else if (i < 4) {
+                        tma_load_4d_pair(ch + i * (kWBytes / 4), &tm_w, fb, k0, n0 + 16 * i, 0, t.e);
                     }
-                } else {
-                    if (lane == 0) tma_load_4d_pair(st, &tm_w, fb, c * kChunkK, n0, 0, t.e);
-                }
-                // this CTA's rows, a multiple of 16, by boxes of falling sizes: lane 4 + i takes 16 << i of them
-                if (!GATHER && lane >= 4 && lane < 8 && (half & (1 << lane))) {
-                    const int r = half & ~((2 << lane) - 1);
-                    tma_load_2d_pair(st + kWBytes + r * 128, &tm_x.of[lane - 4], fb, c * kChunkK, q0 + r);
+                    // ... and 4 to 7 this CTA's rows, a multiple of 16, by boxes of falling sizes: lane i takes 1 << i
+                    if (!GATHER && i >= 4 && (half & (1 << i))) {
+                        const int r = half & ~((2 << i) - 1);
+                        tma_load_2d_pair(ch + kWBytes + r * 128, &tm_x.of[i - 4], fb, k0, q0 + r);
+                    }
                 }
             }
         }
@@ -237,12 +243,14 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint8_t *st = ring + s * stage_bytes;
-                    const uint64_t adesc = smem_desc_sw128(smem_u32(st));
-                    const uint64_t bdesc = smem_desc_sw128(smem_u32(st + kWBytes));
+                    const uint8_t *ch = ring + s * stage_bytes;
+                    for (int j = 0; j < kc; ++j, ch += chunk_bytes) {
+                        const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
+                        const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + kWBytes));
 #pragma unroll
-                    for (int kk = 0; kk < kChunkK / 16; ++kk)
-                        mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < kChunkK / 16; ++kk)
+                            mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || j > 0 || kk > 0) ? 1u : 0u);
+                    }
                     mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
                 }
                 if (!ok) {  // release both epilogues at once
@@ -257,27 +265,34 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             sh.consumed = it;
         }
         __syncwarp();
-    } else if (warp >= 2 + kEpiWarps) {
-        // ---- x by index (both CTAs): eight lanes a row, 16 rows at a time over the four warps ----
+    } else if (GATHER && warp == 2 + kEpiWarps + kGatherWarps) {
+        if (lane == 0) {  // ---- x by index: what has arrived, to the leader's barrier (both CTAs) ----
+            const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
+            int it = 0;
+            bool ok = true;
+            for (long long u = cl; ok && u < units; u += ncl)
+                for (int c = 0; ok && c < C; ++c, ++it) {
+                    ok = mbar_wait(&sh.copied[it % stages], (it / stages) & 1, status, kSiteStage);
+                    fence_proxy_async_smem();  // the copies, seen here, before the MMAs' reads
+                    if (ok) mbar_arrive_remote(full0 + (uint32_t)((it % stages) * sizeof(uint64_t)));
+                }
+            if (!ok) atomicExch(&sh.aborted, 1);
+        }
+        __syncwarp();
+    } else if (GATHER && warp >= 2 + kEpiWarps) {
+        // ---- x by index (both CTAs): eight lanes a row, kGatherRows rows at a time over the warps ----
         const int gt = tid - 32 * (2 + kEpiWarps), r0 = gt >> 3, v = gt & 7;
-        const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
         const uint16_t *x = static_cast<const uint16_t *>(a.x) + 8 * v;
         const uint32_t to0 = smem_u32(ring) + kWBytes + (uint32_t)(r0 * 128 + ((v ^ (r0 & 7)) << 4));
-        int it = 0, handed = 0;  // stages asked for, handed over
+        int it = 0;
         bool ok = true;
-        auto hand = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(full0 + (uint32_t)((handed % stages) * sizeof(uint64_t)));
-            ++handed;
-        };
         for (long long u = cl; ok && u < units; u += ncl) {
             const Unit t = unit_of(sh, a.groups, u, m_tiles);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;
-            const uint16_t *row[kHalf / 16];  // rows past the tile's: its last one again
+            const uint16_t *row[kHalf / kGatherRows];  // rows past the tile's: its last one again
 #pragma unroll
-            for (int i = 0; i < kHalf / 16; ++i) {
-                const int p = min(q0 + r0 + 16 * i, t.p0 + t.rows - 1);
+            for (int i = 0; i < kHalf / kGatherRows; ++i) {
+                const int p = min(q0 + r0 + kGatherRows * i, t.p0 + t.rows - 1);
                 row[i] = x + (size_t)min(max(__ldg(a.rows + p), 0), a.x_rows - 1) * a.K;
             }
             for (int c = 0; c < C; ++c, ++it) {
@@ -288,20 +303,19 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     if (lane == 0) atomicExch(&sh.aborted, 1);
                     break;
                 }
-                const uint32_t to = to0 + (uint32_t)(s * stage_bytes);
-                const uint32_t bytes = c * kChunkK + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
+                uint32_t to = to0 + (uint32_t)(s * stage_bytes);
+                for (int j = 0; j < kc; ++j, to += (uint32_t)chunk_bytes) {
+                    const int k0 = (c * kc + j) * kChunkK;
+                    const uint32_t bytes = k0 + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
 #pragma unroll
-                for (int i = 0; i < kHalf / 16; ++i)
-                    if (16 * i < half) cp_async_16(to + 2048 * i, row[i] + (bytes ? c * kChunkK : 0), bytes);
-                cp_async_commit();
-                if (it - handed >= kGatherAhead) {
-                    cp_async_wait<kGatherAhead>();
-                    hand();
+                    for (int i = 0; i < kHalf / kGatherRows; ++i)
+                        if (r0 + kGatherRows * i < half)
+                            cp_async_16(to + 128 * kGatherRows * i, row[i] + (bytes ? k0 : 0), bytes);
                 }
+                cp_async_arrive(&sh.copied[s]);
             }
         }
-        cp_async_wait<0>();
-        while (ok && handed < it) hand();
+        cp_async_wait_all();
         __syncwarp();
     } else {
         // ---- epilogue: TMEM lane quarter = warp % 4; the quarter's two warps take 16 rows of x in turn ----
@@ -405,17 +419,15 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
 constexpr int kMaxDevices = 64;
 int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
 
+// One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
 constexpr int kSmem = 232448;
-int stages_of(int bt) {
-    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kWBytes + bt * kChunkK);
+int stages_of(int bt, int kc) {
+    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kc * (kWBytes + bt * kChunkK));
     return n < kMaxStages ? n : kMaxStages;
 }
-// One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
-int smem_of(int bt) { return 1024 + stages_of(bt) * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
-static_assert(kGatherAhead < 6, "a stage is handed over before its next use is waited for");
-static_assert(kSmem - 1024 - (int)sizeof(GroupedShared) >= 6 * (kWBytes + kMaxRowsTile * kChunkK), "six stages of the widest");
+int smem_of(int bt, int kc) { return 1024 + stages_of(bt, kc) * kc * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
 
-using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int, int32_t *);
 
 GroupedFn pick(bool swiglu, bool gather) {
     if (swiglu) return gather ? grouped_kernel<true, true> : grouped_kernel<true, false>;
@@ -468,6 +480,7 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     const int full = a.P < a.groups ? a.P : a.groups;  // groups that may have rows
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
+    const int kc = bt <= 64 ? 2 : 1;
     CUtensorMap tw;
     RowMaps tx = {};
     // SwiGLU: blocks of 16 gate rows and their 16 up rows, all of a stage's in one box where no block runs past N
@@ -488,9 +501,9 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, stages_of(bt),
-                                   status);
+    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt, kc), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, kc,
+                                   stages_of(bt, kc), status);
 }
 
 }  // namespace bf16l

@@ -32,6 +32,12 @@ __device__ __forceinline__ void cp_async_16(uint32_t to, const void *from, uint3
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
+// One arrival on an mbarrier of this CTA (of those that it was set up for) when this thread's copies so far are complete.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
 // box_halves x 1 elements and 128-byte swizzle.  Defined in api.cu.  Returns a CUresult value (0 on success).
 int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
