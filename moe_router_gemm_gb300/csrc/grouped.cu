@@ -31,7 +31,8 @@ namespace {
 
 constexpr int kHalf = 128;                        // W rows per CTA
 constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
-constexpr int kMaxStages = 12;
+constexpr int kChunks = 2;  // 64-wide chunks of K in a stage
+constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
 __host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps + 1 : 0)); }
@@ -87,13 +88,13 @@ struct RowMaps {
 template <bool SWIGLU, bool GATHER>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ RowMaps tm_x,
-                   const GroupedArgs a, int w_boxes, int bt, int kc, int stages, int32_t *status) {
+                   const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
     constexpr int kThreads = threads_of(GATHER);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int chunk_bytes = kWBytes + bt * kChunkK;  // W rows, and bt / 2 rows of x, of 128 bytes
-    const int stage_bytes = kc * chunk_bytes;        // kc consecutive chunks of K
+    const int stage_bytes = kChunks * chunk_bytes;
     GroupedShared &sh = *reinterpret_cast<GroupedShared *>(ring + stages * stage_bytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     constexpr int kOuts = SWIGLU ? 128 : 256;  // outputs of a W tile
     const int m_tiles = (a.N + kOuts - 1) / kOuts;
     const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
-    const int C = (a.K + kChunkK * kc - 1) / (kChunkK * kc);  // stages of a tile (zeros past K)
+    const int C = (a.K + kChunkK * kChunks - 1) / (kChunkK * kChunks);  // stages of a tile (zeros past K)
     const uint32_t tmem_cols = 2u * (uint32_t)bt;
 
     if (tid == 0) {
@@ -197,11 +198,11 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
                 if (leader && lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(kc * (2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2))));
+                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(kChunks * (2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2))));
                 // eight lanes a chunk: the first (with four boxes, the first four) bring W ...
-                const int i = lane & 7, k0 = (c * kc + (lane >> 3)) * kChunkK;
+                const int i = lane & 7, k0 = (c * kChunks + (lane >> 3)) * kChunkK;
                 uint8_t *ch = st + (lane >> 3) * chunk_bytes;
-                if (lane >> 3 < kc) {
+                if (lane >> 3 < kChunks) {
                     if (!SWIGLU) {
                         if (i == 0) tma_load_4d_pair(ch, &tm_w, fb, k0, n0, 0, t.e);
                     } else if (w_boxes == 1) {
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                     tc_fence_after();
                     const uint8_t *ch = ring + s * stage_bytes;
-                    for (int j = 0; j < kc; ++j, ch += chunk_bytes) {
+                    for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
                         const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
                         const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + kWBytes));
 #pragma unroll
@@ -304,8 +305,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     break;
                 }
                 uint32_t to = to0 + (uint32_t)(s * stage_bytes);
-                for (int j = 0; j < kc; ++j, to += (uint32_t)chunk_bytes) {
-                    const int k0 = (c * kc + j) * kChunkK;
+                for (int j = 0; j < kChunks; ++j, to += (uint32_t)chunk_bytes) {
+                    const int k0 = (c * kChunks + j) * kChunkK;
                     const uint32_t bytes = k0 + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
@@ -421,13 +422,13 @@ int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
 
 // One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
 constexpr int kSmem = 232448;
-int stages_of(int bt, int kc) {
-    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kc * (kWBytes + bt * kChunkK));
+int stages_of(int bt) {
+    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kChunks * (kWBytes + bt * kChunkK));
     return n < kMaxStages ? n : kMaxStages;
 }
-int smem_of(int bt, int kc) { return 1024 + stages_of(bt, kc) * kc * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
+int smem_of(int bt) { return 1024 + stages_of(bt) * kChunks * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
 
-using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
 
 GroupedFn pick(bool swiglu, bool gather) {
     if (swiglu) return gather ? grouped_kernel<true, true> : grouped_kernel<true, false>;
@@ -480,7 +481,6 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     const int full = a.P < a.groups ? a.P : a.groups;  // groups that may have rows
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
-    const int kc = bt <= 64 ? 2 : 1;
     CUtensorMap tw;
     RowMaps tx = {};
     // SwiGLU: blocks of 16 gate rows and their 16 up rows, all of a stage's in one box where no block runs past N
@@ -501,9 +501,9 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt, kc), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, kc,
-                                   stages_of(bt, kc), status);
+    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, stages_of(bt),
+                                   status);
 }
 
 }  // namespace bf16l
