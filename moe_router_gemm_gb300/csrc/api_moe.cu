@@ -226,7 +226,7 @@ extern "C" int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int gr
     bf16l_device dev;
     const int st = current_device_checked(&dev);
     if (st != BF16L_OK) return st;
-    return result(launch_group_rows(ids, (int)n, k, groups, offsets, rows, place, flags, stream));
+    return result(launch_group_rows(ids, (int)n, k, groups, false, offsets, rows, place, flags, stream));
 }
 
 extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
@@ -249,7 +249,7 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     int32_t *status = nullptr;
     const int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0};
+    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, 0};
     return result(launch_grouped(a, dev.num_sms, flags, stream, status));
 }
 
@@ -272,9 +272,26 @@ extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *p
     return result(launch_combine_rows(y, y_rows, place, weights, addend, out, tokens, k, H, dev.num_sms, flags, stream));
 }
 
+namespace {
+
+// The parts of the adapters' workspace: for few rows the inner values and the shared product, for many the rows' order and
+// the inner values in that order.
+constexpr int kLoraFew = 64;
+struct LoraSpace {
+    size_t first, second, third;  // bytes
+    size_t all() const { return first + second + third; }
+};
+LoraSpace lora_space(int M, int N, int R, int L) {
+    const size_t m = (size_t)M, r = (size_t)R;
+    if (M <= kLoraFew) return {up256(4 * kLoraSplits * m * r), up256(4 * m * (size_t)N), 0};
+    return {up256(4 * ((size_t)L + 1)), up256(4 * m), up256(4 * m * r)};
+}
+
+}  // namespace
+
 extern "C" size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L) {
     if (M <= 0 || N <= 0 || K <= 0 || K % 8 != 0 || R <= 0 || R % 8 != 0 || R > kLoraMaxRank || L <= 0) return 0;
-    return up256(4ull * (size_t)M * (size_t)R) + up256(4ull * (size_t)M * (size_t)N);
+    return lora_space(M, N, R, L).all();
 }
 
 extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b,
@@ -289,19 +306,31 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
         off(ids, 4) || off(workspace, 256))
         return BF16L_EALIGN;
     const uint64_t m = (uint64_t)M, n = (uint64_t)N, k = (uint64_t)K, r = (uint64_t)R, l = (uint64_t)L;
-    if (m * n > kMaxElements || l * r * (n > k ? n : k) > kMaxElements) return BF16L_EINVAL;
+    if (M > kMaxRows || m * n > kMaxElements || l * r * (n > k ? n : k) > kMaxElements) return BF16L_EINVAL;
     const size_t need = bf16_linear_lora_workspace(M, N, K, R, L);
     if (!workspace || workspace_bytes < need) return BF16L_EINVAL;
     const Span outs[2] = {{out, 2 * m * n}, {workspace, need}};
     const Span ins[7] = {{x, 2 * m * k}, {w, 2 * n * k}, {bias, 2 * n}, {a, 2 * l * r * k}, {b, 2 * l * r * n},
                          {scale, 4 * l}, {ids, 4 * m}};
     if (clash(outs, ins)) return BF16L_EINVAL;
-    float *h = static_cast<float *>(workspace);
-    float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(4ull * (size_t)M * (size_t)R));
-    const LoraArgs args = {x, a, b, scale, ids, h, y, out, M, N, K, R, L};
     bf16l_device dev;
-    int st = current_device_checked(&dev);
-    if (st == BF16L_OK) st = result(launch_lora_inner(args, flags, stream));
-    if (st == BF16L_OK) st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
-    return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
+    int32_t *status = nullptr;
+    int st = current_device_status(&dev, &status);
+    if (st != BF16L_OK) return st;
+    const LoraSpace space = lora_space(M, N, R, L);
+    uint8_t *p = static_cast<uint8_t *>(workspace);
+    LoraArgs args = {x, a, b, scale, ids, nullptr, nullptr, out, M, N, K, R, L};
+    if (M <= kLoraFew) {
+        args.h = reinterpret_cast<float *>(p);
+        float *y = reinterpret_cast<float *>(p + space.first);
+        args.y = y;
+        st = result(launch_lora_inner(args, flags, stream));
+        if (st == BF16L_OK) st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
+        return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
+    }
+    int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + space.first);
+    st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
+    if (st != BF16L_OK) return st;
+    return result(launch_lora_grouped(args, w, bias, offsets, rows, p + space.first + space.second, dev.num_sms, flags,
+                                      stream, status));
 }

@@ -22,28 +22,29 @@ struct GroupArgs {
     const int32_t *ids;
     int32_t *offsets, *rows, *place;
     int n, k, groups;
-    int per;  // keys of a warp, a multiple of 32
+    int cols;  // groups, and one more where what belongs to none is ordered behind them
+    int per;   // keys of a warp, a multiple of 32
 };
 
 // Shared memory: the warps' histograms, the CTA's counts, the first position of each group's rows from this CTA.
-__host__ __device__ constexpr int group_smem_bytes(int groups) { return 4 * groups * (kWarps + 2); }
+__host__ __device__ constexpr int group_smem_bytes(int cols) { return 4 * cols * (kWarps + 2); }
 
 __device__ __forceinline__ int key_of(const GroupArgs &a, int i, int end) {
     const int id = i < end ? __ldg(a.ids + i) : -1;
-    return (unsigned)id < (unsigned)a.groups ? id : -1;
+    return (unsigned)id < (unsigned)a.groups ? id : a.cols > a.groups && i < end ? a.groups : -1;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     extern __shared__ int sm[];
     __shared__ int part[kWarps];
-    int *count = sm + kWarps * a.groups, *start = count + a.groups;
+    int *count = sm + kWarps * a.cols, *start = count + a.cols;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // one cluster
-    int *mine = sm + warp * a.groups;
+    int *mine = sm + warp * a.cols;
     const long long lo64 = (long long)(rank * kWarps + warp) * a.per;
     const int lo = (int)(lo64 < a.n ? lo64 : a.n), hi = (int)(lo64 + a.per < a.n ? lo64 + a.per : a.n);
 
-    for (int e = tid; e < kWarps * a.groups; e += kThreads) sm[e] = 0;
+    for (int e = tid; e < kWarps * a.cols; e += kThreads) sm[e] = 0;
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
@@ -55,12 +56,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
         __syncwarp();
     }
     __syncthreads();
-    for (int e = tid; e < a.groups; e += kThreads) {
+    for (int e = tid; e < a.cols; e += kThreads) {
         int sum = 0;
 #pragma unroll 8
         for (int w = 0; w < kWarps; ++w) {
-            const int c = sm[w * a.groups + e];
-            sm[w * a.groups + e] = sum;
+            const int c = sm[w * a.cols + e];
+            sm[w * a.cols + e] = sum;
             sum += c;
         }
         count[e] = sum;
@@ -68,18 +69,20 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     cluster_sync();
 
     // groups up to 1024: one a thread
-    int all = 0, before = 0;
-    if (tid < a.groups) {
+    auto counts = [&](int e, int &all, int &before) {
         for (int c = 0; c < ctas; ++c) {
             int v;
             asm volatile("ld.shared::cluster.u32 %0, [%1];"
                          : "=r"(v)
-                         : "r"(mapa_shared(smem_u32(count + tid), (uint32_t)c))
+                         : "r"(mapa_shared(smem_u32(count + e), (uint32_t)c))
                          : "memory");
             all += v;
             before += c < rank ? v : 0;
         }
-    }
+    };
+    int all = 0, before = 0, none = 0, none_before = 0;
+    if (tid < a.groups) counts(tid, all, before);
+    if (tid == 0 && a.cols > a.groups) counts(a.groups, none, none_before);
     int upto = all;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -100,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     }
     int kept = 0;
     for (int w = 0; w < kWarps; ++w) kept += part[w];
+    if (tid == 0 && a.cols > a.groups) start[a.groups] = kept + none_before;
     __syncthreads();
 
     for (int i0 = lo; i0 < hi; i0 += 32) {
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
             if (at >= 0) a.rows[at] = i / a.k;
         }
     }
+    if (a.cols > a.groups) return;
     for (long long p = kept + (long long)rank * kThreads + tid; p < a.n; p += (long long)ctas * kThreads) a.rows[p] = -1;
 }
 
@@ -200,19 +205,19 @@ int launch_combine(const void *y, long long y_rows, const int32_t *place, const 
 
 int init_group() {
     return (int)cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     group_smem_bytes(kMaxGroups));
+                                     group_smem_bytes(kMaxGroups + 1));
 }
 
-int launch_group_rows(const int32_t *ids, int n, int k, int groups, int32_t *offsets, int32_t *rows, int32_t *place,
-                      uint32_t flags, void *stream) {
+int launch_group_rows(const int32_t *ids, int n, int k, int groups, bool rest, int32_t *offsets, int32_t *rows,
+                      int32_t *place, uint32_t flags, void *stream) {
     const int ctas = n <= 4 * kThreads ? 1 : kCluster;
     const int warps = ctas * kWarps;
-    GroupArgs a = {ids, offsets, rows, place, n, k, groups, 0};
+    GroupArgs a = {ids, offsets, rows, place, n, k, groups, groups + (rest ? 1 : 0), 0};
     a.per = (int)(((long long)n + warps - 1) / warps + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)group_smem_bytes(groups);
+    cfg.dynamicSmemBytes = (size_t)group_smem_bytes(a.cols);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -17,6 +17,14 @@
 //   * fp32 accumulators double-buffered in TMEM;
 //   * SwiGLU: boxes of 16 gate rows and their 16 up rows, so that a warp's 32 lanes hold both: one shuffle for two rows
 //     of x brings them together in fp32, and out is written without the wide product's way through memory.
+// The same kernel runs the two products of a linear's adapters for many rows, ordered by adapter (rows of none last):
+//   * kInner: h = scale_e * x @ A_e^T, the groups being the adapters; out is the value in bf16 and what is left of it, in bf16
+//     again, so that the tensor cores take 16 bits of it;
+//   * kOuter: x @ W^T with 256 rows of x on the M side and 256 W rows on the N side, whose tiles then go on along K with the
+//     adapters that their rows have: 16 ranks a slot, eight slots a stage, each slot a tile of B_e (16 columns, 32-byte
+//     swizzle) against the rows' h, its MMAs writing the TMEM lanes of that adapter's rows alone (the MMA's lane mask), so
+//     that nothing of one adapter, not finite or not, reaches a row of another.  A row of out is written where its row of
+//     x is.
 // Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any remote arrival or copy) and one
 // before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>
@@ -37,6 +45,11 @@ constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
 __host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps + 1 : 0)); }
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kPer = (kMaxGroups + 32 * (2 + kEpiWarps) - 1) / (32 * (2 + kEpiWarps));  // groups of a thread, at most
+constexpr int kRank = 16, kSlots = 2 * kChunkK / kRank;  // ranks of a slot, slots of a stage
+constexpr int kSlotBytes = kHalf * kRank * 2;
+
+enum Mode { kPlain, kSwiglu, kInner, kOuter };
 
 struct GroupedShared {
     uint64_t full[kMaxStages];   // leader only: both CTAs' copies of the stage have landed
@@ -46,10 +59,10 @@ struct GroupedShared {
     uint64_t acc_empty[2];       // leader only: both CTAs' epilogues have read it
     uint32_t tmem_base;
     int32_t bad_pair, aborted, issued, consumed;
-    int32_t part[threads_of(true) / 32];
+    int32_t part[2][threads_of(true) / 32];
     int32_t tiles[kMaxGroups + 1];  // row tiles before each group
-    int32_t first[kMaxGroups];      // first row of each group
-    int32_t count[kMaxGroups];      // its rows
+    int32_t first[kMaxGroups + 1];  // first row of each group; kOuter: of each adapter that has rows, then of the rows of none
+    int32_t count[kMaxGroups];      // its rows; kOuter: which adapter
 };
 
 // Unit u: a row tile of a group and 256 W rows (128 outputs with SwiGLU); row tiles vary fastest.
@@ -57,9 +70,11 @@ struct Unit {
     int e, p0, rows, m;  // group, first position, rows, W tile
     int cols;            // rows rounded up for the MMA
 };
-__device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int groups, long long u, int m_tiles) {
+// ONE: a single group of n rows, in whole tiles of bt; else n groups.
+template <bool ONE>
+__device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int n, int bt, long long u, int m_tiles) {
+    int lo = 0, hi = ONE ? 1 : n;  // tiles[lo] <= q < tiles[hi]
     const int q = (int)(u / m_tiles);
-    int lo = 0, hi = groups;  // tiles[lo] <= q < tiles[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sh.tiles[mid] <= q)
@@ -67,17 +82,65 @@ __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int groups, lon
         else
             hi = mid;
     }
-    const int nt = sh.tiles[lo + 1] - sh.tiles[lo], count = sh.count[lo];
-    const long long local = u - (long long)sh.tiles[lo] * m_tiles;
+    const int before = ONE ? 0 : sh.tiles[lo];
+    const int nt = ONE ? (n + bt - 1) / bt : sh.tiles[lo + 1] - before, count = ONE ? n : sh.count[lo];
+    const long long local = u - (long long)before * m_tiles;
     const int m = (int)(local / nt), t = (int)(local - (long long)m * nt);
     const int each = count / nt, more = count - each * nt;
     Unit r;
     r.e = lo;
     r.m = m;
-    r.rows = each + (t < more);
-    r.p0 = sh.first[lo] + t * each + min(t, more);
-    r.cols = (r.rows + 31) & ~31;
+    r.rows = ONE ? min(bt, n - t * bt) : each + (t < more);
+    r.p0 = ONE ? t * bt : sh.first[lo] + t * each + min(t, more);
+    r.cols = ONE ? bt : (r.rows + 31) & ~31;
     return r;
+}
+
+// kOuter: the adapters of a tile's rows (of those that have rows), and the stages that they add: for each 64 ranks, slots of
+// 16 for one adapter after the other.
+struct Tail {
+    int first, n, R;
+    __device__ __forceinline__ int per(int kb) const { return (min(R - kb * kChunkK, kChunkK) + kRank - 1) / kRank; }
+    __device__ __forceinline__ int stages_of(int kb) const { return (n * per(kb) + kSlots - 1) / kSlots; }
+    __device__ __forceinline__ int stages() const { return n ? stages_of(0) + (R > kChunkK ? stages_of(1) : 0) : 0; }
+};
+struct TailStage {
+    int kb, per, q0, n;  // block of 64 ranks, slots of an adapter in it, first slot, slots
+};
+__device__ __forceinline__ TailStage tail_stage(const Tail &f, int d) {
+    const int s0 = f.stages_of(0);
+    TailStage r;
+    r.kb = d >= s0;
+    r.per = f.per(r.kb);
+    r.q0 = (d - (r.kb ? s0 : 0)) * kSlots;
+    r.n = min(kSlots, f.n * r.per - r.q0);
+    return r;
+}
+__device__ __forceinline__ Tail tail_of(const GroupedShared &sh, int adapters, const Unit &t, int R) {
+    auto below = [&](int p) {  // adapters (and the rows of none) that start below position p
+        int lo = 0, hi = adapters + 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sh.first[mid] < p)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    Tail r;
+    r.R = R;
+    r.first = max(below(t.p0 + 1) - 1, 0);
+    r.n = max(min(below(t.p0 + t.rows), adapters) - r.first, 0);
+    return r;
+}
+// The MMA's lane mask that leaves rows lo .. hi - 1 of a tile's 256 to be written.
+__device__ __forceinline__ void lanes_but(int lo, int hi, uint32_t (&off)[8]) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
+        off[w] = ~((h < 32 ? (1u << h) - 1u : ~0u) & ~(l < 32 ? (1u << l) - 1u : ~0u));
+    }
 }
 
 // Maps of x with boxes of 16, 32, 64 and 128 rows.
@@ -85,16 +148,19 @@ struct RowMaps {
     CUtensorMap of[4];
 };
 
-template <bool SWIGLU, bool GATHER>
+template <int MODE, bool GATHER>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ RowMaps tm_x,
-                   const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ RowMaps tm_x, const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
+    constexpr bool SWIGLU = MODE == kSwiglu;
+    static_assert(GATHER || MODE == kPlain || MODE == kSwiglu, "the adapters' rows go by index");
     constexpr int kThreads = threads_of(GATHER);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int chunk_bytes = kWBytes + bt * kChunkK;  // W rows, and bt / 2 rows of x, of 128 bytes
     const int stage_bytes = kChunks * chunk_bytes;
+    constexpr int kW = MODE == kOuter ? kWBytes : 0, kX = MODE == kOuter ? 0 : kWBytes;  // (the M side's rows first)
     GroupedShared &sh = *reinterpret_cast<GroupedShared *>(ring + stages * stage_bytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -148,33 +214,73 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     pdl_launch_dependents();
     pdl_wait();  // nothing is read before the previous kernel has finished
 
-    // The row tiles before each group: `per` consecutive groups a thread, summed over the block.
-    const int per = (a.groups + kThreads - 1) / kThreads, e0 = tid * per;
-    int mine = 0;
-    for (int e = e0; e < min(e0 + per, a.groups); ++e) {
-        const int lo = min(max(__ldg(a.offsets + e), 0), a.P), hi = min(max(__ldg(a.offsets + e + 1), lo), a.P);
-        sh.first[e] = lo;
-        sh.count[e] = hi - lo;
-        mine += (hi - lo + bt - 1) / bt;
+    // `per` consecutive groups a thread.  First the offsets, made to rise (the largest of those before, over the block) ...
+    const int per = (a.groups + kThreads - 1) / kThreads, e0 = min(tid * per, a.groups), e1 = min(e0 + per, a.groups);
+    int end[kPer + 1];  // clamped offsets of this thread's groups
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) {
+        end[i] = e0 + i <= e1 ? min(max(__ldg(a.offsets + e0 + i), 0), a.P) : 0;
+        if (e0 + i < e1) most = max(most, end[i]);
     }
-    int upto = mine;
+    int upto = most;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto = max(upto, v);
+    }
+    if (lane == 31) sh.part[0][warp] = upto;
+    upto = __shfl_up_sync(kAll, upto, 1);
+    __syncthreads();
+    int before = lane ? upto : 0;
+    for (int w = 0; w < warp; ++w) before = max(before, sh.part[0][w]);
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) before = end[i] = max(before, end[i]);
+    // ... then the row tiles before each group (kOuter: the adapters that have rows).
+    auto weight = [&](int i) {
+        const int n = end[i + 1] - end[i];
+        return MODE == kOuter ? (n > 0 ? 1 : 0) : (n + bt - 1) / bt;
+    };
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (e0 + i < e1) mine += weight(i);
+    upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int v = __shfl_up_sync(kAll, upto, d);
         if (lane >= d) upto += v;
     }
-    if (lane == 31) sh.part[warp] = upto;
+    if (lane == 31) sh.part[1][warp] = upto;
     __syncthreads();
-    int before = upto - mine;
-    for (int w = 0; w < warp; ++w) before += sh.part[w];
-    for (int e = e0; e < min(e0 + per, a.groups); ++e) {
-        sh.tiles[e] = before;
-        before += (sh.count[e] + bt - 1) / bt;
+    before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += sh.part[1][w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (e0 + i >= e1) continue;
+        const int n = weight(i);
+        if (MODE != kOuter) {
+            sh.tiles[e0 + i] = before;
+            sh.first[e0 + i] = end[i];
+            sh.count[e0 + i] = end[i + 1] - end[i];
+        } else if (n) {
+            sh.first[before] = end[i];
+            sh.count[before] = e0 + i;
+        }
+        before += n;
+        if (e0 + i + 1 == a.groups) {
+            sh.tiles[MODE == kOuter ? 0 : a.groups] = before;
+            if (MODE == kOuter) sh.first[before] = end[i + 1];
+        }
     }
-    if (e0 < a.groups && e0 + per >= a.groups) sh.tiles[a.groups] = before;
     __syncthreads();
     const bool bad_pair = sh.bad_pair != 0;  // the same verdict in both CTAs
-    const long long units = (long long)sh.tiles[a.groups] * m_tiles;
+    const int adapters = MODE == kOuter ? sh.tiles[0] : 0;
+    const long long units = (long long)(MODE == kOuter ? (a.P + bt - 1) / bt : sh.tiles[a.groups]) * m_tiles;
+    auto unit = [&](long long u) { return unit_of<MODE == kOuter>(sh, MODE == kOuter ? a.P : a.groups, bt, u, m_tiles); };
+    auto tail = [&](const Unit &t) {
+        return MODE == kOuter ? tail_of(sh, adapters, t, a.R) : Tail{0, 0, 0};
+    };
 
     if (bad_pair) {
         // nothing issued: fall through to the exit barrier
@@ -184,10 +290,11 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         int it = 0;
         bool ok = true;
         for (long long u = cl; ok && u < units; u += ncl) {
-            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const Unit t = unit(u);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
             const int n0 = t.m * kOuts + (int)rank * (kOuts / 2);
-            for (int c = 0; c < C; ++c, ++it) {
+            const Tail f = tail(t);
+            for (int c = 0; c < C + f.stages(); ++c, ++it) {
                 const int s = it % stages;
                 ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -197,6 +304,15 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 }
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
+                if (MODE == kOuter && c >= C) {  // tiles of B
+                    const TailStage g = tail_stage(f, c - C);
+                    const int q = g.q0 + lane;
+                    if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * kSlotBytes));
+                    if (lane < g.n)
+                        tma_load_4d_pair(st + (lane >> 2) * chunk_bytes + kW + (lane & 3) * kSlotBytes, &tm_b, fb,
+                                         g.kb * kChunkK + q % g.per * kRank, n0, 0, sh.count[f.first + q / g.per]);
+                    continue;
+                }
                 if (leader && lane == 0)
                     mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(kChunks * (2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2))));
                 // eight lanes a chunk: the first (with four boxes, the first four) bring W ...
@@ -204,7 +320,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint8_t *ch = st + (lane >> 3) * chunk_bytes;
                 if (lane >> 3 < kChunks) {
                     if (!SWIGLU) {
-                        if (i == 0) tma_load_4d_pair(ch, &tm_w, fb, k0, n0, 0, t.e);
+                        if (i == 0) tma_load_4d_pair(ch + kW, &tm_w, fb, k0, n0, 0, t.e);
                     } else if (w_boxes == 1) {
                         if (i == 0) tma_load_5d_pair(ch, &tm_w, fb, k0, 0, 0, n0 >> 4, t.e);
                     } else if (i < 4) {
@@ -230,14 +346,15 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             int it = 0, tile = 0;
             for (long long u = cl; u < units; u += ncl, ++tile) {
                 sh.consumed = it;
-                const Unit t = unit_of(sh, a.groups, u, m_tiles);
+                const Unit t = unit(u);
                 const uint32_t idesc = idesc_bf16_f32(2 * kHalf, t.cols);
                 const int b = tile & 1;
                 const uint32_t acc = tmem + (uint32_t)(b * bt);
+                const Tail f = tail(t);
                 // Both CTAs' epilogues have read this buffer (used two tiles ago).
                 bool ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
                 tc_fence_after();
-                for (int c = 0; ok && c < C; ++c, ++it) {
+                for (int c = 0; ok && c < C + f.stages(); ++c, ++it) {
                     const int s = it % stages;
                     if (!mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull)) {
                         ok = false;
@@ -245,6 +362,23 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                     tc_fence_after();
                     const uint8_t *ch = ring + s * stage_bytes;
+                    if (MODE == kOuter && c >= C) {
+                        const TailStage g = tail_stage(f, c - C);
+                        const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
+                        int last = -1;
+                        uint32_t off[8];
+                        for (int j = 0; j < g.n; ++j) {
+                            const int q = g.q0 + j, i = f.first + q / g.per, b16 = q % g.per;
+                            if (i != last) lanes_but(sh.first[i] - t.p0, min(sh.first[i + 1] - t.p0, t.rows), off);
+                            last = i;
+                            const uint64_t bdesc =
+                                smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * kSlotBytes));
+                            mma_bf16_pair_lanes(acc, high + 2 * b16, bdesc, idesc, off);
+                            mma_bf16_pair_lanes(acc, low + 2 * b16, bdesc, idesc, off);
+                        }
+                        mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
+                        continue;
+                    }
                     for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
                         const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
                         const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + kWBytes));
@@ -271,12 +405,14 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
             int it = 0;
             bool ok = true;
-            for (long long u = cl; ok && u < units; u += ncl)
-                for (int c = 0; ok && c < C; ++c, ++it) {
+            for (long long u = cl; ok && u < units; u += ncl) {
+                const int n = MODE == kOuter ? C + tail(unit(u)).stages() : C;
+                for (int c = 0; ok && c < n; ++c, ++it) {
                     ok = mbar_wait(&sh.copied[it % stages], (it / stages) & 1, status, kSiteStage);
                     fence_proxy_async_smem();  // the copies, seen here, before the MMAs' reads
                     if (ok) mbar_arrive_remote(full0 + (uint32_t)((it % stages) * sizeof(uint64_t)));
                 }
+            }
             if (!ok) atomicExch(&sh.aborted, 1);
         }
         __syncwarp();
@@ -284,11 +420,11 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         // ---- x by index (both CTAs): eight lanes a row, kGatherRows rows at a time over the warps ----
         const int gt = tid - 32 * (2 + kEpiWarps), r0 = gt >> 3, v = gt & 7;
         const uint16_t *x = static_cast<const uint16_t *>(a.x) + 8 * v;
-        const uint32_t to0 = smem_u32(ring) + kWBytes + (uint32_t)(r0 * 128 + ((v ^ (r0 & 7)) << 4));
+        const uint32_t to0 = smem_u32(ring) + kX + (uint32_t)(r0 * 128 + ((v ^ (r0 & 7)) << 4));
         int it = 0;
         bool ok = true;
         for (long long u = cl; ok && u < units; u += ncl) {
-            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const Unit t = unit(u);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;
             const uint16_t *row[kHalf / kGatherRows];  // rows past the tile's: its last one again
 #pragma unroll
@@ -296,7 +432,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 const int p = min(q0 + r0 + kGatherRows * i, t.p0 + t.rows - 1);
                 row[i] = x + (size_t)min(max(__ldg(a.rows + p), 0), a.x_rows - 1) * a.K;
             }
-            for (int c = 0; c < C; ++c, ++it) {
+            const Tail f = tail(t);
+            for (int c = 0; c < C + f.stages(); ++c, ++it) {
                 const int s = it % stages;
                 ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -305,6 +442,21 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     break;
                 }
                 uint32_t to = to0 + (uint32_t)(s * stage_bytes);
+                if (MODE == kOuter && c >= C) {  // the rows' h: values, then remainders
+                    const int col = tail_stage(f, c - C).kb * kChunkK + 8 * v;
+                    const bool have = col < a.R;  // (R % 8 == 0)
+                    const uint16_t *h = static_cast<const uint16_t *>(a.h) + (have ? col : 0);
+#pragma unroll 4
+                    for (int i = 0; i < kHalf / kGatherRows; ++i) {
+                        const int p = q0 + r0 + kGatherRows * i;
+                        const bool in = have && p < t.p0 + t.rows;
+                        const uint16_t *from = h + (size_t)(in ? p : t.p0) * 2 * a.R;
+                        cp_async_16(to + 128 * kGatherRows * i, from, in ? 16u : 0u);
+                        cp_async_16(to + (uint32_t)chunk_bytes + 128 * kGatherRows * i, from + a.R, in ? 16u : 0u);
+                    }
+                    cp_async_arrive(&sh.copied[s]);
+                    continue;
+                }
                 for (int j = 0; j < kChunks; ++j, to += (uint32_t)chunk_bytes) {
                     const int k0 = (c * kChunks + j) * kChunkK;
                     const uint32_t bytes = k0 + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
@@ -327,19 +479,49 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         const uint16_t *bias = static_cast<const uint16_t *>(a.bias);
         int tile = 0;
         for (long long u = cl; u < units; u += ncl, ++tile) {
-            const Unit t = unit_of(sh, a.groups, u, m_tiles);
+            const Unit t = unit(u);
             const int b = tile & 1;
             // this lane's output, and the W row that it is of
             const int n = t.m * kOuts + (int)rank * (kOuts / 2) +
                           (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
             const int wide = SWIGLU ? 2 * a.N : a.N, wrow = SWIGLU && lane >= 16 ? a.N + n : n;
-            const float lb = bias && n < a.N ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
+            const float f = MODE == kInner && a.scale ? __ldg(a.scale + t.e) : 1.0f;
+            const float lb = MODE != kOuter && bias && n < a.N ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
             const bool ok = mbar_wait(&sh.acc_full[b], (tile >> 1) & 1, status, kSiteAccum);
             tc_fence_after();
             const bool have = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
             const uint32_t acc = lanes + (uint32_t)(b * bt);
             const bool pairs = (a.N & 1) == 0;
-            for (int c0 = 16 * h; have && c0 < t.rows; c0 += 32) {
+            if constexpr (MODE == kOuter) {  // this lane's row of x, 32 outputs at a time
+                const int i = (int)rank * kHalf + quarter * 32 + lane;
+                uint16_t *o = out + (size_t)(i < t.rows ? __ldg(a.rows + t.p0 + i) : 0) * a.N;
+                for (int c0 = 32 * h; have && c0 < kOuts && t.m * kOuts + c0 < a.N; c0 += 64) {
+                    const int n0 = t.m * kOuts + c0;
+                    const float nb = bias_lane(bias, n0, a.N);
+                    uint32_t r0[16], r1[16];
+                    tmem_ld16(acc + (uint32_t)c0, r0);
+                    tmem_ld16(acc + (uint32_t)(c0 + 16), r1);
+                    tmem_ld_wait16(r0);
+                    tmem_ld_wait16(r1);
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = __uint_as_float(r0[j]);
+                        v[16 + j] = __uint_as_float(r1[j]);
+                    }
+                    if (bias) bias_add32(v, nb);
+                    if (i < t.rows && a.N % 8 == 0 && n0 + 32 <= a.N) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) OutStore<uint16_t>::eight(o + n0 + j, v + j);
+                    } else if (i < t.rows) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (n0 + j < a.N) o[n0 + j] = f32_to_bf16(v[j]);
+                    }
+                    __syncwarp();
+                }
+            }
+            for (int c0 = 16 * h; MODE != kOuter && have && c0 < t.rows; c0 += 32) {
                 uint32_t r[16];
                 tmem_ld16(acc + (uint32_t)c0, r);
                 tmem_ld_wait16(r);
@@ -349,7 +531,17 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 // (row of x: c0 + j)
                 uint16_t *o = out + (size_t)(t.p0 + c0) * a.N + n;
                 const int left = t.rows - c0;
-                if constexpr (SWIGLU) {
+                if constexpr (MODE == kInner) {
+                    uint16_t *h = out + (size_t)(t.p0 + c0) * 2 * a.N + n;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n < a.N && j < left) {
+                            const float w = f * v[j];
+                            const uint16_t high = f32_to_bf16(w);
+                            h[(size_t)(2 * j) * a.N] = high;
+                            h[(size_t)(2 * j + 1) * a.N] = isfinite(w) ? f32_to_bf16(w - bf16_to_f32(high)) : 0;
+                        }
+                } else if constexpr (SWIGLU) {
                     float f[8];  // row 2 i (gate lanes) or 2 i + 1 (up lanes) of output n
                     const bool up = lane >= 16;
 #pragma unroll
@@ -428,11 +620,15 @@ int stages_of(int bt) {
 }
 int smem_of(int bt) { return 1024 + stages_of(bt) * kChunks * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
 
-using GroupedFn = void (*)(const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
 
-GroupedFn pick(bool swiglu, bool gather) {
-    if (swiglu) return gather ? grouped_kernel<true, true> : grouped_kernel<true, false>;
-    return gather ? grouped_kernel<false, true> : grouped_kernel<false, false>;
+GroupedFn pick(int mode, bool gather) {
+    switch (mode) {
+        case kInner: return grouped_kernel<kInner, true>;
+        case kOuter: return grouped_kernel<kOuter, true>;
+        case kSwiglu: return gather ? grouped_kernel<kSwiglu, true> : grouped_kernel<kSwiglu, false>;
+        default: return gather ? grouped_kernel<kPlain, true> : grouped_kernel<kPlain, false>;
+    }
 }
 
 cudaLaunchConfig_t config(int clusters, bool gather, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
@@ -452,12 +648,41 @@ cudaLaunchConfig_t config(int clusters, bool gather, int smem, uint32_t flags, v
     return cfg;
 }
 
+// Tiles of up to bt rows; `full`: groups that may have rows.
+int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int full, int num_sms, uint32_t flags, void *stream,
+                int32_t *status) {
+    const bool swiglu = mode == kSwiglu;
+    CUtensorMap tw, tb = {};
+    RowMaps tx = {};
+    // SwiGLU: blocks of 16 gate rows and their 16 up rows, all of a stage's in one box where no block runs past N
+    const int w_boxes = swiglu && a.N % 16 ? 4 : 1;
+    const uint64_t planes = mode == kOuter ? 1 : (uint64_t)a.groups, N = (uint64_t)a.N, K = (uint64_t)a.K;
+    int r = swiglu && w_boxes == 1
+                ? make_tmap_bf16_blocks(&tw, a.w, planes, 2, N, K, 16, 4, kChunkK)
+                : make_tmap_bf16_stack(&tw, a.w, planes, swiglu ? 2 : 1, N, K, swiglu ? 2 : 1, swiglu ? 16 : kHalf, kChunkK);
+    for (int i = 0; i < 4 && !r && !a.rows; ++i)
+        r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, K, 16u << i, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, kHalf, kRank);
+    if (r) return (int)cudaErrorInvalidValue;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
+    // A cluster that cannot be resident with the others would run its tiles after them.
+    const int outs = swiglu ? 128 : 256;
+    const long long units = ((long long)a.P / bt + full) * ((a.N + outs - 1) / outs);  // at most
+    long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
+    if (units < clusters) clusters = units;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr), tw, tb, tx, a, w_boxes, bt, stages_of(bt), status);
+}
+
 }  // namespace
 
 int init_grouped() {
-    for (bool swiglu : {false, true})
+    for (int mode : {kPlain, kSwiglu, kInner, kOuter})
         for (bool gather : {false, true}) {
-            const int e = (int)cudaFuncSetAttribute(pick(swiglu, gather), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            const int e = (int)cudaFuncSetAttribute(pick(mode, gather), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             if (e) return e;
         }
     int dev = 0;
@@ -468,7 +693,7 @@ int init_grouped() {
     cfg.numAttrs = 1;
     int n = 0;
     // A failed query only loses the clamp (launches then use half the SMs' number).
-    if (cudaOccupancyMaxActiveClusters(&n, pick(false, true), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, pick(kPlain, true), &cfg) != cudaSuccess) {
         n = 0;
         (void)cudaGetLastError();
     }
@@ -478,32 +703,27 @@ int init_grouped() {
 
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status) {
     // Rows of a tile: groups of the average size, and of twice that, fit one.
-    const int full = a.P < a.groups ? a.P : a.groups;  // groups that may have rows
+    const int full = a.P < a.groups ? a.P : a.groups;
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
-    CUtensorMap tw;
-    RowMaps tx = {};
-    // SwiGLU: blocks of 16 gate rows and their 16 up rows, all of a stage's in one box where no block runs past N
-    const int w_boxes = a.swiglu && a.N % 16 ? 4 : 1;
-    int r = a.swiglu && w_boxes == 1
-                ? make_tmap_bf16_blocks(&tw, a.w, (uint64_t)a.groups, 2, (uint64_t)a.N, (uint64_t)a.K, 16, 4, kChunkK)
-                : make_tmap_bf16_stack(&tw, a.w, (uint64_t)a.groups, a.swiglu ? 2 : 1, (uint64_t)a.N, (uint64_t)a.K,
-                                       a.swiglu ? 2 : 1, a.swiglu ? 16 : kHalf, kChunkK);
-    for (int i = 0; i < 4 && !r && !a.rows; ++i)
-        r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, (uint64_t)a.K, 16u << i, kChunkK,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (r) return (int)cudaErrorInvalidValue;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
-    // A cluster that cannot be resident with the others would run its tiles after them.
-    const int outs = a.swiglu ? 128 : 256;
-    const long long units = ((long long)a.P / bt + full) * ((a.N + outs - 1) / outs);  // at most
-    long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
-    if (units < clusters) clusters = units;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(a.swiglu != 0, a.rows != nullptr), tw, tx, a, w_boxes, bt, stages_of(bt),
-                                   status);
+    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, nullptr, bt, full, num_sms, flags, stream, status);
+}
+
+int launch_lora_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
+                        void *h, int num_sms, uint32_t flags, void *stream, int32_t *status) {
+    GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, l.R};
+    // The inner product has one W tile: rows of a tile so that there is one for each pair of SMs.
+    const int clusters = num_sms / 2;
+    const int bt = l.M <= 32 * clusters ? 32 : l.M <= 64 * clusters ? 64 : l.M <= 128 * clusters ? 128 : 256;
+    const int r = launch_mode(kInner, a, nullptr, bt, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
+    if (r) return r;
+    a.w = w;
+    a.bias = bias;
+    a.out = l.out;
+    a.N = l.N;
+    a.scale = nullptr;
+    a.h = h;
+    return launch_mode(kOuter, a, l.b, 2 * kHalf, 1, num_sms, flags, stream, status);
 }
 
 }  // namespace bf16l

@@ -38,8 +38,28 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Shared-memory matrix descriptor of a K-major bf16 tile of 16 columns (rows of 32 bytes, groups of eight of 256) in
+// TMA's 32-byte swizzle; fields as smem_desc_sw128, swizzle mode 6.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)6 << 61;
+}
+
+// As mma_bf16_pair, adding to D in the lanes (rows) alone whose bit of `off` is clear: words 0-3 the even CTA's, 4-7 the odd's.
+__device__ __forceinline__ void mma_bf16_pair_lanes(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                    const uint32_t (&off)[8]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+        "r"(off[5]), "r"(off[6]), "r"(off[7])
+        : "memory");
+}
+
 // Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
-// box_halves x 1 elements and 128-byte swizzle.  Defined in api.cu.  Returns a CUresult value (0 on success).
+// box_halves x 1 elements, in the swizzle of box_cols' bytes (128 or 32).  Defined in api.cu.  Returns a CUresult value
+// (0 on success).
 int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
                          uint32_t box_halves, uint32_t box_rows, uint32_t box_cols);
 // The same with the rows in blocks of block_rows (a divisor of rows): a box is box_blocks blocks of every half, in shared

@@ -1,7 +1,10 @@
-// lora.cu — the low-rank adapters' share of a linear: h = scale_a * (x @ A_a^T) for each row's adapter a, then
-// out = y + h @ B_a^T, with y the shared projection in fp32.
+// lora.cu — the low-rank adapters' share of a linear for few rows: h = scale_a * (x @ A_a^T) for each row's adapter a, then
+// out = y + h @ B_a^T, with y the shared projection in fp32, by the dense linear's own kernels between the two.
 //
-// The simple form: a warp for each inner value, a thread for each output.
+// Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
+// spreads over as many SMs as it can: the inner one a row's K over up to kLoraSplits blocks, whose sums the outer one
+// adds, in order, when it reads them.  The inner one also asks L2 for B_a, which the outer one reads when the projection
+// is done.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -11,66 +14,120 @@ namespace bf16l {
 
 namespace {
 
-// h[t][r], 0 for a row without an adapter.
-__global__ void __launch_bounds__(256) lora_inner_kernel(const LoraArgs a) {
+constexpr int kInnerWarps = 4, kRanks = 4;  // ranks that a warp sums at a time
+constexpr int kOuterThreads = 128;
+
+// Parts of K, and the elements of one: as many as bring about two blocks for each SM, none below 512 elements.
+__host__ __device__ inline int lora_splits(int M, int K) {
+    const int want = M >= 304 ? 1 : 304 / M, most = K / 512 > 1 ? K / 512 : 1;
+    const int s = want < most ? want : most;
+    return s < kLoraSplits ? s : kLoraSplits;
+}
+
+__global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a, int splits) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= (long long)a.M * a.R) return;
-    const int t = (int)(i / a.R), r = (int)(i - (long long)t * a.R), id = a.ids[t];
-    float sum = 0.0f;
-    if ((unsigned)id < (unsigned)a.L) {
-        const uint16_t *x = static_cast<const uint16_t *>(a.x) + (size_t)t * a.K;
-        const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r) * a.K;
-        for (int k = 2 * lane; k < a.K; k += 64)
-            sum = fma2_bf16(*reinterpret_cast<const uint32_t *>(x + k), *reinterpret_cast<const uint32_t *>(w + k), sum);
+    const int t = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int id = __ldg(a.ids + t);
+    if ((unsigned)id >= (unsigned)a.L) return;  // (its inner values are not read)
+    if (threadIdx.x == 0) {  // this block's part of B's rows
+        const int n0 = (int)((long long)a.N * s / splits), n1 = (int)((long long)a.N * (s + 1) / splits);
+        const uint16_t *b = static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n0) * a.R;
+        const long long bytes = (long long)(n1 - n0) * a.R * 2;
+        prefetch_l2(b, (uint32_t)(bytes < (1 << 20) ? bytes : 1 << 20));
+    }
+    const int each = ((a.K + splits - 1) / splits + 255) / 256 * 256, k0 = s * each, k1 = min(k0 + each, a.K);
+    const uint16_t *x = static_cast<const uint16_t *>(a.x) + (size_t)t * a.K;
+    const float f = a.scale ? __ldg(a.scale + id) : 1.0f;
+    for (int r0 = kRanks * warp; r0 < a.R; r0 += kRanks * kInnerWarps) {  // (R % 8 == 0)
+        const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r0) * a.K;
+        float sum[kRanks] = {};
+#pragma unroll 2
+        for (int k = k0 + 8 * lane; k < k1; k += 256) {  // (K % 8 == 0)
+            const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
+            uint4 wv[kRanks];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (a.scale) sum *= a.scale[id];
+            for (int r = 0; r < kRanks; ++r) wv[r] = __ldg(reinterpret_cast<const uint4 *>(w + (size_t)r * a.K + k));
+#pragma unroll
+            for (int r = 0; r < kRanks; ++r) {
+                sum[r] = fma2_bf16(xv.x, wv[r].x, sum[r]);
+                sum[r] = fma2_bf16(xv.y, wv[r].y, sum[r]);
+                sum[r] = fma2_bf16(xv.z, wv[r].z, sum[r]);
+                sum[r] = fma2_bf16(xv.w, wv[r].w, sum[r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], d);
+        }
+        if (lane < kRanks) {
+            float v = sum[0];
+#pragma unroll
+            for (int r = 1; r < kRanks; ++r) v = lane == r ? sum[r] : v;
+            a.h[((size_t)s * a.M + t) * a.R + r0 + lane] = f * v;
+        }
     }
-    if (lane == 0) a.h[i] = sum;
 }
 
-__global__ void __launch_bounds__(256) lora_outer_kernel(const LoraArgs a) {
+// One output a thread: its B row is R consecutive values.
+__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArgs a, int splits) {
+    __shared__ float h[kLoraMaxRank];
     pdl_launch_dependents();
     pdl_wait();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (long long)a.M * a.N) return;
-    const int t = (int)(i / a.N), n = (int)(i - (long long)t * a.N), id = a.ids[t];
-    float sum = a.y[i];
-    if ((unsigned)id < (unsigned)a.L) {
-        const uint16_t *b = static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n) * a.R;
-        const float *h = a.h + (size_t)t * a.R;
-        float d = 0.0f;
-        for (int r = 0; r < a.R; ++r) d = fmaf(h[r], bf16_to_f32(b[r]), d);
-        sum += d;
+    const int t = blockIdx.y, n = (int)blockIdx.x * kOuterThreads + (int)threadIdx.x;
+    const int id = __ldg(a.ids + t);
+    const bool has = (unsigned)id < (unsigned)a.L, in = n < a.N;
+    const size_t at = (size_t)t * a.N + n;
+    float sum = in ? a.y[at] : 0.0f;
+    if (has) {
+        if ((int)threadIdx.x < a.R) {
+            float v = 0.0f;
+            for (int s = 0; s < splits; ++s) v += a.h[((size_t)s * a.M + t) * a.R + threadIdx.x];
+            h[threadIdx.x] = v;
+        }
+        __syncthreads();
+        if (in) {
+            const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n) * a.R);
+            float d = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < a.R / 8; ++i) {
+                const uint4 v = __ldg(b + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d = fmaf(h[8 * i + 2 * j], bf16_lo(w[j]), d);
+                    d = fmaf(h[8 * i + 2 * j + 1], bf16_hi(w[j]), d);
+                }
+            }
+            sum += d;
+        }
     }
-    static_cast<uint16_t *>(a.out)[i] = f32_to_bf16(sum);
+    if (in) static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(sum);
 }
 
-int launch(void (*f)(const LoraArgs), long long blocks, const LoraArgs &a, uint32_t flags, void *stream) {
-    if (blocks > 0x7FFFFFFFll) return (int)cudaErrorInvalidValue;
+int launch(void (*f)(const LoraArgs, int), dim3 grid, int threads, const LoraArgs &a, uint32_t flags, void *stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, f, a);
+    return (int)cudaLaunchKernelEx(&cfg, f, a, lora_splits(a.M, a.K));
 }
 
 }  // namespace
 
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream) {
-    return launch(lora_inner_kernel, ((long long)a.M * a.R + 7) / 8, a, flags, stream);
+    return launch(lora_inner_kernel, dim3((unsigned)a.M, (unsigned)lora_splits(a.M, a.K)), 32 * kInnerWarps, a, flags, stream);
 }
 
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {
-    return launch(lora_outer_kernel, ((long long)a.M * a.N + 255) / 256, a, flags, stream);
+    const dim3 grid((unsigned)((a.N + kOuterThreads - 1) / kOuterThreads), (unsigned)a.M);
+    return launch(lora_outer_kernel, grid, kOuterThreads, a, flags, stream);
 }
 
 }  // namespace bf16l

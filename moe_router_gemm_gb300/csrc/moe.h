@@ -42,11 +42,12 @@ int launch_route(const void *logits, int64_t ld, const float *bias, float *weigh
                  int experts, int k, int softmax, int groups, int top_groups, int group_best, int renorm, float scale,
                  int logits_bf16, int num_sms, uint32_t flags, void *stream);
 
-// Rows by group (group.cu): n keys, n + 1024 <= 2^31; and a token's rows summed.
+// Rows by group (group.cu): n keys, n + 65536 < 2^31; rest: rows holds the tokens of no group behind the others', where it
+// has -1 otherwise.  And a token's rows summed.
 constexpr int kMaxGroups = 1024;
 int init_group();
-int launch_group_rows(const int32_t *ids, int n, int k, int groups, int32_t *offsets, int32_t *rows, int32_t *place,
-                      uint32_t flags, void *stream);
+int launch_group_rows(const int32_t *ids, int n, int k, int groups, bool rest, int32_t *offsets, int32_t *rows,
+                      int32_t *place, uint32_t flags, void *stream);
 int launch_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
                         void *out, int64_t tokens, int k, int H, int num_sms, uint32_t flags, void *stream);
 
@@ -56,12 +57,18 @@ struct GroupedArgs {
     const int32_t *offsets, *rows;  // rows null: row p of x is row p of out
     void *out;
     int x_rows, P, groups, N, K, swiglu;
+    // the adapters' products (launch_lora_*)
+    const float *scale;
+    void *h;
+    int R;
 };
 int init_grouped();
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
-// The adapters of a linear (lora.cu): the inner values h[M][R] in fp32, and out from them and the shared product y[M][N].
-constexpr int kLoraMaxRank = 128;
+// The adapters of a linear: the inner values in fp32, as S sums over parts of K that are still to be added up, h[S][M][R], and
+// out from them and the shared product y[M][N] (lora.cu), for few rows; or, rows in the order of their adapters, both
+// products on tensor cores (grouped.cu), the inner values as h[M][2][R] of bf16, value and remainder.
+constexpr int kLoraMaxRank = 128, kLoraSplits = 8;
 struct LoraArgs {
     const void *x, *a, *b;
     const float *scale;
@@ -73,5 +80,7 @@ struct LoraArgs {
 };
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
+int launch_lora_grouped(const LoraArgs &a, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
+                        void *h, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
 }  // namespace bf16l
