@@ -269,7 +269,7 @@ extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *p
     bf16l_device dev;
     const int st = current_device_checked(&dev);
     if (st != BF16L_OK) return st;
-    return result(launch_combine_rows(y, y_rows, place, weights, addend, out, tokens, k, H, dev.num_sms, flags, stream));
+    return result(launch_combine_rows(y, y_rows, place, weights, addend, out, tokens, k, H, flags, stream));
 }
 
 namespace {

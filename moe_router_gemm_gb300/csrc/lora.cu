@@ -3,7 +3,7 @@
 //
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
 // spreads over as many SMs as it can: the inner one a row's K over up to kLoraSplits blocks, whose sums the outer one
-// adds, in order, when it reads them.  The inner one also asks L2 for B_a, which the outer one reads when the projection
+// adds, in order, when it reads them, and four ranks a warp.  The inner one also asks L2 for B_a, which the outer one reads when the projection
 // is done.
 #include <cuda_runtime.h>
 
@@ -17,56 +17,55 @@ namespace {
 constexpr int kInnerWarps = 4, kRanks = 4;  // ranks that a warp sums at a time
 constexpr int kOuterThreads = 128;
 
-// Parts of K, and the elements of one: as many as bring about two blocks for each SM, none below 512 elements.
-__host__ __device__ inline int lora_splits(int M, int K) {
-    const int want = M >= 304 ? 1 : 304 / M, most = K / 512 > 1 ? K / 512 : 1;
-    const int s = want < most ? want : most;
+// Parts of K: none below 512 elements.
+__host__ __device__ inline int lora_splits(int K) {
+    const int s = K / 512 > 1 ? K / 512 : 1;
     return s < kLoraSplits ? s : kLoraSplits;
 }
 
+// A warp sums kRanks ranks of a row over a part of K.
 __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a, int splits) {
     pdl_launch_dependents();
     pdl_wait();
     const int t = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = __ldg(a.ids + t);
     if ((unsigned)id >= (unsigned)a.L) return;  // (its inner values are not read)
-    if (threadIdx.x == 0) {  // this block's part of B's rows
+    if (threadIdx.x == 0 && blockIdx.z == 0) {  // this block's part of B's rows
         const int n0 = (int)((long long)a.N * s / splits), n1 = (int)((long long)a.N * (s + 1) / splits);
         const uint16_t *b = static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n0) * a.R;
         const long long bytes = (long long)(n1 - n0) * a.R * 2;
         prefetch_l2(b, (uint32_t)(bytes < (1 << 20) ? bytes : 1 << 20));
     }
+    const int r0 = kRanks * (kInnerWarps * (int)blockIdx.z + warp);
+    if (r0 >= a.R) return;  // (R % 8 == 0)
     const int each = ((a.K + splits - 1) / splits + 255) / 256 * 256, k0 = s * each, k1 = min(k0 + each, a.K);
     const uint16_t *x = static_cast<const uint16_t *>(a.x) + (size_t)t * a.K;
-    const float f = a.scale ? __ldg(a.scale + id) : 1.0f;
-    for (int r0 = kRanks * warp; r0 < a.R; r0 += kRanks * kInnerWarps) {  // (R % 8 == 0)
-        const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r0) * a.K;
-        float sum[kRanks] = {};
+    const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r0) * a.K;
+    float sum[kRanks] = {};
 #pragma unroll 2
-        for (int k = k0 + 8 * lane; k < k1; k += 256) {  // (K % 8 == 0)
-            const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
-            uint4 wv[kRanks];
+    for (int k = k0 + 8 * lane; k < k1; k += 256) {  // (K % 8 == 0)
+        const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
+        uint4 wv[kRanks];
 #pragma unroll
-            for (int r = 0; r < kRanks; ++r) wv[r] = __ldg(reinterpret_cast<const uint4 *>(w + (size_t)r * a.K + k));
-#pragma unroll
-            for (int r = 0; r < kRanks; ++r) {
-                sum[r] = fma2_bf16(xv.x, wv[r].x, sum[r]);
-                sum[r] = fma2_bf16(xv.y, wv[r].y, sum[r]);
-                sum[r] = fma2_bf16(xv.z, wv[r].z, sum[r]);
-                sum[r] = fma2_bf16(xv.w, wv[r].w, sum[r]);
-            }
-        }
+        for (int r = 0; r < kRanks; ++r) wv[r] = __ldg(reinterpret_cast<const uint4 *>(w + (size_t)r * a.K + k));
 #pragma unroll
         for (int r = 0; r < kRanks; ++r) {
-#pragma unroll
-            for (int d = 16; d; d >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], d);
+            sum[r] = fma2_bf16(xv.x, wv[r].x, sum[r]);
+            sum[r] = fma2_bf16(xv.y, wv[r].y, sum[r]);
+            sum[r] = fma2_bf16(xv.z, wv[r].z, sum[r]);
+            sum[r] = fma2_bf16(xv.w, wv[r].w, sum[r]);
         }
-        if (lane < kRanks) {
-            float v = sum[0];
+    }
 #pragma unroll
-            for (int r = 1; r < kRanks; ++r) v = lane == r ? sum[r] : v;
-            a.h[((size_t)s * a.M + t) * a.R + r0 + lane] = f * v;
-        }
+    for (int r = 0; r < kRanks; ++r) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], d);
+    }
+    if (lane < kRanks) {
+        float v = sum[0];
+#pragma unroll
+        for (int r = 1; r < kRanks; ++r) v = lane == r ? sum[r] : v;
+        a.h[((size_t)s * a.M + t) * a.R + r0 + lane] = a.scale ? __ldg(a.scale + id) * v : v;
     }
 }
 
@@ -116,13 +115,14 @@ int launch(void (*f)(const LoraArgs, int), dim3 grid, int threads, const LoraArg
     attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, f, a, lora_splits(a.M, a.K));
+    return (int)cudaLaunchKernelEx(&cfg, f, a, lora_splits(a.K));
 }
 
 }  // namespace
 
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream) {
-    return launch(lora_inner_kernel, dim3((unsigned)a.M, (unsigned)lora_splits(a.M, a.K)), 32 * kInnerWarps, a, flags, stream);
+    const dim3 grid((unsigned)a.M, (unsigned)lora_splits(a.K), (unsigned)((a.R + kRanks * kInnerWarps - 1) / (kRanks * kInnerWarps)));
+    return launch(lora_inner_kernel, grid, 32 * kInnerWarps, a, flags, stream);
 }
 
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {

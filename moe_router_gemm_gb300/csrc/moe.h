@@ -49,7 +49,7 @@ int init_group();
 int launch_group_rows(const int32_t *ids, int n, int k, int groups, bool rest, int32_t *offsets, int32_t *rows,
                       int32_t *place, uint32_t flags, void *stream);
 int launch_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
-                        void *out, int64_t tokens, int k, int H, int num_sms, uint32_t flags, void *stream);
+                        void *out, int64_t tokens, int k, int H, uint32_t flags, void *stream);
 
 // The linear of grouped rows (grouped.cu); N: columns of out, W has 2 N rows a group with swiglu.
 struct GroupedArgs {
