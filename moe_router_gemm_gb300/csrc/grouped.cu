@@ -40,18 +40,22 @@ namespace {
 constexpr int kHalf = 128;                        // W rows per CTA
 constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
 constexpr int kChunks = 2;  // 64-wide chunks of K in a stage
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
 __host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps + 1 : 0)); }
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kPer = (kMaxGroups + 32 * (2 + kEpiWarps) - 1) / (32 * (2 + kEpiWarps));  // groups of a thread, at most
 constexpr int kRank = 16, kSlots = 2 * kChunkK / kRank;  // ranks of a slot, slots of a stage
-constexpr int kSlotBytes = kHalf * kRank * 2;
+constexpr int kPiece = 32, kPieceBytes = 32 * kPiece * 2;  // kOuter: columns of out that a warp gathers before it stores them
 
 enum Mode { kPlain, kSwiglu, kInner, kOuter };
+// W rows of a CTA and chunk have this much of a stage: kInner's are at most 64 (the MMA's other rows are whatever follows,
+// and so are their lanes of the accumulator, which nobody reads).
+__host__ __device__ constexpr int w_bytes(int mode) { return mode == kInner ? kWBytes / 2 : kWBytes; }
 
 struct GroupedShared {
+    uint8_t piece[kEpiWarps][kPieceBytes];  // kOuter
     uint64_t full[kMaxStages];   // leader only: both CTAs' copies of the stage have landed
     uint64_t empty[kMaxStages];  // both: the MMAs reading the stage are done
     uint64_t copied[kMaxStages]; // this CTA's rows of x by index are in shared memory
@@ -151,26 +155,29 @@ struct RowMaps {
 template <int MODE, bool GATHER>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ RowMaps tm_x, const GroupedArgs a, int w_boxes, int bt, int stages, int32_t *status) {
+                   const __grid_constant__ RowMaps tm_x, const GroupedArgs a, int w_boxes, int bt, int wt, int stages, int32_t *status) {
     constexpr bool SWIGLU = MODE == kSwiglu;
     static_assert(GATHER || MODE == kPlain || MODE == kSwiglu, "the adapters' rows go by index");
     constexpr int kThreads = threads_of(GATHER);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    const int chunk_bytes = kWBytes + bt * kChunkK;  // W rows, and bt / 2 rows of x, of 128 bytes
+    constexpr int kWSpace = w_bytes(MODE);
+    const int chunk_bytes = kWSpace + bt * kChunkK;  // W rows, and bt / 2 rows of x, of 128 bytes
     const int stage_bytes = kChunks * chunk_bytes;
-    constexpr int kW = MODE == kOuter ? kWBytes : 0, kX = MODE == kOuter ? 0 : kWBytes;  // (the M side's rows first)
+    constexpr int kW = MODE == kOuter ? kWBytes : 0, kX = MODE == kOuter ? 0 : kWSpace;  // (the M side's rows first)
     GroupedShared &sh = *reinterpret_cast<GroupedShared *>(ring + stages * stage_bytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    constexpr int kOuts = SWIGLU ? 128 : 256;  // outputs of a W tile
-    const int m_tiles = (a.N + kOuts - 1) / kOuts;
+    // wt: outputs of a W tile, half of them a CTA's (kInner: of its W rows, so that both CTAs have some)
+    const int m_tiles = (a.N + wt - 1) / wt;
+    const uint32_t w_chunk = MODE == kInner || MODE == kOuter ? (uint32_t)wt * kChunkK : (uint32_t)kWBytes;  // bytes of a box
     const int cl = (int)blockIdx.x >> 1, ncl = (int)gridDim.x >> 1;
     const int C = (a.K + kChunkK * kChunks - 1) / (kChunkK * kChunks);  // stages of a tile (zeros past K)
     const uint32_t tmem_cols = 2u * (uint32_t)bt;
+    const int slot_bytes = wt * kRank;  // kOuter: 16 ranks of this CTA's wt / 2 rows of B
 
     if (tid == 0) {
         tma_prefetch_desc(&tm_w);
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         for (long long u = cl; ok && u < units; u += ncl) {
             const Unit t = unit(u);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
-            const int n0 = t.m * kOuts + (int)rank * (kOuts / 2);
+            const int n0 = t.m * wt + (int)rank * (wt / 2);
             const Tail f = tail(t);
             for (int c = 0; c < C + f.stages(); ++c, ++it) {
                 const int s = it % stages;
@@ -307,14 +314,14 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 if (MODE == kOuter && c >= C) {  // tiles of B
                     const TailStage g = tail_stage(f, c - C);
                     const int q = g.q0 + lane;
-                    if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * kSlotBytes));
+                    if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * slot_bytes));
                     if (lane < g.n)
-                        tma_load_4d_pair(st + (lane >> 2) * chunk_bytes + kW + (lane & 3) * kSlotBytes, &tm_b, fb,
+                        tma_load_4d_pair(st + (lane >> 2) * chunk_bytes + kW + (lane & 3) * slot_bytes, &tm_b, fb,
                                          g.kb * kChunkK + q % g.per * kRank, n0, 0, sh.count[f.first + q / g.per]);
                     continue;
                 }
                 if (leader && lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(kChunks * (2 * kWBytes + (GATHER ? 0 : t.cols * kChunkK * 2))));
+                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)kChunks * (2u * w_chunk + (GATHER ? 0u : (uint32_t)(t.cols * kChunkK * 2))));
                 // eight lanes a chunk: the first (with four boxes, the first four) bring W ...
                 const int i = lane & 7, k0 = (c * kChunks + (lane >> 3)) * kChunkK;
                 uint8_t *ch = st + (lane >> 3) * chunk_bytes;
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     // ... and 4 to 7 this CTA's rows, a multiple of 16, by boxes of falling sizes: lane i takes 1 << i
                     if (!GATHER && i >= 4 && (half & (1 << i))) {
                         const int r = half & ~((2 << i) - 1);
-                        tma_load_2d_pair(ch + kWBytes + r * 128, &tm_x.of[i - 4], fb, k0, q0 + r);
+                        tma_load_2d_pair(ch + kX + r * 128, &tm_x.of[i - 4], fb, k0, q0 + r);
                     }
                 }
             }
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             for (long long u = cl; u < units; u += ncl, ++tile) {
                 sh.consumed = it;
                 const Unit t = unit(u);
-                const uint32_t idesc = idesc_bf16_f32(2 * kHalf, t.cols);
+                const uint32_t idesc = idesc_bf16_f32(2 * kHalf, MODE == kOuter ? wt : t.cols);
                 const int b = tile & 1;
                 const uint32_t acc = tmem + (uint32_t)(b * bt);
                 const Tail f = tail(t);
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             if (i != last) lanes_but(sh.first[i] - t.p0, min(sh.first[i + 1] - t.p0, t.rows), off);
                             last = i;
                             const uint64_t bdesc =
-                                smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * kSlotBytes));
+                                smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * slot_bytes));
                             mma_bf16_pair_lanes(acc, high + 2 * b16, bdesc, idesc, off);
                             mma_bf16_pair_lanes(acc, low + 2 * b16, bdesc, idesc, off);
                         }
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                     for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
                         const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
-                        const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + kWBytes));
+                        const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + (MODE == kOuter ? kW : kX)));
 #pragma unroll
                         for (int kk = 0; kk < kChunkK / 16; ++kk)
                             mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || j > 0 || kk > 0) ? 1u : 0u);
@@ -426,7 +433,10 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         for (long long u = cl; ok && u < units; u += ncl) {
             const Unit t = unit(u);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;
-            const uint16_t *row[kHalf / kGatherRows];  // rows past the tile's: its last one again
+            // Rows past the tile's are zero: one row read again by every CTA in their place is a hot spot (128 rows of
+            // 14336 x 4096 with adapters: 74 us for the shared product alone, 44 so).
+            const int have = min(max(t.p0 + t.rows - q0, 0), half);
+            const uint16_t *row[kHalf / kGatherRows];
 #pragma unroll
             for (int i = 0; i < kHalf / kGatherRows; ++i) {
                 const int p = min(q0 + r0 + kGatherRows * i, t.p0 + t.rows - 1);
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     if (lane == 0) atomicExch(&sh.aborted, 1);
                     break;
                 }
-                uint32_t to = to0 + (uint32_t)(s * stage_bytes);
+                const uint32_t to = to0 + (uint32_t)(s * stage_bytes);
                 if (MODE == kOuter && c >= C) {  // the rows' h: values, then remainders
                     const int col = tail_stage(f, c - C).kb * kChunkK + 8 * v;
                     const bool have = col < a.R;  // (R % 8 == 0)
@@ -457,13 +467,26 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     cp_async_arrive(&sh.copied[s]);
                     continue;
                 }
-                for (int j = 0; j < kChunks; ++j, to += (uint32_t)chunk_bytes) {
-                    const int k0 = (c * kChunks + j) * kChunkK;
-                    const uint32_t bytes = k0 + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0; zeros past K)
+                // The copies' own instructions count: two warps issue 32 a stage, and one address serves both chunks.
+                const int k0 = c * kChunks * kChunkK;
+                const uint32_t to2 = to + (uint32_t)chunk_bytes;
+                static_assert(kChunks == 2, "two chunks a stage");
+                if (have == half && k0 + 2 * kChunkK <= a.K) {
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
-                        if (r0 + kGatherRows * i < half)
-                            cp_async_16(to + 128 * kGatherRows * i, row[i] + (bytes ? k0 : 0), bytes);
+                        if (kGatherRows * i < half) {
+                            cp_async_16(to + 128 * kGatherRows * i, row[i] + k0);
+                            cp_async_16(to2 + 128 * kGatherRows * i, row[i] + k0 + kChunkK);
+                        }
+                } else {
+                    const uint32_t in = k0 + 8 * v < a.K ? 16u : 0u, in2 = k0 + kChunkK + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0)
+#pragma unroll
+                    for (int i = 0; i < kHalf / kGatherRows; ++i)
+                        if (kGatherRows * i < half) {
+                            const bool mine = r0 + kGatherRows * i < have;
+                            cp_async_16(to + 128 * kGatherRows * i, row[i] + (in ? k0 : 0), mine ? in : 0u);
+                            cp_async_16(to2 + 128 * kGatherRows * i, row[i] + (in2 ? k0 + kChunkK : 0), mine ? in2 : 0u);
+                        }
                 }
                 cp_async_arrive(&sh.copied[s]);
             }
@@ -482,8 +505,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const Unit t = unit(u);
             const int b = tile & 1;
             // this lane's output, and the W row that it is of
-            const int n = t.m * kOuts + (int)rank * (kOuts / 2) +
-                          (SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
+            const int in_tile = SWIGLU ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
+            const int n = MODE == kInner && in_tile >= wt / 2 ? a.N : t.m * wt + (int)rank * (wt / 2) + in_tile;
             const int wide = SWIGLU ? 2 * a.N : a.N, wrow = SWIGLU && lane >= 16 ? a.N + n : n;
             const float f = MODE == kInner && a.scale ? __ldg(a.scale + t.e) : 1.0f;
             const float lb = MODE != kOuter && bias && n < a.N ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
@@ -492,11 +515,13 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const bool have = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
             const uint32_t acc = lanes + (uint32_t)(b * bt);
             const bool pairs = (a.N & 1) == 0;
-            if constexpr (MODE == kOuter) {  // this lane's row of x, 32 outputs at a time
-                const int i = (int)rank * kHalf + quarter * 32 + lane;
-                uint16_t *o = out + (size_t)(i < t.rows ? __ldg(a.rows + t.p0 + i) : 0) * a.N;
-                for (int c0 = 32 * h; have && c0 < kOuts && t.m * kOuts + c0 < a.N; c0 += 64) {
-                    const int n0 = t.m * kOuts + c0;
+            if constexpr (MODE == kOuter) {  // this lane's row of x, kPiece outputs at a time
+                const int i0 = (int)rank * kHalf + quarter * 32, left = t.rows - i0;  // the warp's first row, its rows
+                uint8_t *piece = sh.piece[warp - 2];
+                const int to = lane < left ? __ldg(a.rows + t.p0 + i0 + lane) : 0;
+                const bool whole = a.N % 8 == 0;
+                for (int c0 = kPiece * h; have && c0 < wt && t.m * wt + c0 < a.N; c0 += 2 * kPiece) {
+                    const int n0 = t.m * wt + c0;
                     const float nb = bias_lane(bias, n0, a.N);
                     uint32_t r0[16], r1[16];
                     tmem_ld16(acc + (uint32_t)c0, r0);
@@ -510,15 +535,30 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                         v[16 + j] = __uint_as_float(r1[j]);
                     }
                     if (bias) bias_add32(v, nb);
-                    if (i < t.rows && a.N % 8 == 0 && n0 + 32 <= a.N) {
+                    __syncwarp();  // the piece before has been read
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) OutStore<uint16_t>::eight(o + n0 + j, v + j);
-                    } else if (i < t.rows) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (n0 + j < a.N) o[n0 + j] = f32_to_bf16(v[j]);
-                    }
+                    for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
+                        *reinterpret_cast<uint4 *>(piece + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
+                            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
                     __syncwarp();
+                    // Four lanes a row, eight rows a store: whole sectors (a row a lane: 8192 x 7168 x 7168 35 us more).
+                    const int u = lane & 3, n = n0 + 8 * u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * k + (lane >> 2), row = __shfl_sync(kAll, to, r);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(piece + 64 * r + 16 * (u ^ ((r >> 1) & 3)));
+                        uint16_t *o = out + (size_t)row * a.N + n;
+                        const bool in = r < left && n < a.N;
+                        if (in && whole) {
+                            *reinterpret_cast<uint4 *>(o) = w;
+                        } else if (in) {
+                            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (n + j < a.N) o[j] = (uint16_t)(j & 1 ? q[j / 2] >> 16 : q[j / 2]);
+                        }
+                    }
                 }
             }
             for (int c0 = 16 * h; MODE != kOuter && have && c0 < t.rows; c0 += 32) {
@@ -612,15 +652,19 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
 constexpr int kMaxDevices = 64;
 int g_clusters[kMaxDevices];  // co-resident clusters of 2, per device
 
-// One CTA per SM (the accumulators may be all of TMEM): the ring takes what memory there is.
+// The ring takes what shared memory there is, up to kMaxStages.
 constexpr int kSmem = 232448;
-int stages_of(int bt) {
-    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kChunks * (kWBytes + bt * kChunkK));
+int stages_of(int mode, int bt) {
+    const int n = (kSmem - 1024 - (int)sizeof(GroupedShared)) / (kChunks * (w_bytes(mode) + bt * kChunkK));
     return n < kMaxStages ? n : kMaxStages;
 }
-int smem_of(int bt) { return 1024 + stages_of(bt) * kChunks * (kWBytes + bt * kChunkK) + (int)sizeof(GroupedShared); }
+int smem_of(int mode, int bt) {
+    const int need = 1024 + stages_of(mode, bt) * kChunks * (w_bytes(mode) + bt * kChunkK) + (int)sizeof(GroupedShared);
+    return need > 116 * 1024 ? need : 116 * 1024;  // one CTA per SM: the accumulators may be all of TMEM
+}
+static_assert(sizeof(GroupedShared) >= kWBytes / 2, "kInner's MMAs read past their rows, within shared memory");
 
-using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int, int32_t *);
 
 GroupedFn pick(int mode, bool gather) {
     switch (mode) {
@@ -648,8 +692,15 @@ cudaLaunchConfig_t config(int clusters, bool gather, int smem, uint32_t flags, v
     return cfg;
 }
 
-// Tiles of up to bt rows; `full`: groups that may have rows.
-int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int full, int num_sms, uint32_t flags, void *stream,
+// Co-resident clusters of 2 of the current device.
+int clusters_of(int num_sms) {
+    int dev = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_clusters[dev] > 0;
+    return known ? g_clusters[dev] : num_sms / 2;
+}
+
+// Tiles of up to bt rows and wt outputs; `full`: groups that may have rows.
+int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int wt, int full, int num_sms, uint32_t flags, void *stream,
                 int32_t *status) {
     const bool swiglu = mode == kSwiglu;
     CUtensorMap tw, tb = {};
@@ -659,22 +710,21 @@ int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int full,
     const uint64_t planes = mode == kOuter ? 1 : (uint64_t)a.groups, N = (uint64_t)a.N, K = (uint64_t)a.K;
     int r = swiglu && w_boxes == 1
                 ? make_tmap_bf16_blocks(&tw, a.w, planes, 2, N, K, 16, 4, kChunkK)
-                : make_tmap_bf16_stack(&tw, a.w, planes, swiglu ? 2 : 1, N, K, swiglu ? 2 : 1, swiglu ? 16 : kHalf, kChunkK);
+                : make_tmap_bf16_stack(&tw, a.w, planes, swiglu ? 2 : 1, N, K, swiglu ? 2 : 1, swiglu ? 16 : (uint32_t)wt / 2,
+                                       kChunkK);
     for (int i = 0; i < 4 && !r && !a.rows; ++i)
         r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, K, 16u << i, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, kHalf, kRank);
+    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
     if (r) return (int)cudaErrorInvalidValue;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
     // A cluster that cannot be resident with the others would run its tiles after them.
-    const int outs = swiglu ? 128 : 256;
-    const long long units = ((long long)a.P / bt + full) * ((a.N + outs - 1) / outs);  // at most
-    long long clusters = g_clusters[dev] > 0 ? g_clusters[dev] : num_sms / 2;
+    const long long units = ((long long)a.P / bt + full) * ((a.N + wt - 1) / wt);  // at most
+    long long clusters = clusters_of(num_sms);
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr), tw, tb, tx, a, w_boxes, bt, stages_of(bt), status);
+    const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(mode, bt), flags, stream, attr);
+    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr), tw, tb, tx, a, w_boxes, bt, wt,
+                                   stages_of(mode, bt), status);
 }
 
 }  // namespace
@@ -706,16 +756,16 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     const int full = a.P < a.groups ? a.P : a.groups;
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
-    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, nullptr, bt, full, num_sms, flags, stream, status);
+    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, nullptr, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status);
 }
 
 int launch_lora_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
                         void *h, int num_sms, uint32_t flags, void *stream, int32_t *status) {
     GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, l.R};
-    // The inner product has one W tile: rows of a tile so that there is one for each pair of SMs.
-    const int clusters = num_sms / 2;
+    // The inner product has one W tile, half of its rows each CTA's: rows of x so that there is a tile for each pair of SMs.
+    const int clusters = clusters_of(num_sms);
     const int bt = l.M <= 32 * clusters ? 32 : l.M <= 64 * clusters ? 64 : l.M <= 128 * clusters ? 128 : 256;
-    const int r = launch_mode(kInner, a, nullptr, bt, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
+    const int r = launch_mode(kInner, a, nullptr, bt, (l.R + 15) / 16 * 16, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
     if (r) return r;
     a.w = w;
     a.bias = bias;
@@ -723,7 +773,19 @@ int launch_lora_grouped(const LoraArgs &l, const void *w, const void *bias, cons
     a.N = l.N;
     a.scale = nullptr;
     a.h = h;
-    return launch_mode(kOuter, a, l.b, 2 * kHalf, 1, num_sms, flags, stream, status);
+    // The outer one: the width that needs the least time, a round of tiles going with its width and a share for x (256 x
+    // 14336 x 4096: 75 tiles of 192 on 76 pairs, 56 of 256).
+    int wt = 256;
+    long long best = 0;
+    for (int w = 256; w >= 128; w -= 32) {
+        const long long units = (((long long)l.M + 255) / 256) * ((l.N + w - 1) / w);
+        const long long cost = (units + clusters - 1) / clusters * (w + 64);
+        if (best == 0 || cost < best) {
+            best = cost;
+            wt = w;
+        }
+    }
+    return launch_mode(kOuter, a, l.b, 256, wt, 1, num_sms, flags, stream, status);
 }
 
 }  // namespace bf16l
