@@ -249,7 +249,7 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     int32_t *status = nullptr;
     const int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, 0};
+    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, nullptr, 0};
     return result(launch_grouped(a, dev.num_sms, flags, stream, status));
 }
 
@@ -274,24 +274,32 @@ extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *p
 
 namespace {
 
-// The parts of the adapters' workspace: for few rows the inner values and the shared product, for many the rows' order and
-// the inner values in that order.
-constexpr int kLoraFew = 64;
-struct LoraSpace {
-    size_t first, second, third;  // bytes
-    size_t all() const { return first + second + third; }
+// How a linear with adapters is done, by sizes alone, and the parts of its workspace.
+//   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, while that is little;
+//     else rows in adapter order on tensor cores.
+//   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows, where they fill half of the
+//     SMs at least; else the dense linear's own kernels (which split K) into fp32, and the adapters' share after it.
+struct LoraWay {
+    bool cores, fused;
+    size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product
 };
-LoraSpace lora_space(int M, int N, int R, int L) {
-    const size_t m = (size_t)M, r = (size_t)R;
-    if (M <= kLoraFew) return {up256(4 * kLoraSplits * m * r), up256(4 * m * (size_t)N), 0};
-    return {up256(4 * ((size_t)L + 1)), up256(4 * m), up256(4 * m * r)};
+LoraWay lora_way(int M, int N, int K, int R, int L) {
+    const uint64_t m = (uint64_t)M, r = (uint64_t)R;
+    LoraWay w;
+    w.cores = m * r * (uint64_t)K * 2 <= 64ull << 20;
+    w.fused = M > 64 && (m + 255) / 256 * (((uint64_t)N + 127) / 128) >= kGb300Sms / 4;
+    w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
+    w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(K) : 1) * 4 * m * r);
+    w.y = w.fused ? 0 : up256(4 * m * (size_t)N);
+    return w;
 }
 
 }  // namespace
 
 extern "C" size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L) {
     if (M <= 0 || N <= 0 || K <= 0 || K % 8 != 0 || R <= 0 || R % 8 != 0 || R > kLoraMaxRank || L <= 0) return 0;
-    return lora_space(M, N, R, L).all();
+    const LoraWay w = lora_way(M, N, K, R, L);
+    return w.order + w.h + w.y;
 }
 
 extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b,
@@ -317,20 +325,19 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     int32_t *status = nullptr;
     int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    const LoraSpace space = lora_space(M, N, R, L);
+    const LoraWay way = lora_way(M, N, K, R, L);
     uint8_t *p = static_cast<uint8_t *>(workspace);
-    LoraArgs args = {x, a, b, scale, ids, nullptr, nullptr, out, M, N, K, R, L};
-    if (M <= kLoraFew) {
-        args.h = reinterpret_cast<float *>(p);
-        float *y = reinterpret_cast<float *>(p + space.first);
-        args.y = y;
-        st = result(launch_lora_inner(args, flags, stream));
-        if (st == BF16L_OK) st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
-        return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
-    }
-    int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + space.first);
-    st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
+    int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + up256(4 * ((size_t)L + 1)));
+    float *y = reinterpret_cast<float *>(p + way.order + way.h);
+    const LoraArgs args = {x, a, b, scale, ids, p + way.order, y, out, M, N, K, R, L,
+                           way.cores && !way.fused ? lora_splits(K) : 0};
+    if (way.order) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
+    if (st == BF16L_OK)
+        st = result(way.cores ? launch_lora_inner(args, flags, stream)
+                              : launch_lora_inner_grouped(args, offsets, rows, dev.num_sms, flags, stream, status));
     if (st != BF16L_OK) return st;
-    return result(launch_lora_grouped(args, w, bias, offsets, rows, p + space.first + space.second, dev.num_sms, flags,
-                                      stream, status));
+    if (way.fused)
+        return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
+    st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
+    return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
 }

@@ -61,6 +61,8 @@ struct GroupedShared {
     uint64_t copied[kMaxStages]; // this CTA's rows of x by index are in shared memory
     uint64_t acc_full[2];        // both: the accumulator holds a finished tile
     uint64_t acc_empty[2];       // leader only: both CTAs' epilogues have read it
+    uint32_t off[kSlots][8];  // kOuter: the lane masks of a stage's slots
+    int32_t column[kSlots];   // ... and their places in a row of h, in 16 bytes
     uint32_t tmem_base;
     int32_t bad_pair, aborted, issued, consumed;
     int32_t part[2][threads_of(true) / 32];
@@ -74,11 +76,15 @@ struct Unit {
     int e, p0, rows, m;  // group, first position, rows, W tile
     int cols;            // rows rounded up for the MMA
 };
+// a / b of what nearly always fits 32 bits (a 64-bit division is a long routine, and the first load waits for this one).
+__device__ __forceinline__ int quotient(long long a, int b) {
+    return a >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
+}
 // ONE: a single group of n rows, in whole tiles of bt; else n groups.
 template <bool ONE>
 __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int n, int bt, long long u, int m_tiles) {
     int lo = 0, hi = ONE ? 1 : n;  // tiles[lo] <= q < tiles[hi]
-    const int q = (int)(u / m_tiles);
+    const int q = quotient(u, m_tiles);
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sh.tiles[mid] <= q)
@@ -89,7 +95,7 @@ __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int n, int bt, 
     const int before = ONE ? 0 : sh.tiles[lo];
     const int nt = ONE ? (n + bt - 1) / bt : sh.tiles[lo + 1] - before, count = ONE ? n : sh.count[lo];
     const long long local = u - (long long)before * m_tiles;
-    const int m = (int)(local / nt), t = (int)(local - (long long)m * nt);
+    const int m = quotient(local, nt), t = (int)(local - (long long)m * nt);
     const int each = count / nt, more = count - each * nt;
     Unit r;
     r.e = lo;
@@ -138,13 +144,10 @@ __device__ __forceinline__ Tail tail_of(const GroupedShared &sh, int adapters, c
     r.n = max(min(below(t.p0 + t.rows), adapters) - r.first, 0);
     return r;
 }
-// The MMA's lane mask that leaves rows lo .. hi - 1 of a tile's 256 to be written.
-__device__ __forceinline__ void lanes_but(int lo, int hi, uint32_t (&off)[8]) {
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
-        off[w] = ~((h < 32 ? (1u << h) - 1u : ~0u) & ~(l < 32 ? (1u << l) - 1u : ~0u));
-    }
+// A word of the MMA's lane mask: bits lo .. hi - 1 (of 0 .. 31) clear, those rows to be written.
+__device__ __forceinline__ uint32_t lanes_but(int lo, int hi) {
+    const int l = min(max(lo, 0), 32), h = min(max(hi, 0), 32);
+    return ~((h < 32 ? (1u << h) - 1u : ~0u) & ~(l < 32 ? (1u << l) - 1u : ~0u));
 }
 
 // Maps of x with boxes of 16, 32, 64 and 128 rows.
@@ -155,7 +158,8 @@ struct RowMaps {
 template <int MODE, bool GATHER>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ RowMaps tm_x, const GroupedArgs a, int w_boxes, int bt, int wt, int stages, int32_t *status) {
+                   const __grid_constant__ RowMaps tm_x, const GroupedArgs a,
+                   int w_boxes, int bt, int wt, int stages, int32_t *status) {
     constexpr bool SWIGLU = MODE == kSwiglu;
     static_assert(GATHER || MODE == kPlain || MODE == kSwiglu, "the adapters' rows go by index");
     constexpr int kThreads = threads_of(GATHER);
@@ -349,62 +353,83 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {  // ---- MMA issuer (leader only) ----
+        if (leader) {  // ---- MMA issuer (leader only): lane 0; all lanes prepare the adapters' masks ----
             int it = 0, tile = 0;
-            for (long long u = cl; u < units; u += ncl, ++tile) {
-                sh.consumed = it;
+            bool ok = true;
+            for (long long u = cl; ok && u < units; u += ncl, ++tile) {
                 const Unit t = unit(u);
-                const uint32_t idesc = idesc_bf16_f32(2 * kHalf, MODE == kOuter ? wt : t.cols);
-                const int b = tile & 1;
-                const uint32_t acc = tmem + (uint32_t)(b * bt);
                 const Tail f = tail(t);
-                // Both CTAs' epilogues have read this buffer (used two tiles ago).
-                bool ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
-                tc_fence_after();
-                for (int c = 0; ok && c < C + f.stages(); ++c, ++it) {
-                    const int s = it % stages;
-                    if (!mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull)) {
-                        ok = false;
-                        break;
-                    }
+                const uint32_t idesc = idesc_bf16_f32(2 * kHalf, MODE == kOuter ? wt : t.cols);
+                const int b = tile & 1, n = C + f.stages();
+                const uint32_t acc = tmem + (uint32_t)(b * bt);
+                if (lane == 0) {
+                    sh.consumed = it;
+                    // Both CTAs' epilogues have read this buffer (used two tiles ago).
+                    ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
                     tc_fence_after();
-                    const uint8_t *ch = ring + s * stage_bytes;
-                    if (MODE == kOuter && c >= C) {
-                        const TailStage g = tail_stage(f, c - C);
-                        const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
-                        int last = -1;
-                        uint32_t off[8];
-                        for (int j = 0; j < g.n; ++j) {
-                            const int q = g.q0 + j, i = f.first + q / g.per, b16 = q % g.per;
-                            if (i != last) lanes_but(sh.first[i] - t.p0, min(sh.first[i + 1] - t.p0, t.rows), off);
-                            last = i;
-                            const uint64_t bdesc =
-                                smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * slot_bytes));
-                            mma_bf16_pair_lanes(acc, high + 2 * b16, bdesc, idesc, off);
-                            mma_bf16_pair_lanes(acc, low + 2 * b16, bdesc, idesc, off);
+                    for (int c = 0; ok && c < C; ++c, ++it) {
+                        const int s = it % stages;
+                        ok = mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint8_t *ch = ring + s * stage_bytes;
+                        for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
+                            const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
+                            const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + (MODE == kOuter ? kW : kX)));
+#pragma unroll
+                            for (int kk = 0; kk < kChunkK / 16; ++kk)
+                                mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || j > 0 || kk > 0) ? 1u : 0u);
                         }
                         mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
-                        continue;
                     }
-                    for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
-                        const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
-                        const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + (MODE == kOuter ? kW : kX)));
-#pragma unroll
-                        for (int kk = 0; kk < kChunkK / 16; ++kk)
-                            mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || j > 0 || kk > 0) ? 1u : 0u);
+                }
+                if (MODE == kOuter) {
+                    it = __shfl_sync(kAll, it, 0);
+                    ok = __shfl_sync(kAll, ok, 0);
+                    for (int c = C; ok && c < n; ++c, ++it) {
+                        // Four lanes a slot: its MMAs' lane mask and its place in h, which one lane would take longer
+                        // to work out than the MMAs take.
+                        const TailStage g = tail_stage(f, c - C);
+                        const int q = g.q0 + (lane >> 2), i = f.first + q / g.per, w = 2 * (lane & 3);
+                        if ((lane >> 2) < g.n) {
+                            const int lo = sh.first[i] - t.p0, hi = min(sh.first[i + 1] - t.p0, t.rows);
+                            sh.off[lane >> 2][w] = lanes_but(lo - 32 * w, hi - 32 * w);
+                            sh.off[lane >> 2][w + 1] = lanes_but(lo - 32 * w - 32, hi - 32 * w - 32);
+                            if (w == 0) sh.column[lane >> 2] = 2 * (q % g.per);
+                        }
+                        __syncwarp();
+                        const int s = it % stages;
+                        if (lane == 0) {
+                            ok = mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull);
+                            tc_fence_after();
+                            const uint8_t *ch = ring + s * stage_bytes;
+                            const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
+                            for (int j = 0; ok && j < g.n; ++j) {
+                                const int col = sh.column[j];
+                                const uint64_t bdesc =
+                                    smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * slot_bytes));
+                                mma_bf16_pair_lanes(acc, high + col, bdesc, idesc, sh.off[j]);
+                                mma_bf16_pair_lanes(acc, low + col, bdesc, idesc, sh.off[j]);
+                            }
+                            if (ok) mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
+                        }
+                        ok = __shfl_sync(kAll, ok, 0);  // (the masks have been read)
+                        if (!ok) break;
                     }
-                    mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
                 }
-                if (!ok) {  // release both epilogues at once
-                    atomicExch(&sh.aborted, 1);
-                    sh.consumed = it;
-                    mbar_arrive(&sh.acc_full[b]);
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&sh.acc_full[b]), 1));
-                    break;
+                if (lane == 0) {
+                    if (ok) {
+                        mma_commit_pair(&sh.acc_full[b], (uint16_t)0x3);
+                    } else {  // release both epilogues at once
+                        atomicExch(&sh.aborted, 1);
+                        sh.consumed = it;
+                        mbar_arrive(&sh.acc_full[b]);
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&sh.acc_full[b]), 1));
+                    }
                 }
-                mma_commit_pair(&sh.acc_full[b], (uint16_t)0x3);
+                ok = __shfl_sync(kAll, ok, 0);
             }
-            sh.consumed = it;
+            if (lane == 0) sh.consumed = it;
         }
         __syncwarp();
     } else if (GATHER && warp == 2 + kEpiWarps + kGatherWarps) {
@@ -452,17 +477,17 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     break;
                 }
                 const uint32_t to = to0 + (uint32_t)(s * stage_bytes);
-                if (MODE == kOuter && c >= C) {  // the rows' h: values, then remainders
+                if (MODE == kOuter && c >= C) {
+                    // The rows' h: values, then remainders.
                     const int col = tail_stage(f, c - C).kb * kChunkK + 8 * v;
-                    const bool have = col < a.R;  // (R % 8 == 0)
-                    const uint16_t *h = static_cast<const uint16_t *>(a.h) + (have ? col : 0);
+                    const uint16_t *h = static_cast<const uint16_t *>(a.h);
 #pragma unroll 4
                     for (int i = 0; i < kHalf / kGatherRows; ++i) {
                         const int p = q0 + r0 + kGatherRows * i;
-                        const bool in = have && p < t.p0 + t.rows;
-                        const uint16_t *from = h + (size_t)(in ? p : t.p0) * 2 * a.R;
+                        const bool in = col < a.R && p < t.p0 + t.rows;
+                        const uint16_t *from = in ? h + (size_t)__ldg(a.rows + p) * 2 * a.R + col : h;
                         cp_async_16(to + 128 * kGatherRows * i, from, in ? 16u : 0u);
-                        cp_async_16(to + (uint32_t)chunk_bytes + 128 * kGatherRows * i, from + a.R, in ? 16u : 0u);
+                        cp_async_16(to + (uint32_t)chunk_bytes + 128 * kGatherRows * i, in ? from + a.R : h, in ? 16u : 0u);
                     }
                     cp_async_arrive(&sh.copied[s]);
                     continue;
@@ -572,15 +597,18 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint16_t *o = out + (size_t)(t.p0 + c0) * a.N + n;
                 const int left = t.rows - c0;
                 if constexpr (MODE == kInner) {
-                    uint16_t *h = out + (size_t)(t.p0 + c0) * 2 * a.N + n;
+                    uint16_t *h = out + n;
+                    const int to = __ldg(a.rows + t.p0 + c0 + min(lane & 15, left - 1));
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 16; ++j) {
+                        const int row = __shfl_sync(kAll, to, j);
                         if (n < a.N && j < left) {
-                            const float w = f * v[j];
-                            const uint16_t high = f32_to_bf16(w);
-                            h[(size_t)(2 * j) * a.N] = high;
-                            h[(size_t)(2 * j + 1) * a.N] = isfinite(w) ? f32_to_bf16(w - bf16_to_f32(high)) : 0;
+                            uint32_t high, low;
+                            two_bf16(f * v[j], high, low);
+                            h[(size_t)row * 2 * a.N] = (uint16_t)high;
+                            h[((size_t)row * 2 + 1) * a.N] = (uint16_t)low;
                         }
+                    }
                 } else if constexpr (SWIGLU) {
                     float f[8];  // row 2 i (gate lanes) or 2 i + 1 (up lanes) of output n
                     const bool up = lane >= 16;
@@ -700,7 +728,7 @@ int clusters_of(int num_sms) {
 }
 
 // Tiles of up to bt rows and wt outputs; `full`: groups that may have rows.
-int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int wt, int full, int num_sms, uint32_t flags, void *stream,
+int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int num_sms, uint32_t flags, void *stream,
                 int32_t *status) {
     const bool swiglu = mode == kSwiglu;
     CUtensorMap tw, tb = {};
@@ -715,7 +743,7 @@ int launch_mode(int mode, const GroupedArgs &a, const void *b, int bt, int wt, i
     for (int i = 0; i < 4 && !r && !a.rows; ++i)
         r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, K, 16u << i, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
+    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, a.b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
     if (r) return (int)cudaErrorInvalidValue;
     // A cluster that cannot be resident with the others would run its tiles after them.
     const long long units = ((long long)a.P / bt + full) * ((a.N + wt - 1) / wt);  // at most
@@ -756,36 +784,35 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     const int full = a.P < a.groups ? a.P : a.groups;
     const long long twice = 2ll * a.P / full;
     const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
-    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, nullptr, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status);
+    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status);
 }
 
-int launch_lora_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
-                        void *h, int num_sms, uint32_t flags, void *stream, int32_t *status) {
-    GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, l.R};
-    // The inner product has one W tile, half of its rows each CTA's: rows of x so that there is a tile for each pair of SMs.
+int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
+                              void *stream, int32_t *status) {
+    const GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, l.h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, nullptr, 0};
+    // One W tile, half of its rows each CTA's: rows of x so that there is a tile for each pair of SMs.
     const int clusters = clusters_of(num_sms);
     const int bt = l.M <= 32 * clusters ? 32 : l.M <= 64 * clusters ? 64 : l.M <= 128 * clusters ? 128 : 256;
-    const int r = launch_mode(kInner, a, nullptr, bt, (l.R + 15) / 16 * 16, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
-    if (r) return r;
-    a.w = w;
-    a.bias = bias;
-    a.out = l.out;
-    a.N = l.N;
-    a.scale = nullptr;
-    a.h = h;
-    // The outer one: the width that needs the least time, a round of tiles going with its width and a share for x (256 x
-    // 14336 x 4096: 75 tiles of 192 on 76 pairs, 56 of 256).
+    return launch_mode(kInner, a, bt, (l.R + 15) / 16 * 16, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
+}
+
+int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
+                              int num_sms, uint32_t flags, void *stream, int32_t *status) {
+    const GroupedArgs a = {l.x, w, bias, offsets, rows, l.out, l.M, l.M, l.L, l.N, l.K, 0, nullptr, l.b, l.h, l.R};
+    // The width that needs the least time, a round of tiles going with its width and a share for x (256 x 14336 x 4096: 75
+    // tiles of 192 on 76 pairs, 56 of 256).
+    const int clusters = clusters_of(num_sms);
     int wt = 256;
     long long best = 0;
-    for (int w = 256; w >= 128; w -= 32) {
-        const long long units = (((long long)l.M + 255) / 256) * ((l.N + w - 1) / w);
-        const long long cost = (units + clusters - 1) / clusters * (w + 64);
+    for (int w0 = 256; w0 >= 128; w0 -= 32) {
+        const long long units = (((long long)l.M + 255) / 256) * ((l.N + w0 - 1) / w0);
+        const long long cost = (units + clusters - 1) / clusters * (w0 + 64);
         if (best == 0 || cost < best) {
             best = cost;
-            wt = w;
+            wt = w0;
         }
     }
-    return launch_mode(kOuter, a, l.b, 256, wt, 1, num_sms, flags, stream, status);
+    return launch_mode(kOuter, a, 256, wt, 1, num_sms, flags, stream, status);
 }
 
 }  // namespace bf16l

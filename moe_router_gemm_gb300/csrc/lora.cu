@@ -2,12 +2,12 @@
 // out = y + h @ B_a^T, with y the shared projection in fp32, by the dense linear's own kernels between the two.
 //
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
-// spreads over as many SMs as it can: the inner one a row's K over up to kLoraSplits blocks, whose sums the outer one
+// spreads over as many SMs as it can: the inner one a row's K over up to eight blocks, whose sums the outer one
 // adds, in order, when it reads them, and four ranks a warp.  The inner one also asks L2 for B_a, which the outer one reads when the projection
 // is done.
 #include <cuda_runtime.h>
 
-#include "common.cuh"
+#include "grouped.cuh"
 #include "moe.h"
 
 namespace bf16l {
@@ -17,14 +17,9 @@ namespace {
 constexpr int kInnerWarps = 4, kRanks = 4;  // ranks that a warp sums at a time
 constexpr int kOuterThreads = 128;
 
-// Parts of K: none below 512 elements.
-__host__ __device__ inline int lora_splits(int K) {
-    const int s = K / 512 > 1 ? K / 512 : 1;
-    return s < kLoraSplits ? s : kLoraSplits;
-}
-
 // A warp sums kRanks ranks of a row over a part of K.
-__global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a, int splits) {
+__global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a) {
+    const int splits = (int)gridDim.y;
     pdl_launch_dependents();
     pdl_wait();
     const int t = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -42,7 +37,7 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
     const uint16_t *x = static_cast<const uint16_t *>(a.x) + (size_t)t * a.K;
     const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r0) * a.K;
     float sum[kRanks] = {};
-#pragma unroll 2
+#pragma unroll 4
     for (int k = k0 + 8 * lane; k < k1; k += 256) {  // (K % 8 == 0)
         const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
         uint4 wv[kRanks];
@@ -65,28 +60,38 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
         float v = sum[0];
 #pragma unroll
         for (int r = 1; r < kRanks; ++r) v = lane == r ? sum[r] : v;
-        a.h[((size_t)s * a.M + t) * a.R + r0 + lane] = a.scale ? __ldg(a.scale + id) * v : v;
+        if (a.scale) v *= __ldg(a.scale + id);
+        if (a.splits) {
+            static_cast<float *>(a.h)[((size_t)s * a.M + t) * a.R + r0 + lane] = v;
+        } else {
+            uint32_t high, low;
+            two_bf16(v, high, low);
+            uint16_t *h = static_cast<uint16_t *>(a.h) + (size_t)t * 2 * a.R + r0 + lane;
+            h[0] = (uint16_t)high;
+            h[a.R] = (uint16_t)low;
+        }
     }
 }
 
 // One output a thread: its B row is R consecutive values.
-__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArgs a, int splits) {
+__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArgs a) {
     __shared__ float h[kLoraMaxRank];
     pdl_launch_dependents();
     pdl_wait();
-    const int t = blockIdx.y, n = (int)blockIdx.x * kOuterThreads + (int)threadIdx.x;
-    const int id = __ldg(a.ids + t);
-    const bool has = (unsigned)id < (unsigned)a.L, in = n < a.N;
-    const size_t at = (size_t)t * a.N + n;
-    float sum = in ? a.y[at] : 0.0f;
-    if (has) {
-        if ((int)threadIdx.x < a.R) {
-            float v = 0.0f;
-            for (int s = 0; s < splits; ++s) v += a.h[((size_t)s * a.M + t) * a.R + threadIdx.x];
-            h[threadIdx.x] = v;
-        }
-        __syncthreads();
-        if (in) {
+    const int t = blockIdx.x, id = __ldg(a.ids + t);
+    const bool has = (unsigned)id < (unsigned)a.L;
+    if (has && (int)threadIdx.x < a.R) {
+        float v = 0.0f;
+        const uint16_t *two = static_cast<const uint16_t *>(a.h) + (size_t)t * 2 * a.R + threadIdx.x;
+        if (!a.splits) v = bf16_to_f32(two[0]) + bf16_to_f32(two[a.R]);
+        for (int s = 0; s < a.splits; ++s) v += static_cast<const float *>(a.h)[((size_t)s * a.M + t) * a.R + threadIdx.x];
+        h[threadIdx.x] = v;
+    }
+    __syncthreads();
+    for (long long n = (long long)blockIdx.y * kOuterThreads + threadIdx.x; n < a.N; n += (long long)gridDim.y * kOuterThreads) {
+        const size_t at = (size_t)t * a.N + n;
+        float sum = a.y[at];
+        if (has) {
             const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n) * a.R);
             float d = 0.0f;
 #pragma unroll 4
@@ -101,11 +106,11 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             }
             sum += d;
         }
+        static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(sum);
     }
-    if (in) static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(sum);
 }
 
-int launch(void (*f)(const LoraArgs, int), dim3 grid, int threads, const LoraArgs &a, uint32_t flags, void *stream) {
+int launch(void (*f)(const LoraArgs), dim3 grid, int threads, const LoraArgs &a, uint32_t flags, void *stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -115,18 +120,26 @@ int launch(void (*f)(const LoraArgs, int), dim3 grid, int threads, const LoraArg
     attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, f, a, lora_splits(a.K));
+    return (int)cudaLaunchKernelEx(&cfg, f, a);
 }
 
 }  // namespace
 
+// None below 512 elements.
+int lora_splits(int K) {
+    const int s = K / 512 > 1 ? K / 512 : 1;
+    return s < 8 ? s : 8;
+}
+
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream) {
-    const dim3 grid((unsigned)a.M, (unsigned)lora_splits(a.K), (unsigned)((a.R + kRanks * kInnerWarps - 1) / (kRanks * kInnerWarps)));
+    const int ranks = kRanks * kInnerWarps;
+    const dim3 grid((unsigned)a.M, (unsigned)(a.splits ? a.splits : 1), (unsigned)((a.R + ranks - 1) / ranks));
     return launch(lora_inner_kernel, grid, 32 * kInnerWarps, a, flags, stream);
 }
 
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {
-    const dim3 grid((unsigned)((a.N + kOuterThreads - 1) / kOuterThreads), (unsigned)a.M);
+    const int blocks = (a.N + kOuterThreads - 1) / kOuterThreads;
+    const dim3 grid((unsigned)a.M, (unsigned)(blocks < 65535 ? blocks : 65535));
     return launch(lora_outer_kernel, grid, kOuterThreads, a, flags, stream);
 }
 

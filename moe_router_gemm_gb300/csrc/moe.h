@@ -57,30 +57,34 @@ struct GroupedArgs {
     const int32_t *offsets, *rows;  // rows null: row p of x is row p of out
     void *out;
     int x_rows, P, groups, N, K, swiglu;
-    // the adapters' products (launch_lora_*)
+    // the adapters' products (launch_lora_*_grouped)
     const float *scale;
-    void *h;
+    const void *b, *h;
     int R;
 };
 int init_grouped();
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
-// The adapters of a linear: the inner values in fp32, as S sums over parts of K that are still to be added up, h[S][M][R], and
-// out from them and the shared product y[M][N] (lora.cu), for few rows; or, rows in the order of their adapters, both
-// products on tensor cores (grouped.cu), the inner values as h[M][2][R] of bf16, value and remainder.
-constexpr int kLoraMaxRank = 128, kLoraSplits = 8;
+// The adapters of a linear.  The inner values h are fp32 sums over `splits` parts of K that are still to be added up,
+// [splits][M][R], or (splits 0) [M][2][R] of bf16, value and remainder.  For rows as they come (lora.cu): the inner product,
+// and out from h and the shared product y[M][N] in fp32.  For rows ordered by adapter (grouped.cu, on tensor cores): the
+// inner product (splits 0), and out from h, x and w.
+constexpr int kLoraMaxRank = 128;
 struct LoraArgs {
     const void *x, *a, *b;
     const float *scale;
     const int32_t *ids;
-    float *h;
+    void *h;
     const float *y;
     void *out;
-    int M, N, K, R, L;
+    int M, N, K, R, L, splits;
 };
+int lora_splits(int K);
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
-int launch_lora_grouped(const LoraArgs &a, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
-                        void *h, int num_sms, uint32_t flags, void *stream, int32_t *status);
+int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
+                              void *stream, int32_t *status);
+int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
+                              int num_sms, uint32_t flags, void *stream, int32_t *status);
 
 }  // namespace bf16l

@@ -230,7 +230,8 @@ def _check_lora(lib, p, what="", **kw):
 
 LORA = [(1, 1, 8, 8, 1), (1, 4096, 4096, 16, 64), (3, 33, 72, 8, 2), (8, 256, 2880, 32, 5), (16, 2112, 7168, 64, 8), (61, 300, 1024, 24, 7),
         (64, 1000, 512, 128, 70), (129, 257, 320, 40, 3), (200, 640, 136, 16, 200), (513, 520, 256, 72, 4), (1030, 384, 640, 64, 9),
-        (2048, 130, 64, 96, 1000), (300, 77, 2048, 8, 1), (2000, 1024, 1024, 128, 2)]
+        (2048, 130, 64, 96, 1000), (300, 77, 2048, 8, 1), (2000, 1024, 1024, 128, 2), (65, 5000, 136, 24, 30), (300, 9999, 72, 8, 100),
+        (1500, 4100, 320, 128, 40), (700, 4104, 2056, 48, 500), (256, 14336, 256, 16, 64), (520, 6144, 640, 80, 3)]
 
 
 @pytest.mark.parametrize("shape", LORA, ids=lambda s: "x".join(map(str, s)))
@@ -246,8 +247,8 @@ def test_linear_lora(lib, shape, runs):
 
 def test_lora_not_finite(lib):
     """A NaN in one adapter reaches its rows alone; rows without an adapter have none of them."""
-    for M in (12, 600):
-        p = _lora_problem(M, 72, 128, 16, 4, 3, bare=0.3, scale=False)
+    for M, N in ((12, 72), (600, 72), (600, 5000), (2000, 1000)):
+        p = _lora_problem(M, N, 128, 16, 4, 3, bare=0.3, scale=False)
         clean = _check_lora(lib, p)
         a, b = p["a"].clone(), p["b"].clone()
         a[1, 3, 7], b[2] = float("nan"), float("inf")
