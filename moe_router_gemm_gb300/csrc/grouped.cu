@@ -150,6 +150,15 @@ __device__ __forceinline__ uint32_t lanes_but(int lo, int hi) {
     return ~((h < 32 ? (1u << h) - 1u : ~0u) & ~(l < 32 ? (1u << l) - 1u : ~0u));
 }
 
+// A role's place in the ring.  (A stage's number divided by the runtime ring depth costs each role some 250 clocks a stage.)
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+};
+
 // Maps of x with boxes of 16, 32, 64 and 128 rows.
 struct RowMaps {
     CUtensorMap of[4];
@@ -299,15 +308,16 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         // ---- TMA producer (both CTAs), the whole warp ----
         const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // leader's full[0]
         int it = 0;
+        Ring r;
         bool ok = true;
         for (long long u = cl; ok && u < units; u += ncl) {
             const Unit t = unit(u);
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
             const int n0 = t.m * wt + (int)rank * (wt / 2);
             const Tail f = tail(t);
-            for (int c = 0; c < C + f.stages(); ++c, ++it) {
-                const int s = it % stages;
-                ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
+            for (int c = 0, n = C + f.stages(); c < n; ++c, ++it, r.next(stages)) {
+                const int s = r.s;
+                ok = mbar_wait(&sh.empty[s], r.phase ^ 1u, status, kSiteEmpty);  // (at once in the first round)
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
                 if (!ok) {
                     if (lane == 0) atomicExch(&sh.aborted, 1);
@@ -339,8 +349,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                     // ... and 4 to 7 this CTA's rows, a multiple of 16, by boxes of falling sizes: lane i takes 1 << i
                     if (!GATHER && i >= 4 && (half & (1 << i))) {
-                        const int r = half & ~((2 << i) - 1);
-                        tma_load_2d_pair(ch + kX + r * 128, &tm_x.of[i - 4], fb, k0, q0 + r);
+                        const int first = half & ~((2 << i) - 1);
+                        tma_load_2d_pair(ch + kX + first * 128, &tm_x.of[i - 4], fb, k0, q0 + first);
                     }
                 }
             }
@@ -348,13 +358,14 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         if (lane == 0) sh.issued = it;
         // Every commit that arrives on this CTA's `empty` barriers has landed before the exit barrier.
         if (ok) {
-            for (int i = (it > stages ? it - stages : 0); i < it; ++i)
-                if (!mbar_wait(&sh.empty[i % stages], (i / stages) & 1, status, kSiteDrain)) break;
+            for (int i = 0; i < stages; ++i, r.next(stages))
+                if (!mbar_wait(&sh.empty[r.s], r.phase ^ 1u, status, kSiteDrain)) break;
         }
         __syncwarp();
     } else if (warp == 1) {
         if (leader) {  // ---- MMA issuer (leader only): lane 0; all lanes prepare the adapters' masks ----
             int it = 0, tile = 0;
+            Ring r;
             bool ok = true;
             for (long long u = cl; ok && u < units; u += ncl, ++tile) {
                 const Unit t = unit(u);
@@ -367,9 +378,9 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     // Both CTAs' epilogues have read this buffer (used two tiles ago).
                     ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
                     tc_fence_after();
-                    for (int c = 0; ok && c < C; ++c, ++it) {
-                        const int s = it % stages;
-                        ok = mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull);
+                    for (int c = 0; ok && c < C; ++c, ++it, r.next(stages)) {
+                        const int s = r.s;
+                        ok = mbar_wait(&sh.full[s], r.phase, status, kSiteFull);
                         if (!ok) break;
                         tc_fence_after();
                         const uint8_t *ch = ring + s * stage_bytes;
@@ -385,8 +396,10 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 }
                 if (MODE == kOuter) {
                     it = __shfl_sync(kAll, it, 0);
+                    r.s = __shfl_sync(kAll, r.s, 0);
+                    r.phase = __shfl_sync(kAll, r.phase, 0);
                     ok = __shfl_sync(kAll, ok, 0);
-                    for (int c = C; ok && c < n; ++c, ++it) {
+                    for (int c = C; ok && c < n; ++c, ++it, r.next(stages)) {
                         // Four lanes a slot: its MMAs' lane mask and its place in h, which one lane would take longer
                         // to work out than the MMAs take.
                         const TailStage g = tail_stage(f, c - C);
@@ -398,9 +411,9 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             if (w == 0) sh.column[lane >> 2] = 2 * (q % g.per);
                         }
                         __syncwarp();
-                        const int s = it % stages;
+                        const int s = r.s;
                         if (lane == 0) {
-                            ok = mbar_wait(&sh.full[s], (it / stages) & 1, status, kSiteFull);
+                            ok = mbar_wait(&sh.full[s], r.phase, status, kSiteFull);
                             tc_fence_after();
                             const uint8_t *ch = ring + s * stage_bytes;
                             const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
@@ -435,14 +448,14 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     } else if (GATHER && warp == 2 + kEpiWarps + kGatherWarps) {
         if (lane == 0) {  // ---- x by index: what has arrived, to the leader's barrier (both CTAs) ----
             const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);
-            int it = 0;
+            Ring r;
             bool ok = true;
             for (long long u = cl; ok && u < units; u += ncl) {
                 const int n = MODE == kOuter ? C + tail(unit(u)).stages() : C;
-                for (int c = 0; ok && c < n; ++c, ++it) {
-                    ok = mbar_wait(&sh.copied[it % stages], (it / stages) & 1, status, kSiteStage);
+                for (int c = 0; ok && c < n; ++c, r.next(stages)) {
+                    ok = mbar_wait(&sh.copied[r.s], r.phase, status, kSiteStage);
                     fence_proxy_async_smem();  // the copies, seen here, before the MMAs' reads
-                    if (ok) mbar_arrive_remote(full0 + (uint32_t)((it % stages) * sizeof(uint64_t)));
+                    if (ok) mbar_arrive_remote(full0 + (uint32_t)(r.s * sizeof(uint64_t)));
                 }
             }
             if (!ok) atomicExch(&sh.aborted, 1);
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         const int gt = tid - 32 * (2 + kEpiWarps), r0 = gt >> 3, v = gt & 7;
         const uint16_t *x = static_cast<const uint16_t *>(a.x) + 8 * v;
         const uint32_t to0 = smem_u32(ring) + kX + (uint32_t)(r0 * 128 + ((v ^ (r0 & 7)) << 4));
-        int it = 0;
+        Ring r;
         bool ok = true;
         for (long long u = cl; ok && u < units; u += ncl) {
             const Unit t = unit(u);
@@ -468,9 +481,9 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 row[i] = x + (size_t)min(max(__ldg(a.rows + p), 0), a.x_rows - 1) * a.K;
             }
             const Tail f = tail(t);
-            for (int c = 0; c < C + f.stages(); ++c, ++it) {
-                const int s = it % stages;
-                ok = it < stages || mbar_wait(&sh.empty[s], ((it / stages) - 1) & 1, status, kSiteEmpty);
+            for (int c = 0, n = C + f.stages(); c < n; ++c, r.next(stages)) {
+                const int s = r.s;
+                ok = mbar_wait(&sh.empty[s], r.phase ^ 1u, status, kSiteEmpty);
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
                 if (!ok) {
                     if (lane == 0) atomicExch(&sh.aborted, 1);
