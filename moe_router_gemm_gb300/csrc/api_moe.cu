@@ -289,9 +289,46 @@ LoraWay lora_way(int M, int N, int K, int R, int L) {
     w.cores = m * r * (uint64_t)K * 2 <= 64ull << 20;
     w.fused = M > 64 && (m + 255) / 256 * (((uint64_t)N + 127) / 128) >= kGb300Sms / 4;
     w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
-    w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(K) : 1) * 4 * m * r);
+    w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(M, K, R) : 1) * 4 * m * r);
     w.y = w.fused ? 0 : up256(4 * m * (size_t)N);
     return w;
+}
+
+// The dense linear's plan for few rows, where its table has no line for most sizes: the forms that lead there, by the fill of
+// the SMs (fp32 out, us; the general rule in brackets): 1 x 4096 x 4096 5.6 (10.6), 8 x 4096 x 4096 6.6 (22.2), 8 x 7168 x
+// 2048 6.2 (22.2), 16 x 4096 x 4096 7.8 (11.7), 32 x 4096 x 4096 10.4 (12.4), 61 x 2112 x 7168 10.9 (15.5), 64 x 7168 x 7168
+// 24.2 (28.2).  Narrow weights stay with the general rule.
+bool few_rows_plan(int M, int N, int K, const bf16l_device &dev, uint32_t flags, bf16l_plan *plan) {
+    bf16l_plan p = {};
+    p.flags = (int32_t)flags;
+    if (N < 1024 || M > 64 || (M > 16 && N > 8192)) return false;  // (64 x 14336 x 4096: 24.9, 31 so)
+    if (M == 1) {  // a warp, or two, for each W row
+        p.kernel = BF16L_KERNEL_WARPROW;
+        p.threads = 256;
+        p.rows_per_cta = N < 4096 ? 2 : 1;
+        p.stages = 4;
+    } else if (M <= 16) {  // 16 W rows for some warps of 16 an SM, all of them at work
+        p.kernel = BF16L_KERNEL_WARPMMA;
+        p.threads = 512;
+        p.tokens_per_cta = 2;
+        p.split_k = 1;
+        p.stages = 1;
+        p.rows_per_cta = 4;
+        while (p.rows_per_cta < 16 && 2 * p.rows_per_cta * ((N + 15) / 16) <= 18 * dev.num_sms) p.rows_per_cta *= 2;
+    } else {  // K over a cluster, two CTAs an SM
+        p.kernel = BF16L_KERNEL_SPLITK;
+        p.threads = kSplitThreads;
+        p.rows_per_cta = N < 6144 ? 64 : 96;
+        p.tokens_per_cta = (M + 7) / 8 * 8;
+        p.stages = 2;
+        p.chunks_per_stage = 2;
+        const int tiles = (N + p.rows_per_cta - 1) / p.rows_per_cta, most = (K + 2 * kChunkK - 1) / (2 * kChunkK);
+        p.split_k = (2 * dev.num_sms - tiles / 2) / tiles;
+        p.split_k = p.split_k < 1 ? 1 : p.split_k > 8 ? 8 : p.split_k;
+        if (p.split_k > most) p.split_k = most;
+    }
+    *plan = p;
+    return check_plan(M, N, K, dev, &p) == BF16L_OK;
 }
 
 }  // namespace
@@ -330,7 +367,7 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + up256(4 * ((size_t)L + 1)));
     float *y = reinterpret_cast<float *>(p + way.order + way.h);
     const LoraArgs args = {x, a, b, scale, ids, p + way.order, y, out, M, N, K, R, L,
-                           way.cores && !way.fused ? lora_splits(K) : 0};
+                           way.cores && !way.fused ? lora_splits(M, K, R) : 0};
     if (way.order) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
     if (st == BF16L_OK)
         st = result(way.cores ? launch_lora_inner(args, flags, stream)
@@ -338,6 +375,8 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     if (st != BF16L_OK) return st;
     if (way.fused)
         return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
-    st = bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
+    bf16l_plan plan;
+    st = few_rows_plan(M, N, K, dev, flags, &plan) ? bf16_linear_f32out_with_plan(x, w, bias, y, M, N, K, &plan, stream)
+                                                   : bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
     return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
 }

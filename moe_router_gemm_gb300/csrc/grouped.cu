@@ -42,7 +42,7 @@ constexpr int kWBytes = kHalf * kChunkK * 2;      // of a stage
 constexpr int kChunks = 2;  // 64-wide chunks of K in a stage
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;
-constexpr int kGatherWarps = 2, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
+constexpr int kGatherWarps = 4, kGatherRows = 4 * kGatherWarps;  // (a warp copies four rows' 128 bytes at a time)
 __host__ __device__ constexpr int threads_of(bool gather) { return 32 * (2 + kEpiWarps + (gather ? kGatherWarps + 1 : 0)); }
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kPer = (kMaxGroups + 32 * (2 + kEpiWarps) - 1) / (32 * (2 + kEpiWarps));  // groups of a thread, at most
@@ -417,12 +417,23 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             tc_fence_after();
                             const uint8_t *ch = ring + s * stage_bytes;
                             const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
+                            uint32_t off[8];
+                            int col = sh.column[0];
+#pragma unroll
+                            for (int w = 0; w < 8; ++w) off[w] = sh.off[0][w];
                             for (int j = 0; ok && j < g.n; ++j) {
-                                const int col = sh.column[j];
                                 const uint64_t bdesc =
                                     smem_desc_sw32(smem_u32(ch + (j >> 2) * chunk_bytes + kW + (j & 3) * slot_bytes));
-                                mma_bf16_pair_lanes(acc, high + col, bdesc, idesc, sh.off[j]);
-                                mma_bf16_pair_lanes(acc, low + col, bdesc, idesc, sh.off[j]);
+                                // the next slot's, while this one's instructions go out
+                                const int next = min(j + 1, kSlots - 1), col2 = sh.column[next];
+                                uint32_t off2[8];
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) off2[w] = sh.off[next][w];
+                                mma_bf16_pair_lanes(acc, high + col, bdesc, idesc, off);
+                                mma_bf16_pair_lanes(acc, low + col, bdesc, idesc, off);
+                                col = col2;
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) off[w] = off2[w];
                             }
                             if (ok) mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
                         }
@@ -505,25 +516,28 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     cp_async_arrive(&sh.copied[s]);
                     continue;
                 }
-                // The copies' own instructions count: two warps issue 32 a stage, and one address serves both chunks.
+                // The copies' own instructions count: four warps issue 16 each a stage, and one address serves all chunks.
                 const int k0 = c * kChunks * kChunkK;
-                const uint32_t to2 = to + (uint32_t)chunk_bytes;
-                static_assert(kChunks == 2, "two chunks a stage");
-                if (have == half && k0 + 2 * kChunkK <= a.K) {
+                if (have == half && k0 + kChunks * kChunkK <= a.K) {
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
                         if (kGatherRows * i < half) {
-                            cp_async_16(to + 128 * kGatherRows * i, row[i] + k0);
-                            cp_async_16(to2 + 128 * kGatherRows * i, row[i] + k0 + kChunkK);
+#pragma unroll
+                            for (int j = 0; j < kChunks; ++j)
+                                cp_async_16(to + j * (uint32_t)chunk_bytes + 128 * kGatherRows * i, row[i] + k0 + j * kChunkK);
                         }
                 } else {
-                    const uint32_t in = k0 + 8 * v < a.K ? 16u : 0u, in2 = k0 + kChunkK + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0)
+                    uint32_t in[kChunks];
+#pragma unroll
+                    for (int j = 0; j < kChunks; ++j) in[j] = k0 + j * kChunkK + 8 * v < a.K ? 16u : 0u;  // (K % 8 == 0)
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
                         if (kGatherRows * i < half) {
                             const bool mine = r0 + kGatherRows * i < have;
-                            cp_async_16(to + 128 * kGatherRows * i, row[i] + (in ? k0 : 0), mine ? in : 0u);
-                            cp_async_16(to2 + 128 * kGatherRows * i, row[i] + (in2 ? k0 + kChunkK : 0), mine ? in2 : 0u);
+#pragma unroll
+                            for (int j = 0; j < kChunks; ++j)
+                                cp_async_16(to + j * (uint32_t)chunk_bytes + 128 * kGatherRows * i,
+                                            row[i] + (in[j] ? k0 + j * kChunkK : 0), mine ? in[j] : 0u);
                         }
                 }
                 cp_async_arrive(&sh.copied[s]);

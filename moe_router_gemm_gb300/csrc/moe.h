@@ -79,7 +79,7 @@ struct LoraArgs {
     void *out;
     int M, N, K, R, L, splits;
 };
-int lora_splits(int K);
+int lora_splits(int M, int K, int R);
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
 int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
