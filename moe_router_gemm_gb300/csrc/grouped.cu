@@ -363,42 +363,42 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (leader) {  // ---- MMA issuer (leader only): lane 0; all lanes prepare the adapters' masks ----
+        // ---- MMA issuer (leader only): the whole warp goes through the loop and one elected lane issues, so that descriptors
+        // are uniform (8 MMAs and a commit 196 clocks; by lane 0 in a branch of its own 555) ----
+        if (leader) {
             int it = 0, tile = 0;
             Ring r;
             bool ok = true;
+            const uint32_t first_lo = (uint32_t)smem_desc_sw128(smem_u32(ring));  // (the low word)
             for (long long u = cl; ok && u < units; u += ncl, ++tile) {
                 const Unit t = unit(u);
                 const Tail f = tail(t);
                 const uint32_t idesc = idesc_bf16_f32(2 * kHalf, MODE == kOuter ? wt : t.cols);
                 const int b = tile & 1, n = C + f.stages();
                 const uint32_t acc = tmem + (uint32_t)(b * bt);
-                if (lane == 0) {
-                    sh.consumed = it;
-                    // Both CTAs' epilogues have read this buffer (used two tiles ago).
-                    ok = tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty);
+                if (lane == 0) sh.consumed = it;
+                // Both CTAs' epilogues have read this buffer (used two tiles ago).
+                ok = __all_sync(kAll, tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty));
+                tc_fence_after();
+                for (int c = 0; ok && c < C; ++c, ++it, r.next(stages)) {
+                    const int s = r.s;
+                    ok = __all_sync(kAll, mbar_wait(&sh.full[s], r.phase, status, kSiteFull));
+                    if (!ok) break;
                     tc_fence_after();
-                    for (int c = 0; ok && c < C; ++c, ++it, r.next(stages)) {
-                        const int s = r.s;
-                        ok = mbar_wait(&sh.full[s], r.phase, status, kSiteFull);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint8_t *ch = ring + s * stage_bytes;
-                        for (int j = 0; j < kChunks; ++j, ch += chunk_bytes) {
-                            const uint64_t adesc = smem_desc_sw128(smem_u32(ch));
-                            const uint64_t bdesc = smem_desc_sw128(smem_u32(ch + (MODE == kOuter ? kW : kX)));
+                    const uint32_t lo = first_lo + (uint32_t)s * (uint32_t)(stage_bytes >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            const uint32_t alo = lo + j * (uint32_t)(chunk_bytes >> 4);
 #pragma unroll
                             for (int kk = 0; kk < kChunkK / 16; ++kk)
-                                mma_bf16_pair(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc, (c > 0 || j > 0 || kk > 0) ? 1u : 0u);
+                                mma_bf16_pair_sw128(acc, alo + 2 * kk, alo + ((MODE == kOuter ? kW : kX) >> 4) + 2 * kk, idesc,
+                                                    j + kk > 0 ? 1u : (uint32_t)c);
                         }
                         mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
                     }
                 }
                 if (MODE == kOuter) {
-                    it = __shfl_sync(kAll, it, 0);
-                    r.s = __shfl_sync(kAll, r.s, 0);
-                    r.phase = __shfl_sync(kAll, r.phase, 0);
-                    ok = __shfl_sync(kAll, ok, 0);
                     for (int c = C; ok && c < n; ++c, ++it, r.next(stages)) {
                         // Four lanes a slot: its MMAs' lane mask and its place in h, which one lane would take longer
                         // to work out than the MMAs take.
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                         }
                         __syncwarp();
                         const int s = r.s;
-                        if (lane == 0) {
+                        if (elect_one()) {
                             ok = mbar_wait(&sh.full[s], r.phase, status, kSiteFull);
                             tc_fence_after();
                             const uint8_t *ch = ring + s * stage_bytes;
@@ -437,11 +437,11 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             }
                             if (ok) mma_commit_pair(&sh.empty[s], (uint16_t)0x3);
                         }
-                        ok = __shfl_sync(kAll, ok, 0);  // (the masks have been read)
+                        ok = __all_sync(kAll, ok);  // (the masks have been read)
                         if (!ok) break;
                     }
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     if (ok) {
                         mma_commit_pair(&sh.acc_full[b], (uint16_t)0x3);
                     } else {  // release both epilogues at once
@@ -451,7 +451,6 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                         mbar_arrive_cluster(mapa_shared(smem_u32(&sh.acc_full[b]), 1));
                     }
                 }
-                ok = __shfl_sync(kAll, ok, 0);
             }
             if (lane == 0) sh.consumed = it;
         }

@@ -27,6 +27,13 @@ __device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // Sixteen bytes to shared memory, asynchronously: those from `bytes` (0 or 16) on are zero and not read.
 __device__ __forceinline__ void cp_async_16(uint32_t to, const void *from, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -47,6 +54,21 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)6 << 61;
+}
+
+// As mma_bf16_pair, the operands given by the low words of their descriptors (smem_desc_sw128's high word is a constant),
+// so that a step along K is one 32-bit addition.
+__device__ __forceinline__ void mma_bf16_pair_sw128(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                                    uint32_t accumulate) {
+    constexpr uint32_t kHigh = (uint32_t)((1024 >> 4) | 1 << 14 | 2u << 29);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(kHigh)
+        : "memory");
 }
 
 // As mma_bf16_pair, adding to D in the lanes (rows) alone whose bit of `off` is clear: words 0-3 the even CTA's, 4-7 the odd's.
