@@ -277,8 +277,9 @@ namespace {
 // How a linear with adapters is done, by sizes alone, and the parts of its workspace.
 //   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, while that is little;
 //     else rows in adapter order on tensor cores.
-//   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows, where they fill half of the
-//     SMs at least; else the dense linear's own kernels (which split K) into fp32, and the adapters' share after it.
+//   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows; for few rows the dense
+//     linear's own kernels, which split K, into fp32 and the adapters' share after it (61 x 2112 x 7168 with rank 32: 20 us,
+//     38 fused; 281 x 322 x 2880: 42 and 20).
 struct LoraWay {
     bool cores, fused;
     size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product
@@ -287,7 +288,7 @@ LoraWay lora_way(int M, int N, int K, int R, int L) {
     const uint64_t m = (uint64_t)M, r = (uint64_t)R;
     LoraWay w;
     w.cores = m * r * (uint64_t)K * 2 <= 64ull << 20;
-    w.fused = M > 64 && (m + 255) / 256 * (((uint64_t)N + 127) / 128) >= kGb300Sms / 4;
+    w.fused = M > 64;
     w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
     w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(M, K, R) : 1) * 4 * m * r);
     w.y = w.fused ? 0 : up256(4 * m * (size_t)N);

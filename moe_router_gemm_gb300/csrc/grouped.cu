@@ -8,7 +8,7 @@
 //
 //   * every CTA turns the offsets into the first tile of each group (a scan in shared memory) and each role finds a tile's
 //     group by bisection;
-//   * warp 0: TMA producer, all its lanes: 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
+//   * warp 0: TMA producer: two chunks of 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
 //     group's weight is zero, not the next group's) and of its half of the tile's rows of x, by boxes of 16 to 128 rows;
 //   * warps 10-13, where `rows` gives the rows of x: 16-byte asynchronous copies from where they are, so that no sorted copy
 //     of x is made; they arrive by themselves on a barrier of the CTA, and warp 14 passes that on to the leader's.  (TMA's gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     if (bad_pair) {
         // nothing issued: fall through to the exit barrier
     } else if (warp == 0) {
-        // ---- TMA producer (both CTAs), the whole warp ----
+        // ---- TMA producer (both CTAs): the whole warp goes through the loop, one elected lane issues ----
         const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0);  // leader's full[0]
         int it = 0;
         Ring r;
@@ -325,32 +325,41 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 }
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
-                if (MODE == kOuter && c >= C) {  // tiles of B
-                    const TailStage g = tail_stage(f, c - C);
-                    const int q = g.q0 + lane;
-                    if (leader && lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * slot_bytes));
-                    if (lane < g.n)
-                        tma_load_4d_pair(st + (lane >> 2) * chunk_bytes + kW + (lane & 3) * slot_bytes, &tm_b, fb,
-                                         g.kb * kChunkK + q % g.per * kRank, n0, 0, sh.count[f.first + q / g.per]);
-                    continue;
-                }
-                if (leader && lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[s], (uint32_t)kChunks * (2u * w_chunk + (GATHER ? 0u : (uint32_t)(t.cols * kChunkK * 2))));
-                // eight lanes a chunk: the first (with four boxes, the first four) bring W ...
-                const int i = lane & 7, k0 = (c * kChunks + (lane >> 3)) * kChunkK;
-                uint8_t *ch = st + (lane >> 3) * chunk_bytes;
-                if (lane >> 3 < kChunks) {
-                    if (!SWIGLU) {
-                        if (i == 0) tma_load_4d_pair(ch + kW, &tm_w, fb, k0, n0, 0, t.e);
-                    } else if (w_boxes == 1) {
-                        if (i == 0) tma_load_5d_pair(ch, &tm_w, fb, k0, 0, 0, n0 >> 4, t.e);
-                    } else if (i < 4) {
-                        tma_load_4d_pair(ch + i * (kWBytes / 4), &tm_w, fb, k0, n0 + 16 * i, 0, t.e);
-                    }
-                    // ... and 4 to 7 this CTA's rows, a multiple of 16, by boxes of falling sizes: lane i takes 1 << i
-                    if (!GATHER && i >= 4 && (half & (1 << i))) {
-                        const int first = half & ~((2 << i) - 1);
-                        tma_load_2d_pair(ch + kX + first * 128, &tm_x.of[i - 4], fb, k0, q0 + first);
+                if (elect_one()) {
+                    if (MODE == kOuter && c >= C) {  // tiles of B
+                        const TailStage g = tail_stage(f, c - C);
+                        if (leader) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * slot_bytes));
+                        int i = f.first + g.q0 / g.per, b16 = g.q0 % g.per;
+                        for (int j = 0; j < g.n; ++j) {
+                            tma_load_4d_pair(st + (j >> 2) * chunk_bytes + kW + (j & 3) * slot_bytes, &tm_b, fb,
+                                             g.kb * kChunkK + b16 * kRank, n0, 0, sh.count[i]);
+                            if (++b16 == g.per) b16 = 0, ++i;
+                        }
+                    } else {
+                        if (leader)
+                            mbar_arrive_expect_tx(&sh.full[s], (uint32_t)kChunks *
+                                                                   (2u * w_chunk + (GATHER ? 0u : (uint32_t)(t.cols * kChunkK * 2))));
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            const int k0 = (c * kChunks + j) * kChunkK;
+                            uint8_t *ch = st + j * chunk_bytes;
+                            if (!SWIGLU) {
+                                tma_load_4d_pair(ch + kW, &tm_w, fb, k0, n0, 0, t.e);
+                            } else if (w_boxes == 1) {
+                                tma_load_5d_pair(ch, &tm_w, fb, k0, 0, 0, n0 >> 4, t.e);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    tma_load_4d_pair(ch + i * (kWBytes / 4), &tm_w, fb, k0, n0 + 16 * i, 0, t.e);
+                            }
+                            // this CTA's rows, a multiple of 16, by boxes of falling sizes
+#pragma unroll
+                            for (int i = 3; i >= 0; --i)
+                                if (!GATHER && (half & (16 << i))) {
+                                    const int first = half & ~((32 << i) - 1);
+                                    tma_load_2d_pair(ch + kX + first * 128, &tm_x.of[i], fb, k0, q0 + first);
+                                }
+                        }
                     }
                 }
             }
