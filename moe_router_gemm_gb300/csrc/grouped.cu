@@ -84,7 +84,7 @@ __device__ __forceinline__ int quotient(long long a, int b) {
 template <bool ONE>
 __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int n, int bt, long long u, int m_tiles) {
     int lo = 0, hi = ONE ? 1 : n;  // tiles[lo] <= q < tiles[hi]
-    const int q = quotient(u, m_tiles);
+    const int q = m_tiles == 1 ? (int)u : quotient(u, m_tiles);
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sh.tiles[mid] <= q)
@@ -95,8 +95,8 @@ __device__ __forceinline__ Unit unit_of(const GroupedShared &sh, int n, int bt, 
     const int before = ONE ? 0 : sh.tiles[lo];
     const int nt = ONE ? (n + bt - 1) / bt : sh.tiles[lo + 1] - before, count = ONE ? n : sh.count[lo];
     const long long local = u - (long long)before * m_tiles;
-    const int m = quotient(local, nt), t = (int)(local - (long long)m * nt);
-    const int each = count / nt, more = count - each * nt;
+    const int m = nt == 1 ? (int)local : quotient(local, nt), t = (int)(local - (long long)m * nt);
+    const int each = nt == 1 ? count : count / nt, more = count - each * nt;
     Unit r;
     r.e = lo;
     r.m = m;
@@ -621,7 +621,9 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                 }
             }
-            for (int c0 = 16 * h; MODE != kOuter && have && c0 < t.rows; c0 += 32) {
+            // (a warp whose outputs all lie past N has nothing to do)
+            const bool any = __any_sync(kAll, n < a.N);
+            for (int c0 = 16 * h; MODE != kOuter && have && any && c0 < t.rows; c0 += 32) {
                 uint32_t r[16];
                 tmem_ld16(acc + (uint32_t)c0, r);
                 tmem_ld_wait16(r);
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     for (int i = 0; i < 8; ++i) {
                         const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 16);
                         const float g = up ? got : v[2 * i], w = up ? v[2 * i + 1] : got;
-                        f[i] = g / (1.0f + expf(-g)) * w;
+                        f[i] = silu(g) * w;
                     }
                     o += up ? a.N : 0;
                     if (pairs) {  // two outputs a store: even lanes take f[i] of their neighbour's output too, odd ones f[i + 1]

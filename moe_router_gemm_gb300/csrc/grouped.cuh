@@ -83,6 +83,20 @@ __device__ __forceinline__ void mma_bf16_pair_lanes(uint32_t d_tmem, uint64_t ad
         : "memory");
 }
 
+// g / (1 + exp(-g)), to a few units in the last place: exp(-g) = 2^t (1 + r ln 2) with t + r = -g log2(e), t rounded and r
+// what the rounding left and the part of log2(e) past 24 bits; a reciprocal and a product for the quotient.  Past 2^126 the
+// reciprocal of 1 + exp(-g) is 0 (the quotient is then below 2^-119).
+__device__ __forceinline__ float silu(float g) {
+    constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float t = -g * kLog2e;
+    const float r = fmaf(-g, kLog2e, -t) - g * kLog2eLow;
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    if (fabsf(t) < 126.0f) e = fmaf(e * r, kLn2, e);  // (2^t finite and not 0, r small)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    return g * q;
+}
+
 // v as the sum of two bf16 values, each the nearest to what is left: off by at most 2^-18 of it.  What is not finite stays
 // alone in the first.
 __device__ __forceinline__ void two_bf16(float v, uint32_t &high, uint32_t &low) {
