@@ -2,8 +2,9 @@
 // with their weights.
 //
 // Grouping is a stable counting sort of n small keys.  Each warp has a run of consecutive keys and a histogram of its own
-// in shared memory; equal keys of a step of 32 find one another with match.any, so that a histogram has one writer and
-// positions do not depend on timing.  The positions then follow from three sums: over the warps of a CTA, over the CTAs of
+// in shared memory; equal keys of a step of 32 find one another by ballots over the key's bits (match.any goes through the
+// different keys one by one: 8192 x 8 keys of 256 groups 10.8 us), so that a histogram has one writer and positions do not
+// depend on timing.  The positions then follow from three sums: over the warps of a CTA, over the CTAs of
 // the one cluster (through distributed shared memory), over the groups.
 #include <cuda_runtime.h>
 
@@ -25,6 +26,8 @@ struct GroupArgs {
     int n, k, groups;
     int cols;  // groups, and one more where what belongs to none is ordered behind them
     int per;   // keys of a warp, a multiple of 32
+    int bits;  // of a key, and of one more than the last
+    int shift;  // log2 of k where k is a power of two, else -1
 };
 
 // Shared memory: the warps' histograms, the CTA's counts, the first position of each group's rows from this CTA.
@@ -52,7 +55,11 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
 
     // A step's key, and its place among the warp's of its group.
     auto count_step = [&](int key) {
-        const unsigned same = __match_any_sync(kAll, key);
+        unsigned same = kAll;  // the lanes that have this key: bit by bit (no key: all bits of the width set, and past the last)
+        for (int b = 0; b < a.bits; ++b) {
+            const unsigned ones = __ballot_sync(kAll, (key >> b) & 1);
+            same &= (key >> b) & 1 ? ones : ~ones;
+        }
         const int at = key >= 0 ? mine[key] + __popc(same & ((1u << lane) - 1u)) : 0;
         __syncwarp();
         if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
@@ -71,31 +78,42 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     __syncthreads();
     for (int e = tid; e < a.cols; e += kThreads) {
         int sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < kWarps; ++w) {
-            const int c = sm[w * a.cols + e];
-            sm[w * a.cols + e] = sum;
-            sum += c;
+        for (int w0 = 0; w0 < kWarps; w0 += 8) {
+            int c[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) c[w] = sm[(w0 + w) * a.cols + e];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                sm[(w0 + w) * a.cols + e] = sum;
+                sum += c[w];
+            }
         }
         count[e] = sum;
     }
     cluster_sync();
 
     // groups up to 1024: one a thread
-    auto counts = [&](int e, int &all, int &before) {
-        for (int c = 0; c < ctas; ++c) {
-            int v;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                         : "=r"(v)
-                         : "r"(mapa_shared(smem_u32(count + e), (uint32_t)c))
-                         : "memory");
-            all += v;
-            before += c < rank ? v : 0;
-        }
-    };
-    int all = 0, before = 0, none = 0, none_before = 0;
-    if (tid < a.groups) counts(tid, all, before);
-    if (tid == 0 && a.cols > a.groups) counts(a.groups, none, none_before);
+    int all = 0, before = 0, none_before = 0;
+    if (ctas == 1) {
+        if (tid < a.groups) all = count[tid];
+    } else {
+        auto counts = [&](int e, int &sum, int &earlier) {  // (all of a cluster's reads on their way together)
+            int v[kCluster];
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c)
+                asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                             : "=r"(v[c])
+                             : "r"(mapa_shared(smem_u32(count + e), (uint32_t)c)));
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c) {
+                sum += v[c];
+                earlier += c < rank ? v[c] : 0;
+            }
+        };
+        int none = 0;
+        if (tid < a.groups) counts(tid, all, before);
+        if (tid == 0 && a.cols > a.groups) counts(a.groups, none, none_before);
+    }
     int upto = all;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -104,9 +122,14 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     }
     if (lane == 31) part[warp] = upto;
     cluster_sync();  // (and no CTA leaves while another reads its counts)
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += part[w];
-    upto += base;
+    int sums = part[lane];  // over the warps up to lane
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(kAll, sums, d);
+        if (lane >= d) sums += v;
+    }
+    const int kept = __shfl_sync(kAll, sums, 31), base = __shfl_sync(kAll, sums, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) upto += base;
     if (tid < a.groups) {
         start[tid] = upto - all + before;
         if (rank == 0) {
@@ -114,8 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
             a.offsets[tid + 1] = upto;
         }
     }
-    int kept = 0;
-    for (int w = 0; w < kWarps; ++w) kept += part[w];
     if (tid == 0 && a.cols > a.groups) start[a.groups] = kept + none_before;
     __syncthreads();
 
@@ -123,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
     auto put = [&](int i, int key, int at) {
         if (i >= hi) return;
         if (a.place) a.place[i] = at;
-        if (key >= 0) a.rows[at] = a.k == 1 ? i : i / a.k;
+        if (key >= 0) a.rows[at] = a.shift >= 0 ? i >> a.shift : i / a.k;
     };
     if (kept_all) {
 #pragma unroll
@@ -163,7 +184,8 @@ constexpr int kCombineThreads = 128, kAtOnce = 8;
 // out[t] = sum over j of weights[t][j] * y[place[t][j]] (+ addend[t]), one vector of BYTES a thread, in fp32, in the order
 // of j, rounded once.  kAtOnce rows' loads go out before the first is used: 8192 x 8 x 7168 with an addend 275 us with one
 // after the other.
-template <int BYTES>
+// PER vectors a thread, kCombineThreads apart, where they are narrow (odd H).
+template <int BYTES, int PER>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict__ place, const float *__restrict__ weights,
                    const uint16_t *__restrict__ addend, uint16_t *__restrict__ out, int blocks_per_row, int k,
@@ -177,15 +199,18 @@ __global__ void __launch_bounds__(kCombineThreads)
     pdl_launch_dependents();
     pdl_wait();
     const long long t = blockIdx.x / blocks_per_row;
-    const int c = ((int)(blockIdx.x - t * blocks_per_row) * kCombineThreads + (int)threadIdx.x) * n;
-    if (c >= H) return;
-    U last;
-    if (addend) last.v = __ldg(reinterpret_cast<const V *>(addend + t * H + c));
-    float sum[n];
+    const int c0 = ((int)(blockIdx.x - t * blocks_per_row) * kCombineThreads * PER + (int)threadIdx.x) * n;
+    U last[PER];
+    float sum[PER][n];
 #pragma unroll
-    for (int i = 0; i < n; ++i) sum[i] = 0.0f;
+    for (int q = 0; q < PER; ++q) {
+        const int c = c0 + q * kCombineThreads * n;
+        if (addend && c < H) last[q].v = __ldg(reinterpret_cast<const V *>(addend + t * H + c));
+#pragma unroll
+        for (int i = 0; i < n; ++i) sum[q][i] = 0.0f;
+    }
     for (int j0 = 0; j0 < k; j0 += kAtOnce) {
-        U u[kAtOnce];
+        U u[kAtOnce][PER];
         float w[kAtOnce];
         bool in[kAtOnce];
 #pragma unroll
@@ -193,7 +218,11 @@ __global__ void __launch_bounds__(kCombineThreads)
             const long long p = j0 + j < k ? __ldg(place + t * k + j0 + j) : -1;
             in[j] = p >= 0 && p < y_rows;
             if (in[j]) {
-                u[j].v = __ldg(reinterpret_cast<const V *>(y + p * H + c));
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const int c = c0 + q * kCombineThreads * n;
+                    if (c < H) u[j][q].v = __ldg(reinterpret_cast<const V *>(y + p * H + c));
+                }
                 w[j] = weights ? __ldg(weights + t * k + j0 + j) : 1.0f;
             }
         }
@@ -201,19 +230,26 @@ __global__ void __launch_bounds__(kCombineThreads)
         for (int j = 0; j < kAtOnce; ++j)
             if (in[j]) {
 #pragma unroll
-                for (int i = 0; i < n; ++i) sum[i] = fmaf(w[j], bf16_to_f32(u[j].h[i]), sum[i]);
+                for (int q = 0; q < PER; ++q)
+#pragma unroll
+                    for (int i = 0; i < n; ++i) sum[q][i] = fmaf(w[j], bf16_to_f32(u[j][q].h[i]), sum[q][i]);
             }
     }
-    U r;
 #pragma unroll
-    for (int i = 0; i < n; ++i) r.h[i] = f32_to_bf16(addend ? sum[i] + bf16_to_f32(last.h[i]) : sum[i]);
-    *reinterpret_cast<V *>(out + t * H + c) = r.v;
+    for (int q = 0; q < PER; ++q) {
+        const int c = c0 + q * kCombineThreads * n;
+        U r;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            r.h[i] = f32_to_bf16(addend ? sum[q][i] + bf16_to_f32(last[q].h[i]) : sum[q][i]);
+        if (c < H) *reinterpret_cast<V *>(out + t * H + c) = r.v;
+    }
 }
 
-template <int BYTES>
+template <int BYTES, int PER>
 int launch_combine(const void *y, long long y_rows, const int32_t *place, const float *weights, const void *addend,
                    void *out, long long tokens, int k, int H, uint32_t flags, void *stream) {
-    const int per_row = H / (BYTES / 2), blocks_per_row = (per_row + kCombineThreads - 1) / kCombineThreads;
+    const int per_block = kCombineThreads * PER, blocks_per_row = (H / (BYTES / 2) + per_block - 1) / per_block;
     const long long most = 0x7FFFFFFFll / blocks_per_row;  // tokens of a launch
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kCombineThreads);
@@ -227,7 +263,7 @@ int launch_combine(const void *y, long long y_rows, const int32_t *place, const 
         const long long now = tokens - t < most ? tokens - t : most;
         cfg.gridDim = dim3((unsigned)(now * blocks_per_row));
         const int r = (int)cudaLaunchKernelEx(
-            &cfg, combine_kernel<BYTES>, static_cast<const uint16_t *>(y), place + t * k, weights ? weights + t * k : nullptr,
+            &cfg, combine_kernel<BYTES, PER>, static_cast<const uint16_t *>(y), place + t * k, weights ? weights + t * k : nullptr,
             addend ? static_cast<const uint16_t *>(addend) + t * H : nullptr, static_cast<uint16_t *>(out) + t * H,
             blocks_per_row, k, y_rows, H);
         if (r) return r;
@@ -245,9 +281,12 @@ int init_group() {
 
 int launch_group_rows(const int32_t *ids, int n, int k, int groups, bool rest, int32_t *offsets, int32_t *rows,
                       int32_t *place, uint32_t flags, void *stream) {
-    const int ctas = n <= 4 * kThreads ? 1 : kCluster;
+    const int ctas = n <= kThreads ? 1 : kCluster;  // (a CTA takes a step of all its warps: 512 x 8 keys 9.8 us in one, 5.5 in 16)
     const int warps = ctas * kWarps;
-    GroupArgs a = {ids, offsets, rows, place, n, k, groups, groups + (rest ? 1 : 0), 0};
+    GroupArgs a = {ids, offsets, rows, place, n, k, groups, groups + (rest ? 1 : 0), 0, 1, -1};
+    for (int s = 0; s < 31; ++s)
+        if (k == 1 << s) a.shift = s;
+    while ((1 << a.bits) <= a.cols) ++a.bits;  // (-1 then differs from every key)
     a.per = (int)(((long long)n + warps - 1) / warps + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -269,8 +308,8 @@ int launch_group_rows(const int32_t *ids, int n, int k, int groups, bool rest, i
 int launch_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
                         void *out, int64_t tokens, int k, int H, uint32_t flags, void *stream) {
     // rows of H elements: the widest vectors that every row of all three starts on
-    const auto f = H % 8 == 0 ? launch_combine<16> : H % 4 == 0 ? launch_combine<8>
-                   : H % 2 == 0 ? launch_combine<4> : launch_combine<2>;
+    const auto f = H % 8 == 0 ? launch_combine<16, 1> : H % 4 == 0 ? launch_combine<8, 2>
+                   : H % 2 == 0 ? launch_combine<4, 4> : launch_combine<2, 4>;
     return f(y, y_rows, place, weights, addend, out, tokens, k, H, flags, stream);
 }
 
