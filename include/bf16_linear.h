@@ -639,7 +639,10 @@ size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
  * K % 8 == 0, groups <= 1024, N and K <= 2^24 (else BF16L_EUNSUPPORTED).  A group's
  * rows give the same bits whatever the other groups hold.  Pointers of bf16 data
  * 16-byte aligned.  BF16L_FLAG_PDL has no effect: which weights are read follows from
- * the offsets.  Launches one kernel.
+ * the offsets.  Few tiles' K is split and summed through `workspace` (256-byte aligned,
+ * needs no initialisation; one call at a time): bf16_linear_grouped_workspace(P, groups,
+ * N, K, swiglu) bytes, 0 where it is not (then it may be NULL); a smaller one is
+ * BF16L_EINVAL.  Launches one kernel, or two.
  *
  * bf16_combine_rows — out[t] = RNE_bf16( sum over j of weights[t][j] *
  *   y[place[t][j]] (+ addend[t]) ), in fp32, in the order of j, the addend last.
@@ -663,7 +666,8 @@ int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int groups, int32
                     int32_t *place, uint32_t flags, bf16l_stream_t stream);
 int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
                         const int32_t *rows, void *out, int64_t P, int groups, int N, int K, int swiglu,
-                        uint32_t flags, bf16l_stream_t stream);
+                        void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream);
+size_t bf16_linear_grouped_workspace(int64_t P, int groups, int N, int K, int swiglu);
 int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *place, const float *weights, const void *addend,
                       void *out, int64_t tokens, int k, int H, uint32_t flags, bf16l_stream_t stream);
 int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b, const float *scale,

@@ -14,7 +14,7 @@ from ._binding import (BF16LinearError, Call, Device, KERNEL_DOTPROD, KERNEL_NAM
                        KERNEL_TILE, LIB_PATH, FLAG_PDL, FLAG_SERIAL, Plan, bf16_linear, bf16_linear_ex, bf16_linear_f32out,
                        bf16_linear_noalloc, bf16_linear_fp8, quant_fp8, fp8_split, quant_mxfp8, bf16_linear_mxfp8,
                        mxfp8_split, Norm, rmsnorm, route, quant_mxfp4, dequant_mxfp4, bf16_linear_mxfp4,
-                       bf16_linear_mxfp4_dynamic, mxfp4_dynamic_workspace, Groups, group_rows, bf16_linear_grouped, combine_rows,
+                       bf16_linear_mxfp4_dynamic, mxfp4_dynamic_workspace, Groups, group_rows, bf16_linear_grouped, grouped_workspace, combine_rows,
                        bf16_linear_lora, lora_workspace, bf16_linear_host,
                        host_staging_bytes, new_host_staging,
                        bf16_linear_with_plan, device_status,

@@ -85,7 +85,8 @@ def _load_calls(lib):
     mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.bf16_rmsnorm, lib.bf16_route, lib.bf16_quant_mxfp4, lib.bf16_dequant_mxfp4, lib.bf16_linear_mxfp4,
         lib.bf16_linear_mxfp4_dynamic, lib.bf16_linear_mxfp4_dynamic_workspace, lib.bf16_group_rows,
-        lib.bf16_linear_grouped, lib.bf16_combine_rows, lib.bf16_linear_lora, lib.bf16_linear_lora_workspace)))
+        lib.bf16_linear_grouped, lib.bf16_combine_rows, lib.bf16_linear_lora, lib.bf16_linear_lora_workspace,
+        lib.bf16_linear_grouped_workspace)))
     return mod
 
 
@@ -165,8 +166,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.bf16_linear_mxfp4_dynamic_workspace.restype = ctypes.c_size_t
         lib.bf16_group_rows.argtypes = [vp, i64, i32, i32, vp, vp, vp, u32, vp]
         lib.bf16_group_rows.restype = i32
-        lib.bf16_linear_grouped.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, u32, vp]
+        lib.bf16_linear_grouped.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, ctypes.c_size_t, u32, vp]
         lib.bf16_linear_grouped.restype = i32
+        lib.bf16_linear_grouped_workspace.argtypes = [i64, i32, i32, i32, i32]
+        lib.bf16_linear_grouped_workspace.restype = ctypes.c_size_t
         lib.bf16_combine_rows.argtypes = [vp, i64, vp, vp, vp, vp, i64, i32, i32, u32, vp]
         lib.bf16_combine_rows.restype = i32
         lib.bf16_linear_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, ctypes.c_size_t, u32, vp]
@@ -869,12 +872,20 @@ def group_rows(ids, groups: int, *, offsets=None, rows=None, place=None, flags: 
     return Groups(offsets, rows, place)
 
 
-def bf16_linear_grouped(x, w, offsets, bias=None, *, rows=None, swiglu: bool = False, out=None, flags: int = 0, stream=None):
+def grouped_workspace(P: int, groups: int, N: int, K: int, swiglu: bool = False) -> int:
+    """Workspace bytes of bf16_linear_grouped for P rows of out (0 where it needs none, and for sizes that it refuses)."""
+    return int(load().bf16_linear_grouped_workspace(P, groups, N, K, bool(swiglu))) if max(P, groups, N, K) < 1 << 31 else 0
+
+
+def bf16_linear_grouped(x, w, offsets, bias=None, *, rows=None, swiglu: bool = False, out=None, workspace=None, flags: int = 0,
+                        stream=None):
     """A linear for each group's rows (bf16_linear_grouped): out[p] = x[p] @ w[e]^T (+ bias[e]) for the positions p from
     offsets[e] to offsets[e + 1], x[rows[p]] where rows (int32) is given.  x[x_rows, K], w[groups, N, K], bias[groups, N] bf16,
     offsets int32 [groups + 1]; out bf16 [len(rows) or x_rows, N], in which rows of no group are not written.  swiglu: w and
-    bias hold N gate rows and N up rows a group, out = silu(gate) * up."""
-    if out is stream is None and _calls is not None:
+    bias hold N gate rows and N up rows a group, out = silu(gate) * up.  `workspace`: a contiguous CUDA tensor of at least
+    grouped_workspace(rows of out, groups, N, K, swiglu) bytes to reuse from call to call on one stream; allocated for the
+    call when None."""
+    if out is workspace is stream is None and _calls is not None:
         r = _calls.linear_grouped(x, w, offsets, bias, rows, swiglu, flags)
         if type(r) is int:
             _raise(r, f"bf16_linear_grouped(x{tuple(x.shape)}, w{tuple(w.shape)}, swiglu={bool(swiglu)})")
@@ -896,8 +907,19 @@ def bf16_linear_grouped(x, w, offsets, bias=None, *, rows=None, swiglu: bool = F
     _fits("bf16_linear_grouped", flags, G, W, K)
     if out is None:
         out = _empty((P, N), bf16, dev, stream)
-    st = _call(load().bf16_linear_grouped, dev, stream, a, xr, b, e, c, d, _need(out, "out", bf16, (P, N), dev), P, G, N, K,
-               bool(swiglu), flags)
+    lib = load()
+    wp, wn = None, 0
+    if workspace is None:
+        wn = lib.bf16_linear_grouped_workspace(P, G, N, K, bool(swiglu))
+        if wn:
+            workspace = _empty((wn,), torch.uint8, dev, stream)
+            wp = workspace.data_ptr()
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on x's device")
+    else:
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _call(lib.bf16_linear_grouped, dev, stream, a, xr, b, e, c, d, _need(out, "out", bf16, (P, N), dev), P, G, N, K,
+               bool(swiglu), wp, wn, flags)
     if st != OK:
         _raise(st, f"bf16_linear_grouped(x{tuple(x.shape)}, w{tuple(w.shape)}, swiglu={bool(swiglu)})")
     return out

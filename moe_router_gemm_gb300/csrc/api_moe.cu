@@ -229,9 +229,16 @@ extern "C" int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int gr
     return result(launch_group_rows(ids, (int)n, k, groups, false, offsets, rows, place, flags, stream));
 }
 
+extern "C" size_t bf16_linear_grouped_workspace(int64_t P, int groups, int N, int K, int swiglu) {
+    if (P <= 0 || P > kMaxRows || groups <= 0 || groups > kMaxGroups || N <= 0 || K <= 0 || N > kMaxWidth || K > kMaxWidth)
+        return 0;
+    const int s = grouped_splits((int)P, groups, N, K, swiglu);
+    return s > 1 ? up256(4 * (size_t)s * (size_t)P * (size_t)N * (swiglu ? 2 : 1)) : 0;
+}
+
 extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
                                    const int32_t *rows, void *out, int64_t P, int groups, int N, int K, int swiglu,
-                                   uint32_t flags, bf16l_stream_t stream) {
+                                   void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream) {
     if (P < 0 || x_rows < 0 || groups <= 0 || N <= 0 || K <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
     if (K % 8 != 0 || groups > kMaxGroups || N > kMaxWidth || K > kMaxWidth) return BF16L_EUNSUPPORTED;
     if (P > kMaxRows || x_rows > kMaxRows) return BF16L_EINVAL;
@@ -241,7 +248,10 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     if (off(x, 16) || off(w, 16) || off(bias, 16) || off(out, 16) || off(offsets, 4) || off(rows, 4)) return BF16L_EALIGN;
     const uint64_t k = (uint64_t)K, wide = (uint64_t)N * (swiglu ? 2 : 1), g = (uint64_t)groups;
     if ((uint64_t)P * wide > kMaxElements || g * wide > kMaxElements / k) return BF16L_EINVAL;
-    const Span outs[1] = {{out, 2ull * (uint64_t)P * (uint64_t)N}};
+    const size_t need = bf16_linear_grouped_workspace(P, groups, N, K, swiglu);
+    if (off(workspace, 256)) return BF16L_EALIGN;
+    if (need && (!workspace || workspace_bytes < need)) return BF16L_EINVAL;
+    const Span outs[2] = {{out, 2ull * (uint64_t)P * (uint64_t)N}, {workspace, need}};
     const Span ins[5] = {{x, 2ull * (uint64_t)x_rows * k}, {w, 2 * g * wide * k}, {bias, 2 * g * wide},
                          {offsets, 4 * (g + 1)}, {rows, 4ull * (uint64_t)P}};
     if (clash(outs, ins)) return BF16L_EINVAL;
@@ -249,7 +259,8 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     int32_t *status = nullptr;
     const int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, nullptr, 0};
+    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, nullptr, 0,
+                           static_cast<float *>(workspace), need ? grouped_splits((int)P, groups, N, K, swiglu) : 1};
     return result(launch_grouped(a, dev.num_sms, flags, stream, status));
 }
 
@@ -282,7 +293,7 @@ namespace {
 //     38 fused; 281 x 322 x 2880: 42 and 20).
 struct LoraWay {
     bool cores, fused;
-    size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product
+    size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product or its parts
 };
 LoraWay lora_way(int M, int N, int K, int R, int L) {
     const uint64_t m = (uint64_t)M, r = (uint64_t)R;
@@ -291,7 +302,8 @@ LoraWay lora_way(int M, int N, int K, int R, int L) {
     w.fused = M > 64;
     w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
     w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(M, K, R) : 1) * 4 * m * r);
-    w.y = w.fused ? 0 : up256(4 * m * (size_t)N);
+    const int parts = w.fused ? lora_outer_splits(M, N, K) : 1;
+    w.y = w.fused && parts == 1 ? 0 : up256((size_t)parts * 4 * m * (size_t)N);
     return w;
 }
 
@@ -368,7 +380,7 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + up256(4 * ((size_t)L + 1)));
     float *y = reinterpret_cast<float *>(p + way.order + way.h);
     const LoraArgs args = {x, a, b, scale, ids, p + way.order, y, out, M, N, K, R, L,
-                           way.cores && !way.fused ? lora_splits(M, K, R) : 0};
+                           way.cores && !way.fused ? lora_splits(M, K, R) : 0, y};
     if (way.order) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
     if (st == BF16L_OK)
         st = result(way.cores ? launch_lora_inner(args, flags, stream)

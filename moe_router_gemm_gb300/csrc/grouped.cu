@@ -25,6 +25,8 @@
 //     swizzle) against the rows' h, its MMAs writing the TMEM lanes of that adapter's rows alone (the MMA's lane mask), so
 //     that nothing of one adapter, not finite or not, reaches a row of another.  A row of out is written where its row of
 //     x is.
+// Where the tiles are too few for the SMs (PARTIAL), each tile's K is split into parts of their own tiles, which leave their
+// fp32 accumulators in a workspace, and sum_kernel adds them up in order.
 // Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any remote arrival or copy) and one
 // before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>
@@ -75,6 +77,7 @@ struct GroupedShared {
 struct Unit {
     int e, p0, rows, m;  // group, first position, rows, W tile
     int cols;            // rows rounded up for the MMA
+    int part, c0, n;     // PARTIAL: which part of K; its first stage, and its stages
 };
 // a / b of what nearly always fits 32 bits (a 64-bit division is a long routine, and the first load waits for this one).
 __device__ __forceinline__ int quotient(long long a, int b) {
@@ -164,7 +167,7 @@ struct RowMaps {
     CUtensorMap of[4];
 };
 
-template <int MODE, bool GATHER>
+template <int MODE, bool GATHER, bool PARTIAL>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ RowMaps tm_x, const GroupedArgs a,
@@ -296,10 +299,18 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
     __syncthreads();
     const bool bad_pair = sh.bad_pair != 0;  // the same verdict in both CTAs
     const int adapters = MODE == kOuter ? sh.tiles[0] : 0;
-    const long long units = (long long)(MODE == kOuter ? (a.P + bt - 1) / bt : sh.tiles[a.groups]) * m_tiles;
-    auto unit = [&](long long u) { return unit_of<MODE == kOuter>(sh, MODE == kOuter ? a.P : a.groups, bt, u, m_tiles); };
-    auto tail = [&](const Unit &t) {
-        return MODE == kOuter ? tail_of(sh, adapters, t, a.R) : Tail{0, 0, 0};
+    const long long units = (long long)(MODE == kOuter ? (a.P + bt - 1) / bt : sh.tiles[a.groups]) * m_tiles *
+                            (PARTIAL ? a.splits : 1);
+    auto unit = [&](long long u) {
+        const int s = PARTIAL ? (int)(u % a.splits) : 0;
+        Unit t = unit_of<MODE == kOuter>(sh, MODE == kOuter ? a.P : a.groups, bt, PARTIAL ? u / a.splits : u, m_tiles);
+        t.part = s;
+        t.c0 = PARTIAL ? C * s / a.splits : 0;
+        t.n = PARTIAL ? C * (s + 1) / a.splits - t.c0 : C;
+        return t;
+    };
+    auto tail = [&](const Unit &t) {  // (with the last part of K)
+        return MODE == kOuter && (!PARTIAL || t.part == a.splits - 1) ? tail_of(sh, adapters, t, a.R) : Tail{0, 0, 0};
     };
 
     if (bad_pair) {
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
             const int n0 = t.m * wt + (int)rank * (wt / 2);
             const Tail f = tail(t);
-            for (int c = 0, n = C + f.stages(); c < n; ++c, ++it, r.next(stages)) {
+            for (int c = 0, n = t.n + f.stages(); c < n; ++c, ++it, r.next(stages)) {
                 const int s = r.s;
                 ok = mbar_wait(&sh.empty[s], r.phase ^ 1u, status, kSiteEmpty);  // (at once in the first round)
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -326,8 +337,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint8_t *st = ring + s * stage_bytes;
                 const uint32_t fb = full0 + (uint32_t)(s * sizeof(uint64_t));
                 if (elect_one()) {
-                    if (MODE == kOuter && c >= C) {  // tiles of B
-                        const TailStage g = tail_stage(f, c - C);
+                    if (MODE == kOuter && c >= t.n) {  // tiles of B
+                        const TailStage g = tail_stage(f, c - t.n);
                         if (leader) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(2 * g.n * slot_bytes));
                         int i = f.first + g.q0 / g.per, b16 = g.q0 % g.per;
                         for (int j = 0; j < g.n; ++j) {
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                                                                    (2u * w_chunk + (GATHER ? 0u : (uint32_t)(t.cols * kChunkK * 2))));
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
-                            const int k0 = (c * kChunks + j) * kChunkK;
+                            const int k0 = ((t.c0 + c) * kChunks + j) * kChunkK;
                             uint8_t *ch = st + j * chunk_bytes;
                             if (!SWIGLU) {
                                 tma_load_4d_pair(ch + kW, &tm_w, fb, k0, n0, 0, t.e);
@@ -383,13 +394,13 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 const Unit t = unit(u);
                 const Tail f = tail(t);
                 const uint32_t idesc = idesc_bf16_f32(2 * kHalf, MODE == kOuter ? wt : t.cols);
-                const int b = tile & 1, n = C + f.stages();
+                const int b = tile & 1, n = t.n + f.stages();
                 const uint32_t acc = tmem + (uint32_t)(b * bt);
                 if (lane == 0) sh.consumed = it;
                 // Both CTAs' epilogues have read this buffer (used two tiles ago).
                 ok = __all_sync(kAll, tile < 2 || mbar_wait(&sh.acc_empty[b], ((tile >> 1) - 1) & 1, status, kSiteTmemEmpty));
                 tc_fence_after();
-                for (int c = 0; ok && c < C; ++c, ++it, r.next(stages)) {
+                for (int c = 0; ok && c < t.n; ++c, ++it, r.next(stages)) {
                     const int s = r.s;
                     ok = __all_sync(kAll, mbar_wait(&sh.full[s], r.phase, status, kSiteFull));
                     if (!ok) break;
@@ -408,10 +419,10 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                 }
                 if (MODE == kOuter) {
-                    for (int c = C; ok && c < n; ++c, ++it, r.next(stages)) {
+                    for (int c = t.n; ok && c < n; ++c, ++it, r.next(stages)) {
                         // Four lanes a slot: its MMAs' lane mask and its place in h, which one lane would take longer
                         // to work out than the MMAs take.
-                        const TailStage g = tail_stage(f, c - C);
+                        const TailStage g = tail_stage(f, c - t.n);
                         const int q = g.q0 + (lane >> 2), i = f.first + q / g.per, w = 2 * (lane & 3);
                         if ((lane >> 2) < g.n) {
                             const int lo = sh.first[i] - t.p0, hi = min(sh.first[i + 1] - t.p0, t.rows);
@@ -470,7 +481,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             Ring r;
             bool ok = true;
             for (long long u = cl; ok && u < units; u += ncl) {
-                const int n = MODE == kOuter ? C + tail(unit(u)).stages() : C;
+                const Unit t = unit(u);
+                const int n = t.n + tail(t).stages();
                 for (int c = 0; ok && c < n; ++c, r.next(stages)) {
                     ok = mbar_wait(&sh.copied[r.s], r.phase, status, kSiteStage);
                     fence_proxy_async_smem();  // the copies, seen here, before the MMAs' reads
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 row[i] = x + (size_t)min(max(__ldg(a.rows + p), 0), a.x_rows - 1) * a.K;
             }
             const Tail f = tail(t);
-            for (int c = 0, n = C + f.stages(); c < n; ++c, r.next(stages)) {
+            for (int c = 0, n = t.n + f.stages(); c < n; ++c, r.next(stages)) {
                 const int s = r.s;
                 ok = mbar_wait(&sh.empty[s], r.phase ^ 1u, status, kSiteEmpty);
                 ok = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -509,9 +521,9 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     break;
                 }
                 const uint32_t to = to0 + (uint32_t)(s * stage_bytes);
-                if (MODE == kOuter && c >= C) {
+                if (MODE == kOuter && c >= t.n) {
                     // The rows' h: values, then remainders.
-                    const int col = tail_stage(f, c - C).kb * kChunkK + 8 * v;
+                    const int col = tail_stage(f, c - t.n).kb * kChunkK + 8 * v;
                     const uint16_t *h = static_cast<const uint16_t *>(a.h);
 #pragma unroll 4
                     for (int i = 0; i < kHalf / kGatherRows; ++i) {
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     continue;
                 }
                 // The copies' own instructions count: four warps issue 16 each a stage, and one address serves all chunks.
-                const int k0 = c * kChunks * kChunkK;
+                const int k0 = (t.c0 + c) * kChunks * kChunkK;
                 if (have == half && k0 + kChunks * kChunkK <= a.K) {
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
@@ -569,7 +581,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const int n = MODE == kInner && in_tile >= wt / 2 ? a.N : t.m * wt + (int)rank * (wt / 2) + in_tile;
             const int wide = SWIGLU ? 2 * a.N : a.N, wrow = SWIGLU && lane >= 16 ? a.N + n : n;
             const float f = MODE == kInner && a.scale ? __ldg(a.scale + t.e) : 1.0f;
-            const float lb = MODE != kOuter && bias && n < a.N ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
+            const float lb = MODE != kOuter && bias && n < a.N && (!PARTIAL || t.part == 0) ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
             const bool ok = mbar_wait(&sh.acc_full[b], (tile >> 1) & 1, status, kSiteAccum);
             tc_fence_after();
             const bool have = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -594,7 +606,20 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                         v[j] = __uint_as_float(r0[j]);
                         v[16 + j] = __uint_as_float(r1[j]);
                     }
-                    if (bias) bias_add32(v, nb);
+                    if (bias && (!PARTIAL || t.part == 0)) bias_add32(v, nb);
+                    if constexpr (PARTIAL) {
+                        float *o = a.sums + ((size_t)t.part * a.P + to) * a.N + n0;
+                        if (lane < left && a.N % 8 == 0 && n0 + 32 <= a.N) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) OutStore<float>::eight(o + j, v + j);
+                        } else if (lane < left) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (n0 + j < a.N) o[j] = v[j];
+                        }
+                        __syncwarp();
+                        continue;
+                    }
                     __syncwarp();  // the piece before has been read
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // 16-byte unit j of the row, at j ^ (row / 2) % 4
@@ -633,7 +658,12 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 // (row of x: c0 + j)
                 uint16_t *o = out + (size_t)(t.p0 + c0) * a.N + n;
                 const int left = t.rows - c0;
-                if constexpr (MODE == kInner) {
+                if constexpr (PARTIAL) {
+                    float *s = a.sums + ((size_t)t.part * a.P + t.p0 + c0) * a.N + n;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n < a.N && j < left) s[(size_t)j * a.N] = v[j];
+                } else if constexpr (MODE == kInner) {
                     uint16_t *h = out + n;
                     const int to = __ldg(a.rows + t.p0 + c0 + min(lane & 15, left - 1));
 #pragma unroll
@@ -731,13 +761,69 @@ static_assert(sizeof(GroupedShared) >= kWBytes / 2, "kInner's MMAs read past the
 
 using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int, int32_t *);
 
-GroupedFn pick(int mode, bool gather) {
+GroupedFn pick(int mode, bool gather, bool partial) {
     switch (mode) {
-        case kInner: return grouped_kernel<kInner, true>;
-        case kOuter: return grouped_kernel<kOuter, true>;
-        case kSwiglu: return gather ? grouped_kernel<kSwiglu, true> : grouped_kernel<kSwiglu, false>;
-        default: return gather ? grouped_kernel<kPlain, true> : grouped_kernel<kPlain, false>;
+        case kInner: return grouped_kernel<kInner, true, false>;
+        case kOuter: return partial ? grouped_kernel<kOuter, true, true> : grouped_kernel<kOuter, true, false>;
+        case kSwiglu: return gather ? grouped_kernel<kSwiglu, true, false> : grouped_kernel<kSwiglu, false, false>;
+        default:
+            if (partial) return gather ? grouped_kernel<kPlain, true, true> : grouped_kernel<kPlain, false, true>;
+            return gather ? grouped_kernel<kPlain, true, false> : grouped_kernel<kPlain, false, false>;
     }
+}
+
+// The parts of K added up, in order: out[p][n] (SwiGLU: of the sums' columns n and N + n), one output a thread.  The rows
+// of no group, before the first and behind the last, stay as they are.
+constexpr int kSumThreads = 256;
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const float *__restrict__ sums, const int32_t *__restrict__ offsets,
+                                                          int groups, int splits, int P, int N, uint16_t *__restrict__ out) {
+    __shared__ int last;
+    pdl_launch_dependents();
+    pdl_wait();
+    int first = 0, end = P;
+    if (offsets) {
+        if (threadIdx.x == 0) last = 0;
+        __syncthreads();
+        int most = 0;
+        for (int e = threadIdx.x; e <= groups; e += kSumThreads) most = max(most, min(max(__ldg(offsets + e), 0), P));
+        most = __reduce_max_sync(kAll, most);
+        if ((threadIdx.x & 31) == 0) atomicMax(&last, most);
+        __syncthreads();
+        first = min(max(__ldg(offsets), 0), P);
+        end = last;
+    }
+    const int wide = SWIGLU ? 2 * N : N;
+    const size_t plane = (size_t)P * wide;
+    for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < (long long)P * N;
+         i += (long long)gridDim.x * kSumThreads) {
+        const int p = (int)(i / N), n = (int)(i - (long long)p * N);
+        if (p < first || p >= end) continue;
+        const float *s = sums + (size_t)p * wide + n;
+        float v = 0.0f, up = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < splits; ++k) {
+            v += s[k * plane];
+            if (SWIGLU) up += s[k * plane + N];
+        }
+        out[i] = f32_to_bf16(SWIGLU ? silu(v) * up : v);
+    }
+}
+
+int launch_sum(bool swiglu, const float *sums, const int32_t *offsets, int groups, int splits, int P, int N, void *out,
+               int num_sms, uint32_t flags, void *stream) {
+    const long long blocks = ((long long)P * N + kSumThreads - 1) / kSumThreads, most = 8ll * num_sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(kSumThreads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, swiglu ? sum_kernel<true> : sum_kernel<false>, sums, offsets, groups, splits, P, N,
+                                   static_cast<uint16_t *>(out));
 }
 
 cudaLaunchConfig_t config(int clusters, bool gather, int smem, uint32_t flags, void *stream, cudaLaunchAttribute *attr) {
@@ -783,12 +869,13 @@ int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int nu
     if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, a.b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
     if (r) return (int)cudaErrorInvalidValue;
     // A cluster that cannot be resident with the others would run its tiles after them.
-    const long long units = ((long long)a.P / bt + full) * ((a.N + wt - 1) / wt);  // at most
+    const long long units = ((long long)a.P / bt + full) * ((a.N + wt - 1) / wt) *
+                            (a.splits > 1 ? a.splits : 1);  // at most
     long long clusters = clusters_of(num_sms);
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(mode, bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr), tw, tb, tx, a, w_boxes, bt, wt,
+    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr, a.splits > 1), tw, tb, tx, a, w_boxes, bt, wt,
                                    stages_of(mode, bt), status);
 }
 
@@ -796,10 +883,12 @@ int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int nu
 
 int init_grouped() {
     for (int mode : {kPlain, kSwiglu, kInner, kOuter})
-        for (bool gather : {false, true}) {
-            const int e = (int)cudaFuncSetAttribute(pick(mode, gather), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-            if (e) return e;
-        }
+        for (bool gather : {false, true})
+            for (bool partial : {false, true}) {
+                const int e = (int)cudaFuncSetAttribute(pick(mode, gather, partial),
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                if (e) return e;
+            }
     int dev = 0;
     const int e = (int)cudaGetDevice(&dev);
     if (e || dev < 0 || dev >= kMaxDevices) return e ? e : (int)cudaErrorInvalidDevice;
@@ -808,7 +897,7 @@ int init_grouped() {
     cfg.numAttrs = 1;
     int n = 0;
     // A failed query only loses the clamp (launches then use half the SMs' number).
-    if (cudaOccupancyMaxActiveClusters(&n, pick(kPlain, true), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, pick(kPlain, true, false), &cfg) != cudaSuccess) {
         n = 0;
         (void)cudaGetLastError();
     }
@@ -816,17 +905,51 @@ int init_grouped() {
     return 0;
 }
 
+namespace {
+
+// Rows of a tile: groups of the average size, and of twice that, fit one.
+int tile_rows(int P, int groups) {
+    const long long twice = 2ll * P / (P < groups ? P : groups);
+    return twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
+}
+
+// Parts of K for `units` tiles: where they leave half of the pairs of SMs without one, as many parts as there are pairs for,
+// at most eight, of four stages at least.
+int parts_of(long long units, int K) {
+    constexpr int pairs = kGb300Sms / 2;
+    if (2 * units > pairs) return 1;
+    const long long stages = K / (kChunkK * kChunks) / 4, s = pairs / units < stages ? pairs / units : stages;
+    return s < 2 ? 1 : s < 8 ? (int)s : 8;
+}
+
+}  // namespace
+
+// (a group of P rows may be one tile more than its share; SwiGLU's wide product is summed as it is)
+int grouped_splits(int P, int groups, int N, int K, int swiglu) {
+    if (P <= 0) return 1;
+    const long long tiles = (long long)P / tile_rows(P, groups) + (P < groups ? P : groups);
+    return parts_of(tiles * (((swiglu ? 2ll : 1ll) * N + 255) / 256), K);
+}
+int lora_outer_splits(int M, int N, int K) {
+    return parts_of(((long long)M + 255) / 256 * (((long long)N + 127) / 128), K);
+}
+
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status) {
-    // Rows of a tile: groups of the average size, and of twice that, fit one.
-    const int full = a.P < a.groups ? a.P : a.groups;
-    const long long twice = 2ll * a.P / full;
-    const int bt = twice <= 32 ? 32 : twice <= 64 ? 64 : twice <= 128 ? 128 : 256;
+    const int full = a.P < a.groups ? a.P : a.groups, bt = tile_rows(a.P, a.groups);
+    if (a.splits > 1) {
+        GroupedArgs p = a;
+        p.N = a.swiglu ? 2 * a.N : a.N;
+        const int r = launch_mode(kPlain, p, bt, 256, full, num_sms, flags, stream, status);
+        if (r) return r;
+        return launch_sum(a.swiglu != 0, a.sums, a.offsets, a.groups, a.splits, a.P, a.N, a.out, num_sms, flags, stream);
+    }
     return launch_mode(a.swiglu ? kSwiglu : kPlain, a, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status);
 }
 
 int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
                               void *stream, int32_t *status) {
-    const GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, l.h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, nullptr, 0};
+    const GroupedArgs a = {l.x, l.a, nullptr, offsets, rows, l.h, l.M, l.M, l.L, l.R, l.K, 0, l.scale, nullptr, nullptr, 0,
+                           nullptr, 1};
     // One W tile, half of its rows each CTA's: rows of x so that there is a tile for each pair of SMs.
     const int clusters = clusters_of(num_sms);
     const int bt = l.M <= 32 * clusters ? 32 : l.M <= 64 * clusters ? 64 : l.M <= 128 * clusters ? 128 : 256;
@@ -835,7 +958,13 @@ int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const i
 
 int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
                               int num_sms, uint32_t flags, void *stream, int32_t *status) {
-    const GroupedArgs a = {l.x, w, bias, offsets, rows, l.out, l.M, l.M, l.L, l.N, l.K, 0, nullptr, l.b, l.h, l.R};
+    const GroupedArgs a = {l.x, w, bias, offsets, rows, l.out, l.M, l.M, l.L, l.N, l.K, 0, nullptr, l.b, l.h, l.R,
+                           l.sums, lora_outer_splits(l.M, l.N, l.K)};
+    if (a.splits > 1) {
+        const int r = launch_mode(kOuter, a, 256, 128, 1, num_sms, flags, stream, status);
+        if (r) return r;
+        return launch_sum(false, a.sums, nullptr, 0, a.splits, a.P, a.N, a.out, num_sms, flags, stream);
+    }
     // The width that needs the least time, a round of tiles going with its width and a share for x (256 x 14336 x 4096: 75
     // tiles of 192 on 76 pairs, 56 of 256).
     const int clusters = clusters_of(num_sms);

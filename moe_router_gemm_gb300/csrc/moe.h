@@ -61,8 +61,13 @@ struct GroupedArgs {
     const float *scale;
     const void *b, *h;
     int R;
+    // K in `splits` parts, whose sums go to sums[splits][P][N] (2 N columns with swiglu) and are added up after it
+    float *sums;
+    int splits;
 };
 int init_grouped();
+int grouped_splits(int P, int groups, int N, int K, int swiglu);
+int lora_outer_splits(int M, int N, int K);
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
 // The adapters of a linear.  The inner values h are fp32 sums over `splits` parts of K that are still to be added up,
@@ -78,6 +83,7 @@ struct LoraArgs {
     const float *y;
     void *out;
     int M, N, K, R, L, splits;
+    float *sums;  // the shared product's parts, where lora_outer_splits is more than 1
 };
 int lora_splits(int M, int K, int R);
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);

@@ -33,6 +33,7 @@ decltype(&bf16_linear_grouped) g_grouped;
 decltype(&bf16_combine_rows) g_combine;
 decltype(&bf16_linear_lora) g_lora;
 decltype(&bf16_linear_lora_workspace) g_lora_workspace;
+decltype(&bf16_linear_grouped_workspace) g_grouped_workspace;
 
 using at::Tensor;
 
@@ -336,10 +337,13 @@ PyObject *linear_grouped(PyObject *, PyObject *const *args, Py_ssize_t n) {
     {
         const Unlocked unlocked;
         out = make(*x, at::kBFloat16, {P, N});
+        Tensor space;  // freed on return, to this stream's own memory
+        const size_t need = g_grouped_workspace(P, (int)G, (int)N, (int)K, swiglu);
+        if (need) space = make(*x, at::kByte, {(int64_t)need});
         st = g_grouped(x->const_data_ptr(), x->size(0), w->const_data_ptr(), bias ? bias->const_data_ptr() : nullptr,
                        static_cast<const int32_t *>(offsets->const_data_ptr()),
                        rows ? static_cast<const int32_t *>(rows->const_data_ptr()) : nullptr, out.data_ptr(), P, (int)G,
-                       (int)N, (int)K, swiglu, flags, stream_of(*x));
+                       (int)N, (int)K, swiglu, need ? space.data_ptr() : nullptr, need, flags, stream_of(*x));
     }
     return st ? PyLong_FromLong(st) : item(out);
     END_HANDLE_TH_ERRORS
@@ -413,9 +417,9 @@ PyObject *linear_lora(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // bind(addresses of the entry points, in the order of the declarations above)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (wrong_count(n, 12)) return nullptr;
-    void *p[12];
-    for (int i = 0; i < 12; ++i) {
+    if (wrong_count(n, 13)) return nullptr;
+    void *p[13];
+    for (int i = 0; i < 13; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -431,6 +435,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     g_combine = reinterpret_cast<decltype(g_combine)>(p[9]);
     g_lora = reinterpret_cast<decltype(g_lora)>(p[10]);
     g_lora_workspace = reinterpret_cast<decltype(g_lora_workspace)>(p[11]);
+    g_grouped_workspace = reinterpret_cast<decltype(g_grouped_workspace)>(p[12]);
     Py_RETURN_NONE;
 }
 

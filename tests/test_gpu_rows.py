@@ -167,6 +167,28 @@ def test_groups_do_not_touch_one_another(lib):
         assert (alone[: ends[e]] == 0).all() and (alone[ends[e + 1]:] == 0).all()
 
 
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 64, 7168), (2, 2, 10, 41, 7168), (1, 4, 8, 300, 2888), (60, 1, 2, 530, 1024), (20, 7, 15, 85, 6792)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_few_tiles(lib, T, k, E, N, K, swiglu):
+    """K in parts, through a workspace whose contents do not matter; rows of no group stay."""
+    for gather in (True, False):
+        p = _problem(T, k, E, N, K, T + k, swiglu, True, gather)
+        got = _check(lib, p, str((T, k, E, N, K)))
+        need = lib.grouped_workspace(T * k, E, N, K, swiglu)
+        assert need > 0
+        space = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+        again = lib.bf16_linear_grouped(p["x"], p["w"], p["offsets"], p["bias"], rows=p["rows"], swiglu=swiglu, workspace=space)
+        assert torch.equal(again, got)
+    p = _problem(12, 0, 3, N, K, 3, swiglu, counts=[2, 0, 5])
+    out = torch.full((12, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    rows = torch.cat([p["rows"], p["rows"][:5]])
+    assert lib.grouped_workspace(12, 3, N, K, swiglu) > 0
+    lib.bf16_linear_grouped(p["x"], p["w"], p["offsets"] + 2, rows=torch.cat([rows[:2], rows[:10]]), swiglu=swiglu, out=out)
+    want, slack = ref.grouped(**p)
+    ref.check(out[2:9], want, slack)
+    assert (out[:2] == 7.0).all() and (out[9:] == 7.0).all()
+
+
 def test_many_weights(lib):
     """Weights past 2^31 elements: an expert far into them."""
     E, N, K = 40, 8192, 7168
@@ -231,7 +253,7 @@ def _check_lora(lib, p, what="", **kw):
 LORA = [(1, 1, 8, 8, 1), (1, 4096, 4096, 16, 64), (3, 33, 72, 8, 2), (8, 256, 2880, 32, 5), (16, 2112, 7168, 64, 8), (61, 300, 1024, 24, 7),
         (64, 1000, 512, 128, 70), (129, 257, 320, 40, 3), (200, 640, 136, 16, 200), (513, 520, 256, 72, 4), (1030, 384, 640, 64, 9),
         (2048, 130, 64, 96, 1000), (300, 77, 2048, 8, 1), (2000, 1024, 1024, 128, 2), (65, 5000, 136, 24, 30), (300, 9999, 72, 8, 100),
-        (1500, 4100, 320, 128, 40), (700, 4104, 2056, 48, 500), (256, 14336, 256, 16, 64), (520, 6144, 640, 80, 3)]
+        (1500, 4100, 320, 128, 40), (435, 377, 5944, 32, 2), (90, 905, 7168, 16, 12), (1081, 116, 2048, 16, 4), (300, 250, 1536, 104, 300), (700, 4104, 2056, 48, 500), (256, 14336, 256, 16, 64), (520, 6144, 640, 80, 3)]
 
 
 @pytest.mark.parametrize("shape", LORA, ids=lambda s: "x".join(map(str, s)))
@@ -378,6 +400,7 @@ def test_refusals(path):
                       (lambda: m.group_rows(ids, 8, flags=3), -1), (lambda: m.group_rows(z(4, 0, d=i32), 8), -1),
                       (lambda: m.bf16_linear_grouped(z(4, 60), z(2, 8, 60), off), -6), (lambda: m.bf16_linear_grouped(x, w, off, flags=1 << 33), -1),
                       (lambda: m.bf16_linear_grouped(x, z(1025, 1, 64), z(1026, d=i32)), -6),
+                      (lambda: m.bf16_linear_grouped(z(2, 7168), z(2, 8, 7168), off, workspace=z(64, d=torch.uint8)), -1),
                       (lambda: m.combine_rows(x, z(4, 0, d=i32)), -1), (lambda: m.combine_rows(x, ids, flags=3), -1),
                       (lambda: m.bf16_linear_lora(x, sh, z(3, 4, 64), z(3, 16, 4), one), -6),
                       (lambda: m.bf16_linear_lora(x, sh, a, b, one, workspace=z(64, d=torch.uint8)), -1)):

@@ -38,8 +38,8 @@ def test_linear_grouped_checks(lib):
     f = lib.load().bf16_linear_grouped
     x, w, b, o, r, y = P[:6]
 
-    def call(x=x, xr=16, w=w, b=None, o=o, r=r, y=y, n=32, g=4, N=24, K=64, s=0, flags=0):
-        return f(x, xr, w, b, o, r, y, n, g, N, K, s, flags, None)
+    def call(x=x, xr=16, w=w, b=None, o=o, r=r, y=y, n=32, g=4, N=24, K=64, s=0, ws=None, wn=0, flags=0):
+        return f(x, xr, w, b, o, r, y, n, g, N, K, s, ws, wn, flags, None)
 
     for bad in (dict(n=-1), dict(xr=-1), dict(g=0), dict(N=0), dict(K=0), dict(K=-8), dict(flags=3), dict(x=None), dict(w=None),
                 dict(o=None), dict(y=None), dict(xr=0), dict(r=None), dict(y=x), dict(y=w), dict(y=at(o, -16)), dict(b=y), dict(r=y),
@@ -50,6 +50,13 @@ def test_linear_grouped_checks(lib):
     for bad in (dict(x=at(x, 2)), dict(w=at(w, 8)), dict(b=at(b, 2)), dict(y=at(y, 4)), dict(o=at(o, 2)), dict(r=at(r, 2))):
         assert call(**bad) == EALIGN, bad
     assert call(n=0, x=None, y=None) == 0 and call(n=0, xr=0, r=None, s=1) == 0
+    few = dict(n=2, g=4, N=64, K=7168)  # two tiles: K in parts
+    need, ws = lib.grouped_workspace(*few.values()), P[6]
+    assert need >= 2 * 4 * 2 * 64 and lib.grouped_workspace(*few.values(), True) >= 2 * 4 * 2 * 128
+    assert call(**few) == call(**few, ws=ws, wn=need - 1) == call(**few, ws=y, wn=need) == call(**few, ws=x, wn=need) == EINVAL
+    assert call(**few, ws=at(ws, 64), wn=need) == EALIGN
+    assert lib.grouped_workspace(65536, 128, 4096, 7168) == lib.grouped_workspace(0, 4, 64, 7168) == 0
+    assert lib.grouped_workspace(2, 1025, 64, 7168) == lib.grouped_workspace(1 << 40, 4, 64, 7168) == 0
 
 
 def test_combine_rows_checks(lib):
