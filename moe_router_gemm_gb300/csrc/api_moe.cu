@@ -233,7 +233,7 @@ extern "C" size_t bf16_linear_grouped_workspace(int64_t P, int groups, int N, in
     if (P <= 0 || P > kMaxRows || groups <= 0 || groups > kMaxGroups || N <= 0 || K <= 0 || N > kMaxWidth || K > kMaxWidth)
         return 0;
     const int s = grouped_splits((int)P, groups, N, K, swiglu);
-    return s > 1 ? up256(4 * (size_t)s * (size_t)P * (size_t)N * (swiglu ? 2 : 1)) : 0;
+    return s > 1 ? up256(4 * (size_t)s * (size_t)P * (size_t)sum_pitch(swiglu ? 2 * N : N)) : 0;
 }
 
 extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
@@ -286,8 +286,9 @@ extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *p
 namespace {
 
 // How a linear with adapters is done, by sizes alone, and the parts of its workspace.
-//   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, while that is little;
-//     else rows in adapter order on tensor cores.
+//   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, or rows in adapter order
+//     on tensor cores, by estimate: (1.5 + K / 1400) us for each 1824 blocks of four ranks of a row, 6 + K / 320 us.
+//     (Whole calls, us: 435 x 377 x 5944 with rank 32 33.1 and 40.6, 2000 x 512 x 512 with rank 64 47.2 and 22.4.)
 //   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows; for few rows the dense
 //     linear's own kernels, which split K, into fp32 and the adapters' share after it (61 x 2112 x 7168 with rank 32: 20 us,
 //     38 fused; 281 x 322 x 2880: 42 and 20).
@@ -298,12 +299,12 @@ struct LoraWay {
 LoraWay lora_way(int M, int N, int K, int R, int L) {
     const uint64_t m = (uint64_t)M, r = (uint64_t)R;
     LoraWay w;
-    w.cores = m * r * (uint64_t)K * 2 <= 64ull << 20;
+    w.cores = m * r / 4 * (2100 + (uint64_t)K) * 320 <= 1824ull * 1400 * (1920 + (uint64_t)K);
     w.fused = M > 64;
     w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
     w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(M, K, R) : 1) * 4 * m * r);
     const int parts = w.fused ? lora_outer_splits(M, N, K) : 1;
-    w.y = w.fused && parts == 1 ? 0 : up256((size_t)parts * 4 * m * (size_t)N);
+    w.y = w.fused && parts == 1 ? 0 : up256((size_t)parts * 4 * m * (size_t)(parts > 1 ? sum_pitch(N) : N));
     return w;
 }
 

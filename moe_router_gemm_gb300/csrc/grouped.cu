@@ -162,10 +162,51 @@ struct Ring {
     }
 };
 
+// Whether `n` rows from position q on are neighbours in x (the whole warp asks).
+__device__ __forceinline__ bool neighbours(const int32_t *rows, int q, int n, int x_rows) {
+    const int lane = threadIdx.x & 31, first = __ldg(rows + q);
+    bool ok = first >= 0 && first <= x_rows - n;
+    for (int i = lane; i < n; i += 32) ok = ok && __ldg(rows + q + i) == first + i;
+    return __all_sync(kAll, ok);
+}
+
 // Maps of x with boxes of 16, 32, 64 and 128 rows.
 struct RowMaps {
     CUtensorMap of[4];
 };
+
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using T = uint4;
+};
+template <>
+struct Word<8> {
+    using T = uint2;
+};
+template <>
+struct Word<4> {
+    using T = uint32_t;
+};
+template <>
+struct Word<2> {
+    using T = uint16_t;
+};
+// A piece of 32 rows by kPiece columns (16-byte unit j of row r at j ^ (r / 2) % 4) to rows of out, BYTES a lane: `rows` of
+// them (lane r's `to` is the row that r goes to), `cols` columns, a multiple of BYTES' elements.
+template <int BYTES>
+__device__ __forceinline__ void store_piece(uint16_t *out, const uint8_t *piece, int to, int rows, int cols, int N, int lane) {
+    using T = typename Word<BYTES>::T;
+    constexpr int lanes = 2 * kPiece / BYTES;  // of a row
+    const int r0 = lane / lanes, byte = lane % lanes * BYTES;
+#pragma unroll
+    for (int k = 0; k < 32; k += 32 / lanes) {
+        const int r = k + r0, row = __shfl_sync(kAll, to, r);
+        const T w = *reinterpret_cast<const T *>(piece + 64 * r + ((byte & ~15) ^ (((r >> 1) & 3) << 4)) + (byte & 15));
+        if (r < rows && byte < 2 * cols) *reinterpret_cast<T *>(out + (size_t)row * N + byte / 2) = w;
+    }
+}
 
 template <int MODE, bool GATHER, bool PARTIAL>
 __global__ void __launch_bounds__(threads_of(GATHER), 1)
@@ -199,6 +240,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
         tma_prefetch_desc(&tm_w);
         if (!GATHER)
             for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tm_x.of[i]);
+        if (MODE == kOuter) tma_prefetch_desc(&tm_x.of[3]);
         for (int s = 0; s < stages; ++s) {
             mbar_init(&sh.full[s], GATHER ? 3 : 1);  // the leader producer's arrive.expect_tx, each CTA's copies of x
             mbar_init(&sh.copied[s], 32 * kGatherWarps);
@@ -326,6 +368,15 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const int half = t.cols >> 1, q0 = t.p0 + (int)rank * half;  // this CTA's rows of x
             const int n0 = t.m * wt + (int)rank * (wt / 2);
             const Tail f = tail(t);
+            // kOuter: whole halves of neighbouring rows come by TMA
+            bool near = false, near_other = false;
+            int near_row = 0;
+            if (MODE == kOuter) {
+                near = t.p0 + t.rows >= q0 + kHalf && neighbours(a.rows, q0, kHalf, a.x_rows);
+                const int other = t.p0 + (int)(rank ^ 1u) * kHalf;
+                near_other = leader && t.p0 + t.rows >= other + kHalf && neighbours(a.rows, other, kHalf, a.x_rows);
+                near_row = near ? __ldg(a.rows + q0) : 0;
+            }
             for (int c = 0, n = t.n + f.stages(); c < n; ++c, ++it, r.next(stages)) {
                 const int s = r.s;
                 ok = mbar_wait(&sh.empty[s], r.phase ^ 1u, status, kSiteEmpty);  // (at once in the first round)
@@ -347,9 +398,11 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             if (++b16 == g.per) b16 = 0, ++i;
                         }
                     } else {
-                        if (leader)
-                            mbar_arrive_expect_tx(&sh.full[s], (uint32_t)kChunks *
-                                                                   (2u * w_chunk + (GATHER ? 0u : (uint32_t)(t.cols * kChunkK * 2))));
+                        if (leader) {
+                            const uint32_t x_bytes = GATHER ? (uint32_t)(near + near_other) * kHalf * kChunkK * 2
+                                                            : (uint32_t)(t.cols * kChunkK * 2);
+                            mbar_arrive_expect_tx(&sh.full[s], (uint32_t)kChunks * (2u * w_chunk + x_bytes));
+                        }
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
                             const int k0 = ((t.c0 + c) * kChunks + j) * kChunkK;
@@ -363,6 +416,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                                 for (int i = 0; i < 4; ++i)
                                     tma_load_4d_pair(ch + i * (kWBytes / 4), &tm_w, fb, k0, n0 + 16 * i, 0, t.e);
                             }
+                            if (MODE == kOuter && near) tma_load_2d_pair(ch + kX, &tm_x.of[3], fb, k0, near_row);
                             // this CTA's rows, a multiple of 16, by boxes of falling sizes
 #pragma unroll
                             for (int i = 3; i >= 0; --i)
@@ -505,6 +559,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             // Rows past the tile's are zero: one row read again by every CTA in their place is a hot spot (128 rows of
             // 14336 x 4096 with adapters: 74 us for the shared product alone, 44 so).
             const int have = min(max(t.p0 + t.rows - q0, 0), half);
+            const bool near = MODE == kOuter && have == kHalf && neighbours(a.rows, q0, kHalf, a.x_rows);  // (they come by TMA)
             const uint16_t *row[kHalf / kGatherRows];
 #pragma unroll
             for (int i = 0; i < kHalf / kGatherRows; ++i) {
@@ -538,7 +593,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 }
                 // The copies' own instructions count: four warps issue 16 each a stage, and one address serves all chunks.
                 const int k0 = (t.c0 + c) * kChunks * kChunkK;
-                if (have == half && k0 + kChunks * kChunkK <= a.K) {
+                if (near) {
+                } else if (have == half && k0 + kChunks * kChunkK <= a.K) {
 #pragma unroll
                     for (int i = 0; i < kHalf / kGatherRows; ++i)
                         if (kGatherRows * i < half) {
@@ -591,7 +647,6 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 const int i0 = (int)rank * kHalf + quarter * 32, left = t.rows - i0;  // the warp's first row, its rows
                 uint8_t *piece = sh.piece[warp - 2];
                 const int to = lane < left ? __ldg(a.rows + t.p0 + i0 + lane) : 0;
-                const bool whole = a.N % 8 == 0;
                 for (int c0 = kPiece * h; have && c0 < wt && t.m * wt + c0 < a.N; c0 += 2 * kPiece) {
                     const int n0 = t.m * wt + c0;
                     const float nb = bias_lane(bias, n0, a.N);
@@ -608,15 +663,10 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                     }
                     if (bias && (!PARTIAL || t.part == 0)) bias_add32(v, nb);
                     if constexpr (PARTIAL) {
-                        float *o = a.sums + ((size_t)t.part * a.P + to) * a.N + n0;
-                        if (lane < left && a.N % 8 == 0 && n0 + 32 <= a.N) {
+                        float *o = a.sums + ((size_t)t.part * a.P + to) * sum_pitch(a.N) + n0;
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) OutStore<float>::eight(o + j, v + j);
-                        } else if (lane < left) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (n0 + j < a.N) o[j] = v[j];
-                        }
+                        for (int j = 0; j < 32; j += 8)
+                            if (lane < left && n0 + j < a.N) OutStore<float>::eight(o + j, v + j);
                         __syncwarp();
                         continue;
                     }
@@ -627,23 +677,17 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
                                        pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
                     __syncwarp();
-                    // Four lanes a row, eight rows a store: whole sectors (a row a lane: 8192 x 7168 x 7168 35 us more).
-                    const int u = lane & 3, n = n0 + 8 * u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 8 * k + (lane >> 2), row = __shfl_sync(kAll, to, r);
-                        const uint4 w = *reinterpret_cast<const uint4 *>(piece + 64 * r + 16 * (u ^ ((r >> 1) & 3)));
-                        uint16_t *o = out + (size_t)row * a.N + n;
-                        const bool in = r < left && n < a.N;
-                        if (in && whole) {
-                            *reinterpret_cast<uint4 *>(o) = w;
-                        } else if (in) {
-                            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (n + j < a.N) o[j] = (uint16_t)(j & 1 ? q[j / 2] >> 16 : q[j / 2]);
-                        }
-                    }
+                    // Neighbouring lanes store a row's 64 bytes, as wide as rows of N start (a row a lane: 8192 x 7168 x
+                    // 7168 35 us more).
+                    const int cols = min(a.N - n0, kPiece);
+                    if (a.N % 8 == 0)
+                        store_piece<16>(out + n0, piece, to, left, cols, a.N, lane);
+                    else if (a.N % 4 == 0)
+                        store_piece<8>(out + n0, piece, to, left, cols, a.N, lane);
+                    else if (a.N % 2 == 0)
+                        store_piece<4>(out + n0, piece, to, left, cols, a.N, lane);
+                    else
+                        store_piece<2>(out + n0, piece, to, left, cols, a.N, lane);
                 }
             }
             // (a warp whose outputs all lie past N has nothing to do)
@@ -659,10 +703,10 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                 uint16_t *o = out + (size_t)(t.p0 + c0) * a.N + n;
                 const int left = t.rows - c0;
                 if constexpr (PARTIAL) {
-                    float *s = a.sums + ((size_t)t.part * a.P + t.p0 + c0) * a.N + n;
+                    float *s = a.sums + ((size_t)t.part * a.P + t.p0 + c0) * sum_pitch(a.N) + n;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (n < a.N && j < left) s[(size_t)j * a.N] = v[j];
+                        if (n < a.N && j < left) s[(size_t)j * sum_pitch(a.N)] = v[j];
                 } else if constexpr (MODE == kInner) {
                     uint16_t *h = out + n;
                     const int to = __ldg(a.rows + t.p0 + c0 + min(lane & 15, left - 1));
@@ -793,13 +837,13 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const float *__restric
         first = min(max(__ldg(offsets), 0), P);
         end = last;
     }
-    const int wide = SWIGLU ? 2 * N : N;
-    const size_t plane = (size_t)P * wide;
+    const int pitch = sum_pitch(SWIGLU ? 2 * N : N);
+    const size_t plane = (size_t)P * pitch;
     for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < (long long)P * N;
          i += (long long)gridDim.x * kSumThreads) {
         const int p = (int)(i / N), n = (int)(i - (long long)p * N);
         if (p < first || p >= end) continue;
-        const float *s = sums + (size_t)p * wide + n;
+        const float *s = sums + (size_t)p * pitch + n;
         float v = 0.0f, up = 0.0f;
 #pragma unroll 8
         for (int k = 0; k < splits; ++k) {
@@ -863,7 +907,7 @@ int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int nu
                 ? make_tmap_bf16_blocks(&tw, a.w, planes, 2, N, K, 16, 4, kChunkK)
                 : make_tmap_bf16_stack(&tw, a.w, planes, swiglu ? 2 : 1, N, K, swiglu ? 2 : 1, swiglu ? 16 : (uint32_t)wt / 2,
                                        kChunkK);
-    for (int i = 0; i < 4 && !r && !a.rows; ++i)
+    for (int i = mode == kOuter ? 3 : 0; i < 4 && !r && (!a.rows || mode == kOuter); ++i)
         r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, K, 16u << i, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, a.b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);

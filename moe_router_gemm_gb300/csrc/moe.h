@@ -61,10 +61,14 @@ struct GroupedArgs {
     const float *scale;
     const void *b, *h;
     int R;
-    // K in `splits` parts, whose sums go to sums[splits][P][N] (2 N columns with swiglu) and are added up after it
+    // K in `splits` parts, whose sums go to sums[splits][P][sum_pitch(N)] (of 2 N with swiglu) and are added up after it
     float *sums;
     int splits;
 };
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr int sum_pitch(int N) { return (N + 7) / 8 * 8; }
 int init_grouped();
 int grouped_splits(int P, int groups, int N, int K, int swiglu);
 int lora_outer_splits(int M, int N, int K);
