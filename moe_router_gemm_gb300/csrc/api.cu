@@ -71,6 +71,7 @@ void init_device(DeviceState &s) {
         if (!e) e = init_mxfp4_split();
         if (!e) e = init_group();
         if (!e) e = init_grouped();
+        if (!e) e = init_lora();
     }
     s.err = e;
 }

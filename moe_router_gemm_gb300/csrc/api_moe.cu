@@ -389,6 +389,8 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     if (st != BF16L_OK) return st;
     if (way.fused)
         return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
+    if (M <= kLoraRows && (int64_t)M * K * 2 <= kLoraRowsSmem)  // (cores, with splits)
+        return result(launch_lora_rows(args, w, bias, flags, stream));
     bf16l_plan plan;
     st = few_rows_plan(M, N, K, dev, flags, &plan) ? bf16_linear_f32out_with_plan(x, w, bias, y, M, N, K, &plan, stream)
                                                    : bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);

@@ -20,8 +20,9 @@ constexpr int kOuterThreads = 128;
 // A block sums kRanks ranks of a row over a part of K, its warps taking 256 elements in turn.
 __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a) {
     __shared__ float part[kInnerWarps][kRanks];
-    pdl_launch_dependents();
+    // The next kernel may start once this one has waited: it then reads nothing but h that could still be written.
     pdl_wait();
+    pdl_launch_dependents();
     const int t = blockIdx.x, s = blockIdx.y, splits = (int)gridDim.y, r0 = kRanks * (int)blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = __ldg(a.ids + t);
@@ -129,6 +130,87 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
     }
 }
 
+// One or two rows: a warp for each W row, its first kAhead vectors of W, and B's row, on their way while the inner kernel
+// still runs (which has let this one start when all kernels before it were done); then the row's h, and one sum over the
+// warp for the shared product and the adapter's.  x in shared memory.  1 x 4096 x 4096 with rank 16 8.7 us (floor 5.0; 9.9
+// with the dense linear's kernel and the outer one), 1 x 2112 x 7168 with rank 32 8.6 (11.3), 1 x 1024 x 1024 3.1 (5.7).
+// Three or four rows took longer so than by the other form, 16 vectors ahead (which halve the resident warps) 11.1.
+constexpr int kRowWarps = 8, kAhead = 8;
+template <int M>
+__global__ void __launch_bounds__(32 * kRowWarps, 4) lora_rows_kernel(const LoraArgs a, const uint16_t *__restrict__ w,
+                                                                   const uint16_t *__restrict__ bias) {
+    extern __shared__ uint4 sx[];
+    const int lane = threadIdx.x & 31, n = (int)blockIdx.x * kRowWarps + (int)(threadIdx.x >> 5);
+    const int vectors = a.K / 8;  // (K % 8 == 0)
+    const bool in = n < a.N;
+    const uint4 *row = reinterpret_cast<const uint4 *>(w + (size_t)(in ? n : 0) * a.K);
+    uint4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (in && 32 * i + lane < vectors) v[i] = ldg_stream_v4(row + 32 * i + lane);
+    const uint4 *x = static_cast<const uint4 *>(a.x);
+    for (int i = threadIdx.x; i < M * vectors; i += 32 * kRowWarps) sx[i] = __ldg(x + i);
+    int id[M];
+    float b[M][kLoraMaxRank / 32];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        id[m] = __ldg(a.ids + m);
+        const bool has = in && (unsigned)id[m] < (unsigned)a.L;
+#pragma unroll
+        for (int q = 0; q < kLoraMaxRank / 32; ++q) {
+            const int r = 32 * q + lane;
+            b[m][q] = has && r < a.R ? bf16_to_f32(__ldg(static_cast<const uint16_t *>(a.b) +
+                                                         ((size_t)id[m] * a.N + n) * a.R + r))
+                                     : 0.0f;
+        }
+    }
+    const float extra = in && bias ? bf16_to_f32(__ldg(bias + n)) : 0.0f;
+    __syncthreads();
+    pdl_launch_dependents();
+    float sum[M] = {};
+    auto add = [&](const uint4 &q, int k) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const uint4 xv = sx[m * vectors + k];
+            sum[m] = fma2_bf16(xv.x, q.x, sum[m]);
+            sum[m] = fma2_bf16(xv.y, q.y, sum[m]);
+            sum[m] = fma2_bf16(xv.z, q.z, sum[m]);
+            sum[m] = fma2_bf16(xv.w, q.w, sum[m]);
+        }
+    };
+    if (in) {
+        for (int k0 = 0; k0 < vectors; k0 += 32 * kAhead) {
+            const int next = k0 + 32 * kAhead;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = k0 + 32 * i + lane;
+                if (k < vectors) add(v[i], k);
+                if (next + 32 * i + lane < vectors) v[i] = ldg_stream_v4(row + next + 32 * i + lane);
+            }
+        }
+    }
+    pdl_wait();  // the inner values
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        if ((unsigned)id[m] >= (unsigned)a.L) continue;
+#pragma unroll
+        for (int q = 0; q < kLoraMaxRank / 32; ++q) {
+            const int r = 32 * q + lane;
+            if (r >= a.R) continue;
+            float h = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) h += static_cast<const float *>(a.h)[((size_t)s * M + m) * a.R + r];
+            sum[m] = fmaf(h, b[m][q], sum[m]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum[m] += __shfl_xor_sync(0xFFFFFFFFu, sum[m], d);
+        if (in && lane == m) static_cast<uint16_t *>(a.out)[(size_t)m * a.N + n] = f32_to_bf16(sum[m] + extra);
+    }
+}
+
 int launch(void (*f)(const LoraArgs), dim3 grid, int threads, const LoraArgs &a, uint32_t flags, void *stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -154,6 +236,28 @@ int lora_splits(int M, int K, int R) {
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream) {
     const dim3 grid((unsigned)a.M, (unsigned)(a.splits ? a.splits : 1), (unsigned)(a.R / kRanks));
     return launch(lora_inner_kernel, grid, 32 * kInnerWarps, a, flags, stream);
+}
+
+int init_lora() {
+    for (auto f : {lora_rows_kernel<1>, lora_rows_kernel<2>}) {
+        const int e = (int)cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kLoraRowsSmem);
+        if (e) return e;
+    }
+    return 0;
+}
+
+int launch_lora_rows(const LoraArgs &a, const void *w, const void *bias, uint32_t flags, void *stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.N + kRowWarps - 1) / kRowWarps));
+    cfg.blockDim = dim3(32 * kRowWarps);
+    cfg.dynamicSmemBytes = (size_t)a.M * a.K * 2;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, a.M == 1 ? lora_rows_kernel<1> : lora_rows_kernel<2>, a, static_cast<const uint16_t *>(w), static_cast<const uint16_t *>(bias));
 }
 
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {

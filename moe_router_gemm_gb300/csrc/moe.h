@@ -92,6 +92,10 @@ struct LoraArgs {
 int lora_splits(int M, int K, int R);
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
+// ... and for at most kLoraRows rows of at most kLoraRowsSmem bytes in all, the shared product and the adapters' at once.
+constexpr int kLoraRows = 2, kLoraRowsSmem = 48 * 1024;
+int init_lora();
+int launch_lora_rows(const LoraArgs &a, const void *w, const void *bias, uint32_t flags, void *stream);
 int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
                               void *stream, int32_t *status);
 int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,

@@ -250,7 +250,7 @@ def _check_lora(lib, p, what="", **kw):
     return got
 
 
-LORA = [(1, 1, 8, 8, 1), (1, 4096, 4096, 16, 64), (3, 33, 72, 8, 2), (8, 256, 2880, 32, 5), (16, 2112, 7168, 64, 8), (61, 300, 1024, 24, 7),
+LORA = [(1, 1, 8, 8, 1), (2, 333, 7168, 40, 3), (4, 1001, 9000, 128, 5), (4, 70, 16384, 16, 2), (1, 515, 4104, 8, 4), (3, 64, 16384, 64, 9), (2, 130, 12288, 128, 3), (2, 65, 12296, 8, 3), (1, 77, 24576, 16, 4), (1, 4096, 4096, 16, 64), (3, 33, 72, 8, 2), (8, 256, 2880, 32, 5), (16, 2112, 7168, 64, 8), (61, 300, 1024, 24, 7),
         (64, 1000, 512, 128, 70), (129, 257, 320, 40, 3), (200, 640, 136, 16, 200), (513, 520, 256, 72, 4), (1030, 384, 640, 64, 9),
         (2048, 130, 64, 96, 1000), (300, 77, 2048, 8, 1), (2000, 1024, 1024, 128, 2), (65, 5000, 136, 24, 30), (300, 9999, 72, 8, 100),
         (1500, 4100, 320, 128, 40), (435, 377, 5944, 32, 2), (90, 905, 7168, 16, 12), (1081, 116, 2048, 16, 4), (300, 250, 1536, 104, 300), (700, 4104, 2056, 48, 500), (256, 14336, 256, 16, 64), (520, 6144, 640, 80, 3)]
