@@ -2,7 +2,8 @@
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--workload router|smallest|decode|mlp|prefill] [--pdl]
-    python bench.py --operators    (the norm, routing and MXFP4 cases of perf/operators.py)
+    python bench.py --operators [norm|rows]    (the norm, routing and MXFP4 cases of perf/operators.py, or the grouped and
+                                               adapters' linears of perf/more_operators.py)
 
 Default workload: the MoE router sweep, M = 1..16 x (K, N) in {(4096,256),
 (6144,256), (7168,256), (7168,384), (2880,128)} (80 shapes), seeded synthetic
@@ -1111,14 +1112,14 @@ def mxfp8_arm(args, points):
 
 
 def operator_floor_us(work, peaks):
-    """The least time of a pass (perf/operators.py: work) at the measured copy and bf16 rates, and which of them sets it."""
+    """The least time of a pass (the case module's work) at the measured copy and bf16 rates, and which of them sets it."""
     by = {"hbm": work["bytes"] / peaks["hbm_gbs"] / 1e3, "bf16 tensor": work["flops"] / peaks["bf16_tflops"] / 1e6}
     bound = max(by, key=by.get)
     return by[bound], bound
 
 
 def operators_arm(args):
-    """The cases of perf/operators.py (norm, routing, MXFP4), one JSON line each.
+    """The cases of perf/operators.py (norm, routing, MXFP4) or perf/more_operators.py, one JSON line each.
 
     device_us: a CUDA graph of calls on three sets of inputs in turn (those of a few megabytes stay in L2), the median of
     --steps replays by events.  call_us: a pass among others from Python, host work included.  plain_us: the plain form's,
@@ -1129,11 +1130,12 @@ def operators_arm(args):
     from moe_router_gemm_gb300 import build as _build
     _build.build()
     lib.load()
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    name = {"norm": "operators", "rows": "more_operators"}[args.operators]
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", f"{name}.py"))
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     peaks = load_peaks()
-    steps, sets, calls = max(args.steps, 1), 3, 24
+    steps, sets, most = max(args.steps, 1), 3, 24
 
     def events(f):
         a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
@@ -1149,6 +1151,7 @@ def operators_arm(args):
 
     for case in mod.listed():
         work = mod.work(case)
+        calls = most if operator_floor_us(work, peaks)[0] < 1000 else sets
         states = [mod.prepare(case, seed) for seed in range(sets)]
         sampler = ClockSampler(torch.cuda.current_device())
         sampler.start()
@@ -1201,8 +1204,9 @@ def main():
                     help="time the per-tensor FP8 linear (bf16_linear_fp8) on the workload's shapes instead")
     ap.add_argument("--mxfp8", action="store_true",
                     help="time the MXFP8 linear (bf16_linear_mxfp8) on the workload's shapes instead")
-    ap.add_argument("--operators", action="store_true",
-                    help="time the norm, routing and MXFP4 cases of perf/operators.py instead")
+    ap.add_argument("--operators", nargs="?", const="norm", choices=["norm", "rows"],
+                    help="time the norm, routing and MXFP4 cases of perf/operators.py, or (rows) the grouped and adapters' "
+                         "linears of perf/more_operators.py, instead")
     ap.add_argument("--pdl", action="store_true",
                     help="launch with programmatic dependent launch (BF16L_FLAG_PDL): back-to-back calls overlap")
     ap.add_argument("--no-pdl-variant", action="store_true",

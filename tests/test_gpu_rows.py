@@ -202,6 +202,30 @@ def test_many_weights(lib):
     ref.check(got, want, slack)
 
 
+def test_long_out(lib):
+    """Rows of out past 2^31 elements, in a group of 270,000 rows, and from x as it stands."""
+    counts, N, K = [3, 269997], 8200, 64
+    for gather in (True, False):
+        p = _problem(1000, 0, 2, N, K, 6, gather=gather, counts=counts)
+        got = lib.bf16_linear_grouped(p["x"], p["w"], p["offsets"], rows=p["rows"])
+        at = torch.tensor([0, 2, 3, 131071, 262144, 269744, 269999], device=DEV)
+        x = p["x"][p["rows"][at].long()] if gather else p["x"][at]
+        off = torch.tensor([0, 2, 7], device=DEV)
+        ref.check(got[at], *ref.grouped(x, p["w"], off, None, None, False))
+        del got, p
+
+
+def test_long_combine(lib):
+    """Rows of y past 2^31 elements."""
+    H = 8192
+    y = torch.zeros(270000, H, dtype=torch.bfloat16, device=DEV)
+    y[269990:] = _bf16(_gen(3), 10, H)
+    place = torch.arange(269990, 270000, device=DEV, dtype=torch.int32).view(5, 2)
+    w = torch.rand(5, 2, generator=_gen(4), device=DEV)
+    got = lib.combine_rows(y, place, w)
+    ref.check(got, *ref.combine(y[269990:], place - 269990, w, None))
+
+
 # ---- combination ----
 
 @pytest.mark.parametrize("T,k,H", [(1, 1, 1), (1, 8, 2048), (4, 8, 7168), (7, 3, 33), (100, 6, 130), (33, 32, 2884), (1000, 2, 66), (2000, 8, 1024)])
@@ -338,6 +362,30 @@ def test_streams_and_graphs_of_the_adapters(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_two_streams_at_once(lib):
+    """Calls on two streams, each with its own workspace, give what they give one after the other."""
+    p = [_problem(T, 4, 9, 500, 712, T, True, True) for T in (300, 3)]
+    q = [_lora_problem(M, 500, 712, 48, 6, M, bias=True) for M in (2, 50, 700)]
+
+    def calls():
+        return ([lib.bf16_linear_grouped(v["x"], v["w"], v["offsets"], v["bias"], rows=v["rows"], swiglu=True) for v in p]
+                + [lib.bf16_linear_lora(v["x"], v["w"], v["a"], v["b"], v["ids"], v["bias"], scale=v["scale"]) for v in q]
+                + [v for n in (5, 5000) for v in lib.group_rows(torch.arange(n, device=DEV, dtype=torch.int32) % 7, 6)])
+
+    want = calls()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(calls())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+    assert lib.device_status() == 0
 
 
 def test_same_bits_again(lib):
