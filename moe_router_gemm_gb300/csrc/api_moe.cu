@@ -391,8 +391,10 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
         return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
     if (M <= kLoraRows && (int64_t)M * K * 2 <= kLoraRowsSmem)  // (cores, with splits)
         return result(launch_lora_rows(args, w, bias, flags, stream));
+    // The product may read its weights as soon as the inner kernel lets it start: that one has waited for all before it.
     bf16l_plan plan;
-    st = few_rows_plan(M, N, K, dev, flags, &plan) ? bf16_linear_f32out_with_plan(x, w, bias, y, M, N, K, &plan, stream)
-                                                   : bf16_linear_f32out(x, w, bias, y, M, N, K, flags, stream);
+    const uint32_t early = flags & BF16L_FLAG_SERIAL ? flags : flags | BF16L_FLAG_PDL;
+    st = few_rows_plan(M, N, K, dev, early, &plan) ? bf16_linear_f32out_with_plan(x, w, bias, y, M, N, K, &plan, stream)
+                                                   : bf16_linear_f32out(x, w, bias, y, M, N, K, early, stream);
     return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
 }
