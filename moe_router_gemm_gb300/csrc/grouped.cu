@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                             ok = mbar_wait(&sh.full[s], r.phase, status, kSiteFull);
                             tc_fence_after();
                             const uint8_t *ch = ring + s * stage_bytes;
-                            const uint64_t high = smem_desc_sw128(smem_u32(ch)), low = smem_desc_sw128(smem_u32(ch + chunk_bytes));
+                            const uint32_t high = first_lo + (uint32_t)s * (uint32_t)(stage_bytes >> 4);
+                            const uint32_t low = high + (uint32_t)(chunk_bytes >> 4);
                             uint32_t off[8];
                             int col = sh.column[0];
 #pragma unroll
@@ -503,8 +504,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
                                 uint32_t off2[8];
 #pragma unroll
                                 for (int w = 0; w < 8; ++w) off2[w] = sh.off[next][w];
-                                mma_bf16_pair_lanes(acc, high + col, bdesc, idesc, off);
-                                mma_bf16_pair_lanes(acc, low + col, bdesc, idesc, off);
+                                mma_bf16_pair_lanes2(acc, high + (uint32_t)col, low + (uint32_t)col, bdesc, idesc, off);
                                 col = col2;
 #pragma unroll
                                 for (int w = 0; w < 8; ++w) off[w] = off2[w];

@@ -71,15 +71,20 @@ __device__ __forceinline__ void mma_bf16_pair_sw128(uint32_t d_tmem, uint32_t al
         : "memory");
 }
 
-// As mma_bf16_pair, adding to D in the lanes (rows) alone whose bit of `off` is clear: words 0-3 the even CTA's, 4-7 the odd's.
-__device__ __forceinline__ void mma_bf16_pair_lanes(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                    const uint32_t (&off)[8]) {
+// Two pair MMAs that add to D in the lanes (rows) alone whose bit of `off` is clear (words 0-3 the even CTA's, 4-7 the
+// odd's): A0 B^T and A1 B^T, the A operands given by their descriptors' low words (128-byte swizzle).
+__device__ __forceinline__ void mma_bf16_pair_lanes2(uint32_t d_tmem, uint32_t alo0, uint32_t alo1, uint64_t bdesc,
+                                                     uint32_t idesc, const uint32_t (&off)[8]) {
+    constexpr uint32_t kHigh = (uint32_t)((1024 >> 4) | 1 << 14 | 2u << 29);
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, c;\n\t"
         "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
-        "r"(off[5]), "r"(off[6]), "r"(off[7])
+        "mov.b64 a, {%1, %13};\n\t"
+        "mov.b64 c, {%2, %13};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, %3, %4, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], c, %3, %4, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}"
+        ::"r"(d_tmem), "r"(alo0), "r"(alo1), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]),
+        "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7]), "n"(kHigh)
         : "memory");
 }
 
