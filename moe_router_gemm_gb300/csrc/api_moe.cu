@@ -299,10 +299,10 @@ struct LoraWay {
 LoraWay lora_way(int M, int N, int K, int R, int L) {
     const uint64_t m = (uint64_t)M, r = (uint64_t)R;
     LoraWay w;
-    w.cores = m * r / 4 * (2100 + (uint64_t)K) * 320 <= 1824ull * 1400 * (1920 + (uint64_t)K);
     w.fused = M > 64;
-    w.order = w.cores && !w.fused ? 0 : up256(4 * ((size_t)L + 1)) + up256(4 * m);
-    w.h = up256((w.cores && !w.fused ? (size_t)lora_splits(M, K, R) : 1) * 4 * m * r);
+    w.cores = !w.fused || m * r / 4 * (2100 + (uint64_t)K) * 320 <= 1824ull * 1400 * (1920 + (uint64_t)K);
+    w.order = w.fused ? up256(4 * ((size_t)L + 1)) + up256(4 * m) : 0;
+    w.h = up256((w.fused ? 1 : (size_t)lora_splits(M, K, R)) * 4 * m * r);
     const int parts = w.fused ? lora_outer_splits(M, N, K) : 1;
     w.y = w.fused && parts == 1 ? 0 : up256((size_t)parts * 4 * m * (size_t)(parts > 1 ? sum_pitch(N) : N));
     return w;
@@ -381,7 +381,7 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + up256(4 * ((size_t)L + 1)));
     float *y = reinterpret_cast<float *>(p + way.order + way.h);
     const LoraArgs args = {x, a, b, scale, ids, p + way.order, y, out, M, N, K, R, L,
-                           way.cores && !way.fused ? lora_splits(M, K, R) : 0, y};
+                           way.fused ? 0 : lora_splits(M, K, R), y};
     if (way.order) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
     if (st == BF16L_OK)
         st = result(way.cores ? launch_lora_inner(args, flags, stream)
@@ -389,7 +389,7 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     if (st != BF16L_OK) return st;
     if (way.fused)
         return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
-    if (M <= kLoraRows && (int64_t)M * K * 2 <= kLoraRowsSmem)  // (cores, with splits)
+    if (M <= kLoraRows && (int64_t)M * K * 2 <= kLoraRowsSmem)  // (few rows: cores, with splits)
         return result(launch_lora_rows(args, w, bias, flags, stream));
     // The product may read its weights as soon as the inner kernel lets it start: that one has waited for all before it.
     bf16l_plan plan;

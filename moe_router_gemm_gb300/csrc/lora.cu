@@ -2,9 +2,10 @@
 // out = y + h @ B_a^T, with y the shared projection in fp32, by the dense linear's own kernels between the two.
 //
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
-// spreads over as many SMs as it can: the inner one takes four ranks of a row a block and its K over up to eight blocks,
-// whose sums the outer one adds, in order, when it reads them.  The inner one also asks L2 for B_a, which the outer one reads when the projection
-// is done.
+// spreads over the SMs: the inner one takes four ranks of a row a block, and splits K over more blocks as long as all are
+// resident at once; the outer one adds those sums, in order, when it reads them.  The inner one also asks L2 for B_a, and the
+// outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with rank 32: 18.2 us, of
+// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.7 (6.6), 64 x 4096 x 4096 with rank 64 27.5 (16.1).
 #include <cuda_runtime.h>
 
 #include "grouped.cuh"
@@ -14,10 +15,16 @@ namespace bf16l {
 
 namespace {
 
-constexpr int kInnerWarps = 4, kRanks = 4;  // ranks of a block
+constexpr int kRanks = 4;  // of a block of the inner kernel
 constexpr int kOuterThreads = 128;
+// (A warp has at least four loads of 512 bytes in flight.)
+__host__ __device__ constexpr int outer_sets(int g) { return g < 4 ? 4 / g : 1; }
 
-// A block sums kRanks ranks of a row over a part of K, its warps taking 256 elements in turn.
+// A block sums kRanks ranks of a row over a part of K, its warps taking 256 elements in turn.  Eight warps of a block and parts
+// of K in multiples of 256 took 0.5 to 1 us less than four warps and multiples of 1024 (8 x 4096 x 4096 r16 11.3 -> 10.3 us,
+// 61 x 2112 x 7168 r32 20.0 -> 19.1) where the blocks are few, and 1 to 4 us more where they are many (inner_warps);
+// eight ranks a block, sixteen warps or more registers were slower.
+template <int kInnerWarps>
 __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a) {
     __shared__ float part[kInnerWarps][kRanks];
     // The next kernel may start once this one has waited: it then reads nothing but h that could still be written.
@@ -35,7 +42,7 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
         prefetch_l2(b, (uint32_t)(bytes < (1 << 20) ? bytes : 1 << 20));
     }
     constexpr int kStep = 256 * kInnerWarps;
-    const int each = ((a.K + splits - 1) / splits + kStep - 1) / kStep * kStep, k0 = s * each, k1 = min(k0 + each, a.K);
+    const int each = ((a.K + splits - 1) / splits + 255) / 256 * 256, k0 = min(s * each, a.K), k1 = min(k0 + each, a.K);
     const uint16_t *x = static_cast<const uint16_t *>(a.x) + (size_t)t * a.K;
     const uint16_t *w = static_cast<const uint16_t *>(a.a) + ((size_t)id * a.R + r0) * a.K;  // (R % 8 == 0)
     float sum[kRanks] = {};
@@ -78,55 +85,76 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
     }
 }
 
-// One output a thread: its B row is R consecutive values, the first kAhead vectors of which are on their way before the
-// block has its h.
+// A row of B (R values) goes to G lanes, G being the power of two from R / 8 up, 16 bytes each, so that a warp reads 512
+// contiguous bytes at a time (where R / 8 is G); G such steps give each lane G parts of G outputs, and exchanging halves of
+// them log2(G) times leaves each lane the sum of one.  The rows of B are on their way while the shared product still runs
+// (which started when the inner kernel had waited for all before it).  With an output a thread and its row of B in one lane
+// 61 x 2112 x 7168 r32 took 18.6 us (18.2 so), 64 x 4096 x 4096 r64 30.9 (27.5), 64 x 7168 x 7168 r128 71 (56).
+template <int G>
 __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArgs a) {
-    constexpr int kAhead = 4;
-    __shared__ float h[kLoraMaxRank];
+    constexpr int kSets = outer_sets(G), kRows = 32 / G;  // sets of 32 outputs; rows of B in a step
     pdl_launch_dependents();
-    pdl_wait();
+    const int lane = threadIdx.x & 31, p = lane & (G - 1), q = lane / G;
     const int t = blockIdx.x, id = __ldg(a.ids + t);
-    const bool has = (unsigned)id < (unsigned)a.L;
-    const uint16_t *B = static_cast<const uint16_t *>(a.b) + (has ? (size_t)id * a.N * a.R : 0);
-    long long n = (long long)blockIdx.y * kOuterThreads + threadIdx.x;
-    uint4 v[kAhead] = {};
-    float y = 0.0f;
+    const bool has = (unsigned)id < (unsigned)a.L && 8 * p < a.R;  // (R % 8 == 0)
+    const uint16_t *B = static_cast<const uint16_t *>(a.b) + (has ? (size_t)id * a.N * a.R + 8 * p : 0);
+    const long long step = (long long)gridDim.y * (kSets * kOuterThreads);
+    long long n = ((long long)blockIdx.y * (kOuterThreads / 32) + (threadIdx.x >> 5)) * (32 * kSets) + q;
+    uint4 v[kSets][G];
     auto load = [&]() {
-        if (n >= a.N) return;
-        y = a.y[(size_t)t * a.N + n];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (has && 8 * i < a.R) v[i] = __ldg(reinterpret_cast<const uint4 *>(B + n * a.R) + i);
+        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const long long i = n + 32 * s + j * kRows;
+                v[s][j] = has && i < a.N ? __ldg(reinterpret_cast<const uint4 *>(B + i * a.R)) : make_uint4(0, 0, 0, 0);
+            }
     };
     load();
-    if (has && (int)threadIdx.x < a.R) {
-        float sum = 0.0f;
-        const uint16_t *two = static_cast<const uint16_t *>(a.h) + (size_t)t * 2 * a.R + threadIdx.x;
-        if (!a.splits) sum = bf16_to_f32(two[0]) + bf16_to_f32(two[a.R]);
-#pragma unroll 8
-        for (int s = 0; s < a.splits; ++s) sum += static_cast<const float *>(a.h)[((size_t)s * a.M + t) * a.R + threadIdx.x];
-        h[threadIdx.x] = sum;
-    }
-    __syncthreads();
-    while (n < a.N) {
-        float d = 0.0f;
-        auto add = [&](const uint4 &q, int i) {
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                d = fmaf(h[8 * i + 2 * j], bf16_lo(w[j]), d);
-                d = fmaf(h[8 * i + 2 * j + 1], bf16_hi(w[j]), d);
-            }
-        };
-        if (has) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (8 * i < a.R) add(v[i], i);
-            for (int i = kAhead; i < a.R / 8; ++i) add(__ldg(reinterpret_cast<const uint4 *>(B + n * a.R) + i), i);
+    pdl_wait();
+    float h[8] = {};
+    if (has) {
+        const float4 *hs = reinterpret_cast<const float4 *>(static_cast<const float *>(a.h) + (size_t)t * a.R + 8 * p);
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s, hs += (size_t)a.M * a.R / 4) {
+            const float4 lo = hs[0], hi = hs[1];
+            h[0] += lo.x, h[1] += lo.y, h[2] += lo.z, h[3] += lo.w;
+            h[4] += hi.x, h[5] += hi.y, h[6] += hi.z, h[7] += hi.w;
         }
-        static_cast<uint16_t *>(a.out)[(size_t)t * a.N + n] = f32_to_bf16(y + d);
-        n += (long long)gridDim.y * kOuterThreads;
-        load();
+    }
+    for (; n - q < a.N; n += step, load()) {
+        float y[kSets];
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const long long i = n + 32 * s + p * kRows;
+            y[s] = i < a.N ? a.y[(size_t)t * a.N + i] : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            float d[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const uint4 b = v[s][j];
+                d[j] = h[0] * bf16_lo(b.x);
+                d[j] = fmaf(h[1], bf16_hi(b.x), d[j]);
+                d[j] = fmaf(h[2], bf16_lo(b.y), d[j]);
+                d[j] = fmaf(h[3], bf16_hi(b.y), d[j]);
+                d[j] = fmaf(h[4], bf16_lo(b.z), d[j]);
+                d[j] = fmaf(h[5], bf16_hi(b.z), d[j]);
+                d[j] = fmaf(h[6], bf16_lo(b.w), d[j]);
+                d[j] = fmaf(h[7], bf16_hi(b.w), d[j]);
+            }
+#pragma unroll
+            for (int w = G / 2; w; w >>= 1)
+#pragma unroll
+                for (int j = 0; j < w; ++j) {
+                    const bool upper = lane & w;
+                    const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? d[j] : d[j + w], w);
+                    d[j] = (upper ? d[j + w] : d[j]) + other;
+                }
+            const long long i = n + 32 * s + p * kRows;
+            if (i < a.N) static_cast<uint16_t *>(a.out)[(size_t)t * a.N + i] = f32_to_bf16(y[s] + d[0]);
+        }
     }
 }
 
@@ -224,18 +252,23 @@ int launch(void (*f)(const LoraArgs), dim3 grid, int threads, const LoraArgs &a,
     return (int)cudaLaunchKernelEx(&cfg, f, a);
 }
 
+// Warps of a block of the inner kernel: eight up to two waves of blocks (65 x 4096 x 4096 r16 30.9 us, 32.0 with four), four
+// above (1024 x 2048 x 2048 r16 28.3, 33.0 with eight; 435 x 377 x 5944 r32 38.9 and 41.8).
+int inner_warps(int M, int R) { return (long long)M * (R / kRanks) <= 8 * kGb300Sms ? 8 : 4; }
+
 }  // namespace
 
-// Blocks for each SM eight times over, none below a step of K.
+// Parts of K: as many as leave all blocks resident at once (four an SM), each long enough for the warps of a block.
 int lora_splits(int M, int K, int R) {
-    const long long blocks = (long long)M * (R / kRanks), want = (8 * kGb300Sms + blocks - 1) / blocks;
-    const long long most = K / (256 * kInnerWarps) < 8 ? K / (256 * kInnerWarps) : 8, s = want < most ? want : most;
-    return s < 1 ? 1 : (int)s;
+    const int blocks = M * (R / kRanks), want = 4 * kGb300Sms / blocks;  // (M <= 64)
+    const int each = 256 * inner_warps(M, R), most = (K + each - 1) / each, s = want < most ? want : most;
+    return s < 1 ? 1 : s > 8 ? 8 : s;
 }
 
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream) {
     const dim3 grid((unsigned)a.M, (unsigned)(a.splits ? a.splits : 1), (unsigned)(a.R / kRanks));
-    return launch(lora_inner_kernel, grid, 32 * kInnerWarps, a, flags, stream);
+    const int warps = inner_warps(a.M, a.R);
+    return launch(warps == 8 ? lora_inner_kernel<8> : lora_inner_kernel<4>, grid, 32 * warps, a, flags, stream);
 }
 
 int init_lora() {
@@ -257,13 +290,18 @@ int launch_lora_rows(const LoraArgs &a, const void *w, const void *bias, uint32_
     attr[0].val.programmaticStreamSerializationAllowed = pdl_attr_of(flags);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, a.M == 1 ? lora_rows_kernel<1> : lora_rows_kernel<2>, a, static_cast<const uint16_t *>(w), static_cast<const uint16_t *>(bias));
+    return (int)cudaLaunchKernelEx(&cfg, a.M == 1 ? lora_rows_kernel<1> : lora_rows_kernel<2>, a,
+                                   static_cast<const uint16_t *>(w), static_cast<const uint16_t *>(bias));
 }
 
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {
-    const int blocks = (a.N + kOuterThreads - 1) / kOuterThreads;
+    int g = 1;
+    while (8 * g < a.R) g *= 2;
+    const long long outputs = (long long)outer_sets(g) * kOuterThreads, blocks = (a.N + outputs - 1) / outputs;
     const dim3 grid((unsigned)a.M, (unsigned)(blocks < 65535 ? blocks : 65535));
-    return launch(lora_outer_kernel, grid, kOuterThreads, a, flags, stream);
+    auto f = g == 1 ? lora_outer_kernel<1> : g == 2 ? lora_outer_kernel<2> : g == 4 ? lora_outer_kernel<4>
+           : g == 8 ? lora_outer_kernel<8> : lora_outer_kernel<16>;
+    return launch(f, grid, kOuterThreads, a, flags, stream);
 }
 
 }  // namespace bf16l
