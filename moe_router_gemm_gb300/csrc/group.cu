@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_kernel(const GroupArgs a) {
 
     for (int e = tid; e < kWarps * a.cols; e += kThreads) sm[e] = 0;
     __syncthreads();
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // (after the wait: the next kernel may rely on all that came before this one)
 
     // A step's key, and its place among the warp's of its group.
     auto count_step = [&](int key) {
