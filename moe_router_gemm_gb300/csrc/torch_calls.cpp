@@ -77,6 +77,14 @@ Tensor make(const Tensor &like, at::ScalarType type, at::IntArrayRef shape) {
     return at::empty(shape, like.options().dtype(type));
 }
 
+// A dense tensor of `base`'s type inside its memory, from element `first` (an allocation takes over a microsecond, this 0.2).
+Tensor part_of(const Tensor &base, int64_t first, at::IntArrayRef shape) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
+    impl->set_sizes_contiguous(shape);
+    impl->set_storage_offset(first);
+    return Tensor(std::move(impl));
+}
+
 bf16l_stream_t stream_of(const Tensor &t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
 PyObject *none() { Py_RETURN_NONE; }
@@ -299,9 +307,11 @@ PyObject *group_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
     int st;
     {
         const Unlocked unlocked;
-        offsets = make(*ids, at::kInt, {groups + 1});
-        rows = make(*ids, at::kInt, {T * k});
-        place = make(*ids, at::kInt, ids->sizes());
+        const int64_t rows_at = (groups + 1 + 63) / 64 * 64, place_at = rows_at + (T * k + 63) / 64 * 64;  // (256 bytes)
+        const Tensor all = make(*ids, at::kInt, {place_at + T * k});
+        offsets = part_of(all, 0, {groups + 1});
+        rows = part_of(all, rows_at, {T * k});
+        place = part_of(all, place_at, ids->sizes());
         st = g_group(static_cast<const int32_t *>(ids->const_data_ptr()), T, (int)k, groups,
                      static_cast<int32_t *>(offsets.data_ptr()), static_cast<int32_t *>(rows.data_ptr()),
                      static_cast<int32_t *>(place.data_ptr()), flags, stream_of(*ids));

@@ -364,6 +364,81 @@ def test_streams_and_graphs_of_the_adapters(lib):
     assert all(torch.equal(a, b) for a, b in zip(o, want))
 
 
+@pytest.mark.parametrize("flags", [0, 2])
+@pytest.mark.parametrize("M,N,K", [(1, 2000, 4096), (2, 2000, 2048), (16, 2000, 2048), (60, 1100, 2048), (100, 1100, 2048), (700, 500, 520)])
+def test_operands_written_just_before(lib, M, N, K, flags):
+    """What the kernel before writes (each operand in turn comes last) is what the adapters' linear reads, on one workspace
+    and with calls right behind one another, eager and in a graph."""
+    R, L = 16, 5
+    problems = [_lora_problem(M, N, K, R, L, seed) for seed in (1, 2, 3)]
+    names = ("x", "w", "a", "b")
+    space = torch.empty(lib.lora_workspace(M, N, K, R, L), dtype=torch.uint8, device=DEV)
+
+    def call(v, ids, scale, out=None):
+        return lib.bf16_linear_lora(v["x"], v["w"], v["a"], v["b"], ids, scale=scale, out=out, workspace=space, flags=flags)
+
+    want = [call(v, v["ids"], v["scale"]) for v in problems]
+    torch.cuda.synchronize()
+    now = {n: torch.zeros_like(problems[0][n]) for n in names}
+    ids = torch.zeros_like(problems[0]["ids"])
+    scale = torch.zeros_like(problems[0]["scale"])
+    one = {n: torch.arange(now[n].numel() // now[n].shape[-1], device=DEV, dtype=torch.int32)[:, None] for n in names}
+
+    def copy(name, v):  # by a kernel that lets the next one start early
+        lib.combine_rows(v[name].reshape(-1, v[name].shape[-1]), one[name], out=now[name].view(-1, now[name].shape[-1]), flags=flags)
+
+    outs = [torch.zeros_like(want[0]) for _ in range(4 * len(problems))]
+
+    def chain():
+        i = 0
+        for last in names:
+            for v in problems:
+                ids.copy_(v["ids"])
+                scale.copy_(v["scale"])
+                for n in names:
+                    if n != last:
+                        copy(n, v)
+                copy(last, v)
+                call(now, ids, scale, outs[i])
+                i += 1
+
+    for _ in range(3):
+        chain()
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            assert torch.equal(o, want[i % len(problems)]), i
+            o.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i % len(problems)]), i
+    assert lib.device_status() == 0
+
+
+def test_groups_are_tensors_of_their_own(lib):
+    ids = torch.randint(0, 5, (67, 3), generator=_gen(1), device=DEV, dtype=torch.int32)
+    got = lib.group_rows(ids, 5)
+    assert [tuple(v.shape) for v in got] == [(6,), (201,), (67, 3)] and all(v.is_contiguous() for v in got)
+    kept = [v.clone() for v in got]
+    for i, v in enumerate(got):  # one filled, the others stay
+        v.fill_(-7)
+        assert all(torch.equal(a, b) for a, b in zip(got[i + 1:], kept[i + 1:]))
+    with torch.inference_mode():
+        assert all(torch.equal(a, b) for a, b in zip(lib.group_rows(ids, 5), kept))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = lib.group_rows(ids, 5)
+    ids.copy_(ids.flip(0))
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(again, lib.group_rows(ids, 5)))
+    got = lib.group_rows(ids[:0], 5)
+    assert [tuple(v.shape) for v in got] == [(6,), (0,), (0, 3)] and not got.offsets.any()
+
+
 def test_two_streams_at_once(lib):
     """Calls on two streams, each with its own workspace, give what they give one after the other."""
     p = [_problem(T, 4, 9, 500, 712, T, True, True) for T in (300, 3)]
