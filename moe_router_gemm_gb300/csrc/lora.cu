@@ -4,8 +4,8 @@
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
 // spreads over the SMs: the inner one takes four ranks of a row a block, and splits K over more blocks as long as all are
 // resident at once; the outer one adds those sums, in order, when it reads them.  The inner one also asks L2 for B_a, and the
-// outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with rank 32: 18.2 us, of
-// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.7 (6.6), 64 x 4096 x 4096 with rank 64 27.5 (16.1).
+// outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with rank 32: 17.9 us, of
+// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with rank 64 26.0 (16.1).
 #include <cuda_runtime.h>
 
 #include "grouped.cuh"
@@ -16,7 +16,7 @@ namespace bf16l {
 namespace {
 
 constexpr int kRanks = 4;  // of a block of the inner kernel
-constexpr int kOuterThreads = 128;
+constexpr int kOuterThreads = 128, kOuterBlocks = 9;
 // (A warp has at least four loads of 512 bytes in flight.)
 __host__ __device__ constexpr int outer_sets(int g) { return g < 4 ? 4 / g : 1; }
 
@@ -106,16 +106,17 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
     const int t = blockIdx.x, id = __ldg(a.ids + t);
     const bool has = (unsigned)id < (unsigned)a.L && 8 * p < a.R;  // (R % 8 == 0)
     const uint16_t *B = static_cast<const uint16_t *>(a.b) + (has ? (size_t)id * a.N * a.R + 8 * p : 0);
-    const long long step = (long long)gridDim.y * (kSets * kOuterThreads);
-    long long n = ((long long)blockIdx.y * (kOuterThreads / 32) + (threadIdx.x >> 5)) * (32 * kSets) + q;
+    const unsigned N = (unsigned)a.N, step = gridDim.y * (kSets * kOuterThreads);  // (together below 2^32)
+    unsigned n = (blockIdx.y * (kOuterThreads / 32) + (threadIdx.x >> 5)) * (32 * kSets) + q;
     uint4 v[kSets][G];
     auto load = [&]() {
+        const uint16_t *row = B + (size_t)n * a.R;
 #pragma unroll
         for (int s = 0; s < kSets; ++s)
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const long long i = n + 32 * s + j * kRows;
-                v[s][j] = has && i < a.N ? __ldg(reinterpret_cast<const uint4 *>(B + i * a.R)) : make_uint4(0, 0, 0, 0);
+                const int i = 32 * s + j * kRows;
+                v[s][j] = has && n + i < N ? __ldg(reinterpret_cast<const uint4 *>(row + i * a.R)) : make_uint4(0, 0, 0, 0);
             }
     };
     load();
@@ -130,12 +131,14 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             h[4] += hi.x, h[5] += hi.y, h[6] += hi.z, h[7] += hi.w;
         }
     }
-    for (; n - q < a.N; n += step, load()) {
+    const float *from = a.y + (size_t)t * N;
+    uint16_t *to = static_cast<uint16_t *>(a.out) + (size_t)t * N;
+    for (; n - q < N; n += step, load()) {
         float y[kSets];
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
-            const long long i = n + 32 * s + p * kRows;
-            y[s] = i < a.N ? a.y[(size_t)t * a.N + i] : 0.0f;
+            const unsigned i = n + 32 * s + p * kRows;
+            y[s] = i < N ? from[i] : 0.0f;
         }
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
@@ -160,8 +163,8 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
                     const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? d[j] : d[j + w], w);
                     d[j] = (upper ? d[j + w] : d[j]) + other;
                 }
-            const long long i = n + 32 * s + p * kRows;
-            if (i < a.N) static_cast<uint16_t *>(a.out)[(size_t)t * a.N + i] = f32_to_bf16(y[s] + d[0]);
+            const unsigned i = n + 32 * s + p * kRows;
+            if (i < N) to[i] = f32_to_bf16(y[s] + d[0]);
         }
     }
 }
@@ -305,8 +308,11 @@ int launch_lora_rows(const LoraArgs &a, const void *w, const void *bias, uint32_
 int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {
     int g = 1;
     while (8 * g < a.R) g *= 2;
-    const long long outputs = (long long)outer_sets(g) * kOuterThreads, blocks = (a.N + outputs - 1) / outputs;
-    const dim3 grid((unsigned)a.M, (unsigned)(blocks < 65535 ? blocks : 65535));
+    const int outputs = outer_sets(g) * kOuterThreads, blocks = (int)(((long long)a.N + outputs - 1) / outputs);
+    // Blocks for one wave, each going on along N: 64 x 7168 x 7168 r128 51.7 us, 53.9 with a block for every 128 outputs, 64 x
+    // 14336 x 4096 r16 36.3 and 37.0.
+    const int most = kOuterBlocks * kGb300Sms / a.M;  // (M <= 64)
+    const dim3 grid((unsigned)a.M, (unsigned)(blocks < most ? blocks : most));
     auto f = g == 1 ? lora_outer_kernel<1> : g == 2 ? lora_outer_kernel<2> : g == 4 ? lora_outer_kernel<4>
            : g == 8 ? lora_outer_kernel<8> : lora_outer_kernel<16>;
     return launch(f, grid, kOuterThreads, a, flags, stream);
