@@ -272,8 +272,8 @@ int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, ui
     const cuuint32_t box[4] = {box_cols, box_rows, box_halves, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return (int)enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    box_cols == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 int make_tmap_bf16_blocks(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,

@@ -259,8 +259,8 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     int32_t *status = nullptr;
     const int st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
-    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr, nullptr, 0,
-                           static_cast<float *>(workspace), need ? grouped_splits((int)P, groups, N, K, swiglu) : 1};
+    const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr,
+                           nullptr, 0, static_cast<float *>(workspace), need ? grouped_splits((int)P, groups, N, K, swiglu) : 1};
     return result(launch_grouped(a, dev.num_sms, flags, stream, status));
 }
 
@@ -288,10 +288,10 @@ namespace {
 // How a linear with adapters is done, by sizes alone, and the parts of its workspace.
 //   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, or rows in adapter order
 //     on tensor cores, by estimate: (1.5 + K / 1400) us for each 1824 blocks of four ranks of a row, 6 + K / 320 us.
-//     (Whole calls, us: 435 x 377 x 5944 with rank 32 33.1 and 40.6, 2000 x 512 x 512 with rank 64 47.2 and 22.4.)
+//     (Whole calls, us: 435 x 377 x 5944 with rank 32 34.9 and 42.0, 2000 x 512 x 512 with rank 64 44.7 and 21.6.)
 //   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows; for few rows the dense
-//     linear's own kernels, which split K, into fp32 and the adapters' share after it (61 x 2112 x 7168 with rank 32: 20 us,
-//     38 fused; 281 x 322 x 2880: 42 and 20).
+//     linear's own kernels, which split K, into fp32 and the adapters' share after it (61 x 2112 x 7168 with rank 32: 18 us,
+//     30 fused; 65 x 4096 x 4096 with rank 16: 35 and 29; 281 x 322 x 2880 with rank 32: 43 and 24).
 struct LoraWay {
     bool cores, fused;
     size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product or its parts

@@ -3,8 +3,9 @@
 //
 // Grouping is a stable counting sort of n small keys.  Each warp has a run of consecutive keys and a histogram of its own
 // in shared memory; equal keys of a step of 32 find one another by ballots over the key's bits (match.any goes through the
-// different keys one by one: 8192 x 8 keys of 256 groups 10.8 us), so that a histogram has one writer and positions do not
-// depend on timing.  The positions then follow from three sums: over the warps of a CTA, over the CTAs of
+// different keys one by one: 8192 x 8 keys of 256 groups 10.8 us, 7.7 so), so that a histogram has one writer and positions
+// do not depend on timing.  It moves less than a megabyte: what bounds it is the chain of a launch, the ballots, three sums and
+// two cluster barriers (16 x 8 keys in one CTA 2.6 us).  The positions then follow from three sums: over the warps of a CTA, over the CTAs of
 // the one cluster (through distributed shared memory), over the groups.
 #include <cuda_runtime.h>
 
@@ -18,7 +19,7 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 32, kThreads = 32 * kWarps;
 constexpr int kCluster = 16;
-constexpr int kKept = 4;  // steps whose keys a warp has in registers; all of its steps up to 32 * kWarps * kCluster * kKept keys
+constexpr int kKept = 4;  // steps whose keys a warp has in registers: all, up to 32 * kWarps * kCluster * kKept keys
 
 struct GroupArgs {
     const int32_t *ids;
@@ -182,9 +183,9 @@ struct Vec<2> {
 constexpr int kCombineThreads = 128, kAtOnce = 8;
 
 // out[t] = sum over j of weights[t][j] * y[place[t][j]] (+ addend[t]), one vector of BYTES a thread, in fp32, in the order
-// of j, rounded once.  kAtOnce rows' loads go out before the first is used: 8192 x 8 x 7168 with an addend 275 us with one
-// after the other.
-// PER vectors a thread, kCombineThreads apart, where they are narrow (odd H).
+// of j, rounded once.  HBM bounds it: every row of y is read once, by one thread for each of its vectors.  kAtOnce rows' loads
+// go out before the first is used: 8192 x 8 x 7168 with an addend 180 us, 96% of the copy rate (275 one after the other).
+// PER vectors a thread, kCombineThreads apart, where they are narrow (odd H): 6418 x 3 x 477 10 us (28 with one).
 template <int BYTES, int PER>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict__ place, const float *__restrict__ weights,

@@ -11,8 +11,9 @@
 //   * warp 0: TMA producer: two chunks of 128 bytes of K a stage of this CTA's own W rows (a 4-D map: a row past the
 //     group's weight is zero, not the next group's) and of its half of the tile's rows of x, by boxes of 16 to 128 rows;
 //   * warps 10-13, where `rows` gives the rows of x: 16-byte asynchronous copies from where they are, so that no sorted copy
-//     of x is made; they arrive by themselves on a barrier of the CTA, and warp 14 passes that on to the leader's.  (TMA's gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs
-//     leaves: 8192 rows of 8 choices, 128 groups, 2 x 2048 x 7168: 9.05 ms.);
+//     of x is made; they arrive by themselves on a barrier of the CTA, and warp 14 passes that on to the leader's.  (TMA's
+//     gather of four rows an instruction takes about 12 clocks a row, three times what a stage of MMAs leaves: 8192 rows of 8
+//     choices, 128 groups, 2 x 2048 x 7168: 9.05 ms, 2.5 so.);
 //   * warp 1 of the even CTA: MMA issuer; warps 2-9: epilogue, two for each quarter of the TMEM lanes;
 //   * fp32 accumulators double-buffered in TMEM;
 //   * SwiGLU: boxes of 16 gate rows and their 16 up rows, so that a warp's 32 lanes hold both: one shuffle for two rows
@@ -27,6 +28,10 @@
 //     x is.
 // Where the tiles are too few for the SMs (PARTIAL), each tile's K is split into parts of their own tiles, which leave their
 // fp32 accumulators in a workspace, and sum_kernel adds them up in order.
+// What bounds it: with a few rows a group HBM, every sought weight being read once (512 rows over 101 weights of 7168 x 2048
+// 429 us, 8 rows over 8 of 2 x 2048 x 7168 72 us: 102% and 96% of the copy rate); with hundreds of rows a group the tensor
+// cores: 1.74 to 1.84 PFLOP/s over one to eight groups while the clock holds, 1.55 over 128 uneven ones, 1.4 where the power
+// limit takes the clock to 1.4 GHz.
 // Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any remote arrival or copy) and one
 // before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>
@@ -637,7 +642,8 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
             const int n = MODE == kInner && in_tile >= wt / 2 ? a.N : t.m * wt + (int)rank * (wt / 2) + in_tile;
             const int wide = SWIGLU ? 2 * a.N : a.N, wrow = SWIGLU && lane >= 16 ? a.N + n : n;
             const float f = MODE == kInner && a.scale ? __ldg(a.scale + t.e) : 1.0f;
-            const float lb = MODE != kOuter && bias && n < a.N && (!PARTIAL || t.part == 0) ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
+            const bool biased = MODE != kOuter && bias && n < a.N && (!PARTIAL || t.part == 0);
+            const float lb = biased ? bf16_to_f32(__ldg(bias + (size_t)t.e * wide + wrow)) : 0.0f;
             const bool ok = mbar_wait(&sh.acc_full[b], (tile >> 1) & 1, status, kSiteAccum);
             tc_fence_after();
             const bool have = __all_sync(kAll, ok && !*((volatile int32_t *)&sh.aborted));
@@ -803,7 +809,8 @@ int smem_of(int mode, int bt) {
 }
 static_assert(sizeof(GroupedShared) >= kWBytes / 2, "kInner's MMAs read past their rows, within shared memory");
 
-using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int, int32_t *);
+using GroupedFn = void (*)(const CUtensorMap, const CUtensorMap, const RowMaps, const GroupedArgs, int, int, int, int,
+                           int32_t *);
 
 GroupedFn pick(int mode, bool gather, bool partial) {
     switch (mode) {
@@ -910,7 +917,8 @@ int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int nu
     for (int i = mode == kOuter ? 3 : 0; i < 4 && !r && (!a.rows || mode == kOuter); ++i)
         r = make_tmap_bf16_2d(&tx.of[i], a.x, (uint64_t)a.x_rows, K, 16u << i, kChunkK, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (!r && mode == kOuter) r = make_tmap_bf16_stack(&tb, a.b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
+    if (!r && mode == kOuter)
+        r = make_tmap_bf16_stack(&tb, a.b, (uint64_t)a.groups, 1, N, (uint64_t)a.R, 1, (uint32_t)wt / 2, kRank);
     if (r) return (int)cudaErrorInvalidValue;
     // A cluster that cannot be resident with the others would run its tiles after them.
     const long long units = ((long long)a.P / bt + full) * ((a.N + wt - 1) / wt) *

@@ -110,7 +110,7 @@ __device__ __forceinline__ void two_bf16(float v, uint32_t &high, uint32_t &low)
 }
 
 // Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
-// box_halves x 1 elements, in the swizzle of box_cols' bytes (128 or 32).  Defined in api.cu.  Returns a CUresult value (0 on success).
+// box_halves x 1 elements, in the swizzle of box_cols' bytes (128 or 32).  Defined in api.cu; a CUresult (0 on success).
 int make_tmap_bf16_stack(CUtensorMap *map, const void *base, uint64_t planes, uint64_t halves, uint64_t rows, uint64_t cols,
                          uint32_t box_halves, uint32_t box_rows, uint32_t box_cols);
 // The same with the rows in blocks of block_rows (a divisor of rows): a box is box_blocks blocks of every half, in shared

@@ -5,7 +5,7 @@
 // spreads over the SMs: the inner one takes four ranks of a row a block, and splits K over more blocks as long as all are
 // resident at once; the outer one adds those sums, in order, when it reads them.  The inner one also asks L2 for B_a, and the
 // outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with rank 32: 17.9 us, of
-// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with rank 64 26.0 (16.1).
+// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with rank 64 26.0.
 #include <cuda_runtime.h>
 
 #include "grouped.cuh"
@@ -20,17 +20,17 @@ constexpr int kOuterThreads = 128, kOuterBlocks = 9;
 // (A warp has at least four loads of 512 bytes in flight.)
 __host__ __device__ constexpr int outer_sets(int g) { return g < 4 ? 4 / g : 1; }
 
-// A block sums kRanks ranks of a row over a part of K, its warps taking 256 elements in turn.  Eight warps of a block and parts
-// of K in multiples of 256 took 0.5 to 1 us less than four warps and multiples of 1024 (8 x 4096 x 4096 r16 11.3 -> 10.3 us,
-// 61 x 2112 x 7168 r32 20.0 -> 19.1) where the blocks are few, and 1 to 4 us more where they are many (inner_warps);
-// eight ranks a block, sixteen warps or more registers were slower.
+// A block sums kRanks ranks of a row over a part of K, its warps taking 256 elements in turn.  Eight warps of a block and
+// parts of K in multiples of 256 took 0.5 to 1 us less than four warps and multiples of 1024 (8 x 4096 x 4096 r16 11.3 -> 10.3
+// us, 61 x 2112 x 7168 r32 20.0 -> 19.1) where the blocks are few, and 1 to 5 us more where they are many (inner_warps); eight
+// ranks a block, sixteen warps or more registers were slower.
 template <int kInnerWarps>
 __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const LoraArgs a) {
     __shared__ float part[kInnerWarps][kRanks];
     // The next kernel may start once this one has waited: it then reads nothing but h that could still be written.  Where the
     // rows are ordered by adapter, the kernel before is the one that orders them, which has waited for all others and which
-    // nothing here depends on: the two run side by side, and one block waits for it at the end, for whoever waits for this one (256 x
-    // 14336 x 4096 r16 50.2 -> 47.2 us; asking L2 for B's rows there, 26 MB, took 2 us more).
+    // nothing here depends on: the two run side by side, and one block waits for it at the end, for whoever waits for this
+    // one (256 x 14336 x 4096 r16 50.2 -> 47.2 us; asking L2 for B's rows there, 26 MB, took 2 us more).
     if (a.splits) pdl_wait();
     pdl_launch_dependents();
     const bool last = !a.splits && (blockIdx.x | blockIdx.z) == 0;
