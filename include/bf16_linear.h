@@ -634,8 +634,8 @@ size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
  * offsets and rows are read on the device: offsets rise, from 0 or more to at most P;
  * where they do not, no position outside 0 .. P - 1 is read or written, and which group
  * a position inside belongs to is not defined.  Rows of out that belong to no group are
- * left as they were.  A value of rows outside
- * 0 .. x_rows - 1 is taken as the nearest row.  rows NULL needs x_rows == P.
+ * left as they were.  A value of rows outside 0 .. x_rows - 1 is taken as the nearest
+ * row.  rows NULL needs x_rows == P.
  * K % 8 == 0, groups <= 1024, N and K <= 2^24 (else BF16L_EUNSUPPORTED).  A group's
  * rows give the same bits whatever the other groups hold.  Pointers of bf16 data
  * 16-byte aligned.  BF16L_FLAG_PDL has no effect: which weights are read follows from
@@ -654,8 +654,9 @@ size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
  *     out[t] = RNE_bf16( x[t] @ w^T (+ bias) + s * (x[t] @ a[id]^T) @ b[id]^T ),
  *     id = ids[t], s = scale[id] (1 when scale is NULL);
  * a row whose id lies outside 0 .. L - 1 has no adapter.  x[M][K], w[N][K], bias[N],
- * a[L][R][K], b[L][N][R], out[M][N] bf16, scale[L] fp32, ids[M].  The inner values
- * and all sums are held in 32 bits, rounded once.  K % 8 == 0, R % 8 == 0, R <= 128, L <= 1024, N
+ * a[L][R][K], b[L][N][R], out[M][N] bf16, scale[L] fp32, ids[M].  All sums are fp32;
+ * the inner values x[t] @ a[id]^T are fp32 too, or (many rows) two bf16 values, within
+ * 2^-18 of it; out is rounded once.  K % 8 == 0, R % 8 == 0, R <= 128, L <= 1024, N
  * and K <= 2^24 (else BF16L_EUNSUPPORTED).  `workspace` (256-byte aligned, needs no
  * initialisation; one call at a time): bf16_linear_lora_workspace(M, N, K, R, L)
  * bytes; a smaller one is BF16L_EINVAL.

@@ -291,6 +291,12 @@ def test_linear_lora(lib, shape, runs):
         assert torch.equal(_check_lora(lib, p, workspace=space), got)
 
 
+@pytest.mark.parametrize("R", range(8, 129, 8))
+@pytest.mark.parametrize("M,N", [(3, 777), (17, 130), (64, 5001)])
+def test_lora_of_every_rank(lib, R, M, N):
+    _check_lora(lib, _lora_problem(M, N, 264, R, 6, R, bias=M == 17))
+
+
 def test_lora_not_finite(lib):
     """A NaN in one adapter reaches its rows alone; rows without an adapter have none of them."""
     for M, N in ((12, 72), (600, 72), (600, 5000), (2000, 1000)):
