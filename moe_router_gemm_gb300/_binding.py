@@ -840,7 +840,7 @@ def group_rows(ids, groups: int, *, offsets=None, rows=None, place=None, flags: 
     """The pairs of ids[tokens, k] or ids[tokens] (int32) ordered by id, equal ids in their own order (bf16_group_rows):
     offsets int32 [groups + 1], where each group's positions start; rows int32 [tokens * k], the token of each position, -1
     past offsets[groups]; place int32 like ids, each pair's position, -1 for an id outside 0 .. groups - 1, which is left
-    out."""
+    out.  Outputs that the call makes may lie in one allocation."""
     if offsets is rows is place is stream is None and _calls is not None:
         r = _calls.group_rows(ids, groups, flags)
         if type(r) is tuple:

@@ -171,9 +171,10 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
 
 // One or two rows: a warp for each W row, its first kAhead vectors of W, and B's row, on their way while the inner kernel
 // still runs (which has let this one start when all kernels before it were done); then the row's h, and one sum over the
-// warp for the shared product and the adapter's.  x in shared memory.  1 x 4096 x 4096 with rank 16 8.7 us (floor 5.0; 9.9
-// with the dense linear's kernel and the outer one), 1 x 2112 x 7168 with rank 32 8.6 (11.3), 1 x 1024 x 1024 3.1 (5.7).
-// Three or four rows took longer so than by the other form, 16 vectors ahead (which halve the resident warps) 11.1.
+// warp for the shared product and the adapter's.  x in shared memory.  1 x 4096 x 4096 with rank 16 8.3 us (floor 5.0; 9.9
+// with the dense linear's kernel and the outer one), 1 x 2112 x 7168 with rank 32 8.6 (11.3), 1 x 1024 x 1024 3.2 (5.7).
+// Three or four rows took longer so than by the other form, 16 vectors ahead (which halve the resident warps) 11.1, and one
+// kernel whose clusters of eight CTAs each work the inner values out 9.0.
 constexpr int kRowWarps = 8, kAhead = 8;
 template <int M>
 __global__ void __launch_bounds__(32 * kRowWarps, 4) lora_rows_kernel(const LoraArgs a, const uint16_t *__restrict__ w,
