@@ -291,20 +291,29 @@ namespace {
 //     (Whole calls, us: 435 x 377 x 5944 with rank 32 34.9 and 42.0, 2000 x 512 x 512 with rank 64 44.7 and 21.6.)
 //   fused: the shared product and the adapters' by one tensor-core kernel on tiles of 256 rows; for few rows the dense
 //     linear's own kernels, which split K, into fp32 and the adapters' share after it (61 x 2112 x 7168 with rank 32: 18 us,
-//     30 fused; 65 x 4096 x 4096 with rank 16: 35 and 29; 281 x 322 x 2880 with rank 32: 43 and 24).
+//     30 fused; 281 x 322 x 2880 with rank 32: 43 and 24).
+//   parted: between the two, the grouped linear's kernel with the rows on its N side, into fp32 parts, and the adapters' share
+//     after it, for which every row reads its own B: up to kPartedRows rows and kPartedWork of M N R (us, fused in brackets:
+//     65 x 4096 x 4096 r16 21.0 (28.8), 128 x 4096 x 4096 r16 25.2 (34.0), 96 x 2112 x 7168 r32 27.8 (35.2), 128 x 2048 x 7168
+//     r64 35.0 (37.5); past the bounds 128 x 14336 x 4096 r16 43.8 (41.7), 256 x 4096 x 4096 r16 34.7 (33.8)).
+constexpr int kPartedRows = 160;
+constexpr uint64_t kPartedWork = 20ull << 20;
 struct LoraWay {
-    bool cores, fused;
+    bool cores, fused, parted;
+    int parts, pitch;
     size_t order, h, y;  // bytes: the rows' order, the inner values, the shared product or its parts
 };
 LoraWay lora_way(int M, int N, int K, int R, int L) {
     const uint64_t m = (uint64_t)M, r = (uint64_t)R;
     LoraWay w;
-    w.fused = M > 64;
+    w.parted = M > 64 && M <= kPartedRows && m * r * (uint64_t)N <= kPartedWork;
+    w.fused = M > 64 && !w.parted;
     w.cores = !w.fused || m * r / 4 * (2100 + (uint64_t)K) * 320 <= 1824ull * 1400 * (1920 + (uint64_t)K);
-    w.order = w.fused ? up256(4 * ((size_t)L + 1)) + up256(4 * m) : 0;
+    w.order = w.fused ? up256(4 * ((size_t)L + 1)) + up256(4 * m) : w.parted ? 256 : 0;
     w.h = up256((w.fused ? 1 : (size_t)lora_splits(M, K, R)) * 4 * m * r);
-    const int parts = w.fused ? lora_outer_splits(M, N, K) : 1;
-    w.y = w.fused && parts == 1 ? 0 : up256((size_t)parts * 4 * m * (size_t)(parts > 1 ? sum_pitch(N) : N));
+    w.parts = w.fused ? lora_outer_splits(M, N, K) : w.parted ? lora_base_splits(M, N, K) : 1;
+    w.pitch = w.parted || w.parts > 1 ? sum_pitch(N) : N;
+    w.y = w.fused && w.parts == 1 ? 0 : up256((size_t)w.parts * 4 * m * (size_t)w.pitch);
     return w;
 }
 
@@ -381,8 +390,9 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     int32_t *offsets = reinterpret_cast<int32_t *>(p), *rows = reinterpret_cast<int32_t *>(p + up256(4 * ((size_t)L + 1)));
     float *y = reinterpret_cast<float *>(p + way.order + way.h);
     const LoraArgs args = {x, a, b, scale, ids, p + way.order, y, out, M, N, K, R, L,
-                           way.fused ? 0 : lora_splits(M, K, R), y};
-    if (way.order) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
+                           way.fused ? 0 : lora_splits(M, K, R), y,
+                           way.parts, way.pitch, way.parted ? offsets : nullptr};
+    if (way.fused) st = result(launch_group_rows(ids, M, 1, L, true, offsets, rows, nullptr, flags, stream));
     if (st == BF16L_OK)
         st = result(way.cores ? launch_lora_inner(args, flags, stream)
                               : launch_lora_inner_grouped(args, offsets, rows, dev.num_sms, flags, stream, status));
@@ -391,6 +401,10 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
         return result(launch_lora_outer_grouped(args, w, bias, offsets, rows, dev.num_sms, flags, stream, status));
     if (M <= kLoraRows && (int64_t)M * K * 2 <= kLoraRowsSmem)  // (few rows: cores, with splits)
         return result(launch_lora_rows(args, w, bias, flags, stream));
+    if (way.parted) {
+        st = result(launch_lora_base(args, w, bias, dev.num_sms, flags, stream, status));
+        return st != BF16L_OK ? st : result(launch_lora_outer(args, flags, stream));
+    }
     // The product may read its weights as soon as the inner kernel lets it start: that one has waited for all before it.
     bf16l_plan plan;
     const uint32_t early = flags & BF16L_FLAG_SERIAL ? flags : flags | BF16L_FLAG_PDL;

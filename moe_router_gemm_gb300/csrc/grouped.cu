@@ -903,7 +903,7 @@ int clusters_of(int num_sms) {
 
 // Tiles of up to bt rows and wt outputs; `full`: groups that may have rows.
 int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int num_sms, uint32_t flags, void *stream,
-                int32_t *status) {
+                int32_t *status, bool partial) {
     const bool swiglu = mode == kSwiglu;
     CUtensorMap tw, tb = {};
     RowMaps tx = {};
@@ -927,7 +927,7 @@ int launch_mode(int mode, const GroupedArgs &a, int bt, int wt, int full, int nu
     if (units < clusters) clusters = units;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config((int)clusters, a.rows != nullptr, smem_of(mode, bt), flags, stream, attr);
-    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr, a.splits > 1), tw, tb, tx, a, w_boxes, bt, wt,
+    return (int)cudaLaunchKernelEx(&cfg, pick(mode, a.rows != nullptr, partial), tw, tb, tx, a, w_boxes, bt, wt,
                                    stages_of(mode, bt), status);
 }
 
@@ -991,11 +991,23 @@ int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stre
     if (a.splits > 1) {
         GroupedArgs p = a;
         p.N = a.swiglu ? 2 * a.N : a.N;
-        const int r = launch_mode(kPlain, p, bt, 256, full, num_sms, flags, stream, status);
+        const int r = launch_mode(kPlain, p, bt, 256, full, num_sms, flags, stream, status, true);
         if (r) return r;
         return launch_sum(a.swiglu != 0, a.sums, a.offsets, a.groups, a.splits, a.P, a.N, a.out, num_sms, flags, stream);
     }
-    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status);
+    return launch_mode(a.swiglu ? kSwiglu : kPlain, a, bt, a.swiglu ? 128 : 256, full, num_sms, flags, stream, status, false);
+}
+
+// (the rows' number is known here: tiles of no more)
+int lora_base_splits(int M, int N, int K) {
+    const int bt = M <= 128 ? 128 : 256;
+    return parts_of(((long long)M + bt - 1) / bt * (((long long)N + 255) / 256), K);
+}
+int launch_lora_base(const LoraArgs &l, const void *w, const void *bias, int num_sms, uint32_t flags, void *stream,
+                     int32_t *status) {
+    const GroupedArgs a = {l.x, w, bias, l.span, nullptr, nullptr, l.M, l.M, 1, l.N, l.K, 0, nullptr, nullptr, nullptr, 0,
+                           l.sums, l.parts};
+    return launch_mode(kPlain, a, l.M <= 128 ? 128 : 256, 256, 1, num_sms, flags, stream, status, true);
 }
 
 int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
@@ -1005,7 +1017,7 @@ int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const i
     // One W tile, half of its rows each CTA's: rows of x so that there is a tile for each pair of SMs.
     const int clusters = clusters_of(num_sms);
     const int bt = l.M <= 32 * clusters ? 32 : l.M <= 64 * clusters ? 64 : l.M <= 128 * clusters ? 128 : 256;
-    return launch_mode(kInner, a, bt, (l.R + 15) / 16 * 16, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status);
+    return launch_mode(kInner, a, bt, (l.R + 15) / 16 * 16, l.M < l.L ? l.M : l.L, num_sms, flags, stream, status, false);
 }
 
 int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,
@@ -1013,7 +1025,7 @@ int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias
     const GroupedArgs a = {l.x, w, bias, offsets, rows, l.out, l.M, l.M, l.L, l.N, l.K, 0, nullptr, l.b, l.h, l.R,
                            l.sums, lora_outer_splits(l.M, l.N, l.K)};
     if (a.splits > 1) {
-        const int r = launch_mode(kOuter, a, 256, 128, 1, num_sms, flags, stream, status);
+        const int r = launch_mode(kOuter, a, 256, 128, 1, num_sms, flags, stream, status, true);
         if (r) return r;
         return launch_sum(false, a.sums, nullptr, 0, a.splits, a.P, a.N, a.out, num_sms, flags, stream);
     }
@@ -1030,7 +1042,7 @@ int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias
             wt = w0;
         }
     }
-    return launch_mode(kOuter, a, 256, wt, 1, num_sms, flags, stream, status);
+    return launch_mode(kOuter, a, 256, wt, 1, num_sms, flags, stream, status, false);
 }
 
 }  // namespace bf16l

@@ -3,9 +3,11 @@
 //
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
 // spreads over the SMs: the inner one takes four ranks of a row a block, and splits K over more blocks as long as all are
-// resident at once; the outer one adds those sums, in order, when it reads them.  The inner one also asks L2 for B_a, and the
-// outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with rank 32: 17.9 us, of
-// which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with rank 64 26.0.
+// resident at once; the outer one adds those sums, and the projection's where that comes in parts, in order, when it reads
+// them.  Up to 64 rows the inner one also asks L2 for B_a (more rows ask for the same ones: 128 x 14336 x 4096 r16 46.2 us,
+// 43.8 without), and the outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with
+// rank 32: 17.9 us, of which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with
+// rank 64 26.0.
 #include <cuda_runtime.h>
 
 #include "grouped.cuh"
@@ -37,11 +39,15 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
     const int t = blockIdx.x, s = blockIdx.y, splits = (int)gridDim.y, r0 = kRanks * (int)blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id = __ldg(a.ids + t);
+    if (a.span && threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) {
+        a.span[0] = 0;
+        a.span[1] = a.M;
+    }
     if ((unsigned)id >= (unsigned)a.L) {  // (its inner values are not read)
         if (last) pdl_wait();
         return;
     }
-    if (threadIdx.x == 0 && a.splits) {  // this block's part of B's rows, for the outer kernel
+    if (threadIdx.x == 0 && a.splits && !a.span) {  // this block's part of B's rows, for the outer kernel
         const int blocks = splits * (int)gridDim.z, i = s + splits * (int)blockIdx.z;
         const int n0 = (int)((long long)a.N * i / blocks), n1 = (int)((long long)a.N * (i + 1) / blocks);
         const uint16_t *b = static_cast<const uint16_t *>(a.b) + ((size_t)id * a.N + n0) * a.R;
@@ -131,14 +137,17 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             h[4] += hi.x, h[5] += hi.y, h[6] += hi.z, h[7] += hi.w;
         }
     }
-    const float *from = a.y + (size_t)t * N;
+    const float *from = a.y + (size_t)t * a.pitch;
+    const size_t plane = (size_t)a.M * a.pitch;
     uint16_t *to = static_cast<uint16_t *>(a.out) + (size_t)t * N;
     for (; n - q < N; n += step, load()) {
         float y[kSets];
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
             const unsigned i = n + 32 * s + p * kRows;
-            y[s] = i < N ? from[i] : 0.0f;
+            y[s] = 0.0f;
+#pragma unroll 4
+            for (int k = 0; i < N && k < a.parts; ++k) y[s] += from[k * plane + i];
         }
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
@@ -272,7 +281,7 @@ int inner_warps(int M, int R) { return (long long)M * (R / kRanks) <= 8 * kGb300
 
 // Parts of K: as many as leave all blocks resident at once (four an SM), each long enough for the warps of a block.
 int lora_splits(int M, int K, int R) {
-    const int blocks = M * (R / kRanks), want = 4 * kGb300Sms / blocks;  // (M <= 64)
+    const int blocks = M * (R / kRanks), want = 4 * kGb300Sms / blocks;  // (few rows)
     const int each = 256 * inner_warps(M, R), most = (K + each - 1) / each, s = want < most ? want : most;
     return s < 1 ? 1 : s > 8 ? 8 : s;
 }
@@ -312,7 +321,7 @@ int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream) {
     const int outputs = outer_sets(g) * kOuterThreads, blocks = (int)(((long long)a.N + outputs - 1) / outputs);
     // Blocks for one wave, each going on along N: 64 x 7168 x 7168 r128 51.7 us, 53.9 with a block for every 128 outputs, 64 x
     // 14336 x 4096 r16 36.3 and 37.0.
-    const int most = kOuterBlocks * kGb300Sms / a.M;  // (M <= 64)
+    const int wave = kOuterBlocks * kGb300Sms / a.M, most = wave > 1 ? wave : 1;
     const dim3 grid((unsigned)a.M, (unsigned)(blocks < most ? blocks : most));
     auto f = g == 1 ? lora_outer_kernel<1> : g == 2 ? lora_outer_kernel<2> : g == 4 ? lora_outer_kernel<4>
            : g == 8 ? lora_outer_kernel<8> : lora_outer_kernel<16>;

@@ -88,6 +88,9 @@ struct LoraArgs {
     void *out;
     int M, N, K, R, L, splits;
     float *sums;  // the shared product's parts, where lora_outer_splits is more than 1
+    // y as `parts` parts of K, rows `pitch` apart, still to be added up; `span`: where the inner kernel puts 0 and M
+    int parts, pitch;
+    int32_t *span;
 };
 int lora_splits(int M, int K, int R);
 int launch_lora_inner(const LoraArgs &a, uint32_t flags, void *stream);
@@ -96,6 +99,10 @@ int launch_lora_outer(const LoraArgs &a, uint32_t flags, void *stream);
 constexpr int kLoraRows = 2, kLoraRowsSmem = 48 * 1024;
 int init_lora();
 int launch_lora_rows(const LoraArgs &a, const void *w, const void *bias, uint32_t flags, void *stream);
+// The shared product into parts of y (sums), with span as its one group's offsets.
+int lora_base_splits(int M, int N, int K);
+int launch_lora_base(const LoraArgs &l, const void *w, const void *bias, int num_sms, uint32_t flags, void *stream,
+                     int32_t *status);
 int launch_lora_inner_grouped(const LoraArgs &l, const int32_t *offsets, const int32_t *rows, int num_sms, uint32_t flags,
                               void *stream, int32_t *status);
 int launch_lora_outer_grouped(const LoraArgs &l, const void *w, const void *bias, const int32_t *offsets, const int32_t *rows,

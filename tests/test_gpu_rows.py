@@ -297,6 +297,26 @@ def test_lora_of_every_rank(lib, R, M, N):
     _check_lora(lib, _lora_problem(M, N, 264, R, 6, R, bias=M == 17))
 
 
+@pytest.mark.parametrize("shape", [(65, 4096, 512, 16, 9), (128, 333, 4096, 8, 3), (129, 6, 8, 128, 2), (160, 1001, 2056, 32, 5),
+                                   (160, 700, 72, 128, 1), (161, 700, 72, 128, 1), (100, 5001, 4096, 40, 30), (97, 1, 7168, 104, 4)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_lora_of_about_a_hundred_rows(lib, shape):
+    M, N, K, R, L = shape
+    for bare in (0.2, 1.0):
+        p = _lora_problem(M, N, K, R, L, sum(shape), bare, bias=bare < 1, scale=bare < 1)
+        got = _check_lora(lib, p, f"{shape} {bare}")
+        space = torch.full((lib.lora_workspace(M, N, K, R, L),), 255, dtype=torch.uint8, device=DEV)
+        assert torch.equal(_check_lora(lib, p, workspace=space), got)
+    p = _lora_problem(M, N, K, R, 4, 3, bare=0.3, scale=False)
+    clean = _check_lora(lib, p)
+    a, b = p["a"].clone(), p["b"].clone()
+    a[1, 3, 7], b[2] = float("nan"), float("inf")
+    got = lib.bf16_linear_lora(p["x"], p["w"], a, b, p["ids"], p["bias"])
+    keep = (p["ids"] != 1) & (p["ids"] != 2)
+    assert torch.equal(got[keep], clean[keep]) and got[p["ids"] == 1].isnan().all()
+    assert not got[p["ids"] == 2].isfinite().any()
+
+
 def test_lora_not_finite(lib):
     """A NaN in one adapter reaches its rows alone; rows without an adapter have none of them."""
     for M, N in ((12, 72), (600, 72), (600, 5000), (2000, 1000)):
