@@ -655,11 +655,11 @@ size_t bf16_linear_mxfp4_dynamic_workspace(int M, int N, int K);
  *     id = ids[t], s = scale[id] (1 when scale is NULL);
  * a row whose id lies outside 0 .. L - 1 has no adapter.  x[M][K], w[N][K], bias[N],
  * a[L][R][K], b[L][N][R], out[M][N] bf16, scale[L] fp32, ids[M].  All sums are fp32;
- * the inner values x[t] @ a[id]^T are fp32 too, or (many rows) two bf16 values, within
- * 2^-18 of it; out is rounded once.  K % 8 == 0, R % 8 == 0, R <= 128, L <= 1024, N
- * and K <= 2^24 (else BF16L_EUNSUPPORTED).  `workspace` (256-byte aligned, needs no
- * initialisation; one call at a time): bf16_linear_lora_workspace(M, N, K, R, L)
- * bytes; a smaller one is BF16L_EINVAL.
+ * the inner values s * (x[t] @ a[id]^T) are fp32 too, or (from 65 rows on) two bf16
+ * values of one sign whose sum is within 2^-16 of it; out is rounded once.  K % 8 == 0,
+ * R % 8 == 0, R <= 128, L <= 1024, N and K <= 2^24 (else BF16L_EUNSUPPORTED).
+ * `workspace` (256-byte aligned, needs no initialisation; one call at a time):
+ * bf16_linear_lora_workspace(M, N, K, R, L) bytes; a smaller one is BF16L_EINVAL.
  *
  * No output may overlap an input or another output, but as said.
  */

@@ -19,8 +19,8 @@
 //   * SwiGLU: boxes of 16 gate rows and their 16 up rows, so that a warp's 32 lanes hold both: one shuffle for two rows
 //     of x brings them together in fp32, and out is written without the wide product's way through memory.
 // The same kernel runs the two products of a linear's adapters for many rows, ordered by adapter (rows of none last):
-//   * kInner: h = scale_e * x @ A_e^T, the groups being the adapters; out is the value in bf16 and what is left of it, in bf16
-//     again, so that the tensor cores take 16 bits of it;
+//   * kInner: h = scale_e * x @ A_e^T, the groups being the adapters; out is the value's first eight bits and the rest, rounded
+//     to eight bits, so that the tensor cores take 16 bits of it;
 //   * kOuter: x @ W^T with 256 rows of x on the M side and 256 W rows on the N side, whose tiles then go on along K with the
 //     adapters that their rows have: 16 ranks a slot, eight slots a stage, each slot a tile of B_e (16 columns, 32-byte
 //     swizzle) against the rows' h, its MMAs writing the TMEM lanes of that adapter's rows alone (the MMA's lane mask), so

@@ -102,11 +102,15 @@ __device__ __forceinline__ float silu(float g) {
     return g * q;
 }
 
-// v as the sum of two bf16 values, each the nearest to what is left: off by at most 2^-18 of it.  What is not finite stays
-// alone in the first.
+// v as the sum of two bf16 values of its own sign: v cut off after eight bits, and the rounded rest, together off by at most
+// 2^-16 of it, or 2^-132.  Products of both with an infinity then make the infinity that v's makes.  (With the first one
+// rounded they are off by at most 2^-17, but a rest of the other sign, or none, makes NaN there: so none is 0 but for v = 0.)
 __device__ __forceinline__ void two_bf16(float v, uint32_t &high, uint32_t &low) {
-    high = f32_to_bf16(v);
-    low = isfinite(v) && isfinite(bf16_to_f32((uint16_t)high)) ? f32_to_bf16(v - bf16_to_f32((uint16_t)high)) : 0u;
+    const uint32_t bits = __float_as_uint(v) >> 16, sign = bits & 0x8000u, least = v != 0.0f;  // (2^-133)
+    high = isnan(v) ? 0x7FFFu : max(bits & 0x7FFFu, least);
+    low = isfinite(v) ? f32_to_bf16(fmaxf(fabsf(v) - bf16_to_f32((uint16_t)high), 0.0f)) : 0u;
+    low = max(low, least) | sign;
+    high |= sign;
 }
 
 // Host: a tensor map of a stack of bf16 matrices [planes][halves][rows][cols], dense, with a box of box_cols x box_rows x
