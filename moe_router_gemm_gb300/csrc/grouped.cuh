@@ -88,18 +88,19 @@ __device__ __forceinline__ void mma_bf16_pair_lanes2(uint32_t d_tmem, uint32_t a
         : "memory");
 }
 
-// g / (1 + exp(-g)), to a few units in the last place: exp(-g) = 2^t (1 + r ln 2) with t + r = -g log2(e), t rounded and r
-// what the rounding left and the part of log2(e) past 24 bits; a reciprocal and a product for the quotient.  Past 2^126 the
-// reciprocal of 1 + exp(-g) is 0 (the quotient is then below 2^-119).
+// g / (1 + exp(-g)), within 2^-20 of it: exp(-g) = 2^t (1 + r ln 2) with t + r = -g log2(e), t rounded and r what the rounding
+// left and the part of log2(e) past 24 bits; a reciprocal and a product for the quotient.  The reciprocal is of a quarter of
+// 1 + exp(-g), since below 2^-126 it would be 0, and of g's quarter the product.  From where exp(-g) overflows (g = -88.73) on
+// the quotient is -0, and NaN for g = -infinity, as both are by a division in fp32.
 __device__ __forceinline__ float silu(float g) {
     constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
     const float t = -g * kLog2e;
     const float r = fmaf(-g, kLog2e, -t) - g * kLog2eLow;
     float e, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    if (fabsf(t) < 126.0f) e = fmaf(e * r, kLn2, e);  // (2^t finite and not 0, r small)
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
-    return g * q;
+    if (fabsf(t) < 128.0f) e = fmaf(e * r, kLn2, e);  // (2^t finite, r small)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(fmaf(0.25f, e, 0.25f)));
+    return 0.25f * g * q;
 }
 
 // v as the sum of two bf16 values of its own sign: v cut off after eight bits, and the rounded rest, together off by at most

@@ -1,4 +1,5 @@
-"""Values at the ends of their range in the adapters' linear: infinities in A and B."""
+"""Values at the ends of their range in the grouped and the adapters' linears: infinities in A and B, gates whose
+exponential nearly overflows."""
 import pytest
 import torch
 
@@ -69,3 +70,62 @@ def test_infinite_inner_values(lib, shape):
     p["b"][0, 4, 1], p["b"][0, 5, 1], p["b"][0, 6, 1], p["b"][1, 2, R - 1] = INF, -INF, 0.0, INF
     p["ids"][: min(M, 2)] = torch.arange(min(M, 2), device=DEV, dtype=torch.int32)
     _check_lora(lib, p, f"{shape}")
+
+
+# ---- SwiGLU ----
+
+# silu's steps, relative errors: the exponential's instruction 2^-22.5 and the correction's rounding 2^-24, the sum 2^-24, the
+# reciprocal 2^-23, the product by g 2^-24, the product by up 2^-24: below 2^-20 in all.
+SILU = 2.0 ** -20
+
+
+def _gates(lib, gate, frac, up, K):
+    """SwiGLU of one row whose gates are gate + frac (a bf16 product by one, and a bf16 bias: exact in fp32 where the sum has
+    24 bits) and whose up values are `up`."""
+    n = gate.numel()
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device=DEV)
+    x[0, 0] = 1.0
+    w = torch.zeros(1, 2 * n, K, dtype=torch.bfloat16, device=DEV)
+    w[0, :n, 0], w[0, n:, 0] = gate, up
+    bias = torch.zeros(1, 2 * n, dtype=torch.bfloat16, device=DEV)
+    bias[0, :n] = frac
+    off = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    assert (lib.grouped_workspace(1, 1, n, K, True) > 0) == (K >= 1024)  # K in parts, or whole
+    got = lib.bf16_linear_grouped(x, w, off, bias, swiglu=True)
+    assert lib.device_status() == 0
+    return got[0]
+
+
+@pytest.mark.parametrize("K", [8, 7168])
+@pytest.mark.parametrize("power", [0, 100, -20])
+def test_silu_over_its_range(lib, K, power):
+    """From the most negative gates whose exponential fp32 holds (exp(88.72) < 2^128) to large ones: off by half a bf16 step
+    and SILU."""
+    whole = torch.arange(-88, 89, device=DEV).repeat_interleave(16).float()
+    frac = (torch.arange(16, device=DEV) / 16.0).repeat(177) * torch.where(whole < 0, -1.0, 1.0)
+    keep = (whole + frac > -88.72)
+    gate, frac = whole[keep].to(torch.bfloat16), (frac[keep] + 2.0 ** -7).to(torch.bfloat16)
+    g = gate.double() + frac.double()
+    assert torch.equal(g.float().double(), g) and (g > -88.7228).all()
+    up = torch.full_like(gate, 2.0 ** power)
+    got = _gates(lib, gate, frac, up, K)
+    want = g / (1 + torch.exp(-g)) * up.double()
+    ref.check(got, want, SILU * want.abs() + 2.0 ** -133, f"2^{power}, K {K}")
+
+
+@pytest.mark.parametrize("K", [8, 7168])
+def test_silu_at_its_ends(lib, K):
+    """Infinite gates and up values, and gates past the exponential's range, as g / (1 + exp(-g)) * u in fp32 has them."""
+    rows = [(-88.0, -0.5, INF, -INF), (-88.0, -0.5, -INF, INF), (-87.0, -0.25, 2.0 ** 120, None), (-88.0, -0.5, 2.0 ** 127, None),
+            (-89.0, 0.0, 3.0, 0.0), (-200.0, 0.0, 2.0 ** 100, 0.0), (-3e38, 0.0, 1.0, 0.0), (-89.0, 0.0, INF, float("nan")),
+            (INF, 0.0, 2.0, INF), (INF, 0.0, -2.0, -INF), (INF, 0.0, 0.0, float("nan")), (-INF, 0.0, 1.0, float("nan")),
+            (3e38, 0.0, 1.0, None), (0.0, 0.0, INF, float("nan")), (0.0, 0.0, 5.0, 0.0), (2.0 ** -120, 0.0, 1.0, None),
+            (float("nan"), 0.0, 1.0, float("nan")), (1.0, 0.0, float("nan"), float("nan"))]
+    col = lambda i: torch.tensor([r[i] for r in rows], device=DEV).to(torch.bfloat16)  # noqa: E731
+    gate, frac, up = col(0), col(1), col(2)
+    g = gate.double() + frac.double()
+    want = g / (1 + torch.exp(-g)) * up.double()
+    said = torch.tensor([float("nan") if r[3] is None else r[3] for r in rows], device=DEV, dtype=torch.float64)
+    want = torch.where(torch.tensor([r[3] is None for r in rows], device=DEV), want, said)
+    got = _gates(lib, gate, frac, up, K)
+    ref.check(got, want, SILU * want.abs().nan_to_num(0.0, 0.0, 0.0) + 2.0 ** -133, f"K {K}")
