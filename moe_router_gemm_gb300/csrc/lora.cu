@@ -1,5 +1,5 @@
-// lora.cu — the low-rank adapters' share of a linear for few rows: h = scale_a * (x @ A_a^T) for each row's adapter a, then
-// out = y + h @ B_a^T, with y the shared projection in fp32, by the dense linear's own kernels between the two.
+// lora.cu — the low-rank adapters' share of a linear for few rows: h = x @ A_a^T for each row's adapter a, then
+// out = y + scale_a * h @ B_a^T, with y the shared projection in fp32, by the dense linear's own kernels between the two.
 //
 // Both kernels stand for little work (131 KB of an adapter of rank 16 and 4096 columns each way) and much latency, so each
 // spreads over the SMs: the inner one takes four ranks of a row a block, and splits K over more blocks as long as all are
@@ -85,10 +85,10 @@ __global__ void __launch_bounds__(32 * kInnerWarps) lora_inner_kernel(const Lora
         float v = part[0][r];
 #pragma unroll
         for (int i = 1; i < kInnerWarps; ++i) v += part[i][r];
-        if (a.scale) v *= __ldg(a.scale + id);
-        if (a.splits) {
+        if (a.splits) {  // (a part of the sum: the scale, which could overflow it, comes with the whole)
             static_cast<float *>(a.h)[((size_t)s * a.M + t) * a.R + r0 + r] = v;
         } else {
+            if (a.scale) v *= __ldg(a.scale + id);
             uint32_t high, low;
             two_bf16(v, high, low);
             uint16_t *h = static_cast<uint16_t *>(a.h) + (size_t)t * 2 * a.R + r0 + r;
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             }
     };
     load();
+    const float f = has && a.scale ? __ldg(a.scale + id) : 1.0f;
     pdl_wait();
     float h[8] = {};
     if (has) {
@@ -136,6 +137,8 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             h[0] += lo.x, h[1] += lo.y, h[2] += lo.z, h[3] += lo.w;
             h[4] += hi.x, h[5] += hi.y, h[6] += hi.z, h[7] += hi.w;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] *= f;
     }
     const float *from = a.y + (size_t)t * a.pitch;
     const size_t plane = (size_t)a.M * a.pitch;
@@ -200,11 +203,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 4) lora_rows_kernel(const Lora
     const uint4 *x = static_cast<const uint4 *>(a.x);
     for (int i = threadIdx.x; i < M * vectors; i += 32 * kRowWarps) sx[i] = __ldg(x + i);
     int id[M];
-    float b[M][kLoraMaxRank / 32];
+    float f[M], b[M][kLoraMaxRank / 32];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         id[m] = __ldg(a.ids + m);
         const bool has = in && (unsigned)id[m] < (unsigned)a.L;
+        f[m] = has && a.scale ? __ldg(a.scale + id[m]) : 1.0f;
 #pragma unroll
         for (int q = 0; q < kLoraMaxRank / 32; ++q) {
             const int r = 32 * q + lane;
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 4) lora_rows_kernel(const Lora
             float h = 0.0f;
 #pragma unroll 4
             for (int s = 0; s < a.splits; ++s) h += static_cast<const float *>(a.h)[((size_t)s * M + m) * a.R + r];
-            sum[m] = fmaf(h, b[m][q], sum[m]);
+            sum[m] = fmaf(f[m] * h, b[m][q], sum[m]);
         }
     }
 #pragma unroll

@@ -74,10 +74,10 @@ int grouped_splits(int P, int groups, int N, int K, int swiglu);
 int lora_outer_splits(int M, int N, int K);
 int launch_grouped(const GroupedArgs &a, int num_sms, uint32_t flags, void *stream, int32_t *status);
 
-// The adapters of a linear.  The inner values h are fp32 sums over `splits` parts of K that are still to be added up,
-// [splits][M][R], or (splits 0) [M][2][R] of bf16, value and remainder.  For rows as they come (lora.cu): the inner product,
-// and out from h and the shared product y[M][N] in fp32.  For rows ordered by adapter (grouped.cu, on tensor cores): the
-// inner product (splits 0), and out from h, x and w.
+// The adapters of a linear.  The inner values h are fp32 sums over `splits` parts of K that are still to be added up and then
+// scaled, [splits][M][R], or (splits 0) scaled, [M][2][R] of bf16, first bits and rest.  For rows as they come (lora.cu): the
+// inner product, and out from h and the shared product y[M][N] in fp32.  For rows ordered by adapter (grouped.cu, on tensor
+// cores): the inner product (splits 0), and out from h, x and w.
 constexpr int kLoraMaxRank = 128;
 struct LoraArgs {
     const void *x, *a, *b;

@@ -1,5 +1,5 @@
-"""Values at the ends of their range in the grouped and the adapters' linears: infinities in A and B, gates whose
-exponential nearly overflows."""
+"""Values at the ends of their range in the grouped and the adapters' linears: infinities in an adapter's B, gates whose
+exponential nearly overflows, scales that overflow a part of a sum."""
 import pytest
 import torch
 
@@ -70,6 +70,22 @@ def test_infinite_inner_values(lib, shape):
     p["b"][0, 4, 1], p["b"][0, 5, 1], p["b"][0, 6, 1], p["b"][1, 2, R - 1] = INF, -INF, 0.0, INF
     p["ids"][: min(M, 2)] = torch.arange(min(M, 2), device=DEV, dtype=torch.int32)
     _check_lora(lib, p, f"{shape}")
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 20, 64, 70, 150, 300])
+def test_scales_that_overflow_parts_of_a_sum(lib, M):
+    """scale * (x @ A^T) is finite, scale times a part of that sum is not; and an infinite scale."""
+    K, N, R, L = 8192, 1100, 8, 3
+    p = _adapters(M, N, K, R, L, M)
+    p["x"] = torch.ones_like(p["x"])
+    a = torch.ones(K, device=DEV)
+    a[K // 2:] = -1.0
+    a[K - 1] = -0.875  # the sum is 0.125, in any order exact
+    p["a"] = a.to(torch.bfloat16).expand(L, R, K).contiguous()
+    p["b"] = p["b"].abs()  # (so that no infinities of both signs meet)
+    p["scale"] = torch.tensor([1e37, INF, -2.5e37], device=DEV)
+    p["ids"] = (torch.arange(M, device=DEV) % L).int()
+    _check_lora(lib, p, f"{M} rows")
 
 
 # ---- SwiGLU ----
