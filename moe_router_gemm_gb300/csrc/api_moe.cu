@@ -285,6 +285,16 @@ extern "C" int bf16_combine_rows(const void *y, int64_t y_rows, const int32_t *p
 
 namespace {
 
+// What the call and its workspace's size refuse alike.
+int check_lora_sizes(int M, int N, int K, int R, int L) {
+    if (M < 0 || N <= 0 || K <= 0 || R <= 0 || L <= 0) return BF16L_EINVAL;
+    if (K % 8 != 0 || R % 8 != 0 || R > kLoraMaxRank || L > kMaxGroups || N > kMaxWidth || K > kMaxWidth)
+        return BF16L_EUNSUPPORTED;
+    if (M == 0) return BF16L_OK;
+    const uint64_t adapters = (uint64_t)L * (uint64_t)R * (uint64_t)(N > K ? N : K);
+    return M > kMaxRows || (uint64_t)M * (uint64_t)N > kMaxElements || adapters > kMaxElements ? BF16L_EINVAL : BF16L_OK;
+}
+
 // How a linear with adapters is done, by sizes alone, and the parts of its workspace.
 //   cores: the inner products row by row on CUDA cores, each row reading its own adapter from L2, or rows in adapter order
 //     on tensor cores, by estimate: (1.5 + K / 1400) us for each 1824 blocks of four ranks of a row, 6 + K / 320 us.
@@ -357,7 +367,7 @@ bool few_rows_plan(int M, int N, int K, const bf16l_device &dev, uint32_t flags,
 }  // namespace
 
 extern "C" size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L) {
-    if (M <= 0 || N <= 0 || K <= 0 || K % 8 != 0 || R <= 0 || R % 8 != 0 || R > kLoraMaxRank || L <= 0) return 0;
+    if (M == 0 || check_lora_sizes(M, N, K, R, L) != BF16L_OK) return 0;
     const LoraWay w = lora_way(M, N, K, R, L);
     return w.order + w.h + w.y;
 }
@@ -365,16 +375,14 @@ extern "C" size_t bf16_linear_lora_workspace(int M, int N, int K, int R, int L) 
 extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, const void *a, const void *b,
                                 const float *scale, const int32_t *ids, void *out, int M, int N, int K, int R, int L,
                                 void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream) {
-    if (M < 0 || N <= 0 || K <= 0 || R <= 0 || L <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
-    if (K % 8 != 0 || R % 8 != 0 || R > kLoraMaxRank || L > kMaxGroups || N > kMaxWidth || K > kMaxWidth)
-        return BF16L_EUNSUPPORTED;
-    if (M == 0) return BF16L_OK;
+    if (!flags_valid(flags)) return BF16L_EINVAL;
+    int st = check_lora_sizes(M, N, K, R, L);
+    if (st != BF16L_OK || M == 0) return st;
     if (!x || !w || !a || !b || !ids || !out) return BF16L_EINVAL;
     if (off(x, 16) || off(w, 16) || off(bias, 16) || off(a, 16) || off(b, 16) || off(out, 16) || off(scale, 4) ||
         off(ids, 4) || off(workspace, 256))
         return BF16L_EALIGN;
     const uint64_t m = (uint64_t)M, n = (uint64_t)N, k = (uint64_t)K, r = (uint64_t)R, l = (uint64_t)L;
-    if (M > kMaxRows || m * n > kMaxElements || l * r * (n > k ? n : k) > kMaxElements) return BF16L_EINVAL;
     const size_t need = bf16_linear_lora_workspace(M, N, K, R, L);
     if (!workspace || workspace_bytes < need) return BF16L_EINVAL;
     const Span outs[2] = {{out, 2 * m * n}, {workspace, need}};
@@ -383,7 +391,7 @@ extern "C" int bf16_linear_lora(const void *x, const void *w, const void *bias, 
     if (clash(outs, ins)) return BF16L_EINVAL;
     bf16l_device dev;
     int32_t *status = nullptr;
-    int st = current_device_status(&dev, &status);
+    st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
     const LoraWay way = lora_way(M, N, K, R, L);
     uint8_t *p = static_cast<uint8_t *>(workspace);

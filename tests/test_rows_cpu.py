@@ -144,3 +144,14 @@ def test_cases_are_what_they_say():
     for _ in range(300):
         w = mod.work(mod.draw(rng))
         assert 0 < w["bytes"] <= most["bytes"] and w["flops"] <= most["flops"]
+
+
+def test_lora_workspace_of_refused_sizes(lib):
+    """No bytes for the sizes that the call refuses, on either side of each bound."""
+    f = lib.lora_workspace
+    top, wide = MAX_ROWS, 1 << 24
+    assert f(16, 24, 64, 8, 1024) > 0 and f(16, wide, 64, 8, 4) > 0 and f(16, 24, wide, 8, 4) > 0 and f(top, 24, 64, 8, 4) > 0
+    for sizes in ((16, 24, 64, 8, 1025), (16, wide + 1, 64, 8, 4), (16, 24, wide + 8, 8, 4), (top + 1, 24, 64, 8, 4), ((1 << 31) - 1, 24, 64, 8, 4),
+                  (100, (1 << 31) - 1, 64, 16, 4), (16, 24, (1 << 31) - 8, 8, 4), (16, 24, 64, 8, (1 << 31) - 1), (16, wide, 64, 128, 1024),
+                  (1 << 20, (1 << 20) + 1, 64, 8, 4), (16, 24, 64, 136, 4), (0, 24, 64, 8, 4)):
+        assert f(*sizes) == 0, sizes
