@@ -229,9 +229,22 @@ extern "C" int bf16_group_rows(const int32_t *ids, int64_t tokens, int k, int gr
     return result(launch_group_rows(ids, (int)n, k, groups, false, offsets, rows, place, flags, stream));
 }
 
+namespace {
+
+// What the call and its workspace's size refuse alike.
+int check_grouped_sizes(int64_t P, int groups, int N, int K, int swiglu) {
+    if (P < 0 || groups <= 0 || N <= 0 || K <= 0) return BF16L_EINVAL;
+    if (K % 8 != 0 || groups > kMaxGroups || N > kMaxWidth || K > kMaxWidth) return BF16L_EUNSUPPORTED;
+    if (P > kMaxRows) return BF16L_EINVAL;
+    if (P == 0) return BF16L_OK;
+    const uint64_t wide = (uint64_t)N * (swiglu ? 2 : 1);
+    return (uint64_t)P * wide > kMaxElements || (uint64_t)groups * wide > kMaxElements / (uint64_t)K ? BF16L_EINVAL : BF16L_OK;
+}
+
+}  // namespace
+
 extern "C" size_t bf16_linear_grouped_workspace(int64_t P, int groups, int N, int K, int swiglu) {
-    if (P <= 0 || P > kMaxRows || groups <= 0 || groups > kMaxGroups || N <= 0 || K <= 0 || N > kMaxWidth || K > kMaxWidth)
-        return 0;
+    if (P == 0 || check_grouped_sizes(P, groups, N, K, swiglu) != BF16L_OK) return 0;
     const int s = grouped_splits((int)P, groups, N, K, swiglu);
     return s > 1 ? up256(4 * (size_t)s * (size_t)P * (size_t)sum_pitch(swiglu ? 2 * N : N)) : 0;
 }
@@ -239,15 +252,15 @@ extern "C" size_t bf16_linear_grouped_workspace(int64_t P, int groups, int N, in
 extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w, const void *bias, const int32_t *offsets,
                                    const int32_t *rows, void *out, int64_t P, int groups, int N, int K, int swiglu,
                                    void *workspace, size_t workspace_bytes, uint32_t flags, bf16l_stream_t stream) {
-    if (P < 0 || x_rows < 0 || groups <= 0 || N <= 0 || K <= 0 || !flags_valid(flags)) return BF16L_EINVAL;
-    if (K % 8 != 0 || groups > kMaxGroups || N > kMaxWidth || K > kMaxWidth) return BF16L_EUNSUPPORTED;
-    if (P > kMaxRows || x_rows > kMaxRows) return BF16L_EINVAL;
+    if (x_rows < 0 || !flags_valid(flags)) return BF16L_EINVAL;
+    int st = check_grouped_sizes(P, groups, N, K, swiglu);
+    if (st != BF16L_OK) return st;
+    if (x_rows > kMaxRows) return BF16L_EINVAL;
     if (P == 0) return BF16L_OK;  // (an empty `rows` may be NULL)
     if (!rows && x_rows != P) return BF16L_EINVAL;
     if (!x || !w || !offsets || !out || x_rows == 0) return BF16L_EINVAL;
     if (off(x, 16) || off(w, 16) || off(bias, 16) || off(out, 16) || off(offsets, 4) || off(rows, 4)) return BF16L_EALIGN;
     const uint64_t k = (uint64_t)K, wide = (uint64_t)N * (swiglu ? 2 : 1), g = (uint64_t)groups;
-    if ((uint64_t)P * wide > kMaxElements || g * wide > kMaxElements / k) return BF16L_EINVAL;
     const size_t need = bf16_linear_grouped_workspace(P, groups, N, K, swiglu);
     if (off(workspace, 256)) return BF16L_EALIGN;
     if (need && (!workspace || workspace_bytes < need)) return BF16L_EINVAL;
@@ -257,7 +270,7 @@ extern "C" int bf16_linear_grouped(const void *x, int64_t x_rows, const void *w,
     if (clash(outs, ins)) return BF16L_EINVAL;
     bf16l_device dev;
     int32_t *status = nullptr;
-    const int st = current_device_status(&dev, &status);
+    st = current_device_status(&dev, &status);
     if (st != BF16L_OK) return st;
     const GroupedArgs a = {x, w, bias, offsets, rows, out, (int)x_rows, (int)P, groups, N, K, swiglu != 0, nullptr, nullptr,
                            nullptr, 0, static_cast<float *>(workspace), need ? grouped_splits((int)P, groups, N, K, swiglu) : 1};

@@ -155,3 +155,12 @@ def test_lora_workspace_of_refused_sizes(lib):
                   (100, (1 << 31) - 1, 64, 16, 4), (16, 24, (1 << 31) - 8, 8, 4), (16, 24, 64, 8, (1 << 31) - 1), (16, wide, 64, 128, 1024),
                   (1 << 20, (1 << 20) + 1, 64, 8, 4), (16, 24, 64, 136, 4), (0, 24, 64, 8, 4)):
         assert f(*sizes) == 0, sizes
+
+
+def test_grouped_workspace_of_refused_sizes(lib):
+    """As above, at sizes of few tiles, whose K would go in parts."""
+    f = lib.grouped_workspace
+    assert f(2, 4, 64, 7168) > 0 and f(1, 1024, 4096, 1 << 18) > 0 and f(1, 1, 64, 1 << 24) > 0 and f(1, 1024, 2048, 1 << 18, True) > 0
+    for sizes in ((2, 4, 64, 7164), (2, 4, 64, 7167), (1, 1024, 4096, (1 << 18) + 8), (1, 1024, 2048, 1 << 19, True), (1, 1, 64, (1 << 24) + 8),
+                  (2, 1025, 64, 7168), (0, 4, 64, 7168), (2, 4, 0, 7168), (-2, 4, 64, 7168), (2, -4, 64, 7168)):
+        assert f(*sizes) == 0, sizes
