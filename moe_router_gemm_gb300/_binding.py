@@ -595,9 +595,14 @@ def _pitch(t, name):
     return ld if ld > cols else cols
 
 
+def _ints(*sizes) -> bool:
+    """Whether the C ABI's ints hold these sizes (ctypes would pass their low 32 bits)."""
+    return all(-(1 << 31) <= v < 1 << 31 for v in sizes)
+
+
 def _fits(what, flags, *sizes):
     """Refuse what the C ABI's 32 bits do not hold (ctypes would pass the low ones)."""
-    if not 0 <= flags < 1 << 32 or any(not -(1 << 31) <= v < 1 << 31 for v in sizes):
+    if not 0 <= flags < 1 << 32 or not _ints(*sizes):
         _raise(EINVAL, f"{what}: sizes {sizes}, flags {flags}")
 
 
@@ -789,7 +794,7 @@ def bf16_linear_mxfp4(xq, xs, wq, ws, bias=None, out=None, flags: int = 0, strea
 
 def mxfp4_dynamic_workspace(M: int, N: int, K: int) -> int:
     """Workspace bytes of bf16_linear_mxfp4_dynamic (0 where the product quantises x itself, and for sizes that it refuses)."""
-    return int(load().bf16_linear_mxfp4_dynamic_workspace(M, N, K)) if max(M, N, K) < 1 << 31 else 0
+    return int(load().bf16_linear_mxfp4_dynamic_workspace(M, N, K)) if _ints(M, N, K) else 0
 
 
 def bf16_linear_mxfp4_dynamic(x, wq, ws, bias=None, out=None, workspace=None, flags: int = 0, stream=None):
@@ -874,7 +879,7 @@ def group_rows(ids, groups: int, *, offsets=None, rows=None, place=None, flags: 
 
 def grouped_workspace(P: int, groups: int, N: int, K: int, swiglu: bool = False) -> int:
     """Workspace bytes of bf16_linear_grouped for P rows of out (0 where it needs none, and for sizes that it refuses)."""
-    return int(load().bf16_linear_grouped_workspace(P, groups, N, K, bool(swiglu))) if max(P, groups, N, K) < 1 << 31 else 0
+    return int(load().bf16_linear_grouped_workspace(P, groups, N, K, bool(swiglu))) if _ints(P, groups, N, K) else 0
 
 
 def bf16_linear_grouped(x, w, offsets, bias=None, *, rows=None, swiglu: bool = False, out=None, workspace=None, flags: int = 0,
@@ -955,7 +960,7 @@ def combine_rows(y, place, weights=None, addend=None, *, out=None, flags: int = 
 
 def lora_workspace(M: int, N: int, K: int, R: int, L: int) -> int:
     """Workspace bytes of bf16_linear_lora (0 for sizes that it refuses)."""
-    return int(load().bf16_linear_lora_workspace(M, N, K, R, L)) if max(M, N, K, R, L) < 1 << 31 else 0
+    return int(load().bf16_linear_lora_workspace(M, N, K, R, L)) if _ints(M, N, K, R, L) else 0
 
 
 def bf16_linear_lora(x, w, a, b, ids, bias=None, *, scale=None, out=None, workspace=None, flags: int = 0, stream=None):

@@ -164,3 +164,13 @@ def test_grouped_workspace_of_refused_sizes(lib):
     for sizes in ((2, 4, 64, 7164), (2, 4, 64, 7167), (1, 1024, 4096, (1 << 18) + 8), (1, 1024, 2048, 1 << 19, True), (1, 1, 64, (1 << 24) + 8),
                   (2, 1025, 64, 7168), (0, 4, 64, 7168), (2, 4, 0, 7168), (-2, 4, 64, 7168), (2, -4, 64, 7168)):
         assert f(*sizes) == 0, sizes
+
+
+@pytest.mark.parametrize("off", [-1 << 32, 1 << 32, -1 << 40])
+def test_workspaces_of_sizes_that_no_int_holds(lib, off):
+    """Their low 32 bits are a size that has a workspace."""
+    for f, sizes in ((lib.lora_workspace, (16, 24, 64, 8, 4)), (lib.grouped_workspace, (2, 4, 64, 7168)),
+                     (lib.mxfp4_dynamic_workspace, (64, 256, 64))):
+        assert f(*sizes) > 0
+        for i, v in enumerate(sizes):
+            assert f(*sizes[:i], v + off, *sizes[i + 1:]) == 0, (f.__name__, i)
