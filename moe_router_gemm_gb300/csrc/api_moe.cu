@@ -341,19 +341,15 @@ LoraWay lora_way(int M, int N, int K, int R, int L) {
 }
 
 // The dense linear's plan for few rows, where its table has no line for most sizes: the forms that lead there, by the fill of
-// the SMs (fp32 out, us; the general rule in brackets): 1 x 4096 x 4096 5.6 (10.6), 8 x 4096 x 4096 6.6 (22.2), 8 x 7168 x
-// 2048 6.2 (22.2), 16 x 4096 x 4096 7.8 (11.7), 32 x 4096 x 4096 10.4 (12.4), 61 x 2112 x 7168 10.9 (15.5), 64 x 7168 x 7168
-// 24.2 (28.2).  Narrow weights stay with the general rule.
+// the SMs (fp32 out, us; the general rule in brackets): 8 x 4096 x 4096 6.6 (22.2), 8 x 7168 x 2048 6.2 (22.2), 16 x 4096 x
+// 4096 7.8 (11.7), 32 x 4096 x 4096 10.4 (12.4), 61 x 2112 x 7168 10.9 (15.5), 64 x 7168 x 7168 24.2 (28.2).  Narrow weights
+// stay with the general rule.  One row comes here with K past 24576 alone (lora_rows): 1 x 1024 x 26000 15.4 (14.1), 1 x 2048 x
+// 26000 16.7 (21.6), 1 x 4096 x 26000 30.4 (42.8).
 bool few_rows_plan(int M, int N, int K, const bf16l_device &dev, uint32_t flags, bf16l_plan *plan) {
     bf16l_plan p = {};
     p.flags = (int32_t)flags;
-    if (N < 1024 || M > 64 || (M > 16 && N > 8192)) return false;  // (64 x 14336 x 4096: 24.9, 31 so)
-    if (M == 1) {  // a warp, or two, for each W row
-        p.kernel = BF16L_KERNEL_WARPROW;
-        p.threads = 256;
-        p.rows_per_cta = N < 4096 ? 2 : 1;
-        p.stages = 4;
-    } else if (M <= 16) {  // 16 W rows for some warps of 16 an SM, all of them at work
+    if (N < (M == 1 ? 2048 : 1024) || M > 64 || (M > 16 && N > 8192)) return false;  // (64 x 14336 x 4096: 24.9, 31 so)
+    if (M <= 16) {  // 16 W rows for some warps of 16 an SM, all of them at work
         p.kernel = BF16L_KERNEL_WARPMMA;
         p.threads = 512;
         p.tokens_per_cta = 2;

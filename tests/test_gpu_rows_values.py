@@ -1,5 +1,5 @@
 """Values at the ends of their range in the grouped and the adapters' linears: infinities in an adapter's B, gates whose
-exponential nearly overflows, scales that overflow a part of a sum."""
+exponential nearly overflows, scales that overflow a part of a sum; and rows too long for the form of one or two rows."""
 import pytest
 import torch
 
@@ -86,6 +86,17 @@ def test_scales_that_overflow_parts_of_a_sum(lib, M):
     p["scale"] = torch.tensor([1e37, INF, -2.5e37], device=DEV)
     p["ids"] = (torch.arange(M, device=DEV) % L).int()
     _check_lora(lib, p, f"{M} rows")
+
+
+@pytest.mark.parametrize("shape", [(1, 1100, 24584, 16, 3), (1, 2100, 24584, 16, 3), (1, 2048, 26000, 16, 3), (1, 1100, 28040, 8, 3), (1, 5001, 30000, 128, 2), (2, 1100, 12296, 16, 3),
+                                   (2, 1025, 20000, 40, 3), (1, 4100, 27000, 16, 2)], ids=lambda s: "x".join(map(str, s)))
+def test_one_or_two_long_rows(lib, shape):
+    """Rows past what the form of one or two rows takes, with weights of enough rows for the plan by the fill of the SMs."""
+    M, N, K, R, L = shape
+    p = _adapters(M, N, K, R, L, K)
+    p["ids"].clamp_(min=0)
+    p["bias"] = _bf16(_gen(1), N)
+    _check_lora(lib, p, f"{shape}")
 
 
 # ---- SwiGLU ----
