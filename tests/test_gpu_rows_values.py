@@ -156,3 +156,27 @@ def test_silu_at_its_ends(lib, K):
     want = torch.where(torch.tensor([r[3] is None for r in rows], device=DEV), want, said)
     got = _gates(lib, gate, frac, up, K)
     ref.check(got, want, SILU * want.abs().nan_to_num(0.0, 0.0, 0.0) + 2.0 ** -133, f"K {K}")
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [192, 4096])
+def test_infinite_and_huge_rows(lib, swiglu, K):
+    """A row with an infinity, and one whose only element is huge, against the definition: infinities of the weights' signs,
+    and with SwiGLU what silu makes of them."""
+    g = _gen(5)
+    E, N, T = 3, 100, 24
+    x = _bf16(g, T, K)
+    w = _bf16(g, E, 2 * N if swiglu else N, K, scale=K ** -0.5)
+    off = torch.tensor([0, 9, 9, T], dtype=torch.int32, device=DEV)
+    x[4, 5], x[17, 5] = INF, -INF
+    x[20], x[8] = 0.0, 0.0
+    x[20, 1], x[8, 2] = 3e38, -3e38
+    got = lib.bf16_linear_grouped(x, w, off, swiglu=swiglu)
+    want, slack = ref.grouped(x, w, off, None, None, swiglu)
+    past = want.abs() > 3.4e38 * (1 + 2.0 ** -8)  # (products of two sums of about 1e37)
+    want = torch.where(past, torch.copysign(torch.full_like(want, INF), want), want)
+    ref.check(got, want, slack, f"swiglu {swiglu}")
+    if swiglu:
+        assert got[4].isinf().any() and got[4].isnan().any() and got[20].isinf().any() and (got[20] == 0).any()
+    else:
+        assert got[4].isinf().all() and got[17].isinf().all()
