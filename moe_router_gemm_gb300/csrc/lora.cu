@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const LoraArg
             h[0] += lo.x, h[1] += lo.y, h[2] += lo.z, h[3] += lo.w;
             h[4] += hi.x, h[5] += hi.y, h[6] += hi.z, h[7] += hi.w;
         }
+    }
+    if (a.scale) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] *= f;
     }
