@@ -29,9 +29,10 @@
 // Where the tiles are too few for the SMs (PARTIAL), each tile's K is split into parts of their own tiles, which leave their
 // fp32 accumulators in a workspace, and sum_kernel adds them up in order.
 // What bounds it: with a few rows a group HBM, every sought weight being read once (512 rows over 101 weights of 7168 x 2048
-// 429 us, 8 rows over 8 of 2 x 2048 x 7168 72 us: 102% and 96% of the copy rate); with hundreds of rows a group the tensor
-// cores: 1.74 to 1.84 PFLOP/s over one to eight groups while the clock holds, 1.55 over 128 uneven ones, 1.4 where the power
-// limit takes the clock to 1.4 GHz.
+// 425 us, 8 rows over 8 of 2 x 2048 x 7168 72 us: 102% and 96% of the copy rate); with hundreds of rows a group the tensor
+// cores: 1.74 to 1.84 PFLOP/s over one to eight groups while the clock holds, 1.6 at the 1.46 GHz that the power limit leaves.
+// 128 uneven groups (65536 rows) take 17% more clocks than even ones of 512: their tiles have 202 rows on average, and every
+// tile takes all of its W rows in (a tile of 160 rows 85% of the time of one of 256).
 // Cross-CTA lifetime: a cluster barrier after set-up (every barrier exists before any remote arrival or copy) and one
 // before TMEM is freed and the CTAs exit.  Every wait is bounded.
 #include <cuda_runtime.h>

@@ -6,7 +6,7 @@
 // resident at once; the outer one adds those sums, and the projection's where that comes in parts, in order, when it reads
 // them.  Up to 64 rows the inner one also asks L2 for B_a (more rows ask for the same ones: 128 x 14336 x 4096 r16 46.2 us,
 // 43.8 without), and the outer one has its rows of B on their way before it waits for the projection.  61 x 2112 x 7168 with
-// rank 32: 17.9 us, of which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with
+// rank 32: 18.3 us, of which the projection alone takes 10.9; 8 x 4096 x 4096 with rank 16 10.4 (6.6), 64 x 4096 x 4096 with
 // rank 64 26.0.
 #include <cuda_runtime.h>
 
